@@ -60,7 +60,7 @@ extern "C" {
 #endif
 
 /* element types */
-enum { RSSM_F32 = 0, RSSM_BF16 = 1 };
+enum { RSSM_F32 = 0, RSSM_BF16 = 1, RSSM_F8E4M3 = 2 /* rms_norm_forward's output only */ };
 
 /* return codes */
 enum {
@@ -76,7 +76,8 @@ enum {
   RSSM_ST_BAD_WRITE_POS = 1, /* write_pos outside [0, L): clamped, row flushed */
   RSSM_ST_RING_OVERFLOW = 2, /* write_pos == L-1 without is_flush: row flushed */
   RSSM_ST_BAD_SLOT = 4,      /* slot index outside [0, num_slots): row skipped */
-  RSSM_ST_BAD_ROW = 8        /* ring reset or row order: row index outside [0, batch) */
+  RSSM_ST_BAD_ROW = 8,       /* ring reset or row order: row index outside [0, batch) */
+  RSSM_ST_BAD_SEQ = 16       /* cu_seqlens not 0 = first <= ... <= last = tokens: clamped */
 };
 
 /*
@@ -469,6 +470,198 @@ int replayssm_check_copy_sources(int32_t n, const int32_t* src_write_pos);
  * RSSM_OK, or RSSM_EINVAL for n_rows < 0 or a NULL pointer with n_rows > 0.
  */
 int replayssm_flush_first_order(int32_t n_rows, const uint8_t* is_flush, int32_t* row_order);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Sequence operators of the same Mamba2 layer: prefill and training.  They
+ * fill the state pools the decode entry points read, and give the gradients.
+ *
+ * Conventions beside the ones above
+ *  - Sequences are packed one after another along the token axis:
+ *    cu_seqlens [seqs + 1] int32, cu_seqlens[0] = 0, non-decreasing, last =
+ *    tokens.  Sequences may be empty.  NULL: one sequence of all tokens
+ *    (seqs = 1).  A table that breaks the rule sets RSSM_ST_BAD_SEQ and is
+ *    clamped; the results are then unspecified.
+ *  - Token strides (*_stride, in elements between two tokens' rows) let an
+ *    operand be a slice of a wider row, such as a projection's output; 0
+ *    means dense.  Rows themselves are contiguous.  Outputs are dense.
+ *  - A workspace is device memory of at least the size its *_workspace
+ *    function returns, 16-byte aligned, written before it is read: no
+ *    content is kept between calls, and calls on different streams need
+ *    workspaces of their own.
+ *  - Sums over tokens, rows and heads are added in a fixed order: the same
+ *    call gives the same bits.
+ */
+enum { RSSM_ACT_NONE = 0, RSSM_ACT_SILU = 1 };
+
+/*
+ * Causal convolution.  Supported: width 2, 3, 4; any number of channels;
+ * pointers aligned to their element type.
+ */
+typedef struct rssm_conv_dims {
+  int32_t tokens;     /* T (decode: batch rows)                             */
+  int32_t seqs;       /* sequences (ignored by the decode step)             */
+  int32_t channels;   /* C                                                  */
+  int32_t width;      /* W                                                  */
+  int32_t num_slots;  /* first dimension of the conv states                 */
+  int32_t io_dtype;   /* x, y, conv states and their gradients              */
+  int32_t activation; /* RSSM_ACT_*                                         */
+  int32_t reserved;
+  int64_t x_stride;
+  int64_t dy_stride;
+} rssm_conv_dims;
+
+/*
+ * causal_conv_forward - for each sequence i and channel c, with row p < 0
+ * taken from the W-1 rows before the sequence (row -1 the latest):
+ *     v_p = bias[c] + sum_{j<W} weight[c,j] * x[p - (W-1) + j, c]
+ *     y[p,c] = v_p * sigmoid(v_p)       (v_p with RSSM_ACT_NONE)
+ *   x [tokens, C] io_dtype; weight [C, W] float32; bias [C] float32 or NULL
+ *   initial_state [num_slots, W-1, C] io_dtype or NULL (zeros), sequence i
+ *     reads slot slot_idx[i] (NULL: i) where has_initial[i] (NULL: all)
+ *   final_state [num_slots, W-1, C] or NULL: the last W-1 rows, same slots;
+ *     may be initial_state itself
+ *   y [tokens, C] io_dtype
+ */
+int causal_conv_forward(const rssm_conv_dims* dims, const void* x, const float* weight,
+                        const float* bias, const int32_t* cu_seqlens,
+                        const void* initial_state, const uint8_t* has_initial,
+                        const int32_t* slot_idx, void* final_state, void* y,
+                        int32_t* status, hipStream_t stream);
+
+/*
+ * causal_conv_backward - gradients of causal_conv_forward's y:
+ *   dx [tokens, C] io_dtype; dweight [C, W], dbias [C] (or NULL) float32;
+ *   dinitial_state [num_slots, W-1, C] io_dtype or NULL: written for every
+ *   sequence's slot, zero where has_initial[i] is 0.
+ */
+size_t causal_conv_backward_workspace(const rssm_conv_dims* dims);
+int causal_conv_backward(const rssm_conv_dims* dims, const void* dy, const void* x,
+                         const float* weight, const float* bias,
+                         const int32_t* cu_seqlens, const void* initial_state,
+                         const uint8_t* has_initial, const int32_t* slot_idx,
+                         void* dx, float* dweight, float* dbias,
+                         void* dinitial_state, void* workspace,
+                         size_t workspace_bytes, int32_t* status, hipStream_t stream);
+
+/*
+ * causal_conv_decode - one token of dims->tokens rows: row b's window is the
+ * W-1 rows of slot slot_idx[b] (NULL: b) and x[b]; new_state's slot gets the
+ * window's last W-1 rows (new_state may be conv_state).  A slot out of range
+ * sets RSSM_ST_BAD_SLOT, its y is NaN and no state is written.
+ */
+int causal_conv_decode(const rssm_conv_dims* dims, const void* x,
+                       const void* conv_state, const float* weight,
+                       const float* bias, const int32_t* slot_idx,
+                       void* new_state, void* y, int32_t* status, hipStream_t stream);
+
+/*
+ * Root-mean-square norm.  dim <= 32768 (counted with each group rounded up to
+ * a multiple of 8); group_size divides dim; pointers aligned to their
+ * element type.
+ */
+typedef struct rssm_norm_dims {
+  int32_t rows;
+  int32_t dim;
+  int32_t group_size;     /* elements that share one mean square            */
+  int32_t io_dtype;       /* x, z, and out unless it is 8-bit               */
+  int32_t residual_dtype; /* RSSM_F32 or io_dtype                           */
+  int32_t out_dtype;      /* io_dtype or RSSM_F8E4M3                        */
+  int32_t scale_block;    /* 8-bit: 0 one scale a row, 128 one a block of   */
+                          /* 128 elements (group_size a multiple of 128)    */
+  float eps;
+  int64_t x_stride;
+  int64_t z_stride;
+  int64_t dy_stride;
+} rssm_norm_dims;
+
+/*
+ * rms_norm_forward -
+ *     h = x + residual (residual_out = h in residual_dtype; the norm reads h
+ *         as stored; residual NULL: h = x)
+ *     u = h * z * sigmoid(z)    (z NULL: u = h)
+ *     y = u * rsqrt(mean over the group of u^2 + eps) * weight
+ *   out = y in io_dtype, or the e4m3 values of y / scale with scale =
+ *   max|y| / 448 over the row or block (1 where that is 0): scale [rows] or
+ *   [rows, dim/128] float32.  residual_out may be residual.
+ */
+int rms_norm_forward(const rssm_norm_dims* dims, const void* x, const float* weight,
+                     const void* z, const void* residual, void* residual_out,
+                     void* out, float* scale, hipStream_t stream);
+
+/*
+ * rms_norm_backward - gradients of y (without residual): dx, dz (z given)
+ * [rows, dim] io_dtype, dweight [dim] float32.
+ */
+size_t rms_norm_backward_workspace(const rssm_norm_dims* dims);
+int rms_norm_backward(const rssm_norm_dims* dims, const void* dy, const void* x,
+                      const float* weight, const void* z, void* dx,
+                      float* dweight, void* dz, void* workspace,
+                      size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Selective scan over whole sequences: the recurrence of ssu_standard_decode
+ * applied to every token.  Supported: headdim in {32, 64, 128}, dstate in
+ * {16, 32, 64, 128, 256}, ngroups divides nheads.  x, z, B, C and dy:
+ * 16-byte aligned, with token strides that are multiples of 16 bytes.
+ */
+typedef struct rssm_scan_dims {
+  int32_t tokens;
+  int32_t seqs;
+  int32_t nheads;
+  int32_t headdim;
+  int32_t dstate;
+  int32_t ngroups;
+  int32_t num_slots;   /* first dimension of initial_state / final_state    */
+  int32_t io_dtype;    /* x, dt, B, C, z, y, dy and the gradients of x, dt, */
+                       /* B, C                                              */
+  int32_t state_dtype; /* initial_state, final_state                        */
+  int32_t dt_softplus; /* nonzero: dt = softplus(dt + dt_bias)              */
+  int64_t x_stride;    /* elements between two tokens of x [T, H, P]        */
+  int64_t dt_stride;   /* dt [T, H]                                         */
+  int64_t B_stride;    /* B [T, G, N]                                       */
+  int64_t C_stride;
+  int64_t z_stride;
+  int64_t dy_stride;
+} rssm_scan_dims;
+
+/*
+ * ssu_scan_forward - for every sequence i (slot s = slot_idx[i], NULL: i) and
+ * head h, from S = initial_state[s, h] (zeros where initial_state is NULL or
+ * has_initial[i] is 0), token by token
+ *     S = exp(dt*A[h]) * S + dt * outer(x, B);  y = S @ C + D[h] * x
+ *     y *= z * sigmoid(z)    (z not NULL)
+ * and final_state[s, h] = S (final_state may be initial_state, or NULL).
+ * y [tokens, H, P] io_dtype.  A slot out of range sets RSSM_ST_BAD_SLOT: its
+ * sequence starts from zeros and stores no state.
+ */
+size_t ssu_scan_forward_workspace(const rssm_scan_dims* dims);
+int ssu_scan_forward(const rssm_scan_dims* dims, const void* x, const void* dt, const float* A,
+                     const void* B, const void* C, const float* D, const void* z,
+                     const float* dt_bias, const int32_t* cu_seqlens,
+                     const void* initial_state, const uint8_t* has_initial,
+                     const int32_t* slot_idx, void* final_state, void* y,
+                     void* workspace, size_t workspace_bytes, int32_t* status,
+                     hipStream_t stream);
+
+/*
+ * ssu_scan_backward - gradients of ssu_scan_forward without z, given dy and
+ * dfinal_state [seqs, H, P, N] float32 (the gradient of each sequence's last
+ * state, by sequence and not by slot; NULL: zeros):
+ *   dx [T, H, P], ddt [T, H], dB, dC [T, G, N] io_dtype;
+ *   dA, dD, ddt_bias [H] float32 (dD and ddt_bias may be NULL);
+ *   dinitial_state [seqs, H, P, N] float32 by sequence, zeros where
+ *   has_initial[i] is 0 (NULL: not computed).
+ */
+size_t ssu_scan_backward_workspace(const rssm_scan_dims* dims);
+int ssu_scan_backward(const rssm_scan_dims* dims, const void* dy, const void* x, const void* dt,
+                      const float* A, const void* B, const void* C, const float* D,
+                      const float* dt_bias, const int32_t* cu_seqlens,
+                      const void* initial_state, const uint8_t* has_initial,
+                      const int32_t* slot_idx, const float* dfinal_state, void* dx,
+                      void* ddt, void* dB, void* dC, float* dA, float* dD,
+                      float* ddt_bias, float* dinitial_state, void* workspace,
+                      size_t workspace_bytes, int32_t* status, hipStream_t stream);
 
 /* Human-readable text of a return code (static storage). */
 const char* replayssm_strerror(int code);

@@ -23,6 +23,8 @@ __all__ = [
     "replayssm_gdn_spec_commit", "replayssm_gdn_spec_verify_flush", "replayssm_gdn_spec_advance",
     "kda_standard_decode", "replayssm_kda_decode", "build_metadata", "flush_first_order",
     "check_copy_sources", "library_path", "load",
+    "ssu_scan_forward", "ssu_scan_backward", "causal_conv_forward", "causal_conv_backward",
+    "causal_conv_decode", "rms_norm_forward", "rms_norm_backward", "ST_BAD_SEQ",
     "RssmError", "ST_BAD_WRITE_POS", "ST_RING_OVERFLOW", "ST_BAD_SLOT",
     "ST_BAD_ROW", "EXPORTS",
 ]
@@ -30,13 +32,17 @@ __all__ = [
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libreplayssm.so")
 
 F32, BF16 = 0, 1
-ST_BAD_WRITE_POS, ST_RING_OVERFLOW, ST_BAD_SLOT, ST_BAD_ROW = 1, 2, 4, 8
+ST_BAD_WRITE_POS, ST_RING_OVERFLOW, ST_BAD_SLOT, ST_BAD_ROW, ST_BAD_SEQ = 1, 2, 4, 8, 16
 EXPORTS = ("ssu_standard_decode", "replayssm_decode", "replayssm_ring_reset",
            "gdn_standard_decode", "replayssm_gdn_decode", "replayssm_gdn_spec_verify",
            "replayssm_gdn_spec_commit", "replayssm_gdn_spec_verify_flush",
            "replayssm_gdn_spec_advance", "kda_standard_decode", "replayssm_kda_decode",
            "replayssm_build_metadata", "replayssm_decode_ordered", "replayssm_flush_first_order",
-           "replayssm_check_copy_sources", "replayssm_strerror", "replayssm_abi_version")
+           "replayssm_check_copy_sources", "replayssm_strerror", "replayssm_abi_version",
+           "ssu_scan_forward", "ssu_scan_forward_workspace", "ssu_scan_backward",
+           "ssu_scan_backward_workspace", "causal_conv_forward", "causal_conv_backward",
+           "causal_conv_backward_workspace", "causal_conv_decode", "rms_norm_forward",
+           "rms_norm_backward", "rms_norm_backward_workspace")
 
 _DT = {torch.float32: F32, torch.bfloat16: BF16}
 
@@ -109,6 +115,7 @@ def load():
     lib.replayssm_strerror.argtypes = [ctypes.c_int]
     lib.replayssm_strerror.restype = ctypes.c_char_p
     lib.replayssm_abi_version.restype = ctypes.c_int
+    sequence.bind(lib)
     _lib = lib
     return lib
 
@@ -577,3 +584,8 @@ def replayssm_gdn_spec_advance(k_ring, g_ring, v_ring, beta_ring, slot_idx, writ
         _ptr(is_flush), _ptr(accepted), _ptr(force_flush), _ptr(next_write_pos),
         _ptr(next_is_flush), _ptr(status), _stream(stream))
     _check("replayssm_gdn_spec_advance", rc)
+
+from . import sequence  # noqa: E402  (uses the helpers above)
+from .sequence import (  # noqa: E402
+    causal_conv_backward, causal_conv_decode, causal_conv_forward, rms_norm_backward,
+    rms_norm_forward, ssu_scan_backward, ssu_scan_forward)

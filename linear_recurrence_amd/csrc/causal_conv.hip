@@ -1,0 +1,560 @@
+// Short causal convolution over the channels of a Mamba2 layer: whole packed
+// sequences (forward, backward) and one decode step.
+//
+//   v_t = bias + sum_j w_j x_{t-(W-1)+j},  y_t = silu(v_t)  (or v_t)
+//
+// Channels are contiguous, so a lane owns eight of them (16 bytes of bf16) and
+// walks along the tokens with the window in registers: every x row is read
+// once per run of tokens, plus W-1 rows where a run starts.  All of it is
+// memory bound (2 W flops per 4 bytes).
+#include "rssm_host.hpp"
+#include "seq_device.hpp"
+
+namespace rssm {
+
+struct ConvArgs {
+  const void* x;
+  const float* weight;
+  const float* bias;
+  const int32_t* cu;
+  const void* init;
+  const uint8_t* has_init;
+  const int32_t* slot_idx;
+  void* final_state;
+  void* y;
+  const void* dy;
+  void* dx;
+  void* dinit;
+  float* part;
+  float* dweight;
+  float* dbias;
+  int32_t* status;
+  long x_stride, dy_stride;
+  int32_t tokens, seqs, channels, num_slots, silu, runs;
+};
+
+constexpr int kFwdRun = 32;   // tokens of a forward run
+constexpr int kBwdRun = 32;   // tokens of one wave's backward run
+constexpr int kBwdWaves = 4;  // runs of one backward workgroup
+
+template <int W>
+struct Taps {
+  float w[W][8], b[8];
+  __device__ inline void load(const ConvArgs& a, int c0, int n) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      b[k] = a.bias && k < n ? a.bias[c0 + k] : 0.f;
+#pragma unroll
+      for (int j = 0; j < W; ++j) w[j][k] = k < n ? a.weight[(long)(c0 + k) * W + j] : 0.f;
+    }
+  }
+  // v of the window h[0..W-1] (oldest first), lane's k-th channel
+  __device__ inline float dot(const float (&h)[W][8], int k) const {
+    float v = b[k];
+#pragma unroll
+    for (int j = 0; j < W; ++j) v = fmaf(w[j][k], h[j][k], v);
+    return v;
+  }
+};
+
+// The slot of sequence i, or -1 (and the status bit) when it is out of range.
+__device__ static inline int conv_slot(const ConvArgs& a, int i) {
+  const int s = a.slot_idx ? a.slot_idx[i] : i;
+  if (s >= 0 && s < a.num_slots) return s;
+  if (a.status) atomicOr(a.status, RSSM_ST_BAD_SLOT);
+  return -1;
+}
+
+// Forward.  Grid: (channel blocks of 64 lanes) x (seqs + runs).  The first
+// `seqs` tiles take one sequence's first W-1 tokens and its final state, so
+// that every read of an initial state and the write of the final one are the
+// same lane's, in that order, and the two may be one pool.  The others take a
+// run of tokens and skip the first W-1 of each sequence.
+template <typename T, int W>
+__global__ void __launch_bounds__(64) conv_fwd_kernel(const ConvArgs a) {
+  const int cblocks = (a.channels + 511) / 512;
+  // a contiguous range of runs per XCD: the rows two runs share stay in one L2
+  const int id = xcd_tile(blockIdx.x, gridDim.x);
+  const int tile = id / cblocks, c0 = (id % cblocks) * 512 + threadIdx.x * 8;
+  if (c0 >= a.channels) return;
+  const int n = a.channels - c0 < 8 ? a.channels - c0 : 8;
+  Taps<W> tp;
+  tp.load(a, c0, n);
+  float h[W][8];
+  const auto emit = [&](long t) {
+    float o[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float v = tp.dot(h, k);
+      o[k] = a.silu ? v * sigmoid_f32(v) : v;
+    }
+    store8<T>(a.y, t * a.channels + c0, n, o);
+  };
+  const auto shift = [&]() {
+#pragma unroll
+    for (int j = 0; j + 1 < W; ++j)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) h[j][k] = h[j + 1][k];
+  };
+  if (tile < a.seqs) {
+    const SeqSpan sp = seq_span(a.cu, tile, a.seqs, a.tokens);
+    if (sp.bad && a.status && c0 == 0) atomicOr(a.status, RSSM_ST_BAD_SEQ);
+    const bool pool = a.init || a.final_state;
+    const int slot = pool ? conv_slot(a, tile) : -1;
+    const bool has = a.init && slot >= 0 && (!a.has_init || a.has_init[tile]);
+    float s[W][8];  // the W-1 rows before the sequence
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s[j][k] = 0.f;
+      if (has) load8<T>(a.init, ((long)slot * (W - 1) + j) * a.channels + c0, n, s[j]);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) h[j + 1][k] = s[j][k];
+    }
+#pragma unroll
+    for (int p = 0; p < W - 1; ++p) {
+      if (p < sp.len) {
+        shift();
+        load8<T>(a.x, (long)(sp.start + p) * a.x_stride + c0, n, h[W - 1]);
+        emit(sp.start + p);
+      }
+    }
+    if (a.final_state && slot >= 0) {
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j) {
+        const int p = sp.len - (W - 1) + j;  // < 0: row p + W-1 before the sequence
+        float r[8];
+        if (p >= 0) {
+          load8<T>(a.x, (long)(sp.start + p) * a.x_stride + c0, n, r);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            r[k] = s[0][k];
+#pragma unroll
+            for (int q = 1; q < W - 1; ++q) r[k] = p + W - 1 == q ? s[q][k] : r[k];
+          }
+        }
+        store8<T>(a.final_state, ((long)slot * (W - 1) + j) * a.channels + c0, n, r);
+      }
+    }
+    return;
+  }
+  const int t0 = (tile - a.seqs) * kFwdRun;
+  const int t1 = t0 + kFwdRun < a.tokens ? t0 + kFwdRun : a.tokens;
+  int i = seq_of_token(a.cu, a.seqs, t0);
+#pragma unroll
+  for (int j = 1; j < W; ++j) {
+    const int t = t0 - W + j;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) h[j][k] = 0.f;
+    if (t >= 0) load8<T>(a.x, (long)t * a.x_stride + c0, n, h[j]);
+  }
+  int t = t0;
+  while (t < t1) {
+    SeqSpan sp = seq_span(a.cu, i, a.seqs, a.tokens);
+    const bool last = i + 1 >= a.seqs;
+    int end = last ? t1 : sp.start + sp.len;
+    if (end > t1) end = t1;
+    const int from = sp.start + W - 1, to = sp.start + sp.len;
+    constexpr int U = 4;  // rows in flight
+    for (; t < end; t += U) {
+      float r[U][8];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (t + u < end) load8<T>(a.x, (long)(t + u) * a.x_stride + c0, n, r[u]);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (t + u < end) {
+          shift();
+#pragma unroll
+          for (int k = 0; k < 8; ++k) h[W - 1][k] = r[u][k];
+          if (t + u >= from && t + u < to) emit(t + u);
+        }
+      }
+    }
+    t = end;
+    if (last) break;
+    ++i;
+  }
+}
+
+// Backward.  dv_t = dy_t silu'(v_t); dx_t = sum_j w_j dv_{t+(W-1)-j};
+// dw_j = sum_t dv_t x_{t-(W-1)+j}; db = sum_t dv_t.  A wave walks its run and
+// W-1 tokens past it (their dv again, so that waves need nothing from each
+// other); the sums over tokens stay in registers, are joined over the
+// workgroup's waves in LDS, in wave order, and go to one row of partial sums
+// per workgroup, which a second launch adds in row order: the result does not
+// depend on timing.
+template <typename T, int W>
+__global__ void __launch_bounds__(64 * kBwdWaves) conv_bwd_kernel(const ConvArgs a) {
+  __shared__ float red[kBwdWaves][W + 1][64][9];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int cblocks = (a.channels + 511) / 512;
+  const int id = xcd_tile(blockIdx.x, gridDim.x);
+  const int tile = id / cblocks, cb = (id % cblocks) * 512, c0 = cb + lane * 8;
+  const int n = a.channels - c0 < 8 ? (a.channels - c0 < 0 ? 0 : a.channels - c0) : 8;
+  float dw[W][8] = {}, db[8] = {};
+  Taps<W> tp;
+  tp.load(a, c0, n);
+  const int t0 = (tile * kBwdWaves + wave) * kBwdRun;
+  const int t1 = t0 + kBwdRun < a.tokens ? t0 + kBwdRun : a.tokens;
+  if (t0 < t1 && n > 0) {
+    int t = t0;
+    for (int i = seq_of_token(a.cu, a.seqs, t0); t < t1 && i < a.seqs; ++i) {
+      const SeqSpan sp = seq_span(a.cu, i, a.seqs, a.tokens);
+      const int send = sp.start + sp.len;
+      const int b = send < t1 ? send : t1;  // this piece: tokens [t, b) of sequence i
+      if (b <= t || t < sp.start) continue;
+      float h[W][8], g[W][8];  // windows of x and dv, oldest first
+      int slot = -1;
+      if (t - sp.start < W - 1 && a.init && (!a.has_init || a.has_init[i])) slot = conv_slot(a, i);
+#pragma unroll
+      for (int j = 1; j < W; ++j) {
+        const int p = t - sp.start - W + j;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) h[j][k] = 0.f, g[j][k] = 0.f;
+        if (p >= 0)
+          load8<T>(a.x, (long)(sp.start + p) * a.x_stride + c0, n, h[j]);
+        else if (slot >= 0)
+          load8<T>(a.init, ((long)slot * (W - 1) + p + W - 1) * a.channels + c0, n, h[j]);
+      }
+      const int stop = b + W - 1;
+      constexpr int U = 4;
+      for (int u0 = t; u0 < stop; u0 += U) {
+        float rx[U][8], ro[U][8];
+#pragma unroll
+        for (int q = 0; q < U; ++q) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) rx[q][k] = 0.f, ro[q][k] = 0.f;
+          if (u0 + q < stop && u0 + q < send) {
+            load8<T>(a.x, (long)(u0 + q) * a.x_stride + c0, n, rx[q]);
+            load8<T>(a.dy, (long)(u0 + q) * a.dy_stride + c0, n, ro[q]);
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < U; ++q) {
+          const int u = u0 + q;
+          if (u < stop) {
+#pragma unroll
+            for (int j = 0; j + 1 < W; ++j)
+#pragma unroll
+              for (int k = 0; k < 8; ++k) h[j][k] = h[j + 1][k], g[j][k] = g[j + 1][k];
+            float o[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              h[W - 1][k] = rx[q][k];
+              float d = ro[q][k];  // 0 past the sequence's end
+              if (a.silu) {
+                const float v = tp.dot(h, k), s = sigmoid_f32(v);
+                d *= s * fmaf(v, 1.f - s, 1.f);
+              }
+              g[W - 1][k] = u < send ? d : 0.f;
+              if (u < b) {
+                db[k] += d;
+#pragma unroll
+                for (int j = 0; j < W; ++j) dw[j][k] = fmaf(d, h[j][k], dw[j][k]);
+              }
+              float s = 0.f;
+#pragma unroll
+              for (int j = 0; j < W; ++j) s = fmaf(tp.w[j][k], g[W - 1 - j][k], s);
+              o[k] = s;
+            }
+            if (u - (W - 1) >= t) store8<T>(a.dx, (long)(u - (W - 1)) * a.channels + c0, n, o);
+          }
+        }
+      }
+      t = b;
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    red[wave][W][lane][k] = db[k];
+#pragma unroll
+    for (int j = 0; j < W; ++j) red[wave][j][lane][k] = dw[j][k];
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < (W + 1) * 512; e += 64 * kBwdWaves) {
+    const int j = e / 512, c = e % 512;
+    if (cb + c < a.channels) {
+      float s = 0.f;
+#pragma unroll
+      for (int w = 0; w < kBwdWaves; ++w) s += red[w][j][c >> 3][c & 7];
+      a.part[((long)tile * (W + 1) + j) * a.channels + cb + c] = s;
+    }
+  }
+}
+
+// dweight [C, W] and dbias [C] from the workgroups' partial sums, rows in
+// order within each of four quarters; and (tiles past the columns) the
+// gradient of the initial states from each sequence's first W-1 tokens.
+template <typename T, int W>
+__global__ void __launch_bounds__(256) conv_bwd_join_kernel(const ConvArgs a) {
+  const long cols = (long)(W + 1) * a.channels;
+  const int cblk = (int)((cols + 63) / 64);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  if ((int)blockIdx.x < cblk) {
+    __shared__ float red[4][64];
+    const long col = (long)blockIdx.x * 64 + lane;
+    float s = 0.f;
+    if (col < cols) {
+      const int per = (a.runs + 3) / 4;
+      const int r1 = (wave + 1) * per < a.runs ? (wave + 1) * per : a.runs;
+#pragma unroll 8
+      for (int r = wave * per; r < r1; ++r) s += a.part[(long)r * cols + col];
+    }
+    red[wave][lane] = s;
+    __syncthreads();
+    if (wave == 0 && col < cols) {
+      s = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+      const int j = (int)(col / a.channels), c = (int)(col % a.channels);
+      if (j < W) {
+        a.dweight[(long)c * W + j] = s;
+      } else if (a.dbias) {
+        a.dbias[c] = s;
+      }
+    }
+    return;
+  }
+  // dinit_k = sum_{j<=k} w_j dv_{k-j}, k = 0 .. W-2 (row k lies W-1-k before
+  // the sequence)
+  const int lanes = (a.channels + 7) / 8;
+  const long id = (long)(blockIdx.x - cblk) * 256 + threadIdx.x;
+  const int i = (int)(id / lanes), c0 = (int)(id % lanes) * 8;
+  if (i >= a.seqs) return;
+  const int n = a.channels - c0 < 8 ? a.channels - c0 : 8;
+  const SeqSpan sp = seq_span(a.cu, i, a.seqs, a.tokens);
+  const int slot = conv_slot(a, i);
+  if (slot < 0) return;
+  const bool has = !a.has_init || a.has_init[i];
+  Taps<W> tp;
+  tp.load(a, c0, n);
+  float h[W][8], g[W][8] = {};  // g[p]: dv of token p
+  const bool live = has && a.init;
+#pragma unroll
+  for (int j = 1; j < W; ++j) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) h[j][k] = 0.f;
+    if (live) load8<T>(a.init, ((long)slot * (W - 1) + j - 1) * a.channels + c0, n, h[j]);
+  }
+#pragma unroll
+  for (int p = 0; p < W - 1; ++p) {
+    if (p < sp.len && live) {
+      float ro[8];
+#pragma unroll
+      for (int j = 0; j + 1 < W; ++j)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) h[j][k] = h[j + 1][k];
+      load8<T>(a.x, (long)(sp.start + p) * a.x_stride + c0, n, h[W - 1]);
+      load8<T>(a.dy, (long)(sp.start + p) * a.dy_stride + c0, n, ro);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        float d = ro[k];
+        if (a.silu) {
+          const float v = tp.dot(h, k), s = sigmoid_f32(v);
+          d *= s * fmaf(v, 1.f - s, 1.f);
+        }
+        g[p][k] = d;
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < W - 1; ++k) {
+    float o[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      o[q] = 0.f;
+#pragma unroll
+      for (int j = 0; j <= k; ++j) o[q] = fmaf(tp.w[j][q], g[k - j][q], o[q]);
+    }
+    store8<T>(a.dinit, ((long)slot * (W - 1) + k) * a.channels + c0, n, o);
+  }
+}
+
+// One decode step: the window is the W-1 state rows and x; the state moves on
+// by one row.  A lane reads all it needs of its channels before it writes, so
+// the new state may be the old one.
+template <typename T, int W>
+__global__ void __launch_bounds__(64) conv_step_kernel(const ConvArgs a) {
+  const int cblocks = (a.channels + 511) / 512;
+  const int row = blockIdx.x / cblocks, c0 = (blockIdx.x % cblocks) * 512 + threadIdx.x * 8;
+  if (c0 >= a.channels) return;
+  const int n = a.channels - c0 < 8 ? a.channels - c0 : 8;
+  const int slot = conv_slot(a, row);
+  float o[8], h[W][8];
+  Taps<W> tp;
+  tp.load(a, c0, n);
+  load8<T>(a.x, (long)row * a.x_stride + c0, n, h[W - 1]);
+  if (slot >= 0) {
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j)
+      load8<T>(a.init, ((long)slot * (W - 1) + j) * a.channels + c0, n, h[j]);
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j)
+      store8<T>(a.final_state, ((long)slot * (W - 1) + j) * a.channels + c0, n, h[j + 1]);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float v = tp.dot(h, k);
+      o[k] = a.silu ? v * sigmoid_f32(v) : v;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) o[k] = __builtin_nanf("");
+  }
+  store8<T>(a.y, (long)row * a.channels + c0, n, o);
+}
+
+static int conv_check(const rssm_conv_dims* d) {
+  if (!d) return RSSM_EINVAL;
+  if (d->tokens < 0 || d->seqs < 0 || d->channels < 1 || d->num_slots < 0) return RSSM_EINVAL;
+  if (d->activation != RSSM_ACT_NONE && d->activation != RSSM_ACT_SILU) return RSSM_EINVAL;
+  if (!valid_dtype(d->io_dtype)) return RSSM_EDTYPE;
+  if (d->width < 2 || d->width > 4) return RSSM_ESHAPE;
+  // pointers are aligned to their element type and the grids fit 31 bits
+  if (((long)d->tokens + d->seqs + 1) * ((d->channels + 511) / 512) > 0x7fffffffL)
+    return RSSM_ESHAPE;
+  return RSSM_OK;
+}
+
+static bool elt_aligned(const void* p, int32_t dtype) {
+  return (reinterpret_cast<uintptr_t>(p) & (dtype == RSSM_F32 ? 3u : 1u)) == 0;
+}
+
+#define RSSM_CONV_PICK(name, d)                                                        \
+  ((d).io_dtype == RSSM_F32                                                            \
+       ? ((d).width == 2   ? reinterpret_cast<const void*>(&name<float, 2>)            \
+          : (d).width == 3 ? reinterpret_cast<const void*>(&name<float, 3>)            \
+                           : reinterpret_cast<const void*>(&name<float, 4>))           \
+       : ((d).width == 2   ? reinterpret_cast<const void*>(&name<bf16, 2>)             \
+          : (d).width == 3 ? reinterpret_cast<const void*>(&name<bf16, 3>)             \
+                           : reinterpret_cast<const void*>(&name<bf16, 4>)))
+
+static long bwd_tiles(const rssm_conv_dims& d) {
+  const long per = kBwdRun * kBwdWaves;
+  return (d.tokens + per - 1) / per;
+}
+
+}  // namespace rssm
+
+using namespace rssm;
+
+static ConvArgs conv_args(const rssm_conv_dims& d) {
+  ConvArgs a{};
+  a.x_stride = d.x_stride ? d.x_stride : d.channels;
+  a.dy_stride = d.dy_stride ? d.dy_stride : d.channels;
+  a.tokens = d.tokens;
+  a.seqs = d.seqs;
+  a.channels = d.channels;
+  a.num_slots = d.num_slots;
+  a.silu = d.activation == RSSM_ACT_SILU;
+  return a;
+}
+
+extern "C" int causal_conv_forward(const rssm_conv_dims* dims, const void* x, const float* weight,
+                                   const float* bias, const int32_t* cu_seqlens,
+                                   const void* initial_state, const uint8_t* has_initial,
+                                   const int32_t* slot_idx, void* final_state, void* y,
+                                   int32_t* status, hipStream_t stream) {
+  int rc = conv_check(dims);
+  if (rc) return rc;
+  const rssm_conv_dims& d = *dims;
+  if (d.seqs == 0) return d.tokens == 0 ? RSSM_OK : RSSM_EINVAL;
+  if (!weight || (d.tokens > 0 && (!x || !y))) return RSSM_EINVAL;
+  if (!cu_seqlens && d.seqs != 1) return RSSM_EINVAL;
+  if (x && (d.x_stride != 0 && d.x_stride < d.channels)) return RSSM_EINVAL;
+  if (!elt_aligned(x, d.io_dtype) || !elt_aligned(y, d.io_dtype) ||
+      !elt_aligned(initial_state, d.io_dtype) || !elt_aligned(final_state, d.io_dtype))
+    return RSSM_EINVAL;
+  ConvArgs a = conv_args(d);
+  a.x = x;
+  a.weight = weight;
+  a.bias = bias;
+  a.cu = cu_seqlens;
+  a.init = initial_state;
+  a.has_init = has_initial;
+  a.slot_idx = slot_idx;
+  a.final_state = final_state;
+  a.y = y;
+  a.status = status;
+  const long tiles = d.seqs + ((long)d.tokens + kFwdRun - 1) / kFwdRun;
+  return launch_kernel(RSSM_CONV_PICK(conv_fwd_kernel, d),
+                       (unsigned)(tiles * ((d.channels + 511) / 512)), 64, 0, stream, a);
+}
+
+extern "C" size_t causal_conv_backward_workspace(const rssm_conv_dims* dims) {
+  if (conv_check(dims)) return 0;
+  return (size_t)bwd_tiles(*dims) * (dims->width + 1) * dims->channels * sizeof(float);
+}
+
+extern "C" int causal_conv_backward(const rssm_conv_dims* dims, const void* dy, const void* x,
+                                    const float* weight, const float* bias,
+                                    const int32_t* cu_seqlens, const void* initial_state,
+                                    const uint8_t* has_initial, const int32_t* slot_idx, void* dx,
+                                    float* dweight, float* dbias, void* dinitial_state,
+                                    void* workspace, size_t workspace_bytes, int32_t* status,
+                                    hipStream_t stream) {
+  int rc = conv_check(dims);
+  if (rc) return rc;
+  const rssm_conv_dims& d = *dims;
+  if (!weight || !dweight) return RSSM_EINVAL;
+  if (d.tokens > 0 && (!x || !dy || !dx || !workspace || d.seqs < 1)) return RSSM_EINVAL;
+  if (!cu_seqlens && d.seqs > 1) return RSSM_EINVAL;
+  if ((d.x_stride != 0 && d.x_stride < d.channels) ||
+      (d.dy_stride != 0 && d.dy_stride < d.channels))
+    return RSSM_EINVAL;
+  if (!elt_aligned(x, d.io_dtype) || !elt_aligned(dy, d.io_dtype) || !elt_aligned(dx, d.io_dtype) ||
+      !elt_aligned(initial_state, d.io_dtype) || !elt_aligned(dinitial_state, d.io_dtype))
+    return RSSM_EINVAL;
+  if (workspace_bytes < causal_conv_backward_workspace(dims)) return RSSM_EINVAL;
+  ConvArgs a = conv_args(d);
+  a.x = x;
+  a.dy = dy;
+  a.weight = weight;
+  a.bias = bias;
+  a.cu = cu_seqlens;
+  a.init = initial_state;
+  a.has_init = has_initial;
+  a.slot_idx = slot_idx;
+  a.dx = dx;
+  a.dweight = dweight;
+  a.dbias = dbias;
+  a.dinit = dinitial_state;
+  a.part = static_cast<float*>(workspace);
+  a.status = status;
+  a.runs = (int32_t)bwd_tiles(d);
+  if (a.runs > 0) {
+    rc = launch_kernel(RSSM_CONV_PICK(conv_bwd_kernel, d),
+                       (unsigned)((long)a.runs * ((d.channels + 511) / 512)), 64 * kBwdWaves, 0,
+                       stream, a);
+    if (rc) return rc;
+  }
+  const long cols = (long)(d.width + 1) * d.channels;
+  const long init = dinitial_state ? ((long)d.seqs * ((d.channels + 7) / 8) + 255) / 256 : 0;
+  return launch_kernel(RSSM_CONV_PICK(conv_bwd_join_kernel, d),
+                       (unsigned)((cols + 63) / 64 + init), 256, 0, stream, a);
+}
+
+extern "C" int causal_conv_decode(const rssm_conv_dims* dims, const void* x,
+                                  const void* conv_state, const float* weight, const float* bias,
+                                  const int32_t* slot_idx, void* new_state, void* y,
+                                  int32_t* status, hipStream_t stream) {
+  int rc = conv_check(dims);
+  if (rc) return rc;
+  const rssm_conv_dims& d = *dims;
+  if (d.tokens == 0) return RSSM_OK;
+  if (!x || !conv_state || !weight || !new_state || !y) return RSSM_EINVAL;
+  if (d.x_stride != 0 && d.x_stride < d.channels) return RSSM_EINVAL;
+  if (!elt_aligned(x, d.io_dtype) || !elt_aligned(y, d.io_dtype) ||
+      !elt_aligned(conv_state, d.io_dtype) || !elt_aligned(new_state, d.io_dtype))
+    return RSSM_EINVAL;
+  ConvArgs a = conv_args(d);
+  a.x = x;
+  a.weight = weight;
+  a.bias = bias;
+  a.init = conv_state;
+  a.slot_idx = slot_idx;
+  a.final_state = new_state;
+  a.y = y;
+  a.status = status;
+  return launch_kernel(RSSM_CONV_PICK(conv_step_kernel, d),
+                       (unsigned)((long)d.tokens * ((d.channels + 511) / 512)), 64, 0, stream, a);
+}

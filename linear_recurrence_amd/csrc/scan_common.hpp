@@ -1,0 +1,227 @@
+// Shared pieces of the selective scan's forward and backward kernels.
+//
+// Tokens of a sequence are taken in chunks of 64.  Within a chunk, with a_t
+// the running sum of dt*A (inclusive) and S the state before it,
+//   y_t   = e^{a_t} S C_t + sum_{s<=t} e^{a_t-a_s} dt_s (C_t.B_s) x_s + D x_t
+//   S'    = e^{a_Q} S + sum_s e^{a_Q-a_s} dt_s x_s B_s^T
+// so all the work is small dense products for the matrix cores.
+//
+// Fragments.  Both operands of a 16x16x32 product give lane l the eight
+// k-values of its row (A) or column (B) l%16; which k they are is free as long
+// as both agree.  Order C: k = 8g + e (g = l/16), contiguous.  Order D:
+// k = 4g + e for e < 4 and 16 + 4g + e - 4 above: what a lane holds of a pair
+// of 16x16 results (rows 4g + r), so a result becomes an operand without
+// moving between lanes.
+#pragma once
+
+#include "rssm_host.hpp"
+#include "seq_device.hpp"
+
+namespace rssm {
+
+constexpr int kQ = 64;  // tokens of a chunk
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+template <typename T> struct Mat;
+
+template <> struct Mat<bf16> {
+  typedef uint16_t E;
+  typedef u32x4 Frag;
+  static constexpr int kPad = 8;    // elements between LDS rows: rows start 4 banks apart
+  static constexpr int kTerms = 3;  // bf16 terms that hold an fp32 value (3 x 8 bits)
+  __device__ static inline Frag rows_c(const E* p) { return *reinterpret_cast<const u32x4*>(p); }
+  __device__ static inline Frag rows_d(const E* p) {
+    const u32x2 a = *reinterpret_cast<const u32x2*>(p);
+    const u32x2 b = *reinterpret_cast<const u32x2*>(p + 16);
+    return Frag{a[0], a[1], b[0], b[1]};
+  }
+  // p: row 4g + (l%16)/4 of the K block, the lane's granule of 4 columns; the
+  // transposing read hands lane l the 4 rows of column l%16
+  __device__ static inline Frag cols(const E* p, int ld) {
+    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
+    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 16 * ld));
+    const u32x2 x = __builtin_bit_cast(u32x2, a), y = __builtin_bit_cast(u32x2, b);
+    return Frag{x[0], x[1], y[0], y[1]};
+  }
+  __device__ static inline f32x4 mma(const Frag& a, const Frag& b, f32x4 c) {
+    return mfma16x16x32_bf16(a, b, c);
+  }
+  __device__ static inline Frag pack(const float* f) { return Elt<bf16>::pack(f); }
+  __device__ static inline void unpack(const Frag& a, float* f) { Elt<bf16>::unpack(a, f); }
+};
+
+template <> struct Mat<float> {
+  typedef float E;
+  struct Frag {
+    float v[8];
+  };
+  static constexpr int kPad = 4;
+  static constexpr int kTerms = 1;
+  __device__ static inline Frag rows_c(const E* p) {
+    Frag f;
+    Elt<float>::unpack(*reinterpret_cast<const u32x4*>(p), f.v);
+    Elt<float>::unpack(*reinterpret_cast<const u32x4*>(p + 4), f.v + 4);
+    return f;
+  }
+  __device__ static inline Frag rows_d(const E* p) {
+    Frag f;
+    Elt<float>::unpack(*reinterpret_cast<const u32x4*>(p), f.v);
+    Elt<float>::unpack(*reinterpret_cast<const u32x4*>(p + 16), f.v + 4);
+    return f;
+  }
+  // p: row 4g of the K block, the lane's column
+  __device__ static inline Frag cols(const E* p, int ld) {
+    Frag f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f.v[e] = p[(e < 4 ? e : 12 + e) * ld];
+    return f;
+  }
+  // fp32 inputs keep fp32 products: eight 16x16x4 steps, step e taking the
+  // lanes' e-th values
+  __device__ static inline f32x4 mma(const Frag& a, const Frag& b, f32x4 c) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[e], b.v[e], c, 0, 0, 0);
+    return c;
+  }
+  __device__ static inline Frag pack(const float* f) {
+    Frag r;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) r.v[e] = f[e];
+    return r;
+  }
+  __device__ static inline void unpack(const Frag& a, float* f) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = a.v[e];
+  }
+};
+
+// A lane's address of a column fragment: K block starting at row k0, the 16
+// columns of a tile that start at c0 and, in a `paired` operand, come in
+// granules of 4 every 8 columns (see tile_col).
+template <typename T, bool PAIRED>
+__device__ static inline const typename Mat<T>::E* cols_at(const typename Mat<T>::E* tile, int ld,
+                                                           int k0, int c0, int lane) {
+  const int i = lane & 15, g = lane >> 4;
+  if constexpr (sizeof(typename Mat<T>::E) == 2)
+    return tile + (k0 + 4 * g + (i >> 2)) * ld + c0 + (i & 3) * (PAIRED ? 8 : 4);
+  else
+    return tile + (k0 + 4 * g) * ld + c0 + (PAIRED ? 8 * (i >> 2) + (i & 3) : i);
+}
+
+// Columns of the two tiles of a pair (32 columns) interleave in granules of 4,
+// tile j's index i standing for column 8*(i/4) + 4*j + i%4: a lane that holds
+// rows 4g..4g+3 of both tiles' results then holds 8 neighbours (16 bytes of
+// bf16), as global loads and stores want them.
+__device__ static inline int pair_base(int tile) { return 32 * (tile >> 1) + 4 * (tile & 1); }
+__device__ static inline int tile_col(int tile, int i) {
+  return pair_base(tile) + 8 * (i >> 2) + (i & 3);
+}
+
+// An fp32 operand as kTerms fragments whose sum it is: each product with an
+// exact operand is then an fp32 one.
+template <typename T, int TERMS>
+struct Split {
+  typename Mat<T>::Frag t[TERMS];
+  __device__ inline void set(const float* f) {
+    float r[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) r[e] = f[e];
+#pragma unroll
+    for (int k = 0; k < TERMS; ++k) {
+      t[k] = Mat<T>::pack(r);
+      if (k + 1 < TERMS) {
+        float q[8];
+        Mat<T>::unpack(t[k], q);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r[e] -= q[e];
+      }
+    }
+  }
+  // this * other (this one the A operand), smallest terms first
+  __device__ inline f32x4 a_times(const typename Mat<T>::Frag& o, f32x4 c) const {
+#pragma unroll
+    for (int k = TERMS - 1; k >= 0; --k) c = Mat<T>::mma(t[k], o, c);
+    return c;
+  }
+  __device__ inline f32x4 b_times(const typename Mat<T>::Frag& o, f32x4 c) const {
+#pragma unroll
+    for (int k = TERMS - 1; k >= 0; --k) c = Mat<T>::mma(o, t[k], c);
+    return c;
+  }
+};
+
+// One row of 16-byte loads from a strided matrix into an LDS tile of kQ rows,
+// zero past `rows` (and past `cols` up to the tile's width).
+template <typename T, int COLS, int TILE, int THREADS>
+__device__ static inline void stage_tile(typename Mat<T>::E* tile, int ld, const void* src,
+                                         long stride, int rows, int tid) {
+  typedef typename Mat<T>::E E;
+  constexpr int V = 16 / sizeof(E), PER = TILE / V;
+  static_assert(kQ * PER % THREADS == 0, "whole passes");
+#pragma unroll
+  for (int q = 0; q < kQ * PER / THREADS; ++q) {
+    const int e = q * THREADS + tid, r = e / PER, c = (e % PER) * V;
+    u32x4 v = {0, 0, 0, 0};
+    if (r < rows && (COLS == TILE || c < COLS))
+      v = *reinterpret_cast<const u32x4*>(static_cast<const E*>(src) + r * stride + c);
+    *reinterpret_cast<u32x4*>(tile + r * ld + c) = v;
+  }
+}
+
+// Inclusive sum over the wave's lanes (0 to 63) in double: decays are
+// differences of these sums, and a large step must not cost the small ones
+// their digits.
+__device__ static inline double wave_cumsum(double v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const double t = __shfl_up(v, o, 64);
+    if (lane >= o) v += t;
+  }
+  return v;
+}
+
+__device__ static inline float exp2_f32(float v) { return __builtin_amdgcn_exp2f(v); }
+
+// log2 of the decay between two tokens, from their sums as (high, low) pairs.
+__device__ static inline float gap2(float2 t, float2 s) { return (t.x - s.x) + (t.y - s.y); }
+
+// Segments: runs of seg tokens (a multiple of kQ) of one sequence, worked on
+// independently.  Segment k of sequence i has the slot start_i/seg + i + k:
+// distinct for all, because a sequence of n tokens spans at least n/seg
+// (rounded up) less one multiples of seg.  At most tokens/seg + seqs slots,
+// so the host needs no lengths.
+struct Segment {
+  int seq, k, tok, len;  // len 0: nothing here, unless `empty`
+  bool first, last, empty, bad;
+};
+__device__ static inline int seg_base(const int32_t* cu, int i, int seg, int tokens) {
+  if (!cu) return 0;
+  const int a = cu[i];
+  return (a < 0 ? 0 : (a > tokens ? tokens : a)) / seg + i;
+}
+__device__ static inline Segment find_segment(const int32_t* cu, int nseq, int tokens, int seg,
+                                              int slot) {
+  int lo = 0, hi = nseq;
+  while (hi - lo > 1) {
+    const int m = (lo + hi) >> 1;
+    if (seg_base(cu, m, seg, tokens) <= slot) lo = m; else hi = m;
+  }
+  const SeqSpan sp = seq_span(cu, lo, nseq, tokens);
+  Segment r;
+  r.seq = lo;
+  r.bad = sp.bad;
+  r.k = slot - seg_base(cu, lo, seg, tokens);
+  const long off = (long)r.k * seg;
+  r.empty = sp.len == 0 && r.k == 0;
+  r.len = r.k < 0 || off >= sp.len ? 0 : (sp.len - off < seg ? (int)(sp.len - off) : seg);
+  r.tok = sp.start + (r.len ? (int)off : 0);
+  r.first = r.k == 0;
+  r.last = off + seg >= sp.len;
+  return r;
+}
+
+static inline long scan_slots(long tokens, long seqs, long seg) { return tokens / seg + seqs; }
+
+}  // namespace rssm

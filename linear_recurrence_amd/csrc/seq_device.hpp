@@ -1,0 +1,99 @@
+// Device helpers of the sequence operators (scan, short convolution, norm).
+#pragma once
+
+#include "rssm_device.hpp"
+
+namespace rssm {
+
+// Sixteen bytes at any element boundary: rows of odd length start anywhere.
+// gfx950 does such a load or store in one instruction.
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef u32x2 u32x2_any __attribute__((aligned(1)));
+
+// Eight consecutive elements as fp32.
+template <typename T> struct Vec8;
+
+template <> struct Vec8<float> {
+  __device__ static inline void load(const void* p, long i, float* f) {
+    const float* q = static_cast<const float*>(p) + i;
+    const u32x4 a = *reinterpret_cast<const u32x4_any*>(q);
+    const u32x4 b = *reinterpret_cast<const u32x4_any*>(q + 4);
+    Elt<float>::unpack(a, f);
+    Elt<float>::unpack(b, f + 4);
+  }
+  __device__ static inline void store(void* p, long i, const float* f) {
+    float* q = static_cast<float*>(p) + i;
+    *reinterpret_cast<u32x4_any*>(q) = Elt<float>::pack(f);
+    *reinterpret_cast<u32x4_any*>(q + 4) = Elt<float>::pack(f + 4);
+  }
+};
+
+template <> struct Vec8<bf16> {
+  __device__ static inline void load(const void* p, long i, float* f) {
+    const uint16_t* q = static_cast<const uint16_t*>(p) + i;
+    const u32x4 v = *reinterpret_cast<const u32x4_any*>(q);
+    Elt<bf16>::unpack(v, f);
+  }
+  __device__ static inline void store(void* p, long i, const float* f) {
+    uint16_t* q = static_cast<uint16_t*>(p) + i;
+    *reinterpret_cast<u32x4_any*>(q) = Elt<bf16>::pack(f);
+  }
+};
+
+// The first n (0..8) of eight consecutive elements; the others read as 0.
+template <typename T>
+__device__ static inline void load8(const void* p, long i, int n, float* f) {
+  if (n == 8) {
+    Vec8<T>::load(p, i, f);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] = k < n ? Elt<T>::load1(p, i + k) : 0.f;
+  }
+}
+template <typename T>
+__device__ static inline void store8(void* p, long i, int n, const float* f) {
+  if (n == 8) {
+    Vec8<T>::store(p, i, f);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < n) Elt<T>::store1(p, i + k, f[k]);
+  }
+}
+
+// sigmoid(v) = 1 / (1 + e^-v); e^-v overflows to Inf below -88, where the
+// quotient is the correct 0.  Hardware exp and reciprocal (about 2 ulp).
+__device__ static inline float sigmoid_f32(float v) {
+  return __builtin_amdgcn_rcpf(1.f + __expf(-v));
+}
+
+// Bounds of sequence i in a packed batch, forced into [0, tokens] so that a
+// malformed table can only give wrong values, never a wrong address.
+struct SeqSpan {
+  int start, len;
+  bool bad;
+};
+__device__ static inline SeqSpan seq_span(const int32_t* cu, int i, int nseq, int tokens) {
+  if (!cu) return {0, tokens, false};
+  const int a = cu[i], b = cu[i + 1];
+  const bool bad = a < 0 || b < a || b > tokens || (i == 0 && a != 0) ||
+                   (i == nseq - 1 && b != tokens);
+  const int s = a < 0 ? 0 : (a > tokens ? tokens : a);
+  const int e = b < s ? s : (b > tokens ? tokens : b);
+  return {s, e - s, bad};
+}
+
+// The last sequence whose start is at or before token t (binary search over
+// the nseq starts; the table is monotone, or the result is merely arbitrary).
+__device__ static inline int seq_of_token(const int32_t* cu, int nseq, int t) {
+  if (!cu) return 0;
+  int lo = 0, hi = nseq;
+  while (hi - lo > 1) {
+    const int m = (lo + hi) >> 1;
+    if (cu[m] <= t) lo = m; else hi = m;
+  }
+  return lo;
+}
+
+}  // namespace rssm
