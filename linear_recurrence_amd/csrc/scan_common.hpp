@@ -19,7 +19,8 @@
 
 namespace rssm {
 
-constexpr int kQ = 64;  // tokens of a chunk
+constexpr int kQ = 64;   // tokens of a chunk
+constexpr int kPT = 32;  // state rows of a wave
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
@@ -48,7 +49,13 @@ template <> struct Mat<bf16> {
   __device__ static inline f32x4 mma(const Frag& a, const Frag& b, f32x4 c) {
     return mfma16x16x32_bf16(a, b, c);
   }
-  __device__ static inline Frag pack(const float* f) { return Elt<bf16>::pack(f); }
+  // one conversion a pair (v_cvt_pk_bf16_f32, to nearest even)
+  __device__ static inline Frag pack(const float* f) {
+    Frag v;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = bf16_pk(f[2 * k], f[2 * k + 1]);
+    return v;
+  }
   __device__ static inline void unpack(const Frag& a, float* f) { Elt<bf16>::unpack(a, f); }
 };
 
@@ -159,10 +166,11 @@ __device__ static inline void stage_tile(typename Mat<T>::E* tile, int ld, const
                                          long stride, int rows, int tid) {
   typedef typename Mat<T>::E E;
   constexpr int V = 16 / sizeof(E), PER = TILE / V;
-  static_assert(kQ * PER % THREADS == 0, "whole passes");
+  constexpr bool kWhole = kQ * PER % THREADS == 0;
 #pragma unroll
-  for (int q = 0; q < kQ * PER / THREADS; ++q) {
+  for (int q = 0; q < (kQ * PER + THREADS - 1) / THREADS; ++q) {
     const int e = q * THREADS + tid, r = e / PER, c = (e % PER) * V;
+    if (!kWhole && e >= kQ * PER) break;
     u32x4 v = {0, 0, 0, 0};
     if (r < rows && (COLS == TILE || c < COLS))
       v = *reinterpret_cast<const u32x4*>(static_cast<const E*>(src) + r * stride + c);
@@ -221,6 +229,147 @@ __device__ static inline Segment find_segment(const int32_t* cu, int nseq, int t
   r.last = off + seg >= sp.len;
   return r;
 }
+
+struct ScanArgs {
+  const void* x;
+  const void* dt;
+  const float* A;
+  const void* B;
+  const void* C;
+  const float* D;
+  const void* z;
+  const float* dt_bias;
+  const int32_t* cu;
+  const void* init;
+  const uint8_t* has_init;
+  const int32_t* slot_idx;
+  void* final_state;
+  void* y;
+  float* seg_state;  // [slots][V][32][N]
+  float* seg_decay;  // [slots][V], log2
+  int32_t* status;
+  long x_stride, dt_stride, B_stride, C_stride, z_stride;
+  int32_t tokens, seqs, nheads, headdim, dstate, ngroups, num_slots, state_bf16, dt_softplus;
+  int32_t seg, vheads, vpg;
+};
+
+__device__ static inline int scan_slot(const ScanArgs& a, int i) {
+  const int s = a.slot_idx ? a.slot_idx[i] : i;
+  return s >= 0 && s < a.num_slots ? s : -1;
+}
+
+__device__ static inline f32x4 load_state4(const void* p, long i, int bf) {
+  f32x4 f;
+  if (bf) {
+    const u32x2 v = *reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(p) + i);
+    f[0] = __uint_as_float(v[0] << 16);
+    f[1] = __uint_as_float(v[0] & 0xffff0000u);
+    f[2] = __uint_as_float(v[1] << 16);
+    f[3] = __uint_as_float(v[1] & 0xffff0000u);
+  } else {
+    f = *reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + i);
+  }
+  return f;
+}
+__device__ static inline void store_state4(void* p, long i, int bf, f32x4 f) {
+  if (bf) {
+    const u32x2 v = {bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3])};
+    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(p) + i) = v;
+  } else {
+    *reinterpret_cast<f32x4*>(static_cast<float*>(p) + i) = f;
+  }
+}
+
+static inline int scan_check(const rssm_scan_dims* d) {
+  if (!d) return RSSM_EINVAL;
+  if (d->tokens < 0 || d->seqs < 0 || d->nheads < 1 || d->ngroups < 1 ||
+      d->nheads % d->ngroups || d->num_slots < 0)
+    return RSSM_EINVAL;
+  if (!valid_dtype(d->io_dtype) || !valid_dtype(d->state_dtype)) return RSSM_EDTYPE;
+  const int P = d->headdim, N = d->dstate;
+  if (!(P == 32 || P == 64 || P == 128)) return RSSM_ESHAPE;
+  if (!(N == 16 || N == 32 || N == 64 || N == 128 || N == 256)) return RSSM_ESHAPE;
+  const long es = d->io_dtype == RSSM_F32 ? 4 : 2;
+  const long hp = (long)d->nheads * P, gn = (long)d->ngroups * N;
+  const int64_t rows[5] = {d->x_stride, d->z_stride, d->dy_stride, d->B_stride, d->C_stride};
+  for (int k = 0; k < 5; ++k)
+    if (rows[k] != 0 && (rows[k] < (k < 3 ? hp : gn) || rows[k] * es % 16)) return RSSM_EINVAL;
+  if (d->dt_stride != 0 && d->dt_stride < d->nheads) return RSSM_EINVAL;
+  return RSSM_OK;
+}
+
+// The sizes and strides of the arguments (a stride of 0 is a dense operand).
+static inline void fill_dims(ScanArgs& a, const rssm_scan_dims& d) {
+  a.x_stride = d.x_stride ? d.x_stride : (long)d.nheads * d.headdim;
+  a.dt_stride = d.dt_stride ? d.dt_stride : d.nheads;
+  a.B_stride = d.B_stride ? d.B_stride : (long)d.ngroups * d.dstate;
+  a.C_stride = d.C_stride ? d.C_stride : (long)d.ngroups * d.dstate;
+  a.z_stride = d.z_stride ? d.z_stride : (long)d.nheads * d.headdim;
+  a.tokens = d.tokens;
+  a.seqs = d.seqs;
+  a.nheads = d.nheads;
+  a.headdim = d.headdim;
+  a.dstate = d.dstate;
+  a.ngroups = d.ngroups;
+  a.num_slots = d.num_slots;
+  a.state_bf16 = d.state_dtype == RSSM_BF16;
+  a.dt_softplus = d.dt_softplus;
+}
+
+// dt and the running sum of dt*A (log2) of a chunk's tokens, one per lane.
+struct ChunkDt {
+  float raw, dt;
+  double cum, all;
+};
+template <typename T>
+__device__ static inline ChunkDt chunk_dt(const ScanArgs& a, int h, float bias, double A2, long t0,
+                                          int rows, int lane) {
+  ChunkDt c;
+  c.raw = c.dt = 0.f;
+  if (lane < rows) {
+    c.raw = Elt<T>::load1(a.dt, (t0 + lane) * a.dt_stride + h) + bias;
+    c.dt = a.dt_softplus ? softplus_exact(c.raw) : c.raw;
+  }
+  c.cum = wave_cumsum((double)c.dt * A2, lane);
+  c.all = __shfl(c.cum, 63, 64);
+  return c;
+}
+
+// acc[nt][pt] += (w * rows of X)^T (rows of Y): X the wave's [64][32] tile, Y
+// the shared [64][N] one, w one weight per token; ROWS: X's columns are the
+// result's rows, otherwise its columns.
+template <typename T, int NT, int LX, int LN, bool ROWS>
+__device__ static inline void rank_update(f32x4 (&acc)[NT][2], const typename Mat<T>::E* X,
+                                          const typename Mat<T>::E* Y, const float* w, int rows,
+                                          int lane) {
+  typedef Mat<T> M;
+  const int g = lane >> 4;
+#pragma unroll 1
+  for (int kb = 0; kb < kQ / 32; ++kb) {
+    if (32 * kb >= rows) break;
+    Split<T, M::kTerms> xs[2];
+    const float* w0 = w + 32 * kb + 4 * g;
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      float f[8];
+      M::unpack(M::cols(cols_at<T, true>(X, LX, 32 * kb, pair_base(p), lane), LX), f);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        f[r] *= w0[r];
+        f[4 + r] *= w0[16 + r];
+      }
+      xs[p].set(f);
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const typename M::Frag y = M::cols(cols_at<T, false>(Y, LN, 32 * kb, 16 * n, lane), LN);
+#pragma unroll
+      for (int p = 0; p < 2; ++p) acc[n][p] = ROWS ? xs[p].a_times(y, acc[n][p]) : xs[p].b_times(y, acc[n][p]);
+    }
+  }
+}
+
+int scan_segment_states(const ScanArgs& args, const rssm_scan_dims& d, hipStream_t stream);
 
 static inline long scan_slots(long tokens, long seqs, long seg) { return tokens / seg + seqs; }
 

@@ -11,6 +11,13 @@ typedef u32x4 u32x4_any __attribute__((aligned(2)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef u32x2 u32x2_any __attribute__((aligned(1)));
 
+// Two fp32 -> packed bf16, round to nearest even, in one instruction.
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+__device__ static inline uint32_t bf16_pk(float lo, float hi) {
+  const f32x2 f = {lo, hi};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f, bf16x2_t));
+}
+
 // Eight consecutive elements as fp32.
 template <typename T> struct Vec8;
 
@@ -37,7 +44,9 @@ template <> struct Vec8<bf16> {
   }
   __device__ static inline void store(void* p, long i, const float* f) {
     uint16_t* q = static_cast<uint16_t*>(p) + i;
-    *reinterpret_cast<u32x4_any*>(q) = Elt<bf16>::pack(f);
+    const u32x4 v = {bf16_pk(f[0], f[1]), bf16_pk(f[2], f[3]), bf16_pk(f[4], f[5]),
+                     bf16_pk(f[6], f[7])};
+    *reinterpret_cast<u32x4_any*>(q) = v;
   }
 };
 
@@ -67,6 +76,12 @@ __device__ static inline void store8(void* p, long i, int n, const float* f) {
 __device__ static inline float sigmoid_f32(float v) {
   return __builtin_amdgcn_rcpf(1.f + __expf(-v));
 }
+
+// softplus(v) = log(1 + e^v): v itself above 20 (exact in fp32).  The library's
+// log1p rather than softplus_f32's hardware log: near 1 that one is off by more
+// than an ulp of the logarithm, which the sums over tokens of the decay's
+// gradient would carry whole.
+__device__ static inline float softplus_exact(float v) { return v > 20.f ? v : log1pf(expf(v)); }
 
 // Bounds of sequence i in a packed batch, forced into [0, tokens] so that a
 // malformed table can only give wrong values, never a wrong address.
