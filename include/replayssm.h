@@ -495,7 +495,7 @@ int replayssm_flush_first_order(int32_t n_rows, const uint8_t* is_flush, int32_t
 enum { RSSM_ACT_NONE = 0, RSSM_ACT_SILU = 1 };
 
 /*
- * Causal convolution.  Supported: width 2, 3, 4; any number of channels;
+ * Causal convolution.  Supported: width 2, 3, 4; 1 to 2^24 channels;
  * pointers aligned to their element type.
  */
 typedef struct rssm_conv_dims {

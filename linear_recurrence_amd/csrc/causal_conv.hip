@@ -408,7 +408,7 @@ static int conv_check(const rssm_conv_dims* d) {
   if (d->tokens < 0 || d->seqs < 0 || d->channels < 1 || d->num_slots < 0) return RSSM_EINVAL;
   if (d->activation != RSSM_ACT_NONE && d->activation != RSSM_ACT_SILU) return RSSM_EINVAL;
   if (!valid_dtype(d->io_dtype)) return RSSM_EDTYPE;
-  if (d->width < 2 || d->width > 4) return RSSM_ESHAPE;
+  if (d->width < 2 || d->width > 4 || d->channels > (1 << 24)) return RSSM_ESHAPE;
   // pointers are aligned to their element type and the grids fit 31 bits
   if (((long)d->tokens + d->seqs + 1) * ((d->channels + 511) / 512) > 0x7fffffffL)
     return RSSM_ESHAPE;

@@ -60,11 +60,16 @@ __global__ void __launch_bounds__(64 * scan_waves(sizeof(typename Mat<T>::E) == 
       if (sg.bad) atomicOr(a.status, RSSM_ST_BAD_SEQ);
       if ((a.init || a.final_state) && pool < 0) atomicOr(a.status, RSSM_ST_BAD_SLOT);
     }
-    const bool from_pool = sg.first && a.init && pool >= 0 && (!a.has_init || a.has_init[sg.seq]);
-    if (live && (from_pool || !sg.first)) {
-      const void* src = sg.first ? a.init : a.seg_state;
-      const int bf = sg.first ? a.state_bf16 : 0;
-      const long base = ((long)(sg.first ? pool : slot) * a.vheads + v) * (kPT * N);
+    // The pool is read here only by a sequence of one segment, whose wave also
+    // writes it: a longer one's first segment takes the copy that the combining
+    // launch left, since its last segment may already have stored the final
+    // state over the initial one.
+    const bool whole = sg.first && sg.last;
+    const bool from_pool = whole && a.init && pool >= 0 && (!a.has_init || a.has_init[sg.seq]);
+    if (live && (from_pool || !whole)) {
+      const void* src = whole ? a.init : a.seg_state;
+      const int bf = whole ? a.state_bf16 : 0;
+      const long base = ((long)(whole ? pool : slot) * a.vheads + v) * (kPT * N);
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -258,7 +263,7 @@ __global__ void __launch_bounds__(256) scan_combine_kernel(const ScanArgs a) {
       own = *p;
       d = exp2_f32(a.seg_decay[at]);
     }
-    if (k) *p = S;
+    *p = S;
 #pragma unroll
     for (int r = 0; r < 4; ++r) S[r] = fmaf(d, S[r], own[r]);
   }
