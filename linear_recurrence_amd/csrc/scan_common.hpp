@@ -57,6 +57,15 @@ template <> struct Mat<bf16> {
     return v;
   }
   __device__ static inline void unpack(const Frag& a, float* f) { Elt<bf16>::unpack(a, f); }
+  // four neighbours
+  typedef u32x2 Four;
+  __device__ static inline Four pack4(const float* f) { return Four{bf16_pk(f[0], f[1]), bf16_pk(f[2], f[3])}; }
+  __device__ static inline void unpack4(Four v, float* f) {
+    f[0] = __uint_as_float(v[0] << 16);
+    f[1] = __uint_as_float(v[0] & 0xffff0000u);
+    f[2] = __uint_as_float(v[1] << 16);
+    f[3] = __uint_as_float(v[1] & 0xffff0000u);
+  }
 };
 
 template <> struct Mat<float> {
@@ -101,6 +110,12 @@ template <> struct Mat<float> {
   __device__ static inline void unpack(const Frag& a, float* f) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) f[e] = a.v[e];
+  }
+  typedef f32x4 Four;
+  __device__ static inline Four pack4(const float* f) { return Four{f[0], f[1], f[2], f[3]}; }
+  __device__ static inline void unpack4(Four v, float* f) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] = v[e];
   }
 };
 

@@ -5,12 +5,12 @@
 // state (forward form: scan_common.hpp):
 //   dx_t = D dy_t + dt_t L_t B_t
 //        = D dy_t + dt_t [ sum_{u>=t} e^{a_u-a_t} (C_u.B_t) dy_u + e^{a_Q-a_t} dS B_t ]
-//   dB_t = dt_t sum_heads [ sum_{u>=t} e^{a_u-a_t} (dy_u.x_t) C_u + e^{a_Q-a_t} dS^T x_t ]
-//   dC_t = sum_heads [ sum_{s<=t} e^{a_t-a_s} dt_s (dy_t.x_s) B_s + e^{a_t} S_in^T dy_t ]
+//   dB_t = sum_heads [ sum_{u>=t} K_ut C_u + dt_t e^{a_Q-a_t} dS^T x_t ]
+//   dC_u = sum_heads [ sum_{t<=u} K_ut B_t + e^{a_u} S_in^T dy_u ]
+//          with K_ut = e^{a_u-a_t} dt_t (dy_u.x_t)
 //   dS' = e^{a_Q} dS + sum_t e^{a_t} dy_t C_t^T      (the chunk before's)
-// and for the decay exponent alpha_t = dt_t A, with w_ut = e^{a_u-a_t} dt_t
-// (C_u.B_t)(dy_u.x_t) for u > t, i_t = e^{a_t} dy_t^T S_in C_t and
-// e_t = e^{a_Q-a_t} x_t^T dS B_t:
+// and for the decay exponent alpha_t = dt_t A, with w_ut = K_ut (C_u.B_t) for
+// u > t, i_t = e^{a_t} dy_t^T S_in C_t and e_t = e^{a_Q-a_t} x_t^T dS B_t:
 //   dalpha_t = sum_{s<t<=u} w_us + sum_{k>=t} i_k + sum_{s<t} dt_s e_s
 //            + e^{a_Q} <S_in, dS>
 // (each sum over one chunk).  The first is summed as it stands, from the tiles'
@@ -18,16 +18,18 @@
 // columns' running sums, whose rounding would not cancel.
 // ddt_t = x_t.L_t B_t + A dalpha_t, times the softplus's derivative.
 //
+// Launches: (1) dt and the decays' running sums of every chunk and head, once
+// for all that follow; (2) both recurrences over the chunks, S_in forward and
+// dS backward, which leave every chunk's in the workspace (with two launches in
+// front where sequences are longer than a segment); (3) everything else, a
+// workgroup for one chunk and several heads of one group, which needs nothing
+// from other chunks; (4) the sums over workgroups, in a fixed order.
+//
 // Everything that reaches an fp32 output (dA, ddt_bias, dinitial_state, and
 // ddt through dalpha) takes its state products with the state as three bf16
-// terms; what only reaches an output in the io type rounds one factor once
-// (dx) or takes two terms (dB, dC, which are sums over heads).
-//
-// A wave owns 32 rows of one head's state.  The states S_in come from a
-// forward launch that leaves every chunk's in the workspace in the layout of
-// the accumulators; the main launch walks a segment's chunks backwards with dS
-// in registers.  dB and dC are joined over a workgroup's waves in LDS and over
-// workgroups by a last launch, in a fixed order.
+// terms.  What only reaches an output in the io type rounds one factor once:
+// dS, e^{a_u-a_t} C_u.B_t (dx) and K (dB, dC) are rounded to the io type, as
+// the outputs themselves are.
 #include "scan_common.hpp"
 
 namespace rssm {
@@ -44,19 +46,18 @@ struct ScanBwdArgs {
   float* dD;
   float* ddt_bias;
   float* dinit;
-  float* chunk_state;  // [chunk slots][V][tiles][64][4]
+  f32x4* dec;          // [chunk slots][H][64]: sum of dt A (log2; high, low), dt, dt before softplus
+  float* chunk_state;  // [chunk slots][V][tiles][64][4]: S_in
+  float* grad_state;   // the same: dS
   float* seg_grad;     // [slots][V][32][N]
   float* grad_decay;   // [slots][V], log2
-  float* ddt_part;     // [V][T]
+  float* ddt_part;     // [units][T]
   float* dB_part;      // [hb][T][G][N]
   float* dC_part;
-  double* head_part;   // [slots][V][3]: dA, ddt_bias, dD
-  long dy_stride, slots;
-  int32_t hb;
+  float* head_part;    // [chunk slots][units][4]: dA, ddt_bias, dD
+  long dy_stride, slots, cslots;
+  int32_t hb, upb, upg, dir_blocks;  // blocks of units in a group, units a block, units a group
 };
-
-// Waves of a workgroup: what the tiles leave room for in 160 KB of LDS.
-constexpr int bwd_waves(bool f32, int n) { return f32 ? (n == 256 ? 1 : 2) : (n == 256 ? 4 : 8); }
 
 // The state tile pair of column tile nt, rows tile_col(pt, 4g + r), column
 // 16 nt + l%16, from natural [32][N] memory.
@@ -65,40 +66,78 @@ __device__ static inline long row_at(int nt, int pt, int r, int lane) {
   return (long)(pair_base(pt) + 8 * (lane >> 4) + r) * N + 16 * nt + (lane & 15);
 }
 
-// GRAD false: forward over a segment from its starting state, leaving each
-// chunk's S_in in the workspace.  GRAD true: backward over a segment from a
-// zero dS, leaving the gradient of its start (what the segment adds).
-template <typename T, int N, bool GRAD>
-__global__ void __launch_bounds__(256) scan_states_kernel(const ScanBwdArgs b) {
+// dt and the running sums of dt*A of one chunk and head, a wave each.
+template <typename T>
+__global__ void __launch_bounds__(256) scan_decay_kernel(const ScanBwdArgs b) {
+  const ScanArgs& a = b.f;
+  const int lane = threadIdx.x & 63, hq = (a.nheads + 3) / 4;
+  const long slot = blockIdx.x / hq;
+  const int h = (int)(blockIdx.x % hq) * 4 + (threadIdx.x >> 6);
+  const Segment sg = find_segment(a.cu, a.seqs, a.tokens, kQ, (int)slot);
+  if (sg.len == 0 || h >= a.nheads) return;
+  const double A2 = (double)a.A[h] * 1.4426950408889634074;
+  const ChunkDt q = chunk_dt<T>(a, h, a.dt_bias ? a.dt_bias[h] : 0.f, A2, sg.tok, sg.len, lane);
+  const float hi = (float)q.cum;
+  b.dec[(slot * a.nheads + h) * kQ + lane] = f32x4{hi, (float)(q.cum - (double)hi), q.dt, q.raw};
+}
+
+__device__ static inline float gap2(f32x4 t, f32x4 s) { return (t[0] - s[0]) + (t[1] - s[1]); }
+__device__ static inline f32x4 lane_of(f32x4 v, int l) {
+  f32x4 o = v;
+  o[0] = __shfl(v[0], l, 64);
+  o[1] = __shfl(v[1], l, 64);
+  return o;
+}
+
+// One of the two recurrences over the chunks of a segment, a wave for 32 rows of
+// one head's state.  Blocks below dir_blocks: S forward; the others: dS
+// backward.  STORE: from the segment's starting value, leaving every chunk's in
+// the workspace (and the gradient of the initial state); otherwise from zero,
+// leaving what the segment adds.  The next chunk's tiles are on their way while
+// one is worked on; two workgroups a compute unit.
+template <typename T, int N, bool STORE>
+__global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 1 : 2)
+    scan_states_kernel(const ScanBwdArgs b) {
   typedef Mat<T> M;
   typedef typename M::E E;
-  constexpr int W = 4;
+  constexpr int W = 4, TH = 64 * W, V = 16 / sizeof(E);
   constexpr int NP = N < 32 ? 32 : N, LN = NP + M::kPad, LX = kPT + M::kPad, NT = N / 16;
+  constexpr int PN = N / V, QN = (kQ * PN + TH - 1) / TH;  // 16-byte pieces of a row, a thread's
+  constexpr int PX = kPT / V, QX = kQ * PX / 64;
   __shared__ __attribute__((aligned(16))) E sB[kQ * LN];
   __shared__ __attribute__((aligned(16))) E sX[W][kQ * LX];
   __shared__ __attribute__((aligned(16))) float sW[W][kQ];
   const ScanArgs& a = b.f;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int hb = (a.vpg + W - 1) / W;
-  const int id = xcd_tile(blockIdx.x, gridDim.x);
+  const bool grad = (int)blockIdx.x >= b.dir_blocks;
+  const int id = xcd_tile(grad ? blockIdx.x - b.dir_blocks : blockIdx.x, b.dir_blocks);
   const int slot = id / (a.ngroups * hb), rest = id % (a.ngroups * hb);
   const int grp = rest / hb, vl = (rest % hb) * W + wave;
   const Segment sg = find_segment(a.cu, a.seqs, a.tokens, a.seg, slot);
-  if (sg.len == 0 || (GRAD && sg.first)) return;
   const bool live = vl < a.vpg;
   const int v = grp * a.vpg + (live ? vl : 0);
+  const long sbase = ((long)sg.seq * a.vheads + v) * (kPT * N);
+  const bool has = a.init && scan_slot(a, sg.seq) >= 0 && (!a.has_init || a.has_init[sg.seq]);
+  if (sg.len == 0) {
+    if (STORE && grad && live && sg.empty && b.dinit) {  // the state passes through
+      for (int e = lane; e < kPT * N; e += 64)
+        b.dinit[sbase + e] = has && b.dfinal ? b.dfinal[sbase + e] : 0.f;
+    }
+    return;
+  }
+  if (!STORE && (grad ? sg.first : sg.last)) return;  // nothing starts from it
   const int slices = a.headdim / kPT, h = v / slices, p0 = (v % slices) * kPT;
-  const double A2 = (double)a.A[h] * 1.4426950408889634074;
-  const float bias = a.dt_bias ? a.dt_bias[h] : 0.f;
   f32x4 S[NT][2];
 #pragma unroll
   for (int n = 0; n < NT; ++n) S[n][0] = S[n][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-  if (!GRAD && live) {
-    const int pool = sg.first && a.init ? scan_slot(a, sg.seq) : -1;
-    const bool from_pool = pool >= 0 && (!a.has_init || a.has_init[sg.seq]);
-    if (!sg.first || from_pool) {
-      const void* src = sg.first ? a.init : a.seg_state;
-      const long base = ((long)(sg.first ? pool : slot) * a.vheads + v) * (kPT * N);
+  if (STORE && live) {
+    const bool edge = grad ? sg.last : sg.first;
+    const void* src = grad ? (edge ? b.dfinal : b.seg_grad) : (edge ? (has ? a.init : nullptr) : a.seg_state);
+    const long base = edge ? (grad ? sbase : ((long)(has ? scan_slot(a, sg.seq) : 0) * a.vheads + v) * (kPT * N))
+                           : ((long)slot * a.vheads + v) * (kPT * N);
+    const bool bf = !grad && edge && a.state_bf16;
+    if (src) {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -106,43 +145,65 @@ __global__ void __launch_bounds__(256) scan_states_kernel(const ScanBwdArgs b) {
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const long e = base + row_at<N>(n, p, r, lane);
-            S[n][p][r] = sg.first && a.state_bf16 ? Elt<bf16>::load1(src, e)
-                                                  : Elt<float>::load1(src, e);
+            S[n][p][r] = bf ? Elt<bf16>::load1(src, e) : Elt<float>::load1(src, e);
           }
     }
   }
+  const E* const nsrc = static_cast<const E*>(grad ? a.C : a.B) + (long)grp * N;
+  const E* const psrc = static_cast<const E*>(grad ? b.dy : a.x) + (long)h * a.headdim + p0;
+  const long nstride = grad ? a.C_stride : a.B_stride, pstride = grad ? b.dy_stride : a.x_stride;
+  float* const out = grad ? b.grad_state : b.chunk_state;
   const long cbase = seg_base(a.cu, sg.seq, kQ, a.tokens) + (long)sg.k * (a.seg / kQ);
   const int chunks = (sg.len + kQ - 1) / kQ;
-  double total = 0.0;
-  for (int ci = 0; ci < chunks; ++ci) {
-    const int c = GRAD ? chunks - 1 - ci : ci;
+  u32x4 rn[QN], rx[QX];
+  f32x4 rq;
+  const auto fetch = [&](int c) {
     const int rows = sg.len - c * kQ < kQ ? sg.len - c * kQ : kQ;
-    const long t0 = sg.tok + c * kQ;
-    if (!GRAD && live) {
-      f32x4* dst = reinterpret_cast<f32x4*>(b.chunk_state) +
-                   ((cbase + c) * a.vheads + v) * (NT * 2 * 64) + lane;
+    const long t0 = sg.tok + (long)c * kQ;
+#pragma unroll
+    for (int q = 0; q < QN; ++q) {
+      const int e = q * TH + (int)threadIdx.x, r = e / PN;
+      rn[q] = u32x4{0, 0, 0, 0};
+      if (r < rows) rn[q] = *reinterpret_cast<const u32x4*>(nsrc + (t0 + r) * nstride + (e % PN) * V);
+    }
+#pragma unroll
+    for (int q = 0; q < QX; ++q) {
+      const int e = q * 64 + lane, r = e / PX;
+      rx[q] = u32x4{0, 0, 0, 0};
+      if (live && r < rows) rx[q] = *reinterpret_cast<const u32x4*>(psrc + (t0 + r) * pstride + (e % PX) * V);
+    }
+    rq = b.dec[((cbase + c) * a.nheads + h) * kQ + lane];
+  };
+  float total = 0.f;
+  fetch(grad ? chunks - 1 : 0);
+  for (int ci = 0; ci < chunks; ++ci) {
+    const int c = grad ? chunks - 1 - ci : ci;
+    const int rows = sg.len - c * kQ < kQ ? sg.len - c * kQ : kQ;
+    if (STORE && live) {
+      f32x4* dst = reinterpret_cast<f32x4*>(out) + ((cbase + c) * a.vheads + v) * (NT * 2 * 64) + lane;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int p = 0; p < 2; ++p) dst[(n * 2 + p) * 64] = S[n][p];
     }
-    if (!GRAD && c + 1 == chunks) break;  // the last chunk's end state is not read
-    __syncthreads();
-    const void* nsrc = GRAD ? a.C : a.B;
-    const long nstride = GRAD ? a.C_stride : a.B_stride;
-    stage_tile<T, N, NP, 64 * W>(sB, LN,
-                                 static_cast<const E*>(nsrc) + t0 * nstride + (long)grp * N,
-                                 nstride, rows, threadIdx.x);
-    const void* psrc = GRAD ? b.dy : a.x;
-    const long pstride = GRAD ? b.dy_stride : a.x_stride;
-    stage_tile<T, kPT, kPT, 64>(sX[wave], LX,
-                                static_cast<const E*>(psrc) + t0 * pstride +
-                                    (long)h * a.headdim + p0,
-                                pstride, live ? rows : 0, lane);
-    const ChunkDt q = chunk_dt<T>(a, h, bias, A2, t0, rows, lane);
-    total += q.all;
-    sW[wave][lane] = GRAD ? exp2_f32((float)q.cum) : q.dt * exp2_f32((float)(q.all - q.cum));
-    const float decay = exp2_f32((float)q.all);
+    // the last value is read only as the gradient of the initial state
+    if (STORE && ci + 1 == chunks && !(grad && sg.first && b.dinit)) break;
+    __syncthreads();  // the previous chunk's tiles are no longer read
+#pragma unroll
+    for (int q = 0; q < QN; ++q) {
+      const int e = q * TH + (int)threadIdx.x, r = e / PN;
+      if (r < kQ) *reinterpret_cast<u32x4*>(sB + r * LN + (e % PN) * V) = rn[q];
+    }
+#pragma unroll
+    for (int q = 0; q < QX; ++q) {
+      const int e = q * 64 + lane;
+      *reinterpret_cast<u32x4*>(&sX[wave][(e / PX) * LX + (e % PX) * V]) = rx[q];
+    }
+    const f32x4 all = lane_of(rq, 63);
+    const float decay = exp2_f32(all[0] + all[1]);
+    total += all[0];
+    sW[wave][lane] = grad ? exp2_f32(rq[0] + rq[1]) : rq[2] * exp2_f32(gap2(all, rq));
+    if (ci + 1 < chunks) fetch(grad ? c - 1 : c + 1);
     __syncthreads();
     if (!live) continue;
 #pragma unroll
@@ -153,25 +214,37 @@ __global__ void __launch_bounds__(256) scan_states_kernel(const ScanBwdArgs b) {
         for (int r = 0; r < 4; ++r) S[n][p][r] *= decay;
     rank_update<T, NT, LX, LN, true>(S, sX[wave], sB, sW[wave], rows, lane);
   }
-  if (GRAD && live) {
+  if (!live) return;
+  if (!STORE) {
     const long base = ((long)slot * a.vheads + v) * (kPT * N);
+    float* const dst = grad ? b.seg_grad : a.seg_state;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int p = 0; p < 2; ++p)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) b.seg_grad[base + row_at<N>(n, p, r, lane)] = S[n][p][r];
-    if (lane == 0) b.grad_decay[(long)slot * a.vheads + v] = (float)total;
+        for (int r = 0; r < 4; ++r) dst[base + row_at<N>(n, p, r, lane)] = S[n][p][r];
+    if (lane == 0) (grad ? b.grad_decay : a.seg_decay)[(long)slot * a.vheads + v] = total;
+  } else if (grad && sg.first && b.dinit) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          b.dinit[sbase + row_at<N>(n, p, r, lane)] = has ? S[n][p][r] : 0.f;
   }
 }
 
-// Each sequence's segments from the last to the first: what a segment adds is
-// replaced by the gradient of its end state (the last one's is dfinal).
-__global__ void __launch_bounds__(256) scan_combine_grad_kernel(const ScanBwdArgs b) {
+// Each sequence's segments in order (from the first to the last for the states,
+// blocks below dir_blocks; from the last to the first for their gradients):
+// what a segment adds is replaced by the value that it starts from.
+__global__ void __launch_bounds__(256) scan_combine_both_kernel(const ScanBwdArgs b) {
   const ScanArgs& a = b.f;
   const int elems = kPT * a.dstate;
   const int per = (elems / 4 + 255) / 256;
-  const long id = blockIdx.x;
+  const bool grad = (int)blockIdx.x >= b.dir_blocks;
+  const long id = grad ? blockIdx.x - b.dir_blocks : blockIdx.x;
   const int e = ((int)(id % per) * 256 + (int)threadIdx.x) * 4;
   const int v = (int)(id / per % a.vheads), i = (int)(id / per / a.vheads);
   if (e >= elems) return;
@@ -179,36 +252,30 @@ __global__ void __launch_bounds__(256) scan_combine_grad_kernel(const ScanBwdArg
   const int segs = (sp.len + a.seg - 1) / a.seg;
   if (segs <= 1) return;
   f32x4 g = {0.f, 0.f, 0.f, 0.f};
-  if (b.dfinal)
-    g = *reinterpret_cast<const f32x4*>(b.dfinal + ((long)i * a.vheads + v) * elems + e);
+  if (grad) {
+    if (b.dfinal) g = *reinterpret_cast<const f32x4*>(b.dfinal + ((long)i * a.vheads + v) * elems + e);
+  } else {
+    const int pool = a.init ? scan_slot(a, i) : -1;
+    if (pool >= 0 && (!a.has_init || a.has_init[i]))
+      g = load_state4(a.init, ((long)pool * a.vheads + v) * elems + e, a.state_bf16);
+  }
+  float* const part = grad ? b.seg_grad : a.seg_state;
+  const float* const dec = grad ? b.grad_decay : a.seg_decay;
   const long base = seg_base(a.cu, i, a.seg, a.tokens);
-  for (int k = segs - 1; k >= 0; --k) {
+  for (int q = 0; q < segs; ++q) {
+    const int k = grad ? segs - 1 - q : q;
     const long at = (base + k) * a.vheads + v;
-    f32x4* const p = reinterpret_cast<f32x4*>(b.seg_grad + at * elems + e);
+    f32x4* const p = reinterpret_cast<f32x4*>(part + at * elems + e);
     f32x4 own = {0.f, 0.f, 0.f, 0.f};
     float d = 0.f;
-    if (k) {
+    if (q + 1 < segs) {
       own = *p;
-      d = exp2_f32(b.grad_decay[at]);
+      d = exp2_f32(dec[at]);
     }
     *p = g;
 #pragma unroll
     for (int r = 0; r < 4; ++r) g[r] = fmaf(d, g[r], own[r]);
   }
-}
-
-// Nothing is scheduled across this point: fully unrolled, the compiler would
-// start every tile's products at once and spill what they leave.
-__device__ static inline void keep_order() { __builtin_amdgcn_sched_barrier(0); }
-
-// The value is unknown from here on: what was computed from it is computed
-// again where it is next needed, instead of being kept in registers (the three
-// passes over the chunk's tiles share their products and decays, 80 registers).
-__device__ static inline void forget(float& v) { asm volatile("" : "+v"(v)); }
-__device__ static inline void forget(u32x4& v) { asm volatile("" : "+v"(v)); }
-__device__ static inline void forget(Mat<float>::Frag& f) {
-#pragma unroll
-  for (int e = 0; e < 8; ++e) forget(f.v[e]);
 }
 
 // Lane moves within a row of 16 lanes (DPP).  Zero where nothing comes in.
@@ -243,466 +310,457 @@ __device__ static inline float sum_g(float v) {
   v += __shfl_xor(v, 16, 64);
   return v + __shfl_xor(v, 32, 64);
 }
-__device__ static inline double wave_sum(double v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
-  return v;
-}
+// The value is unknown from here on: what is worked out from it (addresses,
+// conversions) is worked out again in each round of a loop, instead of being
+// kept in registers across all of them.
+__device__ static inline void forget(int& v) { asm volatile("" : "+v"(v)); }
+__device__ static inline void forget(u32x2& v) { asm volatile("" : "+v"(v)); }
+__device__ static inline void forget(f32x4& v) { asm volatile("" : "+v"(v)); }
 
-template <typename T, int N>
-__global__ void __launch_bounds__(64 * bwd_waves(sizeof(typename Mat<T>::E) == 4, N))
+// Nothing is scheduled across this point: fully unrolled, the compiler would
+// start every tile's products at once and spill what they leave.
+__device__ static inline void keep_order() { __builtin_amdgcn_sched_barrier(0); }
+
+// Inclusive sums over the wave's lanes, up to and from each lane.
+__device__ static inline float upto64(float v, int lane) {
+  v += row_move<0x111>(v);
+  v += row_move<0x112>(v);
+  v += row_move<0x114>(v);
+  v += row_move<0x118>(v);
+  const float a = __shfl(v, 15, 64), b = __shfl(v, 31, 64), c = __shfl(v, 47, 64);
+  const int g = lane >> 4;
+  return v + (g == 0 ? 0.f : (g == 1 ? a : (g == 2 ? a + b : (a + b) + c)));
+}
+__device__ static inline float from64(float v, int lane) {
+  v = from16(v);
+  const float a = __shfl(v, 16, 64), b = __shfl(v, 32, 64), c = __shfl(v, 48, 64);
+  const int g = lane >> 4;
+  return v + (g == 3 ? 0.f : (g == 2 ? c : (g == 1 ? b + c : a + (b + c))));
+}
+__device__ static inline float sum64(float v) { return sum_g(sum16(v)); }
+
+// Waves of a workgroup of the main launch: one for every 32 state columns, four
+// at least (and four for fp32's 256 columns, whose tiles leave no room for more).  State rows of one unit of its work: a head's 64 (or 32), 32 in fp32,
+// whose tiles of 64 would not fit.
+constexpr int bwd_waves(bool f32, int n) { return n == 256 && !f32 ? 8 : 4; }
+static inline int bwd_rows(bool f32, int headdim) { return f32 || headdim == 32 ? 32 : 64; }
+
+// One chunk, the units of one block.  A wave owns 32 state columns: it holds
+// dB and dC of all 64 tokens there in registers and adds every head's to them,
+// so the heads are joined without leaving the workgroup.  The products of the
+// chunk's tokens with each other (dy.x, the decays, C.B, which is the same for
+// all heads) are shared: each wave works out some of the ten 16x16 tiles on and
+// below the diagonal and leaves them in LDS.
+template <typename T, int N, int PB>
+__global__ void __launch_bounds__(64 * bwd_waves(sizeof(typename Mat<T>::E) == 4, N),
+                                  sizeof(typename Mat<T>::E) == 4 ? 1 : 2)
     scan_bwd_kernel(const ScanBwdArgs b) {
   typedef Mat<T> M;
   typedef typename M::E E;
   typedef typename M::Frag Frag;
-  constexpr int W = bwd_waves(sizeof(E) == 4, N), TH = 64 * W;
-  constexpr int NP = N < 32 ? 32 : N, LN = NP + M::kPad, LX = kPT + M::kPad;
-  constexpr int NT = N / 16, KB = NP / 32, T2 = M::kTerms == 1 ? 1 : 2;
-  constexpr int LE = kPT + M::kPad;
-  constexpr int kRed = W * 4 * 64 * 16;              // one n-tile of every wave
-  constexpr int kEx = W * 32 * LE * (int)sizeof(E);  // 32 state columns of every wave
-  constexpr int kShare = 2 * kRed > kEx ? 2 * kRed : kEx;
+  constexpr int W = bwd_waves(sizeof(E) == 4, N), TH = 64 * W, V = 16 / sizeof(E);
+  constexpr int NP = N < 32 ? 32 : N, LN = NP + M::kPad, LX = PB + M::kPad, LM = kQ + M::kPad;
+  constexpr int NT = N / 16, NW = NT < W ? 1 : NT / W, KB = NP / 32, SL = PB / 32;
+  constexpr int PX = PB / V, QX = (kQ * PX + TH - 1) / TH;
+  constexpr int kXY = kQ * LX, kMM = kQ * LM, kS = NP * LX;
+  constexpr int kWork = 2 * kXY + 2 * kMM + kS;
+  static_assert(kWork >= kQ * LN, "C's tile fits where the units work");
   __shared__ __attribute__((aligned(16))) E sB[kQ * LN];
-  __shared__ __attribute__((aligned(16))) E sC[kQ * LN];
-  __shared__ __attribute__((aligned(16))) E sY[W][kQ * LX];
-  __shared__ f32x4 sCB[10][64];
-  __shared__ __attribute__((aligned(16))) char share[kShare];
-  __shared__ float2 sA[W][kQ];
-  __shared__ __attribute__((aligned(16))) float sD[W][kQ];
-  __shared__ __attribute__((aligned(16))) float sE[W][kQ];  // e^{a_t}
+  __shared__ __attribute__((aligned(16))) E work[kWork];
+  __shared__ f32x4 sQ[kQ];
+  __shared__ float sR[kQ][4];       // w: a row's sum over each earlier tile
+  __shared__ float sS[4][kQ];       // w / dt: a column's sum over each later tile
+  __shared__ float sI[kQ], sDQ[kQ], sDD[kQ];
+  __shared__ float sP[W][kQ], sE[W][kQ], sK0[W];
+  E* const sC = work;               // at the start only
+  E* const sX = work;
+  E* const sY = work + kXY;
+  E* const sM = work + 2 * kXY;     // [t][u]: e^{a_u-a_t} C_u.B_t
+  E* const sK = sM + kMM;           // [t][u]: K_ut
+  E* const sG = sK + kMM;           // [n][p]: dS
 
   const ScanArgs& a = b.f;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i16 = lane & 15, g = lane >> 4;
+  const int lane0 = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int lane = lane0, i16 = lane & 15, g = lane >> 4;
   const int id = xcd_tile(blockIdx.x, gridDim.x);
   const int slot = id / (a.ngroups * b.hb), rest = id % (a.ngroups * b.hb);
-  const int grp = rest / b.hb, hblk = rest % b.hb, vl = hblk * W + wave;
-  const Segment sg = find_segment(a.cu, a.seqs, a.tokens, a.seg, slot);
-  const bool live = vl < a.vpg;
-  const int v = grp * a.vpg + (live ? vl : 0);
-  const int slices = a.headdim / kPT, h = v / slices, p0 = (v % slices) * kPT;
-  double* const hp = b.head_part + ((long)slot * a.vheads + v) * 3;
+  const int grp = rest / b.hb, hblk = rest % b.hb;
+  const Segment sg = find_segment(a.cu, a.seqs, a.tokens, kQ, slot);
+  const int u0 = hblk * b.upb, u1 = u0 + b.upb < b.upg ? u0 + b.upb : b.upg;
+  const int units = b.upg * a.ngroups, per = a.headdim / PB;
   if (threadIdx.x == 0 && rest == 0 && sg.first && a.status) {
     if (sg.bad) atomicOr(a.status, RSSM_ST_BAD_SEQ);
     if (a.init && scan_slot(a, sg.seq) < 0) atomicOr(a.status, RSSM_ST_BAD_SLOT);
   }
-  const long sbase = ((long)sg.seq * a.vheads + v) * (kPT * N);
-  const bool has = a.init && scan_slot(a, sg.seq) >= 0 && (!a.has_init || a.has_init[sg.seq]);
+  f32x4* const hp = reinterpret_cast<f32x4*>(b.head_part) + (long)slot * units + grp * b.upg;
   if (sg.len == 0) {
-    if (live && lane < 3) hp[lane] = 0.0;
-    if (live && sg.empty && b.dinit) {  // the state passes through
-      for (int e = lane; e < kPT * N; e += 64)
-        b.dinit[sbase + e] = has && b.dfinal ? b.dfinal[sbase + e] : 0.f;
-    }
+    for (int u = u0 + (int)threadIdx.x; u < u1; u += TH) hp[u] = f32x4{0.f, 0.f, 0.f, 0.f};
     return;
   }
-  const double A2 = (double)a.A[h] * 1.4426950408889634074;
-  const float Ah = a.A[h], bias = a.dt_bias ? a.dt_bias[h] : 0.f, Dh = a.D ? a.D[h] : 0.f;
+  const int rows = sg.len;
+  const long t0 = sg.tok;
 
-  // dS: rows tile_col(pt, 4g + r), columns 16 nt + i16
-  f32x4 S[NT][2];
+  stage_tile<T, N, NP, TH>(sB, LN, static_cast<const E*>(a.B) + t0 * a.B_stride + (long)grp * N,
+                           a.B_stride, rows, threadIdx.x);
+  stage_tile<T, N, NP, TH>(sC, LN, static_cast<const E*>(a.C) + t0 * a.C_stride + (long)grp * N,
+                           a.C_stride, rows, threadIdx.x);
+  __syncthreads();
+  // C_u.B_t of this wave's tiles (rows u, columns t), tile k = iu (iu+1)/2 + j
+  constexpr int KT = (10 + W - 1) / W;
+  f32x4 cb[KT];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) S[n][0] = S[n][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-  if (live && (!sg.last || b.dfinal)) {
-    const float* src = sg.last ? b.dfinal + sbase
-                               : b.seg_grad + ((long)slot * a.vheads + v) * (kPT * N);
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int p = 0; p < 2; ++p)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) S[n][p][r] = src[row_at<N>(n, p, r, lane)];
-  }
-  double sum_a = 0.0, sum_b = 0.0, sum_d = 0.0;
-  const long cbase = seg_base(a.cu, sg.seq, kQ, a.tokens) + (long)sg.k * (a.seg / kQ);
-
-  for (int c = (sg.len + kQ - 1) / kQ - 1; c >= 0; --c) {
-    const int rows = sg.len - c * kQ < kQ ? sg.len - c * kQ : kQ;
-    const long t0 = sg.tok + c * kQ;
-    __syncthreads();
-    stage_tile<T, N, NP, TH>(sB, LN, static_cast<const E*>(a.B) + t0 * a.B_stride + (long)grp * N,
-                             a.B_stride, rows, threadIdx.x);
-    stage_tile<T, N, NP, TH>(sC, LN, static_cast<const E*>(a.C) + t0 * a.C_stride + (long)grp * N,
-                             a.C_stride, rows, threadIdx.x);
-    // x and dy rows 16 j + i16, elements 8g.. (order D of the state's rows)
-    Frag xf[4], yf[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int t = 16 * j + i16;
-      float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      xf[j] = yf[j] = M::pack(z);
-      if (live && t < rows) {
-        const long col = (long)h * a.headdim + p0 + 8 * g;
-        xf[j] = M::rows_c(static_cast<const E*>(a.x) + (t0 + t) * a.x_stride + col);
-        yf[j] = M::rows_c(static_cast<const E*>(b.dy) + (t0 + t) * b.dy_stride + col);
-      }
-      *reinterpret_cast<Frag*>(&sY[wave][t * LX + 8 * g]) = yf[j];
-    }
-    const ChunkDt q = chunk_dt<T>(a, h, bias, A2, t0, rows, lane);
-    {
-      const float hi = (float)q.cum;
-      sA[wave][lane] = make_float2(hi, (float)(q.cum - (double)hi));
-      sD[wave][lane] = q.dt;
-      sE[wave][lane] = exp2_f32((float)q.cum);
-    }
-    const float decay = exp2_f32((float)q.all);
-    const float ahi = (float)q.all, alo = (float)(q.all - (double)ahi);
-    __syncthreads();
-    // C_u.B_t for the ten tiles on and below the diagonal, shared by the heads
-    for (int k = wave; k < 10; k += W) {
+  for (int q = 0; q < KT; ++q) {
+    const int k = wave + q * W;
+    cb[q] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (k < 10) {
       const int iu = k < 1 ? 0 : (k < 3 ? 1 : (k < 6 ? 2 : 3)), j = k - iu * (iu + 1) / 2;
-      f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb)
-        acc = M::mma(M::rows_c(sC + (16 * iu + i16) * LN + 32 * kb + 8 * g),
-                     M::rows_c(sB + (16 * j + i16) * LN + 32 * kb + 8 * g), acc);
-      sCB[k][lane] = acc;
+        cb[q] = M::mma(M::rows_c(sC + (16 * iu + i16) * LN + 32 * kb + 8 * g),
+                       M::rows_c(sB + (16 * j + i16) * LN + 32 * kb + 8 * g), cb[q]);
     }
-    __syncthreads();
+  }
+  // this wave's columns of C as operands (rows n, k tokens) and C's values
+  // where a product's result has them (n = 4g + r, token 16 j + i16); B's are
+  // read again for each unit
+  Frag fc[NW][2];
+  typename M::Four rc[NW][4];
+#pragma unroll
+  for (int q = 0; q < NW; ++q) {
+    const int nt = wave * NW + q;
+    if (nt < NT) {
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+        fc[q][kb] = M::cols(cols_at<T, false>(sC, LN, 32 * kb, 16 * nt, lane), LN);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        rc[q][j] = *reinterpret_cast<const typename M::Four*>(sC + (16 * j + i16) * LN + 16 * nt + 4 * g);
+    }
+  }
+  f32x4 aB[NW][4], aC[NW][4];
+#pragma unroll
+  for (int q = 0; q < NW; ++q)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) aB[q][j] = aC[q][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  __syncthreads();  // C's tile is no longer read
+  // tiles (u, t) = (0, 1) and (2, 3), above the diagonal, are read as zeros
+  for (int e = threadIdx.x; e < 512; e += TH) {
+    const int o = (16 + ((e >> 8) << 5) + ((e >> 4) & 15)) * LM + ((e >> 8) << 5) + (e & 15);
+    Elt<T>::store1(sM, o, 0.f);
+    Elt<T>::store1(sK, o, 0.f);
+  }
+  if (N < NP)
+    for (int e = threadIdx.x; e < (NP - N) * LX; e += TH) Elt<T>::store1(sG, N * LX + e, 0.f);
 
-    // ---- this head's products inside the chunk, rows u, columns t
-    float2 at[4];
-    float dt_t[4];
+  u32x4 rx[QX], ry[QX];
+  f32x4 rq;
+  const auto fetch = [&](int u) {
+    const int hu = grp * b.upg + u, h = hu / per;
+    const long col = (long)h * a.headdim + (long)(hu % per) * PB;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      at[j] = sA[wave][16 * j + i16];
-      dt_t[j] = sD[wave][16 * j + i16];
+    for (int q = 0; q < QX; ++q) {
+      const int e = q * TH + (int)threadIdx.x, r = e / PX, c = (e % PX) * V;
+      rx[q] = ry[q] = u32x4{0, 0, 0, 0};
+      if (r < rows) {
+        rx[q] = *reinterpret_cast<const u32x4*>(static_cast<const E*>(a.x) + (t0 + r) * a.x_stride + col + c);
+        ry[q] = *reinterpret_cast<const u32x4*>(static_cast<const E*>(b.dy) + (t0 + r) * b.dy_stride + col + c);
+      }
     }
-    const auto forget_all = [&]() {
+    rq = b.dec[((long)slot * a.nheads + h) * kQ + lane];
+  };
+  fetch(u0);
+
+#pragma unroll 1
+  for (int u = u0; u < u1; ++u) {
+    const int hu = grp * b.upg + u, h = hu / per, p0 = (hu % per) * PB;
+    int again = 0;
+    lane = lane0;
+    forget(lane);
+    forget(again);
+    i16 = lane & 15;
+    g = lane >> 4;
+    const E* const tB = sB + again;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        forget(xf[j]);
-        forget(yf[j]);
-        forget(at[j].x);
-        forget(at[j].y);
-        forget(dt_t[j]);
-      }
+    for (int q = 0; q < NW; ++q)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) forget(rc[q][j]);
+#pragma unroll
+    for (int q = 0; q < QX; ++q) {
+      const int e = q * TH + (int)threadIdx.x, o = (e / PX) * LX + (e % PX) * V;
+      if (e >= kQ * PX) break;
+      *reinterpret_cast<u32x4*>(sX + o) = rx[q];
+      *reinterpret_cast<u32x4*>(sY + o) = ry[q];
+    }
+    if (wave == 0) sQ[lane] = rq;
+    __syncthreads();
+    if (u + 1 < u1) fetch(u + 1);
+    // the states' first column tile is on its way during the tokens' products
+    const f32x4* const ss = reinterpret_cast<const f32x4*>(b.chunk_state) +
+        ((long)slot * a.vheads + (long)hu * SL) * (NT * 2 * 64) + lane;
+    const f32x4* const gs = reinterpret_cast<const f32x4*>(b.grad_state) +
+        ((long)slot * a.vheads + (long)hu * SL) * (NT * 2 * 64) + lane;
+    f32x4 ls[SL][2], lg[SL][2];
+    const auto load = [&](f32x4 (&l)[SL][2], const f32x4* from, int nt) {
+#pragma unroll
+      for (int s = 0; s < SL; ++s)
+#pragma unroll
+        for (int p = 0; p < 2; ++p) l[s][p] = from[(s * NT + nt) * 128 + p * 64];
     };
-    float my_w = 0.f, my_q = 0.f, my_i = 0.f, my_e = 0.f;
-    float tot[2] = {0.f, 0.f};  // w over (u, s) tiles {2,3} x {0} and {3} x {0,1}
-    {
-      f32x4 X[4][2];  // dx^T: rows tile_col(p, 4g + r), column t
+    if (wave * NW < NT) {
+      load(ls, ss, wave * NW);
+      load(lg, gs, wave * NW);
+    }
+
+    // ---- the tokens' products with each other
 #pragma unroll
-      for (int j = 0; j < 4; ++j) X[j][0] = X[j][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-      // e^{a_Q - a_t} dS B_t: dS goes through LDS (32 columns at a time) to
-      // turn its rows into operand rows, rounded to the io type as dx is
-      E* const ex = reinterpret_cast<E*>(share) + wave * 32 * LE;
+    for (int q = 0; q < KT; ++q) {
+      const int k = wave + q * W;
+      if (k >= 10) break;
+      const int iu = k < 1 ? 0 : (k < 3 ? 1 : (k < 6 ? 2 : 3)), j = k - iu * (iu + 1) / 2;
+      const int t = 16 * j + i16, uu = 16 * iu + 4 * g;
+      f32x4 d = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int kb = 0; kb < KB; ++kb) {
+      for (int s = 0; s < SL; ++s)
+        d = M::mma(M::rows_c(sY + (16 * iu + i16) * LX + 32 * s + 8 * g),
+                   M::rows_c(sX + t * LX + 32 * s + 8 * g), d);
+      const f32x4 qt = sQ[t];
+      float m[4], kk[4], col = 0.f, rw[4], in = 0.f, dd = 0.f;
 #pragma unroll
-        for (int q2 = 0; q2 < 2; ++q2)
-#pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            const int n = 2 * kb + q2;
-            E* const d = ex + (16 * q2 + i16) * LE + pair_base(p) + 8 * g;
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-              Elt<T>::store1(d, r, n < NT ? S[n < NT ? n : 0][p][r] : 0.f);
-          }
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_s_waitcnt(0xc07f);  // the wave's own LDS writes are in
-        __builtin_amdgcn_wave_barrier();
-        Frag sf[2];
-#pragma unroll
-        for (int p = 0; p < 2; ++p)
-          sf[p] = M::cols(cols_at<T, true>(ex, LE, 0, pair_base(p), lane), LE);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const Frag bt = M::rows_d(sB + (16 * j + i16) * LN + 32 * kb + 4 * g);
-#pragma unroll
-          for (int p = 0; p < 2; ++p) X[j][p] = M::mma(sf[p], bt, X[j][p]);
+      for (int r = 0; r < 4; ++r) {
+        const float e = exp2_f32(gap2(sQ[uu + r], qt));
+        const bool on = uu + r >= t;
+        m[r] = on ? e * cb[q][r] : 0.f;
+        kk[r] = on ? e * d[r] * qt[2] : 0.f;
+        const float s = m[r] * d[r];
+        col += s;
+        rw[r] = s * qt[2];
+        if (iu == j) {
+          // within the tile: sum of w_us over s < t <= u, for this t
+          const float p = before16(uu + r > t ? rw[r] : 0.f);
+          in += on ? p : 0.f;
+          dd += uu + r == t ? d[r] : 0.f;
         }
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_s_waitcnt(0xc07f);  // and read before the next columns land
-        __builtin_amdgcn_wave_barrier();
-        keep_order();
       }
-      float racc[4][4] = {};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float et = exp2_f32((ahi - at[j].x) + (alo - at[j].y));
-#pragma unroll
-        for (int p = 0; p < 2; ++p)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) X[j][p][r] *= et;
-        float col = 0.f, in = 0.f, diag = 0.f, dd = 0.f;
-#pragma unroll
-        for (int kb = j / 2; kb < 2; ++kb) {
-          float m1[8];
-#pragma unroll
-          for (int q2 = 0; q2 < 2; ++q2) {
-            const int iu = 2 * kb + q2;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) m1[4 * q2 + r] = 0.f;
-            if (iu < j) continue;
-            const f32x4 dxt = M::mma(yf[iu], xf[j], f32x4{0.f, 0.f, 0.f, 0.f});
-            const f32x4 cb = sCB[iu * (iu + 1) / 2 + j][lane];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const int u = 16 * iu + 4 * g + r, t = 16 * j + i16;
-              const float e = exp2_f32(gap2(sA[wave][u], at[j]));
-              const float m = u >= t ? e * cb[r] : 0.f;
-              const float s = m * dxt[r];
-              m1[4 * q2 + r] = m;
-              if (iu > j) {
-                const float w = s * dt_t[j];
-                col += s;
-                racc[iu][r] += w;
-                if (j == 0 && iu >= 2) tot[0] += w;
-                if (j <= 1 && iu == 3) tot[1] += w;
-              } else {
-                // within the tile: sum of w_us over s < t <= u, for this t
-                const float p = before16(u > t ? s * dt_t[j] : 0.f);
-                in += u >= t ? p : 0.f;
-                diag += u >= t ? s : 0.f;
-                dd += u == t ? dxt[r] : 0.f;
-              }
-            }
-          }
-          const Frag mf = M::pack(m1);
-#pragma unroll
-          for (int p = 0; p < 2; ++p)
-            X[j][p] = M::mma(M::cols(cols_at<T, true>(sY[wave], LX, 32 * kb, pair_base(p), lane),
-                                     LX), mf, X[j][p]);
+      *reinterpret_cast<typename M::Four*>(sM + t * LM + uu) = M::pack4(m);
+      *reinterpret_cast<typename M::Four*>(sK + t * LM + uu) = M::pack4(kk);
+      col = sum_g(col);
+      if (iu == j) {
+        in = sum_g(in);
+        dd = sum_g(dd);
+        if (g == 0) {
+          sI[t] = in;
+          sDQ[t] = col;
+          sDD[t] = dd;
         }
-        // u >= t in this tile's rows, u in later tiles
-        col = sum_g(col);
-        const float w = before16(col * dt_t[j]) + sum_g(in);
-        const float qq = col + sum_g(diag);
-        if (g == j) {
-          my_w = w;
-          my_q = qq;
-        }
-        sum_d += (double)dd;
-        const int t = 16 * j + i16;
-        if (live && t < rows) {
-          float o[8], yv[8];
-          M::unpack(yf[j], yv);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            o[r] = fmaf(Dh, yv[r], dt_t[j] * X[j][0][r]);
-            o[4 + r] = fmaf(Dh, yv[4 + r], dt_t[j] * X[j][1][r]);
-          }
-          Vec8<T>::store(b.dx, (t0 + t) * (long)a.nheads * a.headdim + (long)h * a.headdim + p0 +
-                                   8 * g, o);
-        }
-        keep_order();
-      }
-      // rows' sums over the columns of earlier tiles, u at and after t: token
-      // 16 iu + 4g + r is in the lanes of g, and goes to lane 4g + r first
-#pragma unroll
-      for (int iu = 1; iu < 4; ++iu) {
+      } else {
         float mine = 0.f;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const float got = __shfl(sum16(racc[iu][r]), 16 * (i16 >> 2), 64);
-          mine = (i16 & 3) == r ? got : mine;
+          const float s = sum16(rw[r]);
+          mine = (i16 & 3) == r ? s : mine;
         }
-        mine = from16(mine);
-        if (g == iu) my_w += mine;
+        if (i16 < 4) sR[uu + i16][j] = mine;
+        if (g == 0) sS[iu][t] = col;
       }
-      const float t1 = sum_g(sum16(tot[0])), t2 = sum_g(sum16(tot[1]));
-      my_w += g == 1 ? t1 : (g == 2 ? t2 : 0.f);
-    }
-    __syncthreads();  // the exchange's memory becomes the joining buffers
-    forget_all();
-
-    // ---- dC, then dB: a column tile of 16 at a time over all tokens, joined
-    // over the waves (two buffers: one barrier a tile)
-    f32x4(*const red)[W][4][64] = reinterpret_cast<f32x4(*)[W][4][64]>(share);
-    double k0 = 0.0;
-    const auto join = [&](int buf, int nt, float* part) {
-      for (int e = threadIdx.x; e < 256; e += TH) {
-        const int j = e >> 6, l = e & 63;
-        f32x4 s = red[buf][0][j][l];
-#pragma unroll
-        for (int w = 1; w < W; ++w) {
-          const f32x4 o = red[buf][w][j][l];
-#pragma unroll
-          for (int r = 0; r < 4; ++r) s[r] += o[r];
-        }
-        const int t = 16 * j + (l & 15);
-        if (t < rows)
-          *reinterpret_cast<f32x4*>(part + (((long)hblk * a.tokens + t0 + t) * a.ngroups + grp) * N +
-                                    16 * nt + 4 * (l >> 4)) = s;
-      }
-    };
-    {
-      Split<T, T2> m3[4][2];  // e^{a_t - a_s} dt_s (x_s.dy_t): rows s, columns t
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int kb = 0; kb <= j / 2; ++kb) {
-          float m[8];
-#pragma unroll
-          for (int q2 = 0; q2 < 2; ++q2) {
-            const int is = 2 * kb + q2;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) m[4 * q2 + r] = 0.f;
-            if (is > j) continue;
-            const f32x4 dxt = M::mma(xf[is], yf[j], f32x4{0.f, 0.f, 0.f, 0.f});
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const int s = 16 * is + 4 * g + r, t = 16 * j + i16;
-              const float e = exp2_f32(gap2(at[j], sA[wave][s])) * sD[wave][s];
-              m[4 * q2 + r] = s <= t ? e * dxt[r] : 0.f;
-            }
-          }
-          m3[j][kb].set(m);
-          keep_order();
-        }
-      float dot[4] = {0.f, 0.f, 0.f, 0.f};
-      const f32x4* src = reinterpret_cast<const f32x4*>(b.chunk_state) +
-                         ((cbase + c) * a.vheads + v) * (NT * 2 * 64) + lane;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const f32x4 s0 = live ? src[nt * 128] : f32x4{0.f, 0.f, 0.f, 0.f};
-        const f32x4 s1 = live ? src[nt * 128 + 64] : f32x4{0.f, 0.f, 0.f, 0.f};
-        float f[8], ks = 0.f;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          f[r] = s0[r];
-          f[4 + r] = s1[r];
-          ks = fmaf(s0[r], S[nt][0][r], fmaf(s1[r], S[nt][1][r], ks));
-        }
-        k0 += (double)ks;
-        Split<T, M::kTerms> ss;
-        ss.set(f);
-        Frag bc[2];
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
-          bc[kb] = M::cols(cols_at<T, false>(sB, LN, 32 * kb, 16 * nt, lane), LN);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          f32x4 acc = ss.a_times(yf[j], f32x4{0.f, 0.f, 0.f, 0.f});
-          const E* cp = sC + (16 * j + i16) * LN + 16 * nt + 4 * g;
-          const float et = sE[wave][16 * j + i16];
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            dot[j] = fmaf(acc[r], Elt<T>::load1(cp, r), dot[j]);
-            acc[r] *= et;
-          }
-#pragma unroll
-          for (int kb = 0; kb <= j / 2; ++kb) acc = m3[j][kb].b_times(bc[kb], acc);
-          red[nt & 1][wave][j][lane] = acc;
-          keep_order();
-        }
-        __syncthreads();
-        join(nt & 1, nt, b.dC_part);
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float s = sum_g(dot[j]) * sE[wave][16 * j + i16];
-        if (g == j) my_i = s;
-      }
+      keep_order();
     }
     __syncthreads();
-    forget_all();
-    {
-      Split<T, T2> m2[4][2];  // e^{a_u - a_t} (dy_u.x_t): rows u, columns t
+
+    // ---- dC, dB and the states' part of the decay's gradient
+    const f32x4 qa = sQ[kQ - 1];
+    if (wave * NW < NT) {
+      float et[4], ft[4], dti[4], doti[4], dote[4], k0 = 0.f;
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < 4; ++j) {
+        const f32x4 q = sQ[16 * j + i16];
+        et[j] = exp2_f32(q[0] + q[1]);
+        ft[j] = exp2_f32(gap2(qa, q));
+        dti[j] = q[2] * ft[j];
+        doti[j] = dote[j] = 0.f;
+      }
 #pragma unroll
-        for (int kb = j / 2; kb < 2; ++kb) {
-          float m[8];
+      for (int q = 0; q < NW; ++q) {
+        const int nt = wave * NW + q;
+        Split<T, M::kTerms> hs[SL];
+        const auto split = [&](const f32x4 (&l)[SL][2]) {
 #pragma unroll
-          for (int q2 = 0; q2 < 2; ++q2) {
-            const int iu = 2 * kb + q2;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) m[4 * q2 + r] = 0.f;
-            if (iu < j) continue;
-            const f32x4 dxt = M::mma(yf[iu], xf[j], f32x4{0.f, 0.f, 0.f, 0.f});
+          for (int s = 0; s < SL; ++s) {
+            float f[8];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-              const int u = 16 * iu + 4 * g + r, t = 16 * j + i16;
-              const float e = exp2_f32(gap2(sA[wave][u], at[j]));
-              m[4 * q2 + r] = u >= t ? e * dxt[r] : 0.f;
+              f[r] = l[s][0][r];
+              f[4 + r] = l[s][1][r];
             }
+            hs[s].set(f);
           }
-          m2[j][kb].set(m);
-          keep_order();
-        }
-      float dot[4] = {0.f, 0.f, 0.f, 0.f};
+        };
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float f[8];
+        for (int s = 0; s < SL; ++s)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          f[r] = S[nt][0][r];
-          f[4 + r] = S[nt][1][r];
-        }
-        Split<T, M::kTerms> ss;
-        ss.set(f);
-        Frag cc[2];
+          for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) k0 = fmaf(ls[s][p][r], lg[s][p][r], k0);
+        split(ls);
+        if (q + 1 < NW) load(ls, ss, nt + 1);
+        Frag fb[2];
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb)
-          cc[kb] = M::cols(cols_at<T, false>(sC, LN, 32 * kb, 16 * nt, lane), LN);
+          fb[kb] = M::cols(cols_at<T, false>(tB, LN, 32 * kb, 16 * nt, lane), LN);
+        keep_order();
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          f32x4 acc = ss.a_times(xf[j], f32x4{0.f, 0.f, 0.f, 0.f});
-          const E* bp = sB + (16 * j + i16) * LN + 16 * nt + 4 * g;
-          const float et = exp2_f32((ahi - at[j].x) + (alo - at[j].y));
+          f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int s = 0; s < SL; ++s)
+            acc = hs[s].a_times(M::rows_c(sY + (16 * j + i16) * LX + 32 * s + 8 * g), acc);
+#pragma unroll
+          for (int kb = 0; kb <= j / 2; ++kb)
+            aC[q][j] = M::mma(fb[kb], M::cols(cols_at<T, false>(sK, LM, 32 * kb, 16 * j, lane), LM), aC[q][j]);
+          float cv[4];
+          M::unpack4(rc[q][j], cv);
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            dot[j] = fmaf(acc[r], Elt<T>::load1(bp, r), dot[j]);
-            acc[r] *= et;
+            doti[j] = fmaf(acc[r], cv[r], doti[j]);
+            aC[q][j][r] = fmaf(et[j], acc[r], aC[q][j][r]);
           }
-#pragma unroll
-          for (int kb = j / 2; kb < 2; ++kb) acc = m2[j][kb].b_times(cc[kb], acc);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) acc[r] *= dt_t[j];
-          red[nt & 1][wave][j][lane] = acc;
           keep_order();
         }
-        __syncthreads();
-        join(nt & 1, nt, b.dB_part);
+        split(lg);
+        if (q + 1 < NW) load(lg, gs, nt + 1);
+#pragma unroll
+        for (int s = 0; s < SL; ++s)
+          *reinterpret_cast<Frag*>(sG + (16 * nt + i16) * LX + 32 * s + 8 * g) = hs[s].t[0];
+        keep_order();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int s = 0; s < SL; ++s)
+            acc = hs[s].a_times(M::rows_c(sX + (16 * j + i16) * LX + 32 * s + 8 * g), acc);
+#pragma unroll
+          for (int kb = j / 2; kb < 2; ++kb)
+            aB[q][j] = M::mma(fc[q][kb], M::rows_d(sK + (16 * j + i16) * LM + 32 * kb + 4 * g), aB[q][j]);
+          float bv[4];
+          M::unpack4(*reinterpret_cast<const typename M::Four*>(tB + (16 * j + i16) * LN + 16 * nt + 4 * g), bv);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            dote[j] = fmaf(acc[r], bv[r], dote[j]);
+            aB[q][j][r] = fmaf(dti[j], acc[r], aB[q][j][r]);
+          }
+          keep_order();
+        }
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float s = sum_g(dot[j]) * exp2_f32((ahi - at[j].x) + (alo - at[j].y));
-        if (g == j) my_e = s;
+        const float i = sum_g(doti[j]) * et[j], e = sum_g(dote[j]) * ft[j];
+        if (g == 0) {
+          sP[wave][16 * j + i16] = i;
+          sE[wave][16 * j + i16] = e;
+        }
       }
+      k0 = sum64(k0);
+      if (lane == 0) sK0[wave] = k0;
     }
-    // ---- the decay's gradient, one token per lane
-    k0 = wave_sum(k0) * (double)decay;
+    __syncthreads();
+
+    // ---- dx: a wave takes every other slice of 32 rows and some of the tokens
     {
-      const double back = (double)my_i;
-      const double ahead = (double)q.dt * (double)my_e;
-      const double sb = wave_cumsum(back, lane), sf = wave_cumsum(ahead, lane);
-      const double dal = k0 + (double)my_w + (__shfl(sb, 63, 64) - sb + back) + (sf - ahead);
-      const double sig = a.dt_softplus ? 1.0 / (1.0 + (double)expf(-q.raw)) : 1.0;
-      const double dd = ((double)my_q + (double)my_e + (double)Ah * dal) * sig;
-      if (lane < rows) {
-        sum_a += dal * (double)q.dt;
-        sum_b += dd;
-        if (live) b.ddt_part[(long)v * a.tokens + t0 + lane] = (float)dd;
+      constexpr int NJ = 8 / W;  // token tiles of a wave: j and 3 - j, or one
+      const int jw = wave >> 1;
+      for (int s = wave & 1; s < SL; s += 2) {
+        f32x4 X[NJ][2];
+#pragma unroll
+        for (int q = 0; q < NJ; ++q) X[q][0] = X[q][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) {
+          Frag f[2];
+#pragma unroll
+          for (int p = 0; p < 2; ++p)
+            f[p] = M::cols(cols_at<T, true>(sG, LX, 32 * kb, 32 * s + pair_base(p), lane), LX);
+#pragma unroll
+          for (int q = 0; q < NJ; ++q) {
+            const int j = q ? 3 - jw : jw;
+            const Frag bt = M::rows_d(tB + (16 * j + i16) * LN + 32 * kb + 4 * g);
+#pragma unroll
+            for (int p = 0; p < 2; ++p) X[q][p] = M::mma(f[p], bt, X[q][p]);
+          }
+          keep_order();
+        }
+#pragma unroll
+        for (int q = 0; q < NJ; ++q) {
+          const int j = q ? 3 - jw : jw, t = 16 * j + i16;
+          const f32x4 qt = sQ[t];
+          const float ft = exp2_f32(gap2(qa, qt));
+#pragma unroll
+          for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) X[q][p][r] *= ft;
+          for (int kb = j >> 1; kb < 2; ++kb) {
+            const Frag mf = M::rows_d(sM + t * LM + 32 * kb + 4 * g);
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+              X[q][p] = M::mma(M::cols(cols_at<T, true>(sY, LX, 32 * kb, 32 * s + pair_base(p), lane), LX),
+                               mf, X[q][p]);
+          }
+          if (t < rows) {
+            const float Dh = a.D ? a.D[h] : 0.f;
+            float o[8], yv[8];
+            M::unpack(M::rows_c(sY + t * LX + 32 * s + 8 * g), yv);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              o[r] = fmaf(Dh, yv[r], qt[2] * X[q][0][r]);
+              o[4 + r] = fmaf(Dh, yv[4 + r], qt[2] * X[q][1][r]);
+            }
+            Vec8<T>::store(b.dx, (t0 + t) * (long)a.nheads * a.headdim + (long)h * a.headdim + p0 +
+                                     32 * s + 8 * g, o);
+          }
+        }
       }
     }
-    // ---- the gradient of the chunk before's end state
+    // ---- the decay's gradient, one token per lane; the waves take turns
+    if (wave == (u & (W - 1))) {
+      const f32x4 q = sQ[lane];
+      const float dt = q[2];
+      float row = 0.f, cs = 0.f, pi = 0.f, pe = 0.f, k0 = 0.f;
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+      for (int k = 0; k < 3; ++k) row += k < g ? sR[lane][k] : 0.f;
 #pragma unroll
-      for (int p = 0; p < 2; ++p)
+      for (int k = 1; k < 4; ++k) cs += k > g ? sS[k][lane] : 0.f;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) S[n][p][r] *= decay;
-    rank_update<T, NT, LX, LN, true>(S, sY[wave], sC, sE[wave], rows, lane);
+      for (int w = 0; w < (NT < W ? NT : W); ++w) {
+        pi += sP[w][lane];
+        pe += sE[w][lane];
+        k0 += sK0[w];
+      }
+      // totals of the tiles later and earlier than this token's on either side
+      const float s0 = sum16(g >= 2 ? sR[lane][0] : 0.f), s1 = sum16(g == 3 ? sR[lane][1] : 0.f);
+      const float t20 = __shfl(s0, 32, 64), t30 = __shfl(s0, 48, 64), t31 = __shfl(s1, 48, 64);
+      const float w = sI[lane] + from16(row) + before16(cs * dt) +
+                      (g == 1 ? t20 + t30 : (g == 2 ? t30 + t31 : 0.f));
+      const float ahead = dt * pe;
+      const float dal = k0 * exp2_f32(qa[0] + qa[1]) + w + from64(pi, lane) + (upto64(ahead, lane) - ahead);
+      const float sig = a.dt_softplus ? 1.f / (1.f + expf(-q[3])) : 1.f;
+      const float dd = lane < rows ? (cs + sDQ[lane] + pe + a.A[h] * dal) * sig : 0.f;
+      if (lane < rows) b.ddt_part[(long)hu * a.tokens + t0 + lane] = dd;
+      const float sa = sum64(lane < rows ? dal * dt : 0.f), sb = sum64(dd), sd = sum64(sDD[lane]);
+      if (lane == 0) hp[u] = f32x4{sa, sb, sd, 0.f};
+    }
+    __syncthreads();  // the unit's tiles are no longer read
   }
-  if (!live) return;
-  sum_a = wave_sum(sum_a);
-  sum_b = wave_sum(sum_b);
-  sum_d = wave_sum(sum_d);
-  if (lane == 0) {
-    hp[0] = sum_a;
-    hp[1] = sum_b;
-    hp[2] = sum_d;
-  }
-  if (sg.first && b.dinit) {
+
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+  for (int q = 0; q < NW; ++q) {
+    const int nt = wave * NW + q;
+    if (nt >= NT) break;
 #pragma unroll
-      for (int p = 0; p < 2; ++p)
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          b.dinit[sbase + row_at<N>(n, p, r, lane)] = has ? S[n][p][r] : 0.f;
+    for (int j = 0; j < 4; ++j) {
+      const int t = 16 * j + i16;
+      if (t < rows) {
+        const long o = (((long)hblk * a.tokens + t0 + t) * a.ngroups + grp) * N + 16 * nt + 4 * g;
+        *reinterpret_cast<f32x4*>(b.dB_part + o) = aB[q][j];
+        *reinterpret_cast<f32x4*>(b.dC_part + o) = aC[q][j];
+      }
+    }
   }
 }
 
@@ -730,7 +788,7 @@ __global__ void __launch_bounds__(256) scan_bwd_join_kernel(const ScanBwdArgs b,
     return;
   }
   id -= 2 * nbc;
-  const int slices = a.headdim / kPT;
+  const int units = b.upg * a.ngroups, slices = units / a.nheads;
   if (id < nd) {
     // 64 tokens of 16 heads: read along tokens, written along heads
     __shared__ float tile[64][17];
@@ -758,13 +816,15 @@ __global__ void __launch_bounds__(256) scan_bwd_join_kernel(const ScanBwdArgs b,
   const int h = id * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
   if (h >= a.nheads) return;
   double s[3] = {0.0, 0.0, 0.0};
-  for (long k = lane; k < b.slots * slices; k += 64) {
-    const double* p = b.head_part + ((k / slices) * a.vheads + (long)h * slices + k % slices) * 3;
+  for (long k = lane; k < b.cslots * slices; k += 64) {
+    const f32x4 p = reinterpret_cast<const f32x4*>(b.head_part)[(k / slices) * units + (long)h * slices + k % slices];
 #pragma unroll
-    for (int r = 0; r < 3; ++r) s[r] += p[r];
+    for (int r = 0; r < 3; ++r) s[r] += (double)p[r];
   }
 #pragma unroll
-  for (int r = 0; r < 3; ++r) s[r] = wave_sum(s[r]);
+  for (int r = 0; r < 3; ++r)
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) s[r] += __shfl_xor(s[r], o, 64);
   if (lane == 0) {
     b.dA[h] = (float)s[0];
     if (b.ddt_bias) b.ddt_bias[h] = (float)s[1];
@@ -772,62 +832,81 @@ __global__ void __launch_bounds__(256) scan_bwd_join_kernel(const ScanBwdArgs b,
   }
 }
 
-// Tokens of a backward segment.
+// Tokens of a segment of the recurrences: enough of them, over both directions,
+// to give every one of the 1024 SIMDs two waves, and no shorter than four chunks.
 static int bwd_seg(const rssm_scan_dims& d) {
   const long vheads = (long)d.nheads * (d.headdim / kPT);
-  const long want = (d.tokens * vheads + 2047) / 2048;
+  const long want = (d.tokens * vheads + 1023) / 1024;
   long seg = (want + kQ - 1) / kQ * kQ;
   if (seg < 4 * kQ) seg = 4 * kQ;
   if (seg > 64 * kQ) seg = 64 * kQ;
   return (int)seg;
 }
 
+// Units of a workgroup of the main launch: up to eight, which share the chunk's
+// C.B and join dB and dC without memory, but so few that there are two
+// workgroups for each of the 512 places.
+static int bwd_units(const rssm_scan_dims& d, int upg) {
+  const long blocks = ((long)d.tokens / kQ + d.seqs) * d.ngroups;
+  int n = 8;
+  while (n > 1 && blocks * ((upg + n - 1) / n) < 1024) n >>= 1;
+  return n;
+}
+
 // The workspace, in order; every part a multiple of 16 bytes.
 struct BwdLayout {
-  size_t chunk_state, seg_state, seg_grad, seg_decay, grad_decay, ddt, dB, dC, head, end;
+  size_t dec, chunk_state, grad_state, seg_state, seg_grad, seg_decay, grad_decay, ddt, dB, dC, head, end;
+  int upg, upb, hb;
 };
 static BwdLayout bwd_layout(const rssm_scan_dims& d) {
   const size_t T = d.tokens, n = d.seqs, seg = bwd_seg(d);
   const size_t V = (size_t)d.nheads * (d.headdim / kPT), hpn = (size_t)d.nheads * d.headdim * d.dstate;
   const size_t slots = T / seg + n, cslots = T / kQ + n;
-  const size_t waves = bwd_waves(d.io_dtype == RSSM_F32, d.dstate);
-  const size_t hb = (V / d.ngroups + waves - 1) / waves;
-  const bool many = T > seg;
-  const auto up = [](size_t b) { return (b + 15) / 16 * 16; };
   BwdLayout l;
+  l.upg = d.nheads / d.ngroups * (d.headdim / bwd_rows(d.io_dtype == RSSM_F32, d.headdim));
+  l.upb = bwd_units(d, l.upg);
+  l.hb = (l.upg + l.upb - 1) / l.upb;
+  const size_t units = (size_t)l.upg * d.ngroups;
+  const bool many = T > seg;
   size_t at = 0;
   const auto take = [&](size_t bytes) {
     const size_t p = at;
-    at += up(bytes);
+    at += (bytes + 15) / 16 * 16;
     return p;
   };
+  l.dec = take(cslots * d.nheads * kQ * 16);
   l.chunk_state = take(cslots * hpn * 4);
+  l.grad_state = take(cslots * hpn * 4);
   l.seg_state = take(many ? slots * hpn * 4 : 0);
   l.seg_grad = take(many ? slots * hpn * 4 : 0);
   l.seg_decay = take(many ? slots * V * 4 : 0);
   l.grad_decay = take(many ? slots * V * 4 : 0);
-  l.ddt = take(V * T * 4);
-  l.dB = take(hb * T * d.ngroups * d.dstate * 4);
-  l.dC = take(hb * T * d.ngroups * d.dstate * 4);
-  l.head = take(slots * V * 3 * 8);
+  l.ddt = take(units * T * 4);
+  l.dB = take(l.hb * T * d.ngroups * d.dstate * 4);
+  l.dC = take(l.hb * T * d.ngroups * d.dstate * 4);
+  l.head = take(cslots * units * 16);
   l.end = at;
   return l;
 }
 
-enum { kStates, kGrads, kMain };
+enum { kStates, kSegments, kMain };
+template <typename T, int N>
+static const void* pick_bwd_n(int which, int headdim) {
+  if (which == kStates) return reinterpret_cast<const void*>(&scan_states_kernel<T, N, true>);
+  if (which == kSegments) return reinterpret_cast<const void*>(&scan_states_kernel<T, N, false>);
+  if constexpr (sizeof(typename Mat<T>::E) == 2)
+    if (bwd_rows(false, headdim) == 64) return reinterpret_cast<const void*>(&scan_bwd_kernel<T, N, 64>);
+  return reinterpret_cast<const void*>(&scan_bwd_kernel<T, N, 32>);
+}
 template <typename T>
-static const void* pick_bwd(int which, int n) {
-#define RSSM_SCAN_BWD(N)                                                                    \
-  if (n == N)                                                                               \
-  return which == kStates  ? reinterpret_cast<const void*>(&scan_states_kernel<T, N, false>) \
-         : which == kGrads ? reinterpret_cast<const void*>(&scan_states_kernel<T, N, true>)  \
-                           : reinterpret_cast<const void*>(&scan_bwd_kernel<T, N>)
-  RSSM_SCAN_BWD(16);
-  RSSM_SCAN_BWD(32);
-  RSSM_SCAN_BWD(64);
-  RSSM_SCAN_BWD(128);
-  RSSM_SCAN_BWD(256);
-  return nullptr;
+static const void* pick_bwd(int which, const rssm_scan_dims& d) {
+  switch (d.dstate) {
+    case 16: return pick_bwd_n<T, 16>(which, d.headdim);
+    case 32: return pick_bwd_n<T, 32>(which, d.headdim);
+    case 64: return pick_bwd_n<T, 64>(which, d.headdim);
+    case 128: return pick_bwd_n<T, 128>(which, d.headdim);
+    default: return pick_bwd_n<T, 256>(which, d.headdim);
+  }
 }
 
 }  // namespace rssm
@@ -892,40 +971,52 @@ extern "C" int ssu_scan_backward(const rssm_scan_dims* dims, const void* dy, con
   b.dD = dD;
   b.ddt_bias = ddt_bias;
   b.dinit = dinitial_state;
+  b.dec = reinterpret_cast<f32x4*>(ws + l.dec);
   b.chunk_state = reinterpret_cast<float*>(ws + l.chunk_state);
+  b.grad_state = reinterpret_cast<float*>(ws + l.grad_state);
   b.seg_grad = reinterpret_cast<float*>(ws + l.seg_grad);
   b.grad_decay = reinterpret_cast<float*>(ws + l.grad_decay);
   b.ddt_part = reinterpret_cast<float*>(ws + l.ddt);
   b.dB_part = reinterpret_cast<float*>(ws + l.dB);
   b.dC_part = reinterpret_cast<float*>(ws + l.dC);
-  b.head_part = reinterpret_cast<double*>(ws + l.head);
+  b.head_part = reinterpret_cast<float*>(ws + l.head);
   b.dy_stride = d.dy_stride ? d.dy_stride : (long)d.nheads * d.headdim;
   b.slots = scan_slots(d.tokens, d.seqs, a.seg);
+  b.cslots = scan_slots(d.tokens, d.seqs, kQ);
+  b.upg = l.upg;
+  b.upb = l.upb;
+  b.hb = l.hb;
   const bool f32 = d.io_dtype == RSSM_F32;
-  const int waves = bwd_waves(f32, d.dstate);
-  b.hb = (a.vpg + waves - 1) / waves;
   const long sgrid = b.slots * d.ngroups * ((a.vpg + 3) / 4);
-  const long mgrid = b.slots * d.ngroups * b.hb;
+  const long mgrid = b.cslots * d.ngroups * b.hb;
+  const long dgrid = b.cslots * ((d.nheads + 3) / 4);
   const long cgrid = ((long)kPT * d.dstate / 4 + 255) / 256 * a.vheads * d.seqs;
   const long nbc = ((long)d.tokens * d.ngroups * d.dstate / 8 + 255) / 256;
   const long nd = ((long)d.tokens + 63) / 64 * ((d.nheads + 15) / 16);
   const long jgrid = 2 * nbc + nd + (d.nheads + 3) / 4;
-  if (sgrid > 0x7fffffffL || mgrid > 0x7fffffffL || cgrid > 0x7fffffffL || jgrid > 0x7fffffffL)
+  const long most = 1L << 23;  // 2^32 threads of up to 512
+  if (2 * sgrid >= most || mgrid >= most || dgrid >= most || 2 * cgrid >= most || jgrid >= most)
     return RSSM_ESHAPE;
   const auto go = [&](int which, long grid, int threads) {
-    const void* fn = f32 ? pick_bwd<float>(which, d.dstate) : pick_bwd<bf16>(which, d.dstate);
+    const void* fn = f32 ? pick_bwd<float>(which, d) : pick_bwd<bf16>(which, d);
     return launch_kernel(fn, (unsigned)grid, threads, 0, stream, b);
   };
   if (d.seqs > 0) {
-    if (d.tokens > a.seg) {
-      rc = scan_segment_states(a, d, stream);
-      if (!rc) rc = go(kGrads, sgrid, 256);
+    if (d.tokens > 0)
+      rc = launch_kernel(f32 ? reinterpret_cast<const void*>(&scan_decay_kernel<float>)
+                             : reinterpret_cast<const void*>(&scan_decay_kernel<bf16>),
+                         (unsigned)dgrid, 256, 0, stream, b);
+    if (!rc && d.tokens > a.seg) {
+      b.dir_blocks = (int32_t)sgrid;
+      rc = go(kSegments, 2 * sgrid, 256);
+      b.dir_blocks = (int32_t)cgrid;
       if (!rc)
-        rc = launch_kernel(reinterpret_cast<const void*>(&scan_combine_grad_kernel),
-                           (unsigned)cgrid, 256, 0, stream, b);
+        rc = launch_kernel(reinterpret_cast<const void*>(&scan_combine_both_kernel),
+                           (unsigned)(2 * cgrid), 256, 0, stream, b);
     }
-    if (!rc && d.tokens > 0) rc = go(kStates, sgrid, 256);
-    if (!rc) rc = go(kMain, mgrid, 64 * waves);
+    b.dir_blocks = (int32_t)sgrid;
+    if (!rc) rc = go(kStates, 2 * sgrid, 256);
+    if (!rc) rc = go(kMain, mgrid, 64 * bwd_waves(f32, d.dstate));
     if (rc) return rc;
   }
   int inbc = (int)nbc, ind = (int)nd;

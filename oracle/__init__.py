@@ -31,6 +31,8 @@ Modules
 ``gdn_spec``  GDN speculative verify over drafts and commit with exact fold.
 ``kda``       gated delta rule with a per-key-channel gate (KDA): recurrence
               and ring replay.
+``sequence``  selective scan, causal convolution and RMS norm over packed
+              sequences, with their gradients.
 """
 
-from . import numerics, mamba2, gdn, metadata, gdn_spec, kda  # noqa: F401
+from . import numerics, mamba2, gdn, metadata, gdn_spec, kda, sequence  # noqa: F401
