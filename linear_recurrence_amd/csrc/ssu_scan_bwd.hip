@@ -342,7 +342,7 @@ __device__ static inline float sum64(float v) { return sum_g(sum16(v)); }
 // Waves of a workgroup of the main launch: one for every 32 state columns, four
 // at least (and four for fp32's 256 columns, whose tiles leave no room for more).  State rows of one unit of its work: a head's 64 (or 32), 32 in fp32,
 // whose tiles of 64 would not fit.
-constexpr int bwd_waves(bool f32, int n) { return n == 256 && !f32 ? 8 : 4; }
+constexpr int bwd_waves(bool f32, int n) { return n >= 128 && !f32 ? 8 : 4; }
 static inline int bwd_rows(bool f32, int headdim) { return f32 || headdim == 32 ? 32 : 64; }
 
 // One chunk, the units of one block.  A wave owns 32 state columns: it holds
