@@ -193,6 +193,25 @@ __device__ static inline void stage_tile(typename Mat<T>::E* tile, int ld, const
   }
 }
 
+// The value is unknown from here on: what is worked out from it (addresses,
+// conversions) is worked out again in each round of a loop, instead of being
+// kept in registers across all of them.
+__device__ static inline void forget(int& v) { asm volatile("" : "+v"(v)); }
+__device__ static inline void forget(u32x2& v) { asm volatile("" : "+v"(v)); }
+__device__ static inline void forget(f32x4& v) { asm volatile("" : "+v"(v)); }
+
+// Nothing is scheduled across this point: fully unrolled, the compiler would
+// start every tile's products at once and spill what they leave.
+__device__ static inline void keep_order() { __builtin_amdgcn_sched_barrier(0); }
+
+// A wave's own writes to LDS, before its other lanes read them (and its reads,
+// before they are written over).
+__device__ static inline void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // Inclusive sum over the wave's lanes (0 to 63) in double: decays are
 // differences of these sums, and a large step must not cost the small ones
 // their digits.
@@ -262,10 +281,13 @@ struct ScanArgs {
   void* y;
   float* seg_state;  // [slots][V][32][N]
   float* seg_decay;  // [slots][V], log2
+  f32x4* dec;        // [chunk slots][H][64]: sum of dt A (log2; high, low), dt, dt before softplus
+  void* chunk_state; // [chunk slots][V][32 N]: forward: operands in the io type; backward: S_in, fp32
   int32_t* status;
   long x_stride, dt_stride, B_stride, C_stride, z_stride;
   int32_t tokens, seqs, nheads, headdim, dstate, ngroups, num_slots, state_bf16, dt_softplus;
   int32_t seg, vheads, vpg;
+  int32_t hb, upb, upg;  // blocks of units in a group, units a block, units a group
 };
 
 __device__ static inline int scan_slot(const ScanArgs& a, int i) {
@@ -350,6 +372,33 @@ __device__ static inline ChunkDt chunk_dt(const ScanArgs& a, int h, float bias, 
   return c;
 }
 
+// dt and the running sums of dt*A of one chunk and head, a wave each.
+template <typename T>
+static __global__ void __launch_bounds__(256) scan_decay_kernel(const ScanArgs a) {
+  const int lane = threadIdx.x & 63, hq = (a.nheads + 3) / 4;
+  const long slot = blockIdx.x / hq;
+  const int h = (int)(blockIdx.x % hq) * 4 + (threadIdx.x >> 6);
+  const Segment sg = find_segment(a.cu, a.seqs, a.tokens, kQ, (int)slot);
+  if (sg.len == 0 || h >= a.nheads) return;
+  const double A2 = (double)a.A[h] * 1.4426950408889634074;
+  const ChunkDt q = chunk_dt<T>(a, h, a.dt_bias ? a.dt_bias[h] : 0.f, A2, sg.tok, sg.len, lane);
+  const float hi = (float)q.cum;
+  a.dec[(slot * a.nheads + h) * kQ + lane] = f32x4{hi, (float)(q.cum - (double)hi), q.dt, q.raw};
+}
+template <typename T>
+static inline int launch_decay(const ScanArgs& a, long cslots, hipStream_t stream) {
+  return launch_kernel(reinterpret_cast<const void*>(&scan_decay_kernel<T>),
+                       (unsigned)(cslots * ((a.nheads + 3) / 4)), 256, 0, stream, a);
+}
+
+__device__ static inline float gap2(f32x4 t, f32x4 s) { return (t[0] - s[0]) + (t[1] - s[1]); }
+__device__ static inline f32x4 lane_of(f32x4 v, int l) {
+  f32x4 o = v;
+  o[0] = __shfl(v[0], l, 64);
+  o[1] = __shfl(v[1], l, 64);
+  return o;
+}
+
 // acc[nt][pt] += (w * rows of X)^T (rows of Y): X the wave's [64][32] tile, Y
 // the shared [64][N] one, w one weight per token; ROWS: X's columns are the
 // result's rows, otherwise its columns.
@@ -383,8 +432,6 @@ __device__ static inline void rank_update(f32x4 (&acc)[NT][2], const typename Ma
     }
   }
 }
-
-int scan_segment_states(const ScanArgs& args, const rssm_scan_dims& d, hipStream_t stream);
 
 static inline long scan_slots(long tokens, long seqs, long seg) { return tokens / seg + seqs; }
 

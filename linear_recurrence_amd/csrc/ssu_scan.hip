@@ -1,12 +1,17 @@
 // Selective scan over packed sequences, forward (see scan_common.hpp for the
 // chunked form).
 //
-// A wave owns 32 rows of one head's state and keeps it in
-// registers as it walks the chunks of a segment; the four waves of a workgroup
-// share the group's B and C tiles in LDS.  Sequences longer than a segment take
-// two more launches in front: the segments' end states from zero (the state
-// part alone), then each sequence's running combination of them, which leaves
-// every segment the state it starts from.
+// Long calls: (1) dt and the decays' running sums of every chunk and head; (2)
+// the recurrence over the chunks, a wave for 32 rows of one head's state, which
+// leaves the state before every chunk in the workspace, as operands of the next
+// launch (with two launches in front where sequences are longer than a segment:
+// what each segment adds from zero, then their running combination); (3) the
+// outputs, a workgroup for one chunk and several heads.
+// Short calls (up to kShort tokens) are one launch, in which a wave walks a
+// sequence's chunks with the state in registers.
+//
+// The state enters y rounded to the io type: y is rounded to it too, and D x
+// usually outweighs it.
 #include "scan_common.hpp"
 
 namespace rssm {
@@ -15,12 +20,13 @@ namespace rssm {
 // fit four heads' x beside them in 160 KB.
 constexpr int scan_waves(bool f32, int n) { return f32 && n == 256 ? 2 : 4; }
 
-// OUT: y and the final states; otherwise the segments' end states from zero.
-// Two workgroups a compute unit: 256 registers a lane.
-template <typename T, int N, bool OUT>
+// A short call in one launch: y and the final states, a wave for 32 rows of one
+// head's state and one sequence.  Two workgroups a compute unit: 256 registers a
+// lane.
+template <typename T, int N>
 __global__ void __launch_bounds__(64 * scan_waves(sizeof(typename Mat<T>::E) == 4, N),
                                   sizeof(typename Mat<T>::E) == 4 ? 1 : 2)
-    scan_fwd_kernel(const ScanArgs a) {
+    scan_short_kernel(const ScanArgs a) {
   typedef Mat<T> M;
   typedef typename M::E E;
   typedef typename M::Frag Frag;
@@ -28,9 +34,9 @@ __global__ void __launch_bounds__(64 * scan_waves(sizeof(typename Mat<T>::E) == 
   constexpr int NP = N < 32 ? 32 : N, LN = NP + M::kPad, LX = kPT + M::kPad;
   constexpr int NT = N / 16, KB = NP / 32;
   __shared__ __attribute__((aligned(16))) E sB[kQ * LN];
-  __shared__ __attribute__((aligned(16))) E sC[OUT ? kQ * LN : 16];
+  __shared__ __attribute__((aligned(16))) E sC[kQ * LN];
   __shared__ __attribute__((aligned(16))) E sX[W][kQ * LX];
-  __shared__ f32x4 sCB[OUT ? 10 : 1][64];
+  __shared__ f32x4 sCB[10][64];
   __shared__ float2 sA[W][kQ];
   __shared__ __attribute__((aligned(16))) float sD[W][kQ];  // dt
   __shared__ __attribute__((aligned(16))) float sW[W][kQ];  // weight of x in the state
@@ -41,8 +47,7 @@ __global__ void __launch_bounds__(64 * scan_waves(sizeof(typename Mat<T>::E) == 
   const int slot = id / (a.ngroups * hb), rest = id % (a.ngroups * hb);
   const int grp = rest / hb, vl = (rest % hb) * W + wave;
   const Segment sg = find_segment(a.cu, a.seqs, a.tokens, a.seg, slot);
-  if (sg.len == 0 && !(OUT && sg.empty)) return;
-  if (!OUT && sg.last) return;  // nothing starts from its end
+  if (sg.len == 0 && !sg.empty) return;
   const bool live = vl < a.vpg;
   const int v = grp * a.vpg + (live ? vl : 0);
   const int slices = a.headdim / kPT, h = v / slices, p0 = (v % slices) * kPT;
@@ -53,40 +58,27 @@ __global__ void __launch_bounds__(64 * scan_waves(sizeof(typename Mat<T>::E) == 
   f32x4 S[NT][2];
 #pragma unroll
   for (int n = 0; n < NT; ++n) S[n][0] = S[n][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-  int pool = -1;
-  if constexpr (OUT) {
-    if (a.init || a.final_state) pool = scan_slot(a, sg.seq);
-    if (threadIdx.x == 0 && rest == 0 && sg.first && a.status) {
-      if (sg.bad) atomicOr(a.status, RSSM_ST_BAD_SEQ);
-      if ((a.init || a.final_state) && pool < 0) atomicOr(a.status, RSSM_ST_BAD_SLOT);
-    }
-    // The pool is read here only by a sequence of one segment, whose wave also
-    // writes it: a longer one's first segment takes the copy that the combining
-    // launch left, since its last segment may already have stored the final
-    // state over the initial one.
-    const bool whole = sg.first && sg.last;
-    const bool from_pool = whole && a.init && pool >= 0 && (!a.has_init || a.has_init[sg.seq]);
-    if (live && (from_pool || !whole)) {
-      const void* src = whole ? a.init : a.seg_state;
-      const int bf = whole ? a.state_bf16 : 0;
-      const long base = ((long)(whole ? pool : slot) * a.vheads + v) * (kPT * N);
+  const int pool = a.init || a.final_state ? scan_slot(a, sg.seq) : -1;
+  if (threadIdx.x == 0 && rest == 0 && a.status) {
+    if (sg.bad) atomicOr(a.status, RSSM_ST_BAD_SEQ);
+    if ((a.init || a.final_state) && pool < 0) atomicOr(a.status, RSSM_ST_BAD_SLOT);
+  }
+  if (live && a.init && pool >= 0 && (!a.has_init || a.has_init[sg.seq])) {
+    const long base = ((long)pool * a.vheads + v) * (kPT * N);
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int p = 0; p < 2; ++p)
-          S[n][p] = load_state4(src, base + tile_col(p, i16) * N + 16 * n + 4 * g, bf);
-    }
+      for (int p = 0; p < 2; ++p)
+        S[n][p] = load_state4(a.init, base + tile_col(p, i16) * N + 16 * n + 4 * g, a.state_bf16);
   }
 
-  double total = 0.0;
   for (int c0 = 0; c0 < sg.len; c0 += kQ) {
     const int rows = sg.len - c0 < kQ ? sg.len - c0 : kQ;
     const long t0 = sg.tok + c0;
     __syncthreads();  // the previous chunk's tiles are no longer read
     stage_tile<T, N, NP, TH>(sB, LN, static_cast<const E*>(a.B) + t0 * a.B_stride + (long)grp * N,
                              a.B_stride, rows, threadIdx.x);
-    if constexpr (OUT)
-      stage_tile<T, N, NP, TH>(sC, LN,
+    stage_tile<T, N, NP, TH>(sC, LN,
                                static_cast<const E*>(a.C) + t0 * a.C_stride + (long)grp * N,
                                a.C_stride, rows, threadIdx.x);
     stage_tile<T, kPT, kPT, 64>(sX[wave], LX,
@@ -94,7 +86,6 @@ __global__ void __launch_bounds__(64 * scan_waves(sizeof(typename Mat<T>::E) == 
                                     (long)h * a.headdim + p0,
                                 a.x_stride, live ? rows : 0, lane);
     const ChunkDt q = chunk_dt<T>(a, h, bias, A2, t0, rows, lane);
-    total += q.all;
     {
       const float hi = (float)q.cum;
       sA[wave][lane] = make_float2(hi, (float)(q.cum - (double)hi));
@@ -104,7 +95,7 @@ __global__ void __launch_bounds__(64 * scan_waves(sizeof(typename Mat<T>::E) == 
     const float decay = exp2_f32((float)q.all);
     __syncthreads();
 
-    if constexpr (OUT) {
+    {
       // C_t.B_s for the ten tiles on and above the diagonal (rows s, columns
       // t), shared by the workgroup's heads
       for (int k = wave; k < 10; k += W) {
@@ -119,8 +110,7 @@ __global__ void __launch_bounds__(64 * scan_waves(sizeof(typename Mat<T>::E) == 
       f32x4 Y[4][2];  // y^T: rows tile_col(p, 4g + r), column t = 16 j + i16
 #pragma unroll
       for (int j = 0; j < 4; ++j) Y[j][0] = Y[j][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-      // e^{a_t} S C_t.  The state enters y rounded to the io type: y is
-      // rounded to it too, and D x usually outweighs it
+      // e^{a_t} S C_t
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb) {
         Frag sf[2];
@@ -214,25 +204,326 @@ __global__ void __launch_bounds__(64 * scan_waves(sizeof(typename Mat<T>::E) == 
     rank_update<T, NT, LX, LN, false>(S, sX[wave], sB, sW[wave], rows, lane);
   }
 
-  if (!live) return;
-  if constexpr (OUT) {
-    if (sg.last && a.final_state && pool >= 0) {
-      const long base = ((long)pool * a.vheads + v) * (kPT * N);
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int p = 0; p < 2; ++p)
-          store_state4(a.final_state, base + tile_col(p, i16) * N + 16 * n + 4 * g, a.state_bf16,
-                       S[n][p]);
-    }
-  } else {
-    const long base = ((long)slot * a.vheads + v) * (kPT * N);
+  if (live && a.final_state && pool >= 0) {
+    const long base = ((long)pool * a.vheads + v) * (kPT * N);
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int p = 0; p < 2; ++p)
-        store_state4(a.seg_state, base + tile_col(p, i16) * N + 16 * n + 4 * g, 0, S[n][p]);
-    if (lane == 0) a.seg_decay[(long)slot * a.vheads + v] = (float)total;
+        store_state4(a.final_state, base + tile_col(p, i16) * N + 16 * n + 4 * g, a.state_bf16,
+                     S[n][p]);
+  }
+}
+
+// The recurrence over the chunks of a segment.  STORE: from the state it starts
+// from, leaving the state before every chunk as operands (rows p, k = n in order
+// D) and the final one in its pool; otherwise from zero, leaving what the
+// segment adds.  The next chunk's tiles are on their way while one is worked on.
+template <typename T, int N, bool STORE>
+__global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 1 : (N == 256 ? 2 : 3))
+    scan_fwd_states_kernel(const ScanArgs a) {
+  typedef Mat<T> M;
+  typedef typename M::E E;
+  typedef typename M::Frag Frag;
+  constexpr int W = 4, TH = 64 * W, V = 16 / sizeof(E);
+  constexpr int NP = N < 32 ? 32 : N, LN = NP + M::kPad, LX = kPT + M::kPad, NT = N / 16, KB = NP / 32;
+  constexpr int PN = N / V, QN = (kQ * PN + TH - 1) / TH;  // 16-byte pieces of a row, a thread's
+  constexpr int PX = kPT / V, QX = kQ * PX / 64;
+  __shared__ __attribute__((aligned(16))) E sB[kQ * LN];
+  __shared__ __attribute__((aligned(16))) E sX[W][kQ * LX];
+  __shared__ __attribute__((aligned(16))) float sW[W][kQ];
+  int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int hb = (a.vpg + W - 1) / W;
+  const int id = xcd_tile(blockIdx.x, gridDim.x);
+  const int slot = id / (a.ngroups * hb), rest = id % (a.ngroups * hb);
+  const int grp = rest / hb, vl = (rest % hb) * W + wave;
+  const Segment sg = find_segment(a.cu, a.seqs, a.tokens, a.seg, slot);
+  if (STORE ? sg.len == 0 && !sg.empty : sg.len == 0 || sg.last) return;
+  const bool live = vl < a.vpg;
+  const int v = grp * a.vpg + (live ? vl : 0);
+  const int slices = a.headdim / kPT, h = v / slices, p0 = (v % slices) * kPT;
+  const int pool = a.init || a.final_state ? scan_slot(a, sg.seq) : -1;
+  if (STORE && threadIdx.x == 0 && rest == 0 && sg.first && a.status) {
+    if (sg.bad) atomicOr(a.status, RSSM_ST_BAD_SEQ);
+    if ((a.init || a.final_state) && pool < 0) atomicOr(a.status, RSSM_ST_BAD_SLOT);
+  }
+  // S^T: rows n = 16 nt + 4g + r, columns tile_col(p, l%16)
+  f32x4 S[NT][2];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) S[n][0] = S[n][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const auto place = [&](int n, int p) { return tile_col(p, lane & 15) * N + 16 * n + 4 * (lane >> 4); };
+  // The pool is read here only by a sequence of one segment, whose wave also
+  // writes it: a longer one's first segment takes the copy that the combining
+  // launch left, since its last segment may already have stored the final
+  // state over the initial one.
+  const bool whole = sg.first && sg.last;
+  const bool from_pool = whole && a.init && pool >= 0 && (!a.has_init || a.has_init[sg.seq]);
+  if (STORE && live && (from_pool || !whole)) {
+    const void* src = whole ? a.init : a.seg_state;
+    const long base = ((long)(whole ? pool : slot) * a.vheads + v) * (kPT * N);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int p = 0; p < 2; ++p) S[n][p] = load_state4(src, base + place(n, p), whole ? a.state_bf16 : 0);
+  }
+  const E* const nsrc = static_cast<const E*>(a.B) + (long)grp * N;
+  const E* const psrc = static_cast<const E*>(a.x) + (long)h * a.headdim + p0;
+  const long cbase = seg_base(a.cu, sg.seq, kQ, a.tokens) + (long)sg.k * (a.seg / kQ);
+  const int chunks = (sg.len + kQ - 1) / kQ;
+  u32x4 rn[QN], rx[QX];
+  f32x4 rq;
+  const auto fetch = [&](int c) {
+    const int rows = sg.len - c * kQ < kQ ? sg.len - c * kQ : kQ;
+    const long t0 = sg.tok + (long)c * kQ;
+#pragma unroll
+    for (int q = 0; q < QN; ++q) {
+      const int e = q * TH + tid, r = e / PN;
+      rn[q] = u32x4{0, 0, 0, 0};
+      if (r < rows) rn[q] = *reinterpret_cast<const u32x4*>(nsrc + (t0 + r) * a.B_stride + (e % PN) * V);
+    }
+#pragma unroll
+    for (int q = 0; q < QX; ++q) {
+      const int e = q * 64 + lane, r = e / PX;
+      rx[q] = u32x4{0, 0, 0, 0};
+      if (live && r < rows) rx[q] = *reinterpret_cast<const u32x4*>(psrc + (t0 + r) * a.x_stride + (e % PX) * V);
+    }
+    rq = a.dec[((cbase + c) * a.nheads + h) * kQ + lane];
+  };
+  float total = 0.f;
+  if (chunks) fetch(0);
+  for (int c = 0; c < chunks; ++c) {
+    tid = threadIdx.x;
+    forget(tid);
+    lane = tid & 63;
+    const int rows = sg.len - c * kQ < kQ ? sg.len - c * kQ : kQ;
+    if (STORE && live) {
+      Frag* dst = static_cast<Frag*>(a.chunk_state) + ((cbase + c) * a.vheads + v) * (KB * 2 * 64) + lane;
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          float f[8];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            f[r] = S[2 * kb][p][r];
+            f[4 + r] = 2 * kb + 1 < NT ? S[2 * kb + 1 < NT ? 2 * kb + 1 : 0][p][r] : 0.f;
+          }
+          dst[(kb * 2 + p) * 64] = M::pack(f);
+        }
+    }
+    if (STORE && c + 1 == chunks && !(sg.last && a.final_state)) break;  // the end is not read
+    __syncthreads();  // the previous chunk's tiles are no longer read
+#pragma unroll
+    for (int q = 0; q < QN; ++q) {
+      const int e = q * TH + tid, r = e / PN;
+      if (r < kQ) *reinterpret_cast<u32x4*>(sB + r * LN + (e % PN) * V) = rn[q];
+    }
+#pragma unroll
+    for (int q = 0; q < QX; ++q) {
+      const int e = q * 64 + lane;
+      *reinterpret_cast<u32x4*>(&sX[wave][(e / PX) * LX + (e % PX) * V]) = rx[q];
+    }
+    const f32x4 all = lane_of(rq, 63);
+    const float decay = exp2_f32(all[0] + all[1]);
+    total += all[0];
+    sW[wave][lane] = rq[2] * exp2_f32(gap2(all, rq));
+    if (c + 1 < chunks) fetch(c + 1);
+    __syncthreads();
+    if (!live) continue;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) S[n][p][r] *= decay;
+    rank_update<T, NT, LX, LN, false>(S, sX[wave], sB, sW[wave], rows, lane);
+  }
+  if (!live) return;
+  if (!STORE) {
+    const long base = ((long)slot * a.vheads + v) * (kPT * N);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int p = 0; p < 2; ++p) store_state4(a.seg_state, base + place(n, p), 0, S[n][p]);
+    if (lane == 0) a.seg_decay[(long)slot * a.vheads + v] = total;
+  } else if (sg.last && a.final_state && pool >= 0) {
+    const long base = ((long)pool * a.vheads + v) * (kPT * N);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+        store_state4(a.final_state, base + place(n, p), a.state_bf16, S[n][p]);
+  }
+}
+
+// The outputs of one chunk.  C and the tiles of C.B, the same for all heads of
+// the group, are in LDS; each wave then works alone, a unit (PB state rows of one
+// head) at a time, without a barrier: the waves are at different points, and one's
+// loads pass behind the others' products.
+template <typename T, int N, int PB>
+__global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 1 : 2)
+    scan_fwd_out_kernel(const ScanArgs a) {
+  typedef Mat<T> M;
+  typedef typename M::E E;
+  typedef typename M::Frag Frag;
+  constexpr int W = 4, TH = 64 * W, V = 16 / sizeof(E);
+  constexpr int NP = N < 32 ? 32 : N, LN = NP + M::kPad, LX = PB + M::kPad, KB = NP / 32, SL = PB / 32;
+  constexpr int PX = PB / V, QX = kQ * PX / 64;
+  constexpr int kX = W * kQ * LX > kQ * LN ? W * kQ * LX : kQ * LN;
+  __shared__ __attribute__((aligned(16))) E sC[kQ * LN];
+  __shared__ __attribute__((aligned(16))) E sXB[kX];  // B at first, then each wave's x
+  __shared__ f32x4 sCB[10][64];
+  __shared__ f32x4 sQ[W][kQ];
+  int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int id = xcd_tile(blockIdx.x, gridDim.x);
+  const int slot = id / (a.ngroups * a.hb), rest = id % (a.ngroups * a.hb);
+  const int grp = rest / a.hb, u0 = (rest % a.hb) * a.upb;
+  const int u1 = u0 + a.upb < a.upg ? u0 + a.upb : a.upg, per = a.headdim / PB;
+  const Segment sg = find_segment(a.cu, a.seqs, a.tokens, kQ, slot);
+  if (sg.len == 0) return;
+  const int rows = sg.len;
+  const long t0 = sg.tok;
+  {
+    const int i16 = lane & 15, g = lane >> 4;
+    stage_tile<T, N, NP, TH>(sXB, LN, static_cast<const E*>(a.B) + t0 * a.B_stride + (long)grp * N,
+                             a.B_stride, rows, threadIdx.x);
+    stage_tile<T, N, NP, TH>(sC, LN, static_cast<const E*>(a.C) + t0 * a.C_stride + (long)grp * N,
+                             a.C_stride, rows, threadIdx.x);
+    __syncthreads();
+    // C_t.B_s for the ten tiles on and above the diagonal (rows s, columns t)
+    for (int k = wave; k < 10; k += W) {
+      const int j = k < 1 ? 0 : (k < 3 ? 1 : (k < 6 ? 2 : 3)), i = k - j * (j + 1) / 2;
+      f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb)
+        acc = M::mma(M::rows_c(sXB + (16 * i + i16) * LN + 32 * kb + 8 * g),
+                     M::rows_c(sC + (16 * j + i16) * LN + 32 * kb + 8 * g), acc);
+      sCB[k][lane] = acc;
+    }
+    __syncthreads();
+  }
+  E* const sX = sXB + wave * kQ * LX;
+#pragma unroll 1
+  for (int u = u0 + wave; u < u1; u += W) {
+    const int hu = grp * a.upg + u, h = hu / per, p0 = (hu % per) * PB;
+    lane = threadIdx.x & 63;
+    forget(lane);
+    const int i16 = lane & 15, g = lane >> 4;
+    u32x4 rx[QX];
+#pragma unroll
+    for (int q = 0; q < QX; ++q) {
+      const int e = q * 64 + lane, r = e / PX;
+      rx[q] = u32x4{0, 0, 0, 0};
+      if (r < rows)
+        rx[q] = *reinterpret_cast<const u32x4*>(static_cast<const E*>(a.x) + (t0 + r) * a.x_stride +
+                                                (long)h * a.headdim + p0 + (e % PX) * V);
+    }
+    sQ[wave][lane] = a.dec[((long)slot * a.nheads + h) * kQ + lane];
+    // e^{a_t} S C_t: y^T, rows tile_col(p, 4g + r) of a slice, column t = 16 j + i16
+    f32x4 Y[4][SL][2];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int s = 0; s < SL; ++s) Y[j][s][0] = Y[j][s][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const Frag* const st = static_cast<const Frag*>(a.chunk_state) +
+        ((long)slot * a.vheads + (long)hu * SL) * (KB * 2 * 64) + lane;
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+      Frag sf[SL][2];
+#pragma unroll
+      for (int s = 0; s < SL; ++s)
+#pragma unroll
+        for (int p = 0; p < 2; ++p) sf[s][p] = st[((s * KB + kb) * 2 + p) * 64];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const Frag c = M::rows_d(sC + (16 * j + i16) * LN + 32 * kb + 4 * g);
+#pragma unroll
+        for (int s = 0; s < SL; ++s)
+#pragma unroll
+          for (int p = 0; p < 2; ++p) Y[j][s][p] = M::mma(sf[s][p], c, Y[j][s][p]);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < QX; ++q) {
+      const int e = q * 64 + lane;
+      *reinterpret_cast<u32x4*>(sX + (e / PX) * LX + (e % PX) * V) = rx[q];
+    }
+    wave_sync();
+    f32x4 at[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      at[j] = sQ[wave][16 * j + i16];
+      const float et = exp2_f32(at[j][0] + at[j][1]);
+#pragma unroll
+      for (int s = 0; s < SL; ++s)
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) Y[j][s][p][r] *= et;
+    }
+    // the chunk's own tokens
+#pragma unroll
+    for (int sb = 0; sb < 2; ++sb) {
+      Frag xf[SL][2];
+#pragma unroll
+      for (int s = 0; s < SL; ++s)
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+          xf[s][p] = M::cols(cols_at<T, true>(sX, LX, 32 * sb, 32 * s + pair_base(p), lane), LX);
+#pragma unroll
+      for (int j = 2 * sb; j < 4; ++j) {
+        float w[8];
+#pragma unroll
+        for (int q2 = 0; q2 < 2; ++q2) {
+          const int i = 2 * sb + q2;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) w[4 * q2 + r] = 0.f;
+          if (i > j) continue;
+          const f32x4 cb = sCB[j * (j + 1) / 2 + i][lane];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const f32x4 qs = sQ[wave][16 * i + 4 * g + r];
+            const float m = cb[r] * qs[2] * exp2_f32(gap2(at[j], qs));
+            w[4 * q2 + r] = i < j || 4 * g + r <= i16 ? m : 0.f;
+          }
+        }
+        const Frag wf = M::pack(w);
+#pragma unroll
+        for (int s = 0; s < SL; ++s)
+#pragma unroll
+          for (int p = 0; p < 2; ++p) Y[j][s][p] = M::mma(xf[s][p], wf, Y[j][s][p]);
+        keep_order();
+      }
+    }
+    // D x, the gate, and 8 neighbours of token t to memory
+    const float Dh = a.D ? a.D[h] : 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int t = 16 * j + i16;
+      if (t < rows) {
+#pragma unroll
+        for (int s = 0; s < SL; ++s) {
+          float o[8], xv[8];
+          M::unpack(M::rows_c(sX + t * LX + 32 * s + 8 * g), xv);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            o[r] = fmaf(Dh, xv[r], Y[j][s][0][r]);
+            o[4 + r] = fmaf(Dh, xv[4 + r], Y[j][s][1][r]);
+          }
+          const long col = (long)h * a.headdim + p0 + 32 * s + 8 * g;
+          if (a.z) {
+            float zv[8];
+            Vec8<T>::load(a.z, (t0 + t) * a.z_stride + col, zv);
+#pragma unroll
+            for (int r = 0; r < 8; ++r) o[r] *= zv[r] * sigmoid_f32(zv[r]);
+          }
+          Vec8<T>::store(a.y, (t0 + t) * (long)a.nheads * a.headdim + col, o);
+        }
+      }
+    }
+    wave_sync();  // the next unit's x comes over this one's
   }
 }
 
@@ -269,6 +560,9 @@ __global__ void __launch_bounds__(256) scan_combine_kernel(const ScanArgs a) {
   }
 }
 
+// Calls of up to this many tokens take one launch.
+constexpr int kShort = 256;
+
 // Tokens of a segment: enough segments to give every one of the 1024 SIMDs two
 // waves, but no shorter than four chunks (a segment's state crosses memory
 // four times, 16 bytes an element, beside 64 tokens' x and y of 256).
@@ -281,38 +575,50 @@ static int scan_seg(const rssm_scan_dims& d) {
   return (int)seg;
 }
 
-static size_t scan_states(const rssm_scan_dims& d) {
-  return (size_t)scan_slots(d.tokens, d.seqs, scan_seg(d)) * d.nheads * d.headdim * d.dstate;
-}
-static size_t scan_decays(const rssm_scan_dims& d) {
-  return (size_t)scan_slots(d.tokens, d.seqs, scan_seg(d)) * d.nheads * (d.headdim / kPT);
+// The workspace, in order; every part a multiple of 16 bytes.
+struct FwdLayout {
+  size_t dec, chunk_state, seg_state, seg_decay, end;
+};
+static FwdLayout fwd_layout(const rssm_scan_dims& d) {
+  FwdLayout l{};
+  if (d.tokens <= kShort) return l;
+  const size_t T = d.tokens, n = d.seqs, seg = scan_seg(d), cslots = T / kQ + n, slots = T / seg + n;
+  const size_t V = (size_t)d.nheads * (d.headdim / kPT), np = d.dstate < 32 ? 32 : d.dstate;
+  size_t at = 0;
+  const auto take = [&](size_t bytes) {
+    const size_t p = at;
+    at += (bytes + 15) / 16 * 16;
+    return p;
+  };
+  l.dec = take(cslots * d.nheads * kQ * 16);
+  l.chunk_state = take(cslots * V * kPT * np * (d.io_dtype == RSSM_F32 ? 4 : 2));
+  l.seg_state = take(T > seg ? slots * V * kPT * d.dstate * 4 : 0);
+  l.seg_decay = take(T > seg ? slots * V * 4 : 0);
+  l.end = at;
+  return l;
 }
 
-template <typename T, bool OUT>
-static const void* pick_fwd(int n) {
-#define RSSM_SCAN_FWD(N) if (n == N) return reinterpret_cast<const void*>(&scan_fwd_kernel<T, N, OUT>)
-  RSSM_SCAN_FWD(16);
-  RSSM_SCAN_FWD(32);
-  RSSM_SCAN_FWD(64);
-  RSSM_SCAN_FWD(128);
-  RSSM_SCAN_FWD(256);
-  return nullptr;
+enum { kFwdShort, kFwdSegments, kFwdStates, kFwdOut };
+template <typename T, int N>
+static const void* pick_fwd_n(int which, int headdim) {
+  switch (which) {
+    case kFwdShort: return reinterpret_cast<const void*>(&scan_short_kernel<T, N>);
+    case kFwdSegments: return reinterpret_cast<const void*>(&scan_fwd_states_kernel<T, N, false>);
+    case kFwdStates: return reinterpret_cast<const void*>(&scan_fwd_states_kernel<T, N, true>);
+    default:
+      return headdim == 32 ? reinterpret_cast<const void*>(&scan_fwd_out_kernel<T, N, 32>)
+                           : reinterpret_cast<const void*>(&scan_fwd_out_kernel<T, N, 64>);
+  }
 }
-
-// The segments' end states from zero, then each segment's starting state (the
-// backward pass recomputes the states from them).
-int scan_segment_states(const ScanArgs& a, const rssm_scan_dims& d, hipStream_t stream) {
-  const int waves = scan_waves(d.io_dtype == RSSM_F32, d.dstate);
-  const long hb = (a.vpg + waves - 1) / waves;
-  const long grid = scan_slots(d.tokens, d.seqs, a.seg) * d.ngroups * hb;
-  const long cgrid = ((long)kPT * d.dstate / 4 + 255) / 256 * a.vheads * d.seqs;
-  if (grid > 0x7fffffffL || cgrid > 0x7fffffffL) return RSSM_ESHAPE;
-  const void* fn = d.io_dtype == RSSM_F32 ? pick_fwd<float, false>(d.dstate)
-                                          : pick_fwd<bf16, false>(d.dstate);
-  const int rc = launch_kernel(fn, (unsigned)grid, 64 * waves, 0, stream, a);
-  if (rc) return rc;
-  return launch_kernel(reinterpret_cast<const void*>(&scan_combine_kernel), (unsigned)cgrid, 256,
-                       0, stream, a);
+template <typename T>
+static const void* pick_fwd(int which, const rssm_scan_dims& d) {
+  switch (d.dstate) {
+    case 16: return pick_fwd_n<T, 16>(which, d.headdim);
+    case 32: return pick_fwd_n<T, 32>(which, d.headdim);
+    case 64: return pick_fwd_n<T, 64>(which, d.headdim);
+    case 128: return pick_fwd_n<T, 128>(which, d.headdim);
+    default: return pick_fwd_n<T, 256>(which, d.headdim);
+  }
 }
 
 }  // namespace rssm
@@ -320,8 +626,7 @@ int scan_segment_states(const ScanArgs& a, const rssm_scan_dims& d, hipStream_t 
 using namespace rssm;
 
 extern "C" size_t ssu_scan_forward_workspace(const rssm_scan_dims* dims) {
-  if (scan_check(dims) || dims->tokens <= scan_seg(*dims)) return 0;
-  return sizeof(float) * (scan_states(*dims) + scan_decays(*dims));
+  return scan_check(dims) ? 0 : fwd_layout(*dims).end;
 }
 
 extern "C" int ssu_scan_forward(const rssm_scan_dims* dims, const void* x, const void* dt,
@@ -357,22 +662,49 @@ extern "C" int ssu_scan_forward(const rssm_scan_dims* dims, const void* x, const
   a.slot_idx = slot_idx;
   a.final_state = final_state;
   a.y = y;
-  a.seg_state = static_cast<float*>(workspace);
-  a.seg_decay = need ? a.seg_state + scan_states(d) : nullptr;
   a.status = status;
   fill_dims(a, d);
-  a.seg = scan_seg(d);
   a.vheads = d.nheads * (d.headdim / kPT);
   a.vpg = a.vheads / d.ngroups;
-  const int waves = scan_waves(d.io_dtype == RSSM_F32, d.dstate);
-  const long hb = (a.vpg + waves - 1) / waves;
-  const long grid = scan_slots(d.tokens, d.seqs, a.seg) * d.ngroups * hb;
-  if (grid > 0x7fffffffL) return RSSM_ESHAPE;
   const bool f32 = d.io_dtype == RSSM_F32;
-  if (need) {
-    rc = scan_segment_states(a, d, stream);
-    if (rc) return rc;
+  const long most = 1L << 24;  // 2^32 threads of 256
+  const auto go = [&](int which, long grid, int threads) {
+    const void* fn = f32 ? pick_fwd<float>(which, d) : pick_fwd<bf16>(which, d);
+    return launch_kernel(fn, (unsigned)grid, threads, 0, stream, a);
+  };
+  if (d.tokens <= kShort) {
+    a.seg = kShort + kQ;  // every sequence is one segment
+    const int waves = scan_waves(f32, d.dstate);
+    const long grid = (long)d.seqs * d.ngroups * ((a.vpg + waves - 1) / waves);
+    return grid < most ? go(kFwdShort, grid, 64 * waves) : RSSM_ESHAPE;
   }
-  const void* fn = f32 ? pick_fwd<float, true>(d.dstate) : pick_fwd<bf16, true>(d.dstate);
-  return launch_kernel(fn, (unsigned)grid, 64 * waves, 0, stream, a);
+  const FwdLayout l = fwd_layout(d);
+  char* const ws = static_cast<char*>(workspace);
+  a.dec = reinterpret_cast<f32x4*>(ws + l.dec);
+  a.chunk_state = ws + l.chunk_state;
+  a.seg_state = reinterpret_cast<float*>(ws + l.seg_state);
+  a.seg_decay = reinterpret_cast<float*>(ws + l.seg_decay);
+  a.seg = scan_seg(d);
+  const long cslots = scan_slots(d.tokens, d.seqs, kQ);
+  // Units of a workgroup of the output launch: up to four a wave, which share
+  // the chunk's C.B, but so few that there are two workgroups for each of the
+  // 512 places.
+  a.upg = d.nheads / d.ngroups * (d.headdim == 32 ? 1 : d.headdim / 64);
+  a.upb = 16;
+  while (a.upb > 4 && cslots * d.ngroups * ((a.upg + a.upb - 1) / a.upb) < 1024) a.upb >>= 1;
+  a.hb = (a.upg + a.upb - 1) / a.upb;
+  const long dgrid = cslots * ((d.nheads + 3) / 4);
+  const long sgrid = scan_slots(d.tokens, d.seqs, a.seg) * d.ngroups * ((a.vpg + 3) / 4);
+  const long cgrid = ((long)kPT * d.dstate / 4 + 255) / 256 * a.vheads * d.seqs;
+  const long ogrid = cslots * d.ngroups * a.hb;
+  if (dgrid >= most || sgrid >= most || cgrid >= most || ogrid >= most) return RSSM_ESHAPE;
+  rc = f32 ? launch_decay<float>(a, cslots, stream) : launch_decay<bf16>(a, cslots, stream);
+  if (!rc && d.tokens > a.seg) {
+    rc = go(kFwdSegments, sgrid, 256);
+    if (!rc)
+      rc = launch_kernel(reinterpret_cast<const void*>(&scan_combine_kernel), (unsigned)cgrid, 256,
+                         0, stream, a);
+  }
+  if (!rc) rc = go(kFwdStates, sgrid, 256);
+  return rc ? rc : go(kFwdOut, ogrid, 256);
 }

@@ -46,9 +46,7 @@ struct ScanBwdArgs {
   float* dD;
   float* ddt_bias;
   float* dinit;
-  f32x4* dec;          // [chunk slots][H][64]: sum of dt A (log2; high, low), dt, dt before softplus
-  float* chunk_state;  // [chunk slots][V][tiles][64][4]: S_in
-  float* grad_state;   // the same: dS
+  float* grad_state;   // [chunk slots][V][tiles][64][4]: dS, as chunk_state holds S_in
   float* seg_grad;     // [slots][V][32][N]
   float* grad_decay;   // [slots][V], log2
   float* ddt_part;     // [units][T]
@@ -56,7 +54,7 @@ struct ScanBwdArgs {
   float* dC_part;
   float* head_part;    // [chunk slots][units][4]: dA, ddt_bias, dD
   long dy_stride, slots, cslots;
-  int32_t hb, upb, upg, dir_blocks;  // blocks of units in a group, units a block, units a group
+  int32_t dir_blocks;
 };
 
 // The state tile pair of column tile nt, rows tile_col(pt, 4g + r), column
@@ -66,37 +64,14 @@ __device__ static inline long row_at(int nt, int pt, int r, int lane) {
   return (long)(pair_base(pt) + 8 * (lane >> 4) + r) * N + 16 * nt + (lane & 15);
 }
 
-// dt and the running sums of dt*A of one chunk and head, a wave each.
-template <typename T>
-__global__ void __launch_bounds__(256) scan_decay_kernel(const ScanBwdArgs b) {
-  const ScanArgs& a = b.f;
-  const int lane = threadIdx.x & 63, hq = (a.nheads + 3) / 4;
-  const long slot = blockIdx.x / hq;
-  const int h = (int)(blockIdx.x % hq) * 4 + (threadIdx.x >> 6);
-  const Segment sg = find_segment(a.cu, a.seqs, a.tokens, kQ, (int)slot);
-  if (sg.len == 0 || h >= a.nheads) return;
-  const double A2 = (double)a.A[h] * 1.4426950408889634074;
-  const ChunkDt q = chunk_dt<T>(a, h, a.dt_bias ? a.dt_bias[h] : 0.f, A2, sg.tok, sg.len, lane);
-  const float hi = (float)q.cum;
-  b.dec[(slot * a.nheads + h) * kQ + lane] = f32x4{hi, (float)(q.cum - (double)hi), q.dt, q.raw};
-}
-
-__device__ static inline float gap2(f32x4 t, f32x4 s) { return (t[0] - s[0]) + (t[1] - s[1]); }
-__device__ static inline f32x4 lane_of(f32x4 v, int l) {
-  f32x4 o = v;
-  o[0] = __shfl(v[0], l, 64);
-  o[1] = __shfl(v[1], l, 64);
-  return o;
-}
-
 // One of the two recurrences over the chunks of a segment, a wave for 32 rows of
 // one head's state.  Blocks below dir_blocks: S forward; the others: dS
 // backward.  STORE: from the segment's starting value, leaving every chunk's in
 // the workspace (and the gradient of the initial state); otherwise from zero,
 // leaving what the segment adds.  The next chunk's tiles are on their way while
-// one is worked on; two workgroups a compute unit.
+// one is worked on; three workgroups a compute unit (two with 256 columns).
 template <typename T, int N, bool STORE>
-__global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 1 : 2)
+__global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 1 : (N == 256 ? 2 : 3))
     scan_states_kernel(const ScanBwdArgs b) {
   typedef Mat<T> M;
   typedef typename M::E E;
@@ -108,7 +83,8 @@ __global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 1 : 2)
   __shared__ __attribute__((aligned(16))) E sX[W][kQ * LX];
   __shared__ __attribute__((aligned(16))) float sW[W][kQ];
   const ScanArgs& a = b.f;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int hb = (a.vpg + W - 1) / W;
   const bool grad = (int)blockIdx.x >= b.dir_blocks;
   const int id = xcd_tile(grad ? blockIdx.x - b.dir_blocks : blockIdx.x, b.dir_blocks);
@@ -152,7 +128,7 @@ __global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 1 : 2)
   const E* const nsrc = static_cast<const E*>(grad ? a.C : a.B) + (long)grp * N;
   const E* const psrc = static_cast<const E*>(grad ? b.dy : a.x) + (long)h * a.headdim + p0;
   const long nstride = grad ? a.C_stride : a.B_stride, pstride = grad ? b.dy_stride : a.x_stride;
-  float* const out = grad ? b.grad_state : b.chunk_state;
+  float* const out = grad ? b.grad_state : static_cast<float*>(a.chunk_state);
   const long cbase = seg_base(a.cu, sg.seq, kQ, a.tokens) + (long)sg.k * (a.seg / kQ);
   const int chunks = (sg.len + kQ - 1) / kQ;
   u32x4 rn[QN], rx[QX];
@@ -162,7 +138,7 @@ __global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 1 : 2)
     const long t0 = sg.tok + (long)c * kQ;
 #pragma unroll
     for (int q = 0; q < QN; ++q) {
-      const int e = q * TH + (int)threadIdx.x, r = e / PN;
+      const int e = q * TH + tid, r = e / PN;
       rn[q] = u32x4{0, 0, 0, 0};
       if (r < rows) rn[q] = *reinterpret_cast<const u32x4*>(nsrc + (t0 + r) * nstride + (e % PN) * V);
     }
@@ -172,12 +148,15 @@ __global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 1 : 2)
       rx[q] = u32x4{0, 0, 0, 0};
       if (live && r < rows) rx[q] = *reinterpret_cast<const u32x4*>(psrc + (t0 + r) * pstride + (e % PX) * V);
     }
-    rq = b.dec[((cbase + c) * a.nheads + h) * kQ + lane];
+    rq = a.dec[((cbase + c) * a.nheads + h) * kQ + lane];
   };
   float total = 0.f;
   fetch(grad ? chunks - 1 : 0);
   for (int ci = 0; ci < chunks; ++ci) {
     const int c = grad ? chunks - 1 - ci : ci;
+    tid = threadIdx.x;
+    forget(tid);
+    lane = tid & 63;
     const int rows = sg.len - c * kQ < kQ ? sg.len - c * kQ : kQ;
     if (STORE && live) {
       f32x4* dst = reinterpret_cast<f32x4*>(out) + ((cbase + c) * a.vheads + v) * (NT * 2 * 64) + lane;
@@ -191,7 +170,7 @@ __global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 1 : 2)
     __syncthreads();  // the previous chunk's tiles are no longer read
 #pragma unroll
     for (int q = 0; q < QN; ++q) {
-      const int e = q * TH + (int)threadIdx.x, r = e / PN;
+      const int e = q * TH + tid, r = e / PN;
       if (r < kQ) *reinterpret_cast<u32x4*>(sB + r * LN + (e % PN) * V) = rn[q];
     }
 #pragma unroll
@@ -310,17 +289,6 @@ __device__ static inline float sum_g(float v) {
   v += __shfl_xor(v, 16, 64);
   return v + __shfl_xor(v, 32, 64);
 }
-// The value is unknown from here on: what is worked out from it (addresses,
-// conversions) is worked out again in each round of a loop, instead of being
-// kept in registers across all of them.
-__device__ static inline void forget(int& v) { asm volatile("" : "+v"(v)); }
-__device__ static inline void forget(u32x2& v) { asm volatile("" : "+v"(v)); }
-__device__ static inline void forget(f32x4& v) { asm volatile("" : "+v"(v)); }
-
-// Nothing is scheduled across this point: fully unrolled, the compiler would
-// start every tile's products at once and spill what they leave.
-__device__ static inline void keep_order() { __builtin_amdgcn_sched_barrier(0); }
-
 // Inclusive sums over the wave's lanes, up to and from each lane.
 __device__ static inline float upto64(float v, int lane) {
   v += row_move<0x111>(v);
@@ -383,16 +351,16 @@ __global__ void __launch_bounds__(64 * bwd_waves(sizeof(typename Mat<T>::E) == 4
   const int lane0 = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int lane = lane0, i16 = lane & 15, g = lane >> 4;
   const int id = xcd_tile(blockIdx.x, gridDim.x);
-  const int slot = id / (a.ngroups * b.hb), rest = id % (a.ngroups * b.hb);
-  const int grp = rest / b.hb, hblk = rest % b.hb;
+  const int slot = id / (a.ngroups * a.hb), rest = id % (a.ngroups * a.hb);
+  const int grp = rest / a.hb, hblk = rest % a.hb;
   const Segment sg = find_segment(a.cu, a.seqs, a.tokens, kQ, slot);
-  const int u0 = hblk * b.upb, u1 = u0 + b.upb < b.upg ? u0 + b.upb : b.upg;
-  const int units = b.upg * a.ngroups, per = a.headdim / PB;
+  const int u0 = hblk * a.upb, u1 = u0 + a.upb < a.upg ? u0 + a.upb : a.upg;
+  const int units = a.upg * a.ngroups, per = a.headdim / PB;
   if (threadIdx.x == 0 && rest == 0 && sg.first && a.status) {
     if (sg.bad) atomicOr(a.status, RSSM_ST_BAD_SEQ);
     if (a.init && scan_slot(a, sg.seq) < 0) atomicOr(a.status, RSSM_ST_BAD_SLOT);
   }
-  f32x4* const hp = reinterpret_cast<f32x4*>(b.head_part) + (long)slot * units + grp * b.upg;
+  f32x4* const hp = reinterpret_cast<f32x4*>(b.head_part) + (long)slot * units + grp * a.upg;
   if (sg.len == 0) {
     for (int u = u0 + (int)threadIdx.x; u < u1; u += TH) hp[u] = f32x4{0.f, 0.f, 0.f, 0.f};
     return;
@@ -455,7 +423,7 @@ __global__ void __launch_bounds__(64 * bwd_waves(sizeof(typename Mat<T>::E) == 4
   u32x4 rx[QX], ry[QX];
   f32x4 rq;
   const auto fetch = [&](int u) {
-    const int hu = grp * b.upg + u, h = hu / per;
+    const int hu = grp * a.upg + u, h = hu / per;
     const long col = (long)h * a.headdim + (long)(hu % per) * PB;
 #pragma unroll
     for (int q = 0; q < QX; ++q) {
@@ -466,13 +434,13 @@ __global__ void __launch_bounds__(64 * bwd_waves(sizeof(typename Mat<T>::E) == 4
         ry[q] = *reinterpret_cast<const u32x4*>(static_cast<const E*>(b.dy) + (t0 + r) * b.dy_stride + col + c);
       }
     }
-    rq = b.dec[((long)slot * a.nheads + h) * kQ + lane];
+    rq = a.dec[((long)slot * a.nheads + h) * kQ + lane];
   };
   fetch(u0);
 
 #pragma unroll 1
   for (int u = u0; u < u1; ++u) {
-    const int hu = grp * b.upg + u, h = hu / per, p0 = (hu % per) * PB;
+    const int hu = grp * a.upg + u, h = hu / per, p0 = (hu % per) * PB;
     int again = 0;
     lane = lane0;
     forget(lane);
@@ -495,7 +463,7 @@ __global__ void __launch_bounds__(64 * bwd_waves(sizeof(typename Mat<T>::E) == 4
     __syncthreads();
     if (u + 1 < u1) fetch(u + 1);
     // the states' first column tile is on its way during the tokens' products
-    const f32x4* const ss = reinterpret_cast<const f32x4*>(b.chunk_state) +
+    const f32x4* const ss = static_cast<const f32x4*>(a.chunk_state) +
         ((long)slot * a.vheads + (long)hu * SL) * (NT * 2 * 64) + lane;
     const f32x4* const gs = reinterpret_cast<const f32x4*>(b.grad_state) +
         ((long)slot * a.vheads + (long)hu * SL) * (NT * 2 * 64) + lane;
@@ -778,7 +746,7 @@ __global__ void __launch_bounds__(256) scan_bwd_join_kernel(const ScanBwdArgs b,
     if (e >= tgn) return;
     float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
-    for (int k = 0; k < b.hb; ++k) {
+    for (int k = 0; k < a.hb; ++k) {
       float o[8];
       Vec8<float>::load(part + k * tgn, e, o);
 #pragma unroll
@@ -788,7 +756,7 @@ __global__ void __launch_bounds__(256) scan_bwd_join_kernel(const ScanBwdArgs b,
     return;
   }
   id -= 2 * nbc;
-  const int units = b.upg * a.ngroups, slices = units / a.nheads;
+  const int units = a.upg * a.ngroups, slices = units / a.nheads;
   if (id < nd) {
     // 64 tokens of 16 heads: read along tokens, written along heads
     __shared__ float tile[64][17];
@@ -971,8 +939,8 @@ extern "C" int ssu_scan_backward(const rssm_scan_dims* dims, const void* dy, con
   b.dD = dD;
   b.ddt_bias = ddt_bias;
   b.dinit = dinitial_state;
-  b.dec = reinterpret_cast<f32x4*>(ws + l.dec);
-  b.chunk_state = reinterpret_cast<float*>(ws + l.chunk_state);
+  a.dec = reinterpret_cast<f32x4*>(ws + l.dec);
+  a.chunk_state = ws + l.chunk_state;
   b.grad_state = reinterpret_cast<float*>(ws + l.grad_state);
   b.seg_grad = reinterpret_cast<float*>(ws + l.seg_grad);
   b.grad_decay = reinterpret_cast<float*>(ws + l.grad_decay);
@@ -983,12 +951,12 @@ extern "C" int ssu_scan_backward(const rssm_scan_dims* dims, const void* dy, con
   b.dy_stride = d.dy_stride ? d.dy_stride : (long)d.nheads * d.headdim;
   b.slots = scan_slots(d.tokens, d.seqs, a.seg);
   b.cslots = scan_slots(d.tokens, d.seqs, kQ);
-  b.upg = l.upg;
-  b.upb = l.upb;
-  b.hb = l.hb;
+  a.upg = l.upg;
+  a.upb = l.upb;
+  a.hb = l.hb;
   const bool f32 = d.io_dtype == RSSM_F32;
   const long sgrid = b.slots * d.ngroups * ((a.vpg + 3) / 4);
-  const long mgrid = b.cslots * d.ngroups * b.hb;
+  const long mgrid = b.cslots * d.ngroups * a.hb;
   const long dgrid = b.cslots * ((d.nheads + 3) / 4);
   const long cgrid = ((long)kPT * d.dstate / 4 + 255) / 256 * a.vheads * d.seqs;
   const long nbc = ((long)d.tokens * d.ngroups * d.dstate / 8 + 255) / 256;
@@ -1003,9 +971,7 @@ extern "C" int ssu_scan_backward(const rssm_scan_dims* dims, const void* dy, con
   };
   if (d.seqs > 0) {
     if (d.tokens > 0)
-      rc = launch_kernel(f32 ? reinterpret_cast<const void*>(&scan_decay_kernel<float>)
-                             : reinterpret_cast<const void*>(&scan_decay_kernel<bf16>),
-                         (unsigned)dgrid, 256, 0, stream, b);
+      rc = f32 ? launch_decay<float>(a, b.cslots, stream) : launch_decay<bf16>(a, b.cslots, stream);
     if (!rc && d.tokens > a.seg) {
       b.dir_blocks = (int32_t)sgrid;
       rc = go(kSegments, 2 * sgrid, 256);
