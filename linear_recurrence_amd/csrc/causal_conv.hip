@@ -36,20 +36,49 @@ struct ConvArgs {
 constexpr int kFwdRun = 32;   // tokens of a forward run
 constexpr int kBwdRun = 32;   // tokens of one wave's backward run
 constexpr int kBwdWaves = 4;  // runs of one backward workgroup
+constexpr int kBwdChan = 4;   // channels of a lane there
+constexpr int kStepRows = 4;  // batch rows of a wave of a large decode step
 
-template <int W>
+// The weights of K channels: K W consecutive floats.
+template <int W, int K>
 struct Taps {
-  float w[W][8], b[8];
+  float w[W][K], b[K];
   __device__ inline void load(const ConvArgs& a, int c0, int n) {
+    if (n == K) {
+      typedef f32x4 f32x4_any __attribute__((aligned(4)));
+      float f[W * K];
+      const float* const q = a.weight + (long)c0 * W;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+      for (int v = 0; v < W * K; v += 4) {
+        const f32x4 x = *reinterpret_cast<const f32x4_any*>(q + v);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) f[v + r] = x[r];
+      }
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        b[k] = 0.f;
+#pragma unroll
+        for (int j = 0; j < W; ++j) w[j][k] = f[k * W + j];
+      }
+      if (a.bias) {
+#pragma unroll
+        for (int k = 0; k < K; k += 4) {
+          const f32x4 x = *reinterpret_cast<const f32x4_any*>(a.bias + c0 + k);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) b[k + r] = x[r];
+        }
+      }
+      return;
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
       b[k] = a.bias && k < n ? a.bias[c0 + k] : 0.f;
 #pragma unroll
       for (int j = 0; j < W; ++j) w[j][k] = k < n ? a.weight[(long)(c0 + k) * W + j] : 0.f;
     }
   }
   // v of the window h[0..W-1] (oldest first), lane's k-th channel
-  __device__ inline float dot(const float (&h)[W][8], int k) const {
+  __device__ inline float dot(const float (&h)[W][K], int k) const {
     float v = b[k];
 #pragma unroll
     for (int j = 0; j < W; ++j) v = fmaf(w[j][k], h[j][k], v);
@@ -78,7 +107,7 @@ __global__ void __launch_bounds__(64) conv_fwd_kernel(const ConvArgs a) {
   const int tile = id / cblocks, c0 = (id % cblocks) * 512 + threadIdx.x * 8;
   if (c0 >= a.channels) return;
   const int n = a.channels - c0 < 8 ? a.channels - c0 : 8;
-  Taps<W> tp;
+  Taps<W, 8> tp;
   tp.load(a, c0, n);
   float h[W][8];
   const auto emit = [&](long t) {
@@ -158,16 +187,28 @@ __global__ void __launch_bounds__(64) conv_fwd_kernel(const ConvArgs a) {
     const int from = sp.start + W - 1, to = sp.start + sp.len;
     constexpr int U = 4;  // rows in flight
     for (; t < end; t += U) {
-      float r[U][8];
+      RawK<T, 8> r[U];
+      const auto next = [&](int u) {
+        shift();
+        r[u].get(h[W - 1]);
+      };
+      if (t >= from && t + U <= to && t + U <= end) {  // nearly all: no conditions
+#pragma unroll
+        for (int u = 0; u < U; ++u) r[u].load(a.x, (long)(t + u) * a.x_stride + c0, n);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          next(u);
+          emit(t + u);
+        }
+        continue;
+      }
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        if (t + u < end) load8<T>(a.x, (long)(t + u) * a.x_stride + c0, n, r[u]);
+        if (t + u < end) r[u].load(a.x, (long)(t + u) * a.x_stride + c0, n);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         if (t + u < end) {
-          shift();
-#pragma unroll
-          for (int k = 0; k < 8; ++k) h[W - 1][k] = r[u][k];
+          next(u);
           if (t + u >= from && t + u < to) emit(t + u);
         }
       }
@@ -184,17 +225,19 @@ __global__ void __launch_bounds__(64) conv_fwd_kernel(const ConvArgs a) {
 // other); the sums over tokens stay in registers, are joined over the
 // workgroup's waves in LDS, in wave order, and go to one row of partial sums
 // per workgroup, which a second launch adds in row order: the result does not
-// depend on timing.
+// depend on timing.  A lane owns four channels: eight would take 232 registers
+// and leave two waves a SIMD.
 template <typename T, int W>
 __global__ void __launch_bounds__(64 * kBwdWaves) conv_bwd_kernel(const ConvArgs a) {
-  __shared__ float red[kBwdWaves][W + 1][64][9];
+  constexpr int K = kBwdChan, CB = 64 * K;
+  __shared__ float red[kBwdWaves][W + 1][64][K + 1];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int cblocks = (a.channels + 511) / 512;
+  const int cblocks = (a.channels + CB - 1) / CB;
   const int id = xcd_tile(blockIdx.x, gridDim.x);
-  const int tile = id / cblocks, cb = (id % cblocks) * 512, c0 = cb + lane * 8;
-  const int n = a.channels - c0 < 8 ? (a.channels - c0 < 0 ? 0 : a.channels - c0) : 8;
-  float dw[W][8] = {}, db[8] = {};
-  Taps<W> tp;
+  const int tile = id / cblocks, cb = (id % cblocks) * CB, c0 = cb + lane * K;
+  const int n = a.channels - c0 < K ? (a.channels - c0 < 0 ? 0 : a.channels - c0) : K;
+  float dw[W][K] = {}, db[K] = {};
+  Taps<W, K> tp;
   tp.load(a, c0, n);
   const int t0 = (tile * kBwdWaves + wave) * kBwdRun;
   const int t1 = t0 + kBwdRun < a.tokens ? t0 + kBwdRun : a.tokens;
@@ -205,80 +248,94 @@ __global__ void __launch_bounds__(64 * kBwdWaves) conv_bwd_kernel(const ConvArgs
       const int send = sp.start + sp.len;
       const int b = send < t1 ? send : t1;  // this piece: tokens [t, b) of sequence i
       if (b <= t || t < sp.start) continue;
-      float h[W][8], g[W][8];  // windows of x and dv, oldest first
+      float h[W][K], g[W][K];  // windows of x and dv, oldest first
       int slot = -1;
       if (t - sp.start < W - 1 && a.init && (!a.has_init || a.has_init[i])) slot = conv_slot(a, i);
 #pragma unroll
       for (int j = 1; j < W; ++j) {
         const int p = t - sp.start - W + j;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) h[j][k] = 0.f, g[j][k] = 0.f;
+        RawK<T, K> r;
+        r.zero();
         if (p >= 0)
-          load8<T>(a.x, (long)(sp.start + p) * a.x_stride + c0, n, h[j]);
+          r.load(a.x, (long)(sp.start + p) * a.x_stride + c0, n);
         else if (slot >= 0)
-          load8<T>(a.init, ((long)slot * (W - 1) + p + W - 1) * a.channels + c0, n, h[j]);
+          r.load(a.init, ((long)slot * (W - 1) + p + W - 1) * a.channels + c0, n);
+        r.get(h[j]);
+#pragma unroll
+        for (int k = 0; k < K; ++k) g[j][k] = 0.f;
       }
       const int stop = b + W - 1;
       constexpr int U = 4;
+      RawK<T, K> rx[U], ro[U];
+      // token u of the piece; INNER: well inside it
+      const auto token = [&](int q, int u, auto inner) {
+        constexpr bool INNER = decltype(inner)::value;
+#pragma unroll
+        for (int j = 0; j + 1 < W; ++j)
+#pragma unroll
+          for (int k = 0; k < K; ++k) h[j][k] = h[j + 1][k], g[j][k] = g[j + 1][k];
+        float o[K], d[K];
+        rx[q].get(h[W - 1]);
+        ro[q].get(d);  // 0 past the sequence's end
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          if (a.silu) {
+            const float v = tp.dot(h, k), s = sigmoid_f32(v);
+            d[k] *= s * fmaf(v, 1.f - s, 1.f);
+          }
+          g[W - 1][k] = INNER || u < send ? d[k] : 0.f;
+          if (INNER || u < b) {
+            db[k] += d[k];
+#pragma unroll
+            for (int j = 0; j < W; ++j) dw[j][k] = fmaf(d[k], h[j][k], dw[j][k]);
+          }
+          float s = 0.f;
+#pragma unroll
+          for (int j = 0; j < W; ++j) s = fmaf(tp.w[j][k], g[W - 1 - j][k], s);
+          o[k] = s;
+        }
+        if (INNER || u - (W - 1) >= t) store_k<T, K>(a.dx, (long)(u - (W - 1)) * a.channels + c0, n, o);
+      };
       for (int u0 = t; u0 < stop; u0 += U) {
-        float rx[U][8], ro[U][8];
+        if (u0 >= t + W - 1 && u0 + U <= b) {
+#pragma unroll
+          for (int q = 0; q < U; ++q) {
+            rx[q].load(a.x, (long)(u0 + q) * a.x_stride + c0, n);
+            ro[q].load(a.dy, (long)(u0 + q) * a.dy_stride + c0, n);
+          }
+#pragma unroll
+          for (int q = 0; q < U; ++q) token(q, u0 + q, std::true_type{});
+          continue;
+        }
 #pragma unroll
         for (int q = 0; q < U; ++q) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) rx[q][k] = 0.f, ro[q][k] = 0.f;
+          rx[q].zero();
+          ro[q].zero();
           if (u0 + q < stop && u0 + q < send) {
-            load8<T>(a.x, (long)(u0 + q) * a.x_stride + c0, n, rx[q]);
-            load8<T>(a.dy, (long)(u0 + q) * a.dy_stride + c0, n, ro[q]);
+            rx[q].load(a.x, (long)(u0 + q) * a.x_stride + c0, n);
+            ro[q].load(a.dy, (long)(u0 + q) * a.dy_stride + c0, n);
           }
         }
 #pragma unroll
-        for (int q = 0; q < U; ++q) {
-          const int u = u0 + q;
-          if (u < stop) {
-#pragma unroll
-            for (int j = 0; j + 1 < W; ++j)
-#pragma unroll
-              for (int k = 0; k < 8; ++k) h[j][k] = h[j + 1][k], g[j][k] = g[j + 1][k];
-            float o[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              h[W - 1][k] = rx[q][k];
-              float d = ro[q][k];  // 0 past the sequence's end
-              if (a.silu) {
-                const float v = tp.dot(h, k), s = sigmoid_f32(v);
-                d *= s * fmaf(v, 1.f - s, 1.f);
-              }
-              g[W - 1][k] = u < send ? d : 0.f;
-              if (u < b) {
-                db[k] += d;
-#pragma unroll
-                for (int j = 0; j < W; ++j) dw[j][k] = fmaf(d, h[j][k], dw[j][k]);
-              }
-              float s = 0.f;
-#pragma unroll
-              for (int j = 0; j < W; ++j) s = fmaf(tp.w[j][k], g[W - 1 - j][k], s);
-              o[k] = s;
-            }
-            if (u - (W - 1) >= t) store8<T>(a.dx, (long)(u - (W - 1)) * a.channels + c0, n, o);
-          }
-        }
+        for (int q = 0; q < U; ++q)
+          if (u0 + q < stop) token(q, u0 + q, std::false_type{});
       }
       t = b;
     }
   }
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
+  for (int k = 0; k < K; ++k) {
     red[wave][W][lane][k] = db[k];
 #pragma unroll
     for (int j = 0; j < W; ++j) red[wave][j][lane][k] = dw[j][k];
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < (W + 1) * 512; e += 64 * kBwdWaves) {
-    const int j = e / 512, c = e % 512;
+  for (int e = threadIdx.x; e < (W + 1) * CB; e += 64 * kBwdWaves) {
+    const int j = e / CB, c = e % CB;
     if (cb + c < a.channels) {
       float s = 0.f;
 #pragma unroll
-      for (int w = 0; w < kBwdWaves; ++w) s += red[w][j][c >> 3][c & 7];
+      for (int w = 0; w < kBwdWaves; ++w) s += red[w][j][c / K][c % K];
       a.part[((long)tile * (W + 1) + j) * a.channels + cb + c] = s;
     }
   }
@@ -326,7 +383,7 @@ __global__ void __launch_bounds__(256) conv_bwd_join_kernel(const ConvArgs a) {
   const int slot = conv_slot(a, i);
   if (slot < 0) return;
   const bool has = !a.has_init || a.has_init[i];
-  Taps<W> tp;
+  Taps<W, 8> tp;
   tp.load(a, c0, n);
   float h[W][8], g[W][8] = {};  // g[p]: dv of token p
   const bool live = has && a.init;
@@ -372,35 +429,55 @@ __global__ void __launch_bounds__(256) conv_bwd_join_kernel(const ConvArgs a) {
 
 // One decode step: the window is the W-1 state rows and x; the state moves on
 // by one row.  A lane reads all it needs of its channels before it writes, so
-// the new state may be the old one.
-template <typename T, int W>
+// the new state may be the old one.  A wave takes R rows of the batch, all of
+// whose loads are under way at once, with one read of the weights.
+template <typename T, int W, int R>
 __global__ void __launch_bounds__(64) conv_step_kernel(const ConvArgs a) {
   const int cblocks = (a.channels + 511) / 512;
-  const int row = blockIdx.x / cblocks, c0 = (blockIdx.x % cblocks) * 512 + threadIdx.x * 8;
+  const int row0 = blockIdx.x / cblocks * R, c0 = (blockIdx.x % cblocks) * 512 + threadIdx.x * 8;
   if (c0 >= a.channels) return;
   const int n = a.channels - c0 < 8 ? a.channels - c0 : 8;
-  const int slot = conv_slot(a, row);
-  float o[8], h[W][8];
-  Taps<W> tp;
-  tp.load(a, c0, n);
-  load8<T>(a.x, (long)row * a.x_stride + c0, n, h[W - 1]);
-  if (slot >= 0) {
+  int slot[R];
+  RawK<T, 8> r[R][W];
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j)
-      load8<T>(a.init, ((long)slot * (W - 1) + j) * a.channels + c0, n, h[j]);
+  for (int q = 0; q < R; ++q) slot[q] = row0 + q < a.tokens ? conv_slot(a, row0 + q) : -1;
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j)
-      store8<T>(a.final_state, ((long)slot * (W - 1) + j) * a.channels + c0, n, h[j + 1]);
+  for (int q = 0; q < R; ++q) {
+    if (row0 + q < a.tokens) r[q][W - 1].load(a.x, (long)(row0 + q) * a.x_stride + c0, n);
+    if (slot[q] >= 0) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float v = tp.dot(h, k);
-      o[k] = a.silu ? v * sigmoid_f32(v) : v;
+      for (int j = 0; j < W - 1; ++j)
+        r[q][j].load(a.init, ((long)slot[q] * (W - 1) + j) * a.channels + c0, n);
     }
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) o[k] = __builtin_nanf("");
   }
-  store8<T>(a.y, (long)row * a.channels + c0, n, o);
+  Taps<W, 8> tp;
+  tp.load(a, c0, n);
+#pragma unroll
+  for (int q = 0; q < R; ++q) {
+    if (row0 + q >= a.tokens) break;
+    float o[8], h[W][8];
+    if (slot[q] >= 0) {
+#pragma unroll
+      for (int j = 0; j < W; ++j) r[q][j].get(h[j]);
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j)
+        store8<T>(a.final_state, ((long)slot[q] * (W - 1) + j) * a.channels + c0, n, h[j + 1]);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float v = tp.dot(h, k);
+        o[k] = a.silu ? v * sigmoid_f32(v) : v;
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) o[k] = __builtin_nanf("");
+    }
+    store8<T>(a.y, (long)(row0 + q) * a.channels + c0, n, o);
+  }
+}
+template <typename T, int W>
+static const void* pick_step(int rows) {
+  return rows == 1 ? reinterpret_cast<const void*>(&conv_step_kernel<T, W, 1>)
+                   : reinterpret_cast<const void*>(&conv_step_kernel<T, W, kStepRows>);
 }
 
 static int conv_check(const rssm_conv_dims* d) {
@@ -523,7 +600,8 @@ extern "C" int causal_conv_backward(const rssm_conv_dims* dims, const void* dy, 
   a.runs = (int32_t)bwd_tiles(d);
   if (a.runs > 0) {
     rc = launch_kernel(RSSM_CONV_PICK(conv_bwd_kernel, d),
-                       (unsigned)((long)a.runs * ((d.channels + 511) / 512)), 64 * kBwdWaves, 0,
+                       (unsigned)((long)a.runs * ((d.channels + 64 * kBwdChan - 1) / (64 * kBwdChan))),
+                       64 * kBwdWaves, 0,
                        stream, a);
     if (rc) return rc;
   }
@@ -555,6 +633,12 @@ extern "C" int causal_conv_decode(const rssm_conv_dims* dims, const void* x,
   a.final_state = new_state;
   a.y = y;
   a.status = status;
-  return launch_kernel(RSSM_CONV_PICK(conv_step_kernel, d),
-                       (unsigned)((long)d.tokens * ((d.channels + 511) / 512)), 64, 0, stream, a);
+  // several rows a wave where that still leaves one for every SIMD
+  const long cblocks = (d.channels + 511) / 512;
+  const int rows = d.tokens * cblocks >= 1024 * kStepRows ? kStepRows : 1;
+  const bool f32 = d.io_dtype == RSSM_F32;
+  const void* fn = d.width == 2   ? (f32 ? pick_step<float, 2>(rows) : pick_step<bf16, 2>(rows))
+                   : d.width == 3 ? (f32 ? pick_step<float, 3>(rows) : pick_step<bf16, 3>(rows))
+                                  : (f32 ? pick_step<float, 4>(rows) : pick_step<bf16, 4>(rows));
+  return launch_kernel(fn, (unsigned)((d.tokens + rows - 1) / rows * cblocks), 64, 0, stream, a);
 }

@@ -235,15 +235,68 @@ __global__ void __launch_bounds__(T) norm_fwd_kernel(const NormArgs a) {
   }
 }
 
+// The same for two values a vector at once; a group's sums replace its first
+// vector's values.
+template <int T, int V>
+__device__ static inline void group_sums2(const NormArgs& a, float (&s)[V], float (&d)[V],
+                                          const int (&g)[V], float2* lds) {
+  const int lane = threadIdx.x & 63;
+  if (a.ngroups == 1) {
+    float2 t = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int v = 0; v < V; ++v) t.x += s[v], t.y += d[v];
+    t.x = group_sum<64>(t.x);
+    t.y = group_sum<64>(t.y);
+    if constexpr (T > 64) {
+      __syncthreads();
+      if (lane == 0) lds[threadIdx.x >> 6] = t;
+      __syncthreads();
+      t = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < T / 64; ++w) t.x += lds[w].x, t.y += lds[w].y;
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) s[v] = t.x, d[v] = t.y;
+    return;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int q = v * T + threadIdx.x;
+    if (q < a.nvec) lds[q] = make_float2(s[v], d[v]);
+  }
+  __syncthreads();
+  for (int k = threadIdx.x >> 6; k < a.ngroups; k += T / 64) {
+    float2 t = make_float2(0.f, 0.f);
+    for (int j = lane; j < a.gvec; j += 64) {
+      const float2 o = lds[k * a.gvec + j];
+      t.x += o.x;
+      t.y += o.y;
+    }
+    t.x = group_sum<64>(t.x);
+    t.y = group_sum<64>(t.y);
+    if (lane == 0) lds[k * a.gvec] = t;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const float2 t = g[v] < a.ngroups ? lds[g[v] * a.gvec] : make_float2(0.f, 0.f);
+    s[v] = t.x;
+    d[v] = t.y;
+  }
+}
+
 // With r = rsqrt(mean(u^2) + eps) and t = dy * weight:
 //   du = r (t - u r^2 mean(t u)),  dweight = sum_rows dy u r,
 //   dh = du silu(z),  dz = du h silu'(z).
 // A workgroup takes every gridDim-th row and keeps its share of dweight in
 // registers; one row of partial sums per workgroup, added in order by a
-// second launch.
+// second launch.  The inputs stay as they are stored (half the registers of
+// fp32), and the next row's are on their way while one is worked on.
 template <typename E, int T, int V>
 __global__ void __launch_bounds__(T) norm_bwd_kernel(const NormArgs a) {
-  extern __shared__ float lds[];
+  extern __shared__ float2 lds2[];
+  constexpr bool kAhead = V <= 2;
   Lay<T, V> l;
   l.set(a);
   float dw[V][8];
@@ -251,51 +304,68 @@ __global__ void __launch_bounds__(T) norm_bwd_kernel(const NormArgs a) {
   for (int v = 0; v < V; ++v)
 #pragma unroll
     for (int k = 0; k < 8; ++k) dw[v][k] = 0.f;
-  for (long row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    float h[V][8], z[V][8], o[V][8], s[V], tot[V], dot[V];
+  struct Row {
+    RawK<E, 8> x[V], o[V], z[V];
+    __device__ inline void load(const NormArgs& a, const Lay<T, V>& l, long row) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      load8<E>(a.x, row * a.x_stride + l.i[v], l.n[v], h[v]);
-      load8<E>(a.dy, row * a.dy_stride + l.i[v], l.n[v], o[v]);
-      if (a.z) load8<E>(a.z, row * a.z_stride + l.i[v], l.n[v], z[v]);
+      for (int v = 0; v < V; ++v) {
+        x[v].load(a.x, row * a.x_stride + l.i[v], l.n[v]);
+        o[v].load(a.dy, row * a.dy_stride + l.i[v], l.n[v]);
+        if (a.z) z[v].load(a.z, row * a.z_stride + l.i[v], l.n[v]);
+      }
     }
+  };
+  Row now, next;
+  if (kAhead && (long)blockIdx.x < a.rows) next.load(a, l, blockIdx.x);
+  for (long row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    if constexpr (kAhead) {
+      now = next;
+      if (row + gridDim.x < a.rows) next.load(a, l, row + gridDim.x);
+    } else {
+      now.load(a, l, row);
+    }
+    float s[V], dot[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       s[v] = dot[v] = 0.f;
-      float w[8];
+      float w[8], x[8], o[8], z[8];
       load8<float>(a.weight, l.i[v], l.n[v], w);
+      now.x[v].get(x);
+      now.o[v].get(o);
+      if (a.z) now.z[v].get(z);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const float u = a.z ? h[v][k] * (z[v][k] * sigmoid_f32(z[v][k])) : h[v][k];
+        const float u = a.z ? x[k] * (z[k] * sigmoid_f32(z[k])) : x[k];
         s[v] = fmaf(u, u, s[v]);
-        dot[v] = fmaf(u, o[v][k] * w[k], dot[v]);
+        dot[v] = fmaf(u, o[k] * w[k], dot[v]);
       }
     }
-    group_sums<T, V>(a, s, l.g, lds, tot);
-    group_sums<T, V>(a, dot, l.g, lds, dot);
+    group_sums2<T, V>(a, s, dot, l.g, lds2);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const float r = __builtin_amdgcn_rsqf(tot[v] * a.inv_group + a.eps);
+      const float r = __builtin_amdgcn_rsqf(s[v] * a.inv_group + a.eps);
       const float c = r * r * (dot[v] * a.inv_group);
-      float w[8], gz[8];
+      float w[8], x[8], o[8], z[8];
       load8<float>(a.weight, l.i[v], l.n[v], w);
+      now.x[v].get(x);
+      now.o[v].get(o);
+      if (a.z) now.z[v].get(z);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const float x = h[v][k];
         float gate = 1.f, dgate = 0.f;
         if (a.z) {
-          const float sg = sigmoid_f32(z[v][k]);
-          gate = z[v][k] * sg;
-          dgate = sg * fmaf(z[v][k], 1.f - sg, 1.f);
+          const float sg = sigmoid_f32(z[k]);
+          gate = z[k] * sg;
+          dgate = sg * fmaf(z[k], 1.f - sg, 1.f);
         }
-        const float u = x * gate;
-        const float du = r * (o[v][k] * w[k] - u * c);
-        dw[v][k] = fmaf(o[v][k], u * r, dw[v][k]);
-        h[v][k] = du * gate;
-        gz[k] = du * x * dgate;
+        const float u = x[k] * gate;
+        const float du = r * (o[k] * w[k] - u * c);
+        dw[v][k] = fmaf(o[k], u * r, dw[v][k]);
+        z[k] = du * x[k] * dgate;
+        x[k] = du * gate;
       }
-      store8<E>(a.dx, row * a.dim + l.i[v], l.n[v], h[v]);
-      if (a.z) store8<E>(a.dz, row * a.dim + l.i[v], l.n[v], gz);
+      store8<E>(a.dx, row * a.dim + l.i[v], l.n[v], x);
+      if (a.z) store8<E>(a.dz, row * a.dim + l.i[v], l.n[v], z);
     }
   }
 #pragma unroll
@@ -324,36 +394,42 @@ __global__ void __launch_bounds__(256) norm_bwd_join_kernel(const NormArgs a) {
   }
 }
 
-// Threads of a row's workgroup and vectors a lane: rows up to 512 elements
-// take one wave (no barrier), up to 8192 four waves, up to 32768 sixteen.
+// Threads of a row's workgroup and vectors a lane: rows up to 1024 elements
+// take one wave (no barrier), up to 4096 four waves, up to 8192 four (forward)
+// or eight (backward, which holds two rows of three tensors), up to 32768
+// sixteen.
 struct NormShape {
   int threads, vecs;
 };
-static NormShape norm_shape(int nvec) {
+static NormShape norm_shape(int nvec, bool backward) {
   if (nvec <= 64) return {64, 1};
   if (nvec <= 128) return {64, 2};
   if (nvec <= 256) return {256, 1};
   if (nvec <= 512) return {256, 2};
-  if (nvec <= 1024) return {256, 4};
+  if (nvec <= 1024) return backward ? NormShape{512, 2} : NormShape{256, 4};
   if (nvec <= 2048) return {1024, 2};
   return {1024, 4};
 }
 
-#define RSSM_NORM_CASE(name, E, T, V) \
-  if (sh.threads == T && sh.vecs == V) return reinterpret_cast<const void*>(&name<E, T, V>)
-#define RSSM_NORM_PICK(name)                                                 \
+template <int T, int V>
+static bool norm_is(const NormShape& sh) {
+  return sh.threads == T && sh.vecs == V;
+}
+#define RSSM_NORM_CASE(name, E, ...)                                        \
+  if (norm_is<__VA_ARGS__>(sh)) return reinterpret_cast<const void*>(&name<E, __VA_ARGS__>)
+#define RSSM_NORM_PICK(name, ...)                                               \
   template <typename E>                                                      \
   static const void* pick_##name(const NormShape& sh) {                      \
     RSSM_NORM_CASE(name, E, 64, 1);                                          \
     RSSM_NORM_CASE(name, E, 64, 2);                                          \
     RSSM_NORM_CASE(name, E, 256, 1);                                         \
     RSSM_NORM_CASE(name, E, 256, 2);                                         \
-    RSSM_NORM_CASE(name, E, 256, 4);                                         \
+    RSSM_NORM_CASE(name, E, __VA_ARGS__);                                    \
     RSSM_NORM_CASE(name, E, 1024, 2);                                        \
     return reinterpret_cast<const void*>(&name<E, 1024, 4>);                 \
   }
-RSSM_NORM_PICK(norm_fwd_kernel)
-RSSM_NORM_PICK(norm_bwd_kernel)
+RSSM_NORM_PICK(norm_fwd_kernel, 256, 4)
+RSSM_NORM_PICK(norm_bwd_kernel, 512, 2)
 
 static int norm_check(const rssm_norm_dims* d, NormArgs* a) {
   if (!d) return RSSM_EINVAL;
@@ -401,9 +477,16 @@ static bool elt_aligned(const void* p, bool f32) {
   return (reinterpret_cast<uintptr_t>(p) & (f32 ? 3u : 1u)) == 0;
 }
 
-// Workgroups of the backward pass: two of four waves a compute unit, so that
-// one row's loads overlap another's sums, and no more than there are rows.
-static int bwd_parts(int rows) { return rows < 1024 ? rows : 1024; }
+// Workgroups of the backward pass: sixteen waves a compute unit (what their
+// registers leave room for), and no more than there are rows.
+static int bwd_parts(const NormArgs& a) {
+  const int most = 256 * 1024 / norm_shape(a.nvec, true).threads;
+  const int cap = most < 2048 ? most : 2048;
+  return a.rows < cap ? a.rows : cap;
+}
+static size_t norm_bwd_lds(const NormArgs& a) {
+  return sizeof(float2) * (a.ngroups > 1 ? (size_t)a.nvec : 16);
+}
 
 }  // namespace rssm
 
@@ -429,7 +512,7 @@ extern "C" int rms_norm_forward(const rssm_norm_dims* dims, const void* x, const
   a.res_out = residual_out;
   a.out = out;
   a.scale = scale;
-  const NormShape sh = norm_shape(a.nvec);
+  const NormShape sh = norm_shape(a.nvec, false);
   const void* fn = f32 ? pick_norm_fwd_kernel<float>(sh) : pick_norm_fwd_kernel<bf16>(sh);
   return launch_kernel(fn, (unsigned)a.rows, (unsigned)sh.threads, norm_lds(a), stream, a);
 }
@@ -437,7 +520,7 @@ extern "C" int rms_norm_forward(const rssm_norm_dims* dims, const void* x, const
 extern "C" size_t rms_norm_backward_workspace(const rssm_norm_dims* dims) {
   NormArgs a{};
   if (norm_check(dims, &a)) return 0;
-  return sizeof(float) * (size_t)bwd_parts(a.rows) * a.dim;
+  return sizeof(float) * (size_t)bwd_parts(a) * a.dim;
 }
 
 extern "C" int rms_norm_backward(const rssm_norm_dims* dims, const void* dy, const void* x,
@@ -462,11 +545,11 @@ extern "C" int rms_norm_backward(const rssm_norm_dims* dims, const void* dy, con
   a.dz = dz;
   a.dweight = dweight;
   a.part = static_cast<float*>(workspace);
-  a.parts = bwd_parts(a.rows);
+  a.parts = bwd_parts(a);
   if (a.rows > 0) {
-    const NormShape sh = norm_shape(a.nvec);
+    const NormShape sh = norm_shape(a.nvec, true);
     const void* fn = f32 ? pick_norm_bwd_kernel<float>(sh) : pick_norm_bwd_kernel<bf16>(sh);
-    rc = launch_kernel(fn, (unsigned)a.parts, (unsigned)sh.threads, norm_lds(a), stream, a);
+    rc = launch_kernel(fn, (unsigned)a.parts, (unsigned)sh.threads, norm_bwd_lds(a), stream, a);
     if (rc) return rc;
   }
   return launch_kernel(reinterpret_cast<const void*>(&norm_bwd_join_kernel),

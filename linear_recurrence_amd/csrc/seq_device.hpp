@@ -1,6 +1,8 @@
 // Device helpers of the sequence operators (scan, short convolution, norm).
 #pragma once
 
+#include <type_traits>
+
 #include "rssm_device.hpp"
 
 namespace rssm {
@@ -68,6 +70,70 @@ __device__ static inline void store8(void* p, long i, int n, const float* f) {
 #pragma unroll
     for (int k = 0; k < 8; ++k)
       if (k < n) Elt<T>::store1(p, i + k, f[k]);
+  }
+}
+
+// K consecutive elements (8 or 4) as they are stored.
+template <typename T, int K>
+struct RawK {
+  static constexpr int kWords = K * (sizeof(T) == 4 ? 4 : 2) / 8;  // pairs of 32 bits
+  u32x2 v[kWords];
+  __device__ inline void zero() {
+#pragma unroll
+    for (int q = 0; q < kWords; ++q) v[q] = u32x2{0, 0};
+  }
+  // the first n of them, the others 0
+  __device__ inline void load(const void* p, long i, int n) {
+    typedef typename std::conditional<sizeof(T) == 4, uint32_t, uint16_t>::type E;
+    const E* const q = static_cast<const E*>(p) + i;
+    if (n == K) {
+      if constexpr (kWords == 1) {
+        v[0] = *reinterpret_cast<const u32x2_any*>(q);
+      } else {
+#pragma unroll
+        for (int w = 0; w < kWords; w += 2) {
+          const u32x4 x = *reinterpret_cast<const u32x4_any*>(q + w * (8 / sizeof(E)));
+          v[w] = u32x2{x[0], x[1]};
+          v[w + 1] = u32x2{x[2], x[3]};
+        }
+      }
+    } else {
+      constexpr int kPer = 4 / sizeof(E);
+#pragma unroll
+      for (int w = 0; w < 2 * kWords; ++w) {
+        uint32_t x = 0;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k)
+          if (w * kPer + k < n) x |= (uint32_t)q[w * kPer + k] << (16 * k);
+        v[w >> 1][w & 1] = x;
+      }
+    }
+  }
+  __device__ inline void get(float* f) const {
+#pragma unroll
+    for (int w = 0; w < 2 * kWords; ++w) {
+      const uint32_t x = v[w >> 1][w & 1];
+      if constexpr (sizeof(T) == 4) {
+        f[w] = __uint_as_float(x);
+      } else {
+        f[2 * w] = __uint_as_float(x << 16);
+        f[2 * w + 1] = __uint_as_float(x & 0xffff0000u);
+      }
+    }
+  }
+};
+template <typename T, int K>
+__device__ static inline void store_k(void* p, long i, int n, const float* f) {
+  if constexpr (K == 8) {
+    store8<T>(p, i, n, f);
+  } else if (n < K) {
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      if (k < n) Elt<T>::store1(p, i + k, f[k]);
+  } else if constexpr (sizeof(T) == 4) {
+    *reinterpret_cast<u32x4_any*>(static_cast<float*>(p) + i) = Elt<float>::pack(f);
+  } else {
+    *reinterpret_cast<u32x2_any*>(static_cast<uint16_t*>(p) + i) = u32x2{bf16_pk(f[0], f[1]), bf16_pk(f[2], f[3])};
   }
 }
 
