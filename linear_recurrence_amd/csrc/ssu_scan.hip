@@ -219,6 +219,7 @@ __global__ void __launch_bounds__(64 * scan_waves(sizeof(typename Mat<T>::E) == 
 // from, leaving the state before every chunk as operands (rows p, k = n in order
 // D) and the final one in its pool; otherwise from zero, leaving what the
 // segment adds.  The next chunk's tiles are on their way while one is worked on.
+// Slots without a segment lie in runs, so blocks go to the dies in turn.
 template <typename T, int N, bool STORE>
 __global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 1 : (N == 256 ? 2 : 3))
     scan_fwd_states_kernel(const ScanArgs a) {
@@ -235,7 +236,7 @@ __global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 1 : (N 
   int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int hb = (a.vpg + W - 1) / W;
-  const int id = xcd_tile(blockIdx.x, gridDim.x);
+  const int id = blockIdx.x;
   const int slot = id / (a.ngroups * hb), rest = id % (a.ngroups * hb);
   const int grp = rest / hb, vl = (rest % hb) * W + wave;
   const Segment sg = find_segment(a.cu, a.seqs, a.tokens, a.seg, slot);

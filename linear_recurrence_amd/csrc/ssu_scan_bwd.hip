@@ -27,9 +27,10 @@
 //
 // Everything that reaches an fp32 output (dA, ddt_bias, dinitial_state, and
 // ddt through dalpha) takes its state products with the state as three bf16
-// terms.  What only reaches an output in the io type rounds one factor once:
-// dS, e^{a_u-a_t} C_u.B_t (dx) and K (dB, dC) are rounded to the io type, as
-// the outputs themselves are.
+// terms.  What only reaches an output in the io type rounds one factor: dS and
+// e^{a_u-a_t} C_u.B_t (dx, where D dy usually outweighs them) once, to the io
+// type; K (dB, dC, sums over heads in which nothing outweighs it) to two terms:
+// one would take their error from 1.0 to 1.4 times that of rounding the result.
 #include "scan_common.hpp"
 
 namespace rssm {
@@ -70,6 +71,7 @@ __device__ static inline long row_at(int nt, int pt, int r, int lane) {
 // the workspace (and the gradient of the initial state); otherwise from zero,
 // leaving what the segment adds.  The next chunk's tiles are on their way while
 // one is worked on; three workgroups a compute unit (two with 256 columns).
+// Slots without a segment lie in runs, so blocks go to the dies in turn.
 template <typename T, int N, bool STORE>
 __global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 1 : (N == 256 ? 2 : 3))
     scan_states_kernel(const ScanBwdArgs b) {
@@ -87,7 +89,7 @@ __global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 1 : (N 
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int hb = (a.vpg + W - 1) / W;
   const bool grad = (int)blockIdx.x >= b.dir_blocks;
-  const int id = xcd_tile(grad ? blockIdx.x - b.dir_blocks : blockIdx.x, b.dir_blocks);
+  const int id = grad ? blockIdx.x - b.dir_blocks : blockIdx.x;
   const int slot = id / (a.ngroups * hb), rest = id % (a.ngroups * hb);
   const int grp = rest / hb, vl = (rest % hb) * W + wave;
   const Segment sg = find_segment(a.cu, a.seqs, a.tokens, a.seg, slot);
@@ -307,14 +309,19 @@ __device__ static inline float from64(float v, int lane) {
 }
 __device__ static inline float sum64(float v) { return sum_g(sum16(v)); }
 
-// Waves of a workgroup of the main launch: one for every 32 state columns, four
-// at least (and four for fp32's 256 columns, whose tiles leave no room for more).  State rows of one unit of its work: a head's 64 (or 32), 32 in fp32,
-// whose tiles of 64 would not fit.
+// Waves of a workgroup of the main launch: four, or eight from 128 state columns
+// on (and four for fp32's 256 columns, whose tiles leave no room for more).
 constexpr int bwd_waves(bool f32, int n) { return n >= 128 && !f32 ? 8 : 4; }
-static inline int bwd_rows(bool f32, int headdim) { return f32 || headdim == 32 ? 32 : 64; }
+// State rows of one unit of its work: 64 of a head, or 32 (headdim 32; fp32, whose
+// tiles of 64 would not fit; 256 columns, whose registers would not).
+static inline int bwd_rows(const rssm_scan_dims& d) {
+  return d.io_dtype == RSSM_F32 || d.headdim == 32 || d.dstate == 256 ? 32 : 64;
+}
 
-// One chunk, the units of one block.  A wave owns 32 state columns: it holds
-// dB and dC of all 64 tokens there in registers and adds every head's to them,
+// One chunk, the units of one block.  A wave owns N/W state columns (16 at 128;
+// with 32, 157 registers were spilled and the launch took 1195 us instead of
+// 771): it holds dB and dC of all 64 tokens there in registers and adds every
+// head's to them,
 // so the heads are joined without leaving the workgroup.  The products of the
 // chunk's tokens with each other (dy.x, the decays, C.B, which is the same for
 // all heads) are shared: each wave works out some of the ten 16x16 tiles on and
@@ -331,7 +338,8 @@ __global__ void __launch_bounds__(64 * bwd_waves(sizeof(typename Mat<T>::E) == 4
   constexpr int NT = N / 16, NW = NT < W ? 1 : NT / W, KB = NP / 32, SL = PB / 32;
   constexpr int PX = PB / V, QX = (kQ * PX + TH - 1) / TH;
   constexpr int kXY = kQ * LX, kMM = kQ * LM, kS = NP * LX;
-  constexpr int kWork = 2 * kXY + 2 * kMM + kS;
+  constexpr int T2 = M::kTerms == 1 ? 1 : 2;  // terms of K
+  constexpr int kWork = 2 * kXY + (1 + T2) * kMM + kS;
   static_assert(kWork >= kQ * LN, "C's tile fits where the units work");
   __shared__ __attribute__((aligned(16))) E sB[kQ * LN];
   __shared__ __attribute__((aligned(16))) E work[kWork];
@@ -344,8 +352,8 @@ __global__ void __launch_bounds__(64 * bwd_waves(sizeof(typename Mat<T>::E) == 4
   E* const sX = work;
   E* const sY = work + kXY;
   E* const sM = work + 2 * kXY;     // [t][u]: e^{a_u-a_t} C_u.B_t
-  E* const sK = sM + kMM;           // [t][u]: K_ut
-  E* const sG = sK + kMM;           // [n][p]: dS
+  E* const sK = sM + kMM;           // [t][u]: K_ut, then its second term
+  E* const sG = sK + T2 * kMM;      // [n][p]: dS
 
   const ScanArgs& a = b.f;
   const int lane0 = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -416,6 +424,7 @@ __global__ void __launch_bounds__(64 * bwd_waves(sizeof(typename Mat<T>::E) == 4
     const int o = (16 + ((e >> 8) << 5) + ((e >> 4) & 15)) * LM + ((e >> 8) << 5) + (e & 15);
     Elt<T>::store1(sM, o, 0.f);
     Elt<T>::store1(sK, o, 0.f);
+    if (T2 == 2) Elt<T>::store1(sK + kMM, o, 0.f);
   }
   if (N < NP)
     for (int e = threadIdx.x; e < (NP - N) * LX; e += TH) Elt<T>::store1(sG, N * LX + e, 0.f);
@@ -437,6 +446,16 @@ __global__ void __launch_bounds__(64 * bwd_waves(sizeof(typename Mat<T>::E) == 4
     rq = a.dec[((long)slot * a.nheads + h) * kQ + lane];
   };
   fetch(u0);
+  // a unit's states in this wave's column tile nt
+  f32x4 ls[SL][2], lg[SL][2];
+  const auto load = [&](f32x4 (&l)[SL][2], const void* from, int u, int nt) {
+    const f32x4* const p = static_cast<const f32x4*>(from) +
+        ((long)slot * a.vheads + (long)(grp * a.upg + u) * SL) * (NT * 2 * 64) + lane;
+#pragma unroll
+    for (int s = 0; s < SL; ++s)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) l[s][q] = p[(s * NT + nt) * 128 + q * 64];
+  };
 
 #pragma unroll 1
   for (int u = u0; u < u1; ++u) {
@@ -463,20 +482,9 @@ __global__ void __launch_bounds__(64 * bwd_waves(sizeof(typename Mat<T>::E) == 4
     __syncthreads();
     if (u + 1 < u1) fetch(u + 1);
     // the states' first column tile is on its way during the tokens' products
-    const f32x4* const ss = static_cast<const f32x4*>(a.chunk_state) +
-        ((long)slot * a.vheads + (long)hu * SL) * (NT * 2 * 64) + lane;
-    const f32x4* const gs = reinterpret_cast<const f32x4*>(b.grad_state) +
-        ((long)slot * a.vheads + (long)hu * SL) * (NT * 2 * 64) + lane;
-    f32x4 ls[SL][2], lg[SL][2];
-    const auto load = [&](f32x4 (&l)[SL][2], const f32x4* from, int nt) {
-#pragma unroll
-      for (int s = 0; s < SL; ++s)
-#pragma unroll
-        for (int p = 0; p < 2; ++p) l[s][p] = from[(s * NT + nt) * 128 + p * 64];
-    };
     if (wave * NW < NT) {
-      load(ls, ss, wave * NW);
-      load(lg, gs, wave * NW);
+      load(ls, a.chunk_state, u, wave * NW);
+      load(lg, b.grad_state, u, wave * NW);
     }
 
     // ---- the tokens' products with each other
@@ -510,7 +518,15 @@ __global__ void __launch_bounds__(64 * bwd_waves(sizeof(typename Mat<T>::E) == 4
         }
       }
       *reinterpret_cast<typename M::Four*>(sM + t * LM + uu) = M::pack4(m);
-      *reinterpret_cast<typename M::Four*>(sK + t * LM + uu) = M::pack4(kk);
+      const typename M::Four k1 = M::pack4(kk);
+      *reinterpret_cast<typename M::Four*>(sK + t * LM + uu) = k1;
+      if constexpr (T2 == 2) {
+        float q1[4];
+        M::unpack4(k1, q1);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) kk[r] -= q1[r];
+        *reinterpret_cast<typename M::Four*>(sK + kMM + t * LM + uu) = M::pack4(kk);
+      }
       col = sum_g(col);
       if (iu == j) {
         in = sum_g(in);
@@ -569,7 +585,7 @@ __global__ void __launch_bounds__(64 * bwd_waves(sizeof(typename Mat<T>::E) == 4
 #pragma unroll
             for (int r = 0; r < 4; ++r) k0 = fmaf(ls[s][p][r], lg[s][p][r], k0);
         split(ls);
-        if (q + 1 < NW) load(ls, ss, nt + 1);
+        if (q + 1 < NW) load(ls, a.chunk_state, u, nt + 1);
         Frag fb[2];
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb)
@@ -583,7 +599,10 @@ __global__ void __launch_bounds__(64 * bwd_waves(sizeof(typename Mat<T>::E) == 4
             acc = hs[s].a_times(M::rows_c(sY + (16 * j + i16) * LX + 32 * s + 8 * g), acc);
 #pragma unroll
           for (int kb = 0; kb <= j / 2; ++kb)
-            aC[q][j] = M::mma(fb[kb], M::cols(cols_at<T, false>(sK, LM, 32 * kb, 16 * j, lane), LM), aC[q][j]);
+#pragma unroll
+            for (int e = T2 - 1; e >= 0; --e)
+              aC[q][j] = M::mma(fb[kb], M::cols(cols_at<T, false>(sK + e * kMM, LM, 32 * kb, 16 * j, lane), LM),
+                                aC[q][j]);
           float cv[4];
           M::unpack4(rc[q][j], cv);
 #pragma unroll
@@ -594,7 +613,7 @@ __global__ void __launch_bounds__(64 * bwd_waves(sizeof(typename Mat<T>::E) == 4
           keep_order();
         }
         split(lg);
-        if (q + 1 < NW) load(lg, gs, nt + 1);
+        if (q + 1 < NW) load(lg, b.grad_state, u, nt + 1);
 #pragma unroll
         for (int s = 0; s < SL; ++s)
           *reinterpret_cast<Frag*>(sG + (16 * nt + i16) * LX + 32 * s + 8 * g) = hs[s].t[0];
@@ -607,7 +626,10 @@ __global__ void __launch_bounds__(64 * bwd_waves(sizeof(typename Mat<T>::E) == 4
             acc = hs[s].a_times(M::rows_c(sX + (16 * j + i16) * LX + 32 * s + 8 * g), acc);
 #pragma unroll
           for (int kb = j / 2; kb < 2; ++kb)
-            aB[q][j] = M::mma(fc[q][kb], M::rows_d(sK + (16 * j + i16) * LM + 32 * kb + 4 * g), aB[q][j]);
+#pragma unroll
+            for (int e = T2 - 1; e >= 0; --e)
+              aB[q][j] = M::mma(fc[q][kb], M::rows_d(sK + e * kMM + (16 * j + i16) * LM + 32 * kb + 4 * g),
+                                aB[q][j]);
           float bv[4];
           M::unpack4(*reinterpret_cast<const typename M::Four*>(tB + (16 * j + i16) * LN + 16 * nt + 4 * g), bv);
 #pragma unroll
@@ -811,13 +833,17 @@ static int bwd_seg(const rssm_scan_dims& d) {
   return (int)seg;
 }
 
-// Units of a workgroup of the main launch: up to eight, which share the chunk's
+// Units of a workgroup of the main launch: up to sixteen, which share the chunk's
 // C.B and join dB and dC without memory, but so few that there are two
-// workgroups for each of the 512 places.
+// workgroups for each place (one a compute unit with eight waves, two with
+// four).  8 x 2048 tokens of 80 heads: 16 units 1059 us, 8 1104, 4 1194; two
+// uneven sequences of 1291 tokens, 128 heads in 8 groups: two workgroups a place
+// 237 us, one 254, four 259.
 static int bwd_units(const rssm_scan_dims& d, int upg) {
   const long blocks = ((long)d.tokens / kQ + d.seqs) * d.ngroups;
-  int n = 8;
-  while (n > 1 && blocks * ((upg + n - 1) / n) < 1024) n >>= 1;
+  const long least = bwd_waves(d.io_dtype == RSSM_F32, d.dstate) == 8 ? 512 : 1024;
+  int n = 16;
+  while (n > 1 && blocks * ((upg + n - 1) / n) < least) n >>= 1;
   return n;
 }
 
@@ -831,7 +857,7 @@ static BwdLayout bwd_layout(const rssm_scan_dims& d) {
   const size_t V = (size_t)d.nheads * (d.headdim / kPT), hpn = (size_t)d.nheads * d.headdim * d.dstate;
   const size_t slots = T / seg + n, cslots = T / kQ + n;
   BwdLayout l;
-  l.upg = d.nheads / d.ngroups * (d.headdim / bwd_rows(d.io_dtype == RSSM_F32, d.headdim));
+  l.upg = d.nheads / d.ngroups * (d.headdim / bwd_rows(d));
   l.upb = bwd_units(d, l.upg);
   l.hb = (l.upg + l.upb - 1) / l.upb;
   const size_t units = (size_t)l.upg * d.ngroups;
@@ -859,21 +885,21 @@ static BwdLayout bwd_layout(const rssm_scan_dims& d) {
 
 enum { kStates, kSegments, kMain };
 template <typename T, int N>
-static const void* pick_bwd_n(int which, int headdim) {
+static const void* pick_bwd_n(int which, const rssm_scan_dims& d) {
   if (which == kStates) return reinterpret_cast<const void*>(&scan_states_kernel<T, N, true>);
   if (which == kSegments) return reinterpret_cast<const void*>(&scan_states_kernel<T, N, false>);
-  if constexpr (sizeof(typename Mat<T>::E) == 2)
-    if (bwd_rows(false, headdim) == 64) return reinterpret_cast<const void*>(&scan_bwd_kernel<T, N, 64>);
+  if constexpr (sizeof(typename Mat<T>::E) == 2 && N < 256)
+    if (bwd_rows(d) == 64) return reinterpret_cast<const void*>(&scan_bwd_kernel<T, N, 64>);
   return reinterpret_cast<const void*>(&scan_bwd_kernel<T, N, 32>);
 }
 template <typename T>
 static const void* pick_bwd(int which, const rssm_scan_dims& d) {
   switch (d.dstate) {
-    case 16: return pick_bwd_n<T, 16>(which, d.headdim);
-    case 32: return pick_bwd_n<T, 32>(which, d.headdim);
-    case 64: return pick_bwd_n<T, 64>(which, d.headdim);
-    case 128: return pick_bwd_n<T, 128>(which, d.headdim);
-    default: return pick_bwd_n<T, 256>(which, d.headdim);
+    case 16: return pick_bwd_n<T, 16>(which, d);
+    case 32: return pick_bwd_n<T, 32>(which, d);
+    case 64: return pick_bwd_n<T, 64>(which, d);
+    case 128: return pick_bwd_n<T, 128>(which, d);
+    default: return pick_bwd_n<T, 256>(which, d);
   }
 }
 
