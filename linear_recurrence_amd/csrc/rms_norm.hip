@@ -401,7 +401,8 @@ __global__ void __launch_bounds__(256) norm_bwd_join_kernel(const NormArgs a) {
 struct NormShape {
   int threads, vecs;
 };
-static NormShape norm_shape(int nvec, bool backward) {
+static NormShape norm_shape(int nvec, bool backward, int rows = 1 << 30) {
+  if (!backward && rows <= 256 && nvec > 256 && nvec <= 1024) return {1024, 1};
   if (nvec <= 64) return {64, 1};
   if (nvec <= 128) return {64, 2};
   if (nvec <= 256) return {256, 1};
@@ -512,8 +513,11 @@ extern "C" int rms_norm_forward(const rssm_norm_dims* dims, const void* x, const
   a.res_out = residual_out;
   a.out = out;
   a.scale = scale;
-  const NormShape sh = norm_shape(a.nvec, false);
+  const NormShape sh = norm_shape(a.nvec, false, a.rows);
   const void* fn = f32 ? pick_norm_fwd_kernel<float>(sh) : pick_norm_fwd_kernel<bf16>(sh);
+  if (norm_is<1024, 1>(sh))
+    fn = f32 ? reinterpret_cast<const void*>(&norm_fwd_kernel<float, 1024, 1>)
+             : reinterpret_cast<const void*>(&norm_fwd_kernel<bf16, 1024, 1>);
   return launch_kernel(fn, (unsigned)a.rows, (unsigned)sh.threads, norm_lds(a), stream, a);
 }
 

@@ -167,11 +167,6 @@ struct Split {
     for (int k = TERMS - 1; k >= 0; --k) c = Mat<T>::mma(t[k], o, c);
     return c;
   }
-  __device__ inline f32x4 b_times(const typename Mat<T>::Frag& o, f32x4 c) const {
-#pragma unroll
-    for (int k = TERMS - 1; k >= 0; --k) c = Mat<T>::mma(o, t[k], c);
-    return c;
-  }
 };
 
 // One row of 16-byte loads from a strided matrix into an LDS tile of kQ rows,
@@ -424,11 +419,23 @@ __device__ static inline void rank_update(f32x4 (&acc)[NT][2], const typename Ma
       }
       xs[p].set(f);
     }
+    // two column tiles at a time, the terms outside: four products in a row that
+    // do not wait for each other
+    constexpr int U = NT < 2 ? 1 : 2;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const typename M::Frag y = M::cols(cols_at<T, false>(Y, LN, 32 * kb, 16 * n, lane), LN);
+    for (int n = 0; n < NT; n += U) {
+      typename M::Frag y[U];
 #pragma unroll
-      for (int p = 0; p < 2; ++p) acc[n][p] = ROWS ? xs[p].a_times(y, acc[n][p]) : xs[p].b_times(y, acc[n][p]);
+      for (int q = 0; q < U; ++q)
+        y[q] = M::cols(cols_at<T, false>(Y, LN, 32 * kb, 16 * (n + q), lane), LN);
+#pragma unroll
+      for (int k = M::kTerms - 1; k >= 0; --k)
+#pragma unroll
+        for (int q = 0; q < U; ++q)
+#pragma unroll
+          for (int p = 0; p < 2; ++p)
+            acc[n + q][p] = ROWS ? M::mma(xs[p].t[k], y[q], acc[n + q][p])
+                                 : M::mma(y[q], xs[p].t[k], acc[n + q][p]);
     }
   }
 }

@@ -546,18 +546,31 @@ __global__ void __launch_bounds__(256) scan_combine_kernel(const ScanArgs a) {
   if (pool >= 0 && (!a.has_init || a.has_init[i]))
     S = load_state4(a.init, ((long)pool * a.vheads + v) * elems + e, a.state_bf16);
   const long base = seg_base(a.cu, i, a.seg, a.tokens);
-  for (int k = 0; k < segs; ++k) {
-    const long at = (base + k) * a.vheads + v;
-    f32x4* const p = reinterpret_cast<f32x4*>(a.seg_state + at * elems + e);
-    f32x4 own = {0.f, 0.f, 0.f, 0.f};
-    float d = 0.f;
-    if (k + 1 < segs) {
-      own = *p;
-      d = exp2_f32(a.seg_decay[at]);
-    }
-    *p = S;
+  // eight segments' loads at a time: one after another they would take a
+  // memory latency each
+  constexpr int U = 8;
+  for (int k0 = 0; k0 < segs; k0 += U) {
+    f32x4 own[U];
+    float d[U];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) S[r] = fmaf(d, S[r], own[r]);
+    for (int q = 0; q < U; ++q) {
+      const int k = k0 + q;
+      own[q] = f32x4{0.f, 0.f, 0.f, 0.f};
+      d[q] = 0.f;
+      if (k + 1 < segs) {
+        const long at = (base + k) * a.vheads + v;
+        own[q] = *reinterpret_cast<const f32x4*>(a.seg_state + at * elems + e);
+        d[q] = a.seg_decay[at];
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < U; ++q) {
+      if (k0 + q >= segs) break;
+      *reinterpret_cast<f32x4*>(a.seg_state + ((base + k0 + q) * a.vheads + v) * elems + e) = S;
+      const float w = exp2_f32(d[q]);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) S[r] = fmaf(w, S[r], own[q][r]);
+    }
   }
 }
 
@@ -688,11 +701,12 @@ extern "C" int ssu_scan_forward(const rssm_scan_dims* dims, const void* x, const
   a.seg = scan_seg(d);
   const long cslots = scan_slots(d.tokens, d.seqs, kQ);
   // Units of a workgroup of the output launch: up to four a wave, which share
-  // the chunk's C.B, but so few that there are two workgroups for each of the
-  // 512 places.
+  // the chunk's C.B, but so few that there is a workgroup for every compute unit.
+  // 4096 tokens of 80 heads: 16 units 118 us, 8 127; 16383: 16 units 452 us, 8
+  // 456, 32 472.
   a.upg = d.nheads / d.ngroups * (d.headdim == 32 ? 1 : d.headdim / 64);
   a.upb = 16;
-  while (a.upb > 4 && cslots * d.ngroups * ((a.upg + a.upb - 1) / a.upb) < 1024) a.upb >>= 1;
+  while (a.upb > 4 && cslots * d.ngroups * ((a.upg + a.upb - 1) / a.upb) < 256) a.upb >>= 1;
   a.hb = (a.upg + a.upb - 1) / a.upb;
   const long dgrid = cslots * ((d.nheads + 3) / 4);
   const long sgrid = scan_slots(d.tokens, d.seqs, a.seg) * d.ngroups * ((a.vpg + 3) / 4);

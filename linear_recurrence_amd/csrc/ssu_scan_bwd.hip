@@ -243,19 +243,29 @@ __global__ void __launch_bounds__(256) scan_combine_both_kernel(const ScanBwdArg
   float* const part = grad ? b.seg_grad : a.seg_state;
   const float* const dec = grad ? b.grad_decay : a.seg_decay;
   const long base = seg_base(a.cu, i, a.seg, a.tokens);
-  for (int q = 0; q < segs; ++q) {
-    const int k = grad ? segs - 1 - q : q;
-    const long at = (base + k) * a.vheads + v;
-    f32x4* const p = reinterpret_cast<f32x4*>(part + at * elems + e);
-    f32x4 own = {0.f, 0.f, 0.f, 0.f};
-    float d = 0.f;
-    if (q + 1 < segs) {
-      own = *p;
-      d = exp2_f32(dec[at]);
-    }
-    *p = g;
+  constexpr int U = 8;  // loads in flight: one after another would take a memory latency each
+  for (int q0 = 0; q0 < segs; q0 += U) {
+    f32x4 own[U];
+    float d[U];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) g[r] = fmaf(d, g[r], own[r]);
+    for (int q = 0; q < U; ++q) {
+      own[q] = f32x4{0.f, 0.f, 0.f, 0.f};
+      d[q] = 0.f;
+      if (q0 + q + 1 < segs) {
+        const long at = (base + (grad ? segs - 1 - q0 - q : q0 + q)) * a.vheads + v;
+        own[q] = *reinterpret_cast<const f32x4*>(part + at * elems + e);
+        d[q] = dec[at];
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < U; ++q) {
+      if (q0 + q >= segs) break;
+      const long at = (base + (grad ? segs - 1 - q0 - q : q0 + q)) * a.vheads + v;
+      *reinterpret_cast<f32x4*>(part + at * elems + e) = g;
+      const float w = exp2_f32(d[q]);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) g[r] = fmaf(w, g[r], own[q][r]);
+    }
   }
 }
 
