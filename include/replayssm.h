@@ -582,8 +582,9 @@ typedef struct rssm_norm_dims {
  *     u = h * z * sigmoid(z)    (z NULL: u = h)
  *     y = u * rsqrt(mean over the group of u^2 + eps) * weight
  *   out = y in io_dtype, or the e4m3 values of y / scale with scale =
- *   max|y| / 448 over the row or block (1 where that is 0): scale [rows] or
- *   [rows, dim/128] float32.  residual_out may be residual.
+ *   max|y| / 448 over the row or block (1 where that is 0, and at least the
+ *   smallest normal number): scale [rows] or [rows, dim/128] float32.
+ *   residual_out may be residual.
  */
 int rms_norm_forward(const rssm_norm_dims* dims, const void* x, const float* weight,
                      const void* z, const void* residual, void* residual_out,
@@ -633,7 +634,10 @@ typedef struct rssm_scan_dims {
  *     y *= z * sigmoid(z)    (z not NULL)
  * and final_state[s, h] = S (final_state may be initial_state, or NULL).
  * y [tokens, H, P] io_dtype.  A slot out of range sets RSSM_ST_BAD_SLOT: its
- * sequence starts from zeros and stores no state.
+ * sequence starts from zeros and stores no state.  Tokens are worked on in
+ * chunks of 64 of one sequence: a NaN or infinity in a token's x may also show
+ * in the up to 63 tokens of its sequence and chunk before it, and never in
+ * another sequence.  Calls of up to 256 tokens need no workspace.
  */
 size_t ssu_scan_forward_workspace(const rssm_scan_dims* dims);
 int ssu_scan_forward(const rssm_scan_dims* dims, const void* x, const void* dt, const float* A,

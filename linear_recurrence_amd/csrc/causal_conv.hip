@@ -6,7 +6,9 @@
 // Channels are contiguous, so a lane owns eight of them (16 bytes of bf16) and
 // walks along the tokens with the window in registers: every x row is read
 // once per run of tokens, plus W-1 rows where a run starts.  All of it is
-// memory bound (2 W flops per 4 bytes).
+// memory bound (2 W flops per 4 bytes).  5376 channels, W 4, bf16: 16383 tokens
+// forward 76 us (0.35 GB, 4.6 TB/s), 16384 backward 129 us (0.53 GB, 4.1 TB/s),
+// 512 decode rows 11 us (44 MB, 4.0 TB/s).
 #include "rssm_host.hpp"
 #include "seq_device.hpp"
 
@@ -633,7 +635,8 @@ extern "C" int causal_conv_decode(const rssm_conv_dims* dims, const void* x,
   a.final_state = new_state;
   a.y = y;
   a.status = status;
-  // several rows a wave where that still leaves one for every SIMD
+  // several rows a wave where that still leaves one for every SIMD (512 rows of
+  // 5376 channels: 11 us with four, 26 with one and element-wise weight loads)
   const long cblocks = (d.channels + 511) / 512;
   const int rows = d.tokens * cblocks >= 1024 * kStepRows ? kStepRows : 1;
   const bool f32 = d.io_dtype == RSSM_F32;

@@ -9,7 +9,8 @@
 // to 32 elements a lane), so each input is read once.  The row is cut into
 // vectors of eight elements that never cross a group's border (a group's last
 // vector may be shorter), so any length and any start works with the same
-// 16-byte loads.
+// 16-byte loads.  16383 rows of 2560 with an fp32 residual and e4m3 output 88 us
+// (0.46 GB, 5.2 TB/s); 8192 gated rows of 8192 backward 164 us (0.67 GB, 4.1 TB/s).
 #include "rssm_host.hpp"
 #include "seq_device.hpp"
 
@@ -402,6 +403,8 @@ struct NormShape {
   int threads, vecs;
 };
 static NormShape norm_shape(int nvec, bool backward, int rows = 1 << 30) {
+  // at most one row a compute unit: all of it at once (64 rows of 5120: 6.5 us
+  // instead of 8.8)
   if (!backward && rows <= 256 && nvec > 256 && nvec <= 1024) return {1024, 1};
   if (nvec <= 64) return {64, 1};
   if (nvec <= 128) return {64, 2};

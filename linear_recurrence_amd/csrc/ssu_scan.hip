@@ -22,7 +22,7 @@ constexpr int scan_waves(bool f32, int n) { return f32 && n == 256 ? 2 : 4; }
 
 // A short call in one launch: y and the final states, a wave for 32 rows of one
 // head's state and one sequence.  Two workgroups a compute unit: 256 registers a
-// lane.
+// lane.  61 fp32 tokens of 8 heads (dstate 16): 13 us, a serial chain.
 template <typename T, int N>
 __global__ void __launch_bounds__(64 * scan_waves(sizeof(typename Mat<T>::E) == 4, N),
                                   sizeof(typename Mat<T>::E) == 4 ? 1 : 2)
@@ -220,6 +220,8 @@ __global__ void __launch_bounds__(64 * scan_waves(sizeof(typename Mat<T>::E) == 
 // D) and the final one in its pool; otherwise from zero, leaving what the
 // segment adds.  The next chunk's tiles are on their way while one is worked on.
 // Slots without a segment lie in runs, so blocks go to the dies in turn.
+// 16383 tokens of 80 heads: 171 us storing (0.5 GB: 2.9 TB/s), 109 us not; the
+// vector unit's splitting of w x into three bf16 terms is the largest part.
 template <typename T, int N, bool STORE>
 __global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 1 : (N == 256 ? 2 : 3))
     scan_fwd_states_kernel(const ScanArgs a) {
@@ -361,7 +363,8 @@ __global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 1 : (N 
 // The outputs of one chunk.  C and the tiles of C.B, the same for all heads of
 // the group, are in LDS; each wave then works alone, a unit (PB state rows of one
 // head) at a time, without a barrier: the waves are at different points, and one's
-// loads pass behind the others' products.
+// loads pass behind the others' products.  16383 tokens of 80 heads: 168 us, 0.67 GB
+// (4.0 TB/s), half of it the states.
 template <typename T, int N, int PB>
 __global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 1 : 2)
     scan_fwd_out_kernel(const ScanArgs a) {
@@ -574,7 +577,8 @@ __global__ void __launch_bounds__(256) scan_combine_kernel(const ScanArgs a) {
   }
 }
 
-// Calls of up to this many tokens take one launch.
+// Calls of up to this many tokens take one launch: four chunks' chain at most,
+// where the other way is three launches (17 us of launches and latency) or five.
 constexpr int kShort = 256;
 
 // Tokens of a segment: enough segments to give every one of the 1024 SIMDs two

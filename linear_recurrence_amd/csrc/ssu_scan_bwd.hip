@@ -71,7 +71,9 @@ __device__ static inline long row_at(int nt, int pt, int r, int lane) {
 // the workspace (and the gradient of the initial state); otherwise from zero,
 // leaving what the segment adds.  The next chunk's tiles are on their way while
 // one is worked on; three workgroups a compute unit (two with 256 columns).
-// Slots without a segment lie in runs, so blocks go to the dies in turn.
+// Slots without a segment lie in runs, so blocks go to the dies in turn (in
+// contiguous ranges one die had twice the others': 484 us instead of 365 for
+// 8 x 2048 tokens of 80 heads, which write 1.34 GB).
 template <typename T, int N, bool STORE>
 __global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 1 : (N == 256 ? 2 : 3))
     scan_states_kernel(const ScanBwdArgs b) {
