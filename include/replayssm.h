@@ -637,7 +637,7 @@ typedef struct rssm_scan_dims {
  * sequence starts from zeros and stores no state.  Tokens are worked on in
  * chunks of 64 of one sequence: a NaN or infinity in a token's x may also show
  * in the up to 63 tokens of its sequence and chunk before it, and never in
- * another sequence.  Calls of up to 256 tokens need no workspace.
+ * another sequence.  Calls of up to 128 tokens need no workspace.
  */
 size_t ssu_scan_forward_workspace(const rssm_scan_dims* dims);
 int ssu_scan_forward(const rssm_scan_dims* dims, const void* x, const void* dt, const float* A,

@@ -577,9 +577,10 @@ __global__ void __launch_bounds__(256) scan_combine_kernel(const ScanArgs a) {
   }
 }
 
-// Calls of up to this many tokens take one launch: four chunks' chain at most,
-// where the other way is three launches (17 us of launches and latency) or five.
-constexpr int kShort = 256;
+// Calls of up to this many tokens take one launch, a chain of two chunks at most;
+// the other way is three launches.  One bf16 sequence, 80 heads, dstate 128: 128
+// tokens 22 us (26 the other way), 256 35 us (33), 512 61 us (56).
+constexpr int kShort = 128;
 
 // Tokens of a segment: enough segments to give every one of the 1024 SIMDs two
 // waves, but no shorter than four chunks (a segment's state crosses memory
