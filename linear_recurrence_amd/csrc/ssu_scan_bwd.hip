@@ -331,8 +331,8 @@ static inline int bwd_rows(const rssm_scan_dims& d) {
 }
 
 // One chunk, the units of one block.  A wave owns N/W state columns (16 at 128;
-// with 32, 157 registers were spilled and the launch took 1195 us instead of
-// 771): it holds dB and dC of all 64 tokens there in registers and adds every
+// with 32, 157 registers were spilled and the launch took 1195 us instead of 771
+// at the time): it holds dB and dC of all 64 tokens there in registers and adds every
 // head's to them,
 // so the heads are joined without leaving the workgroup.  The products of the
 // chunk's tokens with each other (dy.x, the decays, C.B, which is the same for
@@ -483,6 +483,14 @@ __global__ void __launch_bounds__(64 * bwd_waves(sizeof(typename Mat<T>::E) == 4
     for (int q = 0; q < NW; ++q)
 #pragma unroll
       for (int j = 0; j < 4; ++j) forget(rc[q][j]);
+    // The states' first column tile is on its way during the tokens' products.
+    // Unconditional from 64 columns on: behind a condition these loads could not
+    // be told from the x and dy in flight, whose wait then took them in (1165 us
+    // instead of 1088 for 8 x 2048 tokens of 80 heads).
+    if (NT >= W || wave * NW < NT) {
+      load(ls, a.chunk_state, u, wave * NW);
+      load(lg, b.grad_state, u, wave * NW);
+    }
 #pragma unroll
     for (int q = 0; q < QX; ++q) {
       const int e = q * TH + (int)threadIdx.x, o = (e / PX) * LX + (e % PX) * V;
@@ -493,12 +501,6 @@ __global__ void __launch_bounds__(64 * bwd_waves(sizeof(typename Mat<T>::E) == 4
     if (wave == 0) sQ[lane] = rq;
     __syncthreads();
     if (u + 1 < u1) fetch(u + 1);
-    // the states' first column tile is on its way during the tokens' products
-    if (wave * NW < NT) {
-      load(ls, a.chunk_state, u, wave * NW);
-      load(lg, b.grad_state, u, wave * NW);
-    }
-
     // ---- the tokens' products with each other
 #pragma unroll
     for (int q = 0; q < KT; ++q) {
