@@ -167,6 +167,12 @@ struct Split {
     for (int k = TERMS - 1; k >= 0; --k) c = Mat<T>::mma(t[k], o, c);
     return c;
   }
+  // other * this (this one the B operand)
+  __device__ inline f32x4 b_times(const typename Mat<T>::Frag& o, f32x4 c) const {
+#pragma unroll
+    for (int k = TERMS - 1; k >= 0; --k) c = Mat<T>::mma(o, t[k], c);
+    return c;
+  }
 };
 
 // One row of 16-byte loads from a strided matrix into an LDS tile of kQ rows,
@@ -277,7 +283,7 @@ struct ScanArgs {
   float* seg_state;  // [slots][V][32][N]
   float* seg_decay;  // [slots][V], log2
   f32x4* dec;        // [chunk slots][H][64]: sum of dt A (log2; high, low), dt, dt before softplus
-  void* chunk_state; // [chunk slots][V][32 N]: forward: operands in the io type; backward: S_in, fp32
+  void* chunk_state; // [chunk slots][V][32 N], fp32: the state before the chunk
   int32_t* status;
   long x_stride, dt_stride, B_stride, C_stride, z_stride;
   int32_t tokens, seqs, nheads, headdim, dstate, ngroups, num_slots, state_bf16, dt_softplus;

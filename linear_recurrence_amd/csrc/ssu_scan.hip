@@ -3,15 +3,17 @@
 //
 // Long calls: (1) dt and the decays' running sums of every chunk and head; (2)
 // the recurrence over the chunks, a wave for 32 rows of one head's state, which
-// leaves the state before every chunk in the workspace, as operands of the next
-// launch (with two launches in front where sequences are longer than a segment:
-// what each segment adds from zero, then their running combination); (3) the
-// outputs, a workgroup for one chunk and several heads.
+// leaves the state before every chunk in the workspace, in fp32 (with two
+// launches in front where sequences are longer than a segment: what each segment
+// adds from zero, then their running combination); (3) the outputs, a workgroup
+// for one chunk and several heads.
 // Short calls (up to kShort tokens) are one launch, in which a wave walks a
 // sequence's chunks with the state in registers.
 //
-// The state enters y rounded to the io type: y is rounded to it too, and D x
-// usually outweighs it.
+// Both factors of y that are fp32, the state and dt e^{a_t-a_s} C_t.B_s, enter
+// its products as three bf16 terms (fp32 inputs: as they are), so nothing is
+// rounded to the io type but y itself.  One term would take y's error without D
+// from 1.0 to 1.4 times that of rounding y.
 #include "scan_common.hpp"
 
 namespace rssm {
@@ -113,7 +115,7 @@ __global__ void __launch_bounds__(64 * scan_waves(sizeof(typename Mat<T>::E) == 
       // e^{a_t} S C_t
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb) {
-        Frag sf[2];
+        Split<T, M::kTerms> sf[2];
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
           float f[8];
@@ -122,13 +124,13 @@ __global__ void __launch_bounds__(64 * scan_waves(sizeof(typename Mat<T>::E) == 
             f[r] = S[2 * kb][p][r];
             f[4 + r] = 2 * kb + 1 < NT ? S[2 * kb + 1 < NT ? 2 * kb + 1 : 0][p][r] : 0.f;
           }
-          sf[p] = M::pack(f);
+          sf[p].set(f);
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const Frag c = M::rows_d(sC + (16 * j + i16) * LN + 32 * kb + 4 * g);
 #pragma unroll
-          for (int p = 0; p < 2; ++p) Y[j][p] = M::mma(sf[p], c, Y[j][p]);
+          for (int p = 0; p < 2; ++p) Y[j][p] = sf[p].a_times(c, Y[j][p]);
         }
       }
       float2 at[4];
@@ -166,9 +168,11 @@ __global__ void __launch_bounds__(64 * scan_waves(sizeof(typename Mat<T>::E) == 
               w[4 * q2 + r] = i < j || 4 * g + r <= i16 ? m : 0.f;
             }
           }
-          const Frag wf = M::pack(w);
+          Split<T, M::kTerms> wf;
+          wf.set(w);
 #pragma unroll
-          for (int p = 0; p < 2; ++p) Y[j][p] = M::mma(xf[p], wf, Y[j][p]);
+          for (int p = 0; p < 2; ++p) Y[j][p] = wf.b_times(xf[p], Y[j][p]);
+          keep_order();
         }
       }
       // D x, the gate, and 8 neighbours of token t to memory
@@ -216,20 +220,18 @@ __global__ void __launch_bounds__(64 * scan_waves(sizeof(typename Mat<T>::E) == 
 }
 
 // The recurrence over the chunks of a segment.  STORE: from the state it starts
-// from, leaving the state before every chunk as operands (rows p, k = n in order
-// D) and the final one in its pool; otherwise from zero, leaving what the
-// segment adds.  The next chunk's tiles are on their way while one is worked on.
+// from, leaving the state before every chunk (the tiles as the lanes hold them)
+// and the final one in its pool; otherwise from zero, leaving what the segment
+// adds.  The next chunk's tiles are on their way while one is worked on.
 // Slots without a segment lie in runs, so blocks go to the dies in turn.
-// 16383 tokens of 80 heads: 171 us storing (0.5 GB: 2.9 TB/s), 109 us not; the
-// vector unit's splitting of w x into three bf16 terms is the largest part.
+// 16383 tokens of 80 heads: 219 us storing (0.84 GB: 3.8 TB/s), 110 us not.
 template <typename T, int N, bool STORE>
 __global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 1 : (N == 256 ? 2 : 3))
     scan_fwd_states_kernel(const ScanArgs a) {
   typedef Mat<T> M;
   typedef typename M::E E;
-  typedef typename M::Frag Frag;
   constexpr int W = 4, TH = 64 * W, V = 16 / sizeof(E);
-  constexpr int NP = N < 32 ? 32 : N, LN = NP + M::kPad, LX = kPT + M::kPad, NT = N / 16, KB = NP / 32;
+  constexpr int NP = N < 32 ? 32 : N, LN = NP + M::kPad, LX = kPT + M::kPad, NT = N / 16;
   constexpr int PN = N / V, QN = (kQ * PN + TH - 1) / TH;  // 16-byte pieces of a row, a thread's
   constexpr int PX = kPT / V, QX = kQ * PX / 64;
   __shared__ __attribute__((aligned(16))) E sB[kQ * LN];
@@ -301,19 +303,11 @@ __global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 1 : (N 
     lane = tid & 63;
     const int rows = sg.len - c * kQ < kQ ? sg.len - c * kQ : kQ;
     if (STORE && live) {
-      Frag* dst = static_cast<Frag*>(a.chunk_state) + ((cbase + c) * a.vheads + v) * (KB * 2 * 64) + lane;
+      f32x4* dst = static_cast<f32x4*>(a.chunk_state) + ((cbase + c) * a.vheads + v) * (NT * 2 * 64) + lane;
 #pragma unroll
-      for (int kb = 0; kb < KB; ++kb)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          float f[8];
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            f[r] = S[2 * kb][p][r];
-            f[4 + r] = 2 * kb + 1 < NT ? S[2 * kb + 1 < NT ? 2 * kb + 1 : 0][p][r] : 0.f;
-          }
-          dst[(kb * 2 + p) * 64] = M::pack(f);
-        }
+        for (int p = 0; p < 2; ++p) dst[(n * 2 + p) * 64] = S[n][p];
     }
     if (STORE && c + 1 == chunks && !(sg.last && a.final_state)) break;  // the end is not read
     __syncthreads();  // the previous chunk's tiles are no longer read
@@ -363,8 +357,8 @@ __global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 1 : (N 
 // The outputs of one chunk.  C and the tiles of C.B, the same for all heads of
 // the group, are in LDS; each wave then works alone, a unit (PB state rows of one
 // head) at a time, without a barrier: the waves are at different points, and one's
-// loads pass behind the others' products.  16383 tokens of 80 heads: 168 us, 0.67 GB
-// (4.0 TB/s), half of it the states.
+// loads pass behind the others' products.  16383 tokens of 80 heads: 283 us, 1.0 GB
+// (3.6 TB/s), two thirds of it the states.
 template <typename T, int N, int PB>
 __global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 1 : 2)
     scan_fwd_out_kernel(const ScanArgs a) {
@@ -372,7 +366,8 @@ __global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 1 : 2)
   typedef typename M::E E;
   typedef typename M::Frag Frag;
   constexpr int W = 4, TH = 64 * W, V = 16 / sizeof(E);
-  constexpr int NP = N < 32 ? 32 : N, LN = NP + M::kPad, LX = PB + M::kPad, KB = NP / 32, SL = PB / 32;
+  constexpr int NP = N < 32 ? 32 : N, LN = NP + M::kPad, LX = PB + M::kPad;
+  constexpr int NT = N / 16, KB = NP / 32, SL = PB / 32;
   constexpr int PX = PB / V, QX = kQ * PX / 64;
   constexpr int kX = W * kQ * LX > kQ * LN ? W * kQ * LX : kQ * LN;
   __shared__ __attribute__((aligned(16))) E sC[kQ * LN];
@@ -431,22 +426,27 @@ __global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 1 : 2)
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int s = 0; s < SL; ++s) Y[j][s][0] = Y[j][s][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-    const Frag* const st = static_cast<const Frag*>(a.chunk_state) +
-        ((long)slot * a.vheads + (long)hu * SL) * (KB * 2 * 64) + lane;
+    const f32x4* const st = static_cast<const f32x4*>(a.chunk_state) +
+        ((long)slot * a.vheads + (long)hu * SL) * (NT * 2 * 64) + lane;
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb) {
-      Frag sf[SL][2];
+      Split<T, M::kTerms> sf[SL][2];
 #pragma unroll
       for (int s = 0; s < SL; ++s)
 #pragma unroll
-        for (int p = 0; p < 2; ++p) sf[s][p] = st[((s * KB + kb) * 2 + p) * 64];
+        for (int p = 0; p < 2; ++p) {
+          const f32x4 lo = st[((s * NT + 2 * kb) * 2 + p) * 64];
+          const f32x4 hi = 2 * kb + 1 < NT ? st[((s * NT + 2 * kb + 1) * 2 + p) * 64] : f32x4{0.f, 0.f, 0.f, 0.f};
+          const float f[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+          sf[s][p].set(f);
+        }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const Frag c = M::rows_d(sC + (16 * j + i16) * LN + 32 * kb + 4 * g);
 #pragma unroll
         for (int s = 0; s < SL; ++s)
 #pragma unroll
-          for (int p = 0; p < 2; ++p) Y[j][s][p] = M::mma(sf[s][p], c, Y[j][s][p]);
+          for (int p = 0; p < 2; ++p) Y[j][s][p] = sf[s][p].a_times(c, Y[j][s][p]);
       }
     }
 #pragma unroll
@@ -493,11 +493,12 @@ __global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 1 : 2)
             w[4 * q2 + r] = i < j || 4 * g + r <= i16 ? m : 0.f;
           }
         }
-        const Frag wf = M::pack(w);
+        Split<T, M::kTerms> wf;
+        wf.set(w);
 #pragma unroll
         for (int s = 0; s < SL; ++s)
 #pragma unroll
-          for (int p = 0; p < 2; ++p) Y[j][s][p] = M::mma(xf[s][p], wf, Y[j][s][p]);
+          for (int p = 0; p < 2; ++p) Y[j][s][p] = wf.b_times(xf[s][p], Y[j][s][p]);
         keep_order();
       }
     }
@@ -602,7 +603,7 @@ static FwdLayout fwd_layout(const rssm_scan_dims& d) {
   FwdLayout l{};
   if (d.tokens <= kShort) return l;
   const size_t T = d.tokens, n = d.seqs, seg = scan_seg(d), cslots = T / kQ + n, slots = T / seg + n;
-  const size_t V = (size_t)d.nheads * (d.headdim / kPT), np = d.dstate < 32 ? 32 : d.dstate;
+  const size_t V = (size_t)d.nheads * (d.headdim / kPT);
   size_t at = 0;
   const auto take = [&](size_t bytes) {
     const size_t p = at;
@@ -610,7 +611,7 @@ static FwdLayout fwd_layout(const rssm_scan_dims& d) {
     return p;
   };
   l.dec = take(cslots * d.nheads * kQ * 16);
-  l.chunk_state = take(cslots * V * kPT * np * (d.io_dtype == RSSM_F32 ? 4 : 2));
+  l.chunk_state = take(cslots * V * kPT * d.dstate * 4);
   l.seg_state = take(T > seg ? slots * V * kPT * d.dstate * 4 : 0);
   l.seg_decay = take(T > seg ? slots * V * 4 : 0);
   l.end = at;
