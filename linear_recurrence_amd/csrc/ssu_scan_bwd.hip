@@ -25,12 +25,12 @@
 // workgroup for one chunk and several heads of one group, which needs nothing
 // from other chunks; (4) the sums over workgroups, in a fixed order.
 //
-// Everything that reaches an fp32 output (dA, ddt_bias, dinitial_state, and
-// ddt through dalpha) takes its state products with the state as three bf16
-// terms.  What only reaches an output in the io type rounds one factor: dS and
-// e^{a_u-a_t} C_u.B_t (dx, where D dy usually outweighs them) once, to the io
-// type; K (dB, dC, sums over heads in which nothing outweighs it) to two terms:
-// one would take their error from 1.0 to 1.4 times that of rounding the result.
+// Every factor that is not an input (S_in, dS, K and e^{a_u-a_t} C_u.B_t) enters
+// its products as three bf16 terms (fp32 inputs: as it is), so nothing is rounded
+// to the io type but the results.  Two terms would be 5% faster (8 x 2048 tokens of
+// 80 heads 1156 us instead of 1240) and leave three times the fp32 sums' own
+// error in dB and dC; one would take dx's error without D to 1.4 times that of
+// rounding it.
 #include "scan_common.hpp"
 
 namespace rssm {
@@ -331,13 +331,11 @@ static inline int bwd_rows(const rssm_scan_dims& d) {
 }
 
 // One chunk, the units of one block.  A wave owns N/W state columns (16 at 128;
-// with 32, 157 registers were spilled and the launch took 1195 us instead of 771
-// at the time): it holds dB and dC of all 64 tokens there in registers and adds every
-// head's to them,
-// so the heads are joined without leaving the workgroup.  The products of the
-// chunk's tokens with each other (dy.x, the decays, C.B, which is the same for
-// all heads) are shared: each wave works out some of the ten 16x16 tiles on and
-// below the diagonal and leaves them in LDS.
+// with 32, 157 registers were spilled): it holds dB and dC of all 64 tokens there in
+// registers and adds every head's to them, so the heads are joined without leaving
+// the workgroup.  The products of the chunk's tokens with each other (dy.x, the
+// decays, C.B, which is the same for all heads) are shared: each wave works out
+// some of the ten 16x16 tiles on and below the diagonal and leaves them in LDS.
 template <typename T, int N, int PB>
 __global__ void __launch_bounds__(64 * bwd_waves(sizeof(typename Mat<T>::E) == 4, N),
                                   sizeof(typename Mat<T>::E) == 4 ? 1 : 2)
@@ -350,11 +348,17 @@ __global__ void __launch_bounds__(64 * bwd_waves(sizeof(typename Mat<T>::E) == 4
   constexpr int NT = N / 16, NW = NT < W ? 1 : NT / W, KB = NP / 32, SL = PB / 32;
   constexpr int PX = PB / V, QX = (kQ * PX + TH - 1) / TH;
   constexpr int kXY = kQ * LX, kMM = kQ * LM, kS = NP * LX;
-  constexpr int T2 = M::kTerms == 1 ? 1 : 2;  // terms of K
-  constexpr int kWork = 2 * kXY + (1 + T2) * kMM + kS;
+  constexpr int TK = M::kTerms;
+  // bf16 with 64 columns: dS's terms take K's place, at the price of a barrier, since
+  // beside it they would leave room for one workgroup a compute unit instead of
+  // two (8 x 2048 tokens of 80 heads: 819 us instead of 1083).
+  constexpr bool kOver = sizeof(E) == 2 && N == 64 && PB == 64;
+  static_assert(!kOver || (NW == 1 && NT == W && kS <= kMM), "each wave keeps its tile until K is read");
+  constexpr int kWork = 2 * kXY + TK * (kOver ? kMM : kMM + kS);
   static_assert(kWork >= kQ * LN, "C's tile fits where the units work");
   __shared__ __attribute__((aligned(16))) E sB[kQ * LN];
   __shared__ __attribute__((aligned(16))) E work[kWork];
+  __shared__ f32x4 sCB[10][64];     // C_u.B_t by tiles
   __shared__ f32x4 sQ[kQ];
   __shared__ float sR[kQ][4];       // w: a row's sum over each earlier tile
   __shared__ float sS[4][kQ];       // w / dt: a column's sum over each later tile
@@ -363,9 +367,8 @@ __global__ void __launch_bounds__(64 * bwd_waves(sizeof(typename Mat<T>::E) == 4
   E* const sC = work;               // at the start only
   E* const sX = work;
   E* const sY = work + kXY;
-  E* const sM = work + 2 * kXY;     // [t][u]: e^{a_u-a_t} C_u.B_t
-  E* const sK = sM + kMM;           // [t][u]: K_ut, then its second term
-  E* const sG = sK + T2 * kMM;      // [n][p]: dS
+  E* const sK = work + 2 * kXY;     // [t][u]: K_ut's terms, one after another
+  E* const sG = kOver ? sK : sK + TK * kMM;  // [n][p]: dS's terms
 
   const ScanArgs& a = b.f;
   const int lane0 = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -406,6 +409,7 @@ __global__ void __launch_bounds__(64 * bwd_waves(sizeof(typename Mat<T>::E) == 4
       for (int kb = 0; kb < KB; ++kb)
         cb[q] = M::mma(M::rows_c(sC + (16 * iu + i16) * LN + 32 * kb + 8 * g),
                        M::rows_c(sB + (16 * j + i16) * LN + 32 * kb + 8 * g), cb[q]);
+      sCB[k][lane] = cb[q];
     }
   }
   // this wave's columns of C as operands (rows n, k tokens) and C's values
@@ -432,14 +436,18 @@ __global__ void __launch_bounds__(64 * bwd_waves(sizeof(typename Mat<T>::E) == 4
     for (int j = 0; j < 4; ++j) aB[q][j] = aC[q][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   __syncthreads();  // C's tile is no longer read
   // tiles (u, t) = (0, 1) and (2, 3), above the diagonal, are read as zeros
-  for (int e = threadIdx.x; e < 512; e += TH) {
-    const int o = (16 + ((e >> 8) << 5) + ((e >> 4) & 15)) * LM + ((e >> 8) << 5) + (e & 15);
-    Elt<T>::store1(sM, o, 0.f);
-    Elt<T>::store1(sK, o, 0.f);
-    if (T2 == 2) Elt<T>::store1(sK + kMM, o, 0.f);
-  }
+  const auto clear = [&]() {
+    for (int e = threadIdx.x; e < TK * 128; e += TH) {
+      const int at = ((e >> 6) & 1) * 32, row = 16 + at + ((e >> 2) & 15);
+      *reinterpret_cast<typename M::Four*>(sK + (e >> 7) * kMM + row * LM + at + 4 * (e & 3)) =
+          typename M::Four{0, 0};
+    }
+  };
+  if (!kOver) clear();
   if (N < NP)
-    for (int e = threadIdx.x; e < (NP - N) * LX; e += TH) Elt<T>::store1(sG, N * LX + e, 0.f);
+    for (int e = threadIdx.x; e < (NP - N) * LX; e += TH)
+#pragma unroll
+      for (int k = 0; k < TK; ++k) Elt<T>::store1(sG + k * kS, N * LX + e, 0.f);
 
   u32x4 rx[QX], ry[QX];
   f32x4 rq;
@@ -499,6 +507,7 @@ __global__ void __launch_bounds__(64 * bwd_waves(sizeof(typename Mat<T>::E) == 4
       *reinterpret_cast<u32x4*>(sY + o) = ry[q];
     }
     if (wave == 0) sQ[lane] = rq;
+    if (kOver) clear();  // dS's terms lay there
     __syncthreads();
     if (u + 1 < u1) fetch(u + 1);
     // ---- the tokens' products with each other
@@ -514,14 +523,13 @@ __global__ void __launch_bounds__(64 * bwd_waves(sizeof(typename Mat<T>::E) == 4
         d = M::mma(M::rows_c(sY + (16 * iu + i16) * LX + 32 * s + 8 * g),
                    M::rows_c(sX + t * LX + 32 * s + 8 * g), d);
       const f32x4 qt = sQ[t];
-      float m[4], kk[4], col = 0.f, rw[4], in = 0.f, dd = 0.f;
+      float kk[4], col = 0.f, rw[4], in = 0.f, dd = 0.f;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const float e = exp2_f32(gap2(sQ[uu + r], qt));
         const bool on = uu + r >= t;
-        m[r] = on ? e * cb[q][r] : 0.f;
         kk[r] = on ? e * d[r] * qt[2] : 0.f;
-        const float s = m[r] * d[r];
+        const float s = on ? e * cb[q][r] * d[r] : 0.f;
         col += s;
         rw[r] = s * qt[2];
         if (iu == j) {
@@ -531,15 +539,16 @@ __global__ void __launch_bounds__(64 * bwd_waves(sizeof(typename Mat<T>::E) == 4
           dd += uu + r == t ? d[r] : 0.f;
         }
       }
-      *reinterpret_cast<typename M::Four*>(sM + t * LM + uu) = M::pack4(m);
-      const typename M::Four k1 = M::pack4(kk);
-      *reinterpret_cast<typename M::Four*>(sK + t * LM + uu) = k1;
-      if constexpr (T2 == 2) {
-        float q1[4];
-        M::unpack4(k1, q1);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) kk[r] -= q1[r];
-        *reinterpret_cast<typename M::Four*>(sK + kMM + t * LM + uu) = M::pack4(kk);
+      for (int k = 0; k < TK; ++k) {
+        const typename M::Four k1 = M::pack4(kk);
+        *reinterpret_cast<typename M::Four*>(sK + k * kMM + t * LM + uu) = k1;
+        if (k + 1 < TK) {
+          float q1[4];
+          M::unpack4(k1, q1);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) kk[r] -= q1[r];
+        }
       }
       col = sum_g(col);
       if (iu == j) {
@@ -566,6 +575,7 @@ __global__ void __launch_bounds__(64 * bwd_waves(sizeof(typename Mat<T>::E) == 4
 
     // ---- dC, dB and the states' part of the decay's gradient
     const f32x4 qa = sQ[kQ - 1];
+    Split<T, TK> kept[SL];  // dS's terms, until they may be written
     if (wave * NW < NT) {
       float et[4], ft[4], dti[4], doti[4], dote[4], k0 = 0.f;
 #pragma unroll
@@ -579,7 +589,7 @@ __global__ void __launch_bounds__(64 * bwd_waves(sizeof(typename Mat<T>::E) == 4
 #pragma unroll
       for (int q = 0; q < NW; ++q) {
         const int nt = wave * NW + q;
-        Split<T, M::kTerms> hs[SL];
+        Split<T, TK> hs[SL];
         const auto split = [&](const f32x4 (&l)[SL][2]) {
 #pragma unroll
           for (int s = 0; s < SL; ++s) {
@@ -614,7 +624,7 @@ __global__ void __launch_bounds__(64 * bwd_waves(sizeof(typename Mat<T>::E) == 4
 #pragma unroll
           for (int kb = 0; kb <= j / 2; ++kb)
 #pragma unroll
-            for (int e = T2 - 1; e >= 0; --e)
+            for (int e = TK - 1; e >= 0; --e)
               aC[q][j] = M::mma(fb[kb], M::cols(cols_at<T, false>(sK + e * kMM, LM, 32 * kb, 16 * j, lane), LM),
                                 aC[q][j]);
           float cv[4];
@@ -628,9 +638,16 @@ __global__ void __launch_bounds__(64 * bwd_waves(sizeof(typename Mat<T>::E) == 4
         }
         split(lg);
         if (q + 1 < NW) load(lg, b.grad_state, u, nt + 1);
+        if constexpr (kOver) {
 #pragma unroll
-        for (int s = 0; s < SL; ++s)
-          *reinterpret_cast<Frag*>(sG + (16 * nt + i16) * LX + 32 * s + 8 * g) = hs[s].t[0];
+          for (int s = 0; s < SL; ++s) kept[s] = hs[s];
+        } else {
+#pragma unroll
+          for (int s = 0; s < SL; ++s)
+#pragma unroll
+            for (int k = 0; k < TK; ++k)
+              *reinterpret_cast<Frag*>(sG + k * kS + (16 * nt + i16) * LX + 32 * s + 8 * g) = hs[s].t[k];
+        }
         keep_order();
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -641,7 +658,7 @@ __global__ void __launch_bounds__(64 * bwd_waves(sizeof(typename Mat<T>::E) == 4
 #pragma unroll
           for (int kb = j / 2; kb < 2; ++kb)
 #pragma unroll
-            for (int e = T2 - 1; e >= 0; --e)
+            for (int e = TK - 1; e >= 0; --e)
               aB[q][j] = M::mma(fc[q][kb], M::rows_d(sK + e * kMM + (16 * j + i16) * LM + 32 * kb + 4 * g),
                                 aB[q][j]);
           float bv[4];
@@ -666,6 +683,14 @@ __global__ void __launch_bounds__(64 * bwd_waves(sizeof(typename Mat<T>::E) == 4
       if (lane == 0) sK0[wave] = k0;
     }
     __syncthreads();
+    if constexpr (kOver) {
+#pragma unroll
+      for (int s = 0; s < SL; ++s)
+#pragma unroll
+        for (int k = 0; k < TK; ++k)
+          *reinterpret_cast<Frag*>(sG + k * kS + (16 * wave + i16) * LX + 32 * s + 8 * g) = kept[s].t[k];
+      __syncthreads();
+    }
 
     // ---- dx: a wave takes every other slice of 32 rows and some of the tokens
     {
@@ -677,16 +702,20 @@ __global__ void __launch_bounds__(64 * bwd_waves(sizeof(typename Mat<T>::E) == 4
         for (int q = 0; q < NJ; ++q) X[q][0] = X[q][1] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) {
-          Frag f[2];
+          Frag f[2][TK];
 #pragma unroll
           for (int p = 0; p < 2; ++p)
-            f[p] = M::cols(cols_at<T, true>(sG, LX, 32 * kb, 32 * s + pair_base(p), lane), LX);
+#pragma unroll
+            for (int k = 0; k < TK; ++k)
+              f[p][k] = M::cols(cols_at<T, true>(sG + k * kS, LX, 32 * kb, 32 * s + pair_base(p), lane), LX);
 #pragma unroll
           for (int q = 0; q < NJ; ++q) {
             const int j = q ? 3 - jw : jw;
             const Frag bt = M::rows_d(tB + (16 * j + i16) * LN + 32 * kb + 4 * g);
 #pragma unroll
-            for (int p = 0; p < 2; ++p) X[q][p] = M::mma(f[p], bt, X[q][p]);
+            for (int k = TK - 1; k >= 0; --k)
+#pragma unroll
+              for (int p = 0; p < 2; ++p) X[q][p] = M::mma(f[p][k], bt, X[q][p]);
           }
           keep_order();
         }
@@ -700,11 +729,24 @@ __global__ void __launch_bounds__(64 * bwd_waves(sizeof(typename Mat<T>::E) == 4
 #pragma unroll
             for (int r = 0; r < 4; ++r) X[q][p][r] *= ft;
           for (int kb = j >> 1; kb < 2; ++kb) {
-            const Frag mf = M::rows_d(sM + t * LM + 32 * kb + 4 * g);
+            // e^{a_u-a_t} C_u.B_t, as a product's result holds it and an operand wants it
+            float m[8];
+#pragma unroll
+            for (int h2 = 0; h2 < 2; ++h2) {
+              const int iu = 2 * kb + h2, uu = 16 * iu + 4 * g;
+              const f32x4 c = sCB[iu < j ? 0 : iu * (iu + 1) / 2 + j][lane];
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                const float e = exp2_f32(gap2(sQ[uu + r], qt)) * c[r];
+                m[4 * h2 + r] = uu + r >= t ? e : 0.f;
+              }
+            }
+            Split<T, TK> mf;
+            mf.set(m);
 #pragma unroll
             for (int p = 0; p < 2; ++p)
-              X[q][p] = M::mma(M::cols(cols_at<T, true>(sY, LX, 32 * kb, 32 * s + pair_base(p), lane), LX),
-                               mf, X[q][p]);
+              X[q][p] = mf.b_times(M::cols(cols_at<T, true>(sY, LX, 32 * kb, 32 * s + pair_base(p), lane), LX),
+                                   X[q][p]);
           }
           if (t < rows) {
             const float Dh = a.D ? a.D[h] : 0.f;

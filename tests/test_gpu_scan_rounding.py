@@ -37,3 +37,16 @@ def test_forward(lens, shape, io):
     want, _ = Q.scan_forward(**a)
     mag, _ = Q.scan_magnitude(**a)
     _near(s.forward(D=None), want, HALF[io] * abs(want) + E32 * mag, "y")
+
+
+@pytest.mark.parametrize("io", [F32, BF16])
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "H{H}P{P}N{N}G{G}".format(**s))
+def test_backward(shape, io):
+    s = Scan([150, 70], io=io, seed=6, **shape)
+    a = s.oracle_inputs()
+    a.update(D=None, dlast=_np(s.dlast))
+    want = Q.scan_backward(_np(s.dy), **a)
+    mag = Q.scan_backward(_np(s.dy), **a, magnitude=True)
+    got = s.backward(D=None)
+    for k in ("dx", "dB", "dC"):
+        _near(got[k], want[k], HALF[io] * abs(want[k]) + E32 * mag[k], k)
