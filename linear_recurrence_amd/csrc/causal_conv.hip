@@ -351,6 +351,7 @@ __global__ void __launch_bounds__(256) conv_bwd_join_kernel(const ConvArgs a) {
   const long cols = (long)(W + 1) * a.channels;
   const int cblk = (int)((cols + 63) / 64);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  if (blockIdx.x == 0) check_table(a.cu, a.seqs, a.tokens, a.status);
   if ((int)blockIdx.x < cblk) {
     __shared__ float red[4][64];
     const long col = (long)blockIdx.x * 64 + lane;

@@ -165,6 +165,15 @@ __device__ static inline SeqSpan seq_span(const int32_t* cu, int i, int nseq, in
   return {s, e - s, bad};
 }
 
+// All of the table, by one workgroup: a kernel whose work is found by searching
+// the table does not meet every entry of one that is not monotone.
+__device__ static inline void check_table(const int32_t* cu, int nseq, int tokens, int32_t* status) {
+  if (!cu || !status) return;
+  bool bad = false;
+  for (int i = threadIdx.x; i < nseq; i += blockDim.x) bad |= seq_span(cu, i, nseq, tokens).bad;
+  if (bad) atomicOr(status, RSSM_ST_BAD_SEQ);
+}
+
 // The last sequence whose start is at or before token t (binary search over
 // the nseq starts; the table is monotone, or the result is merely arbitrary).
 __device__ static inline int seq_of_token(const int32_t* cu, int nseq, int t) {
