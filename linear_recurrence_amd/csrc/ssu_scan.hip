@@ -249,10 +249,8 @@ __global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 1 : (N 
   const int v = grp * a.vpg + (live ? vl : 0);
   const int slices = a.headdim / kPT, h = v / slices, p0 = (v % slices) * kPT;
   const int pool = a.init || a.final_state ? scan_slot(a, sg.seq) : -1;
-  if (STORE && threadIdx.x == 0 && rest == 0 && sg.first && a.status) {
-    if (sg.bad) atomicOr(a.status, RSSM_ST_BAD_SEQ);
-    if ((a.init || a.final_state) && pool < 0) atomicOr(a.status, RSSM_ST_BAD_SLOT);
-  }
+  if (STORE && threadIdx.x == 0 && rest == 0 && sg.first && a.status && (a.init || a.final_state) && pool < 0)
+    atomicOr(a.status, RSSM_ST_BAD_SLOT);
   // S^T: rows n = 16 nt + 4g + r, columns tile_col(p, l%16)
   f32x4 S[NT][2];
 #pragma unroll

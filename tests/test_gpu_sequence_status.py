@@ -40,3 +40,24 @@ def test_conv_backward_reports_a_bad_table(table, tokens, initial):
     good = [0] * n + [tokens]
     R.causal_conv_backward(x, x, w, cu_seqlens=_table(*good), initial_state=init, status=status)
     assert int(status) == 0
+
+
+@pytest.mark.parametrize("table", [(0, 1000, 200, 2000), (1000, 200, 2000), (0, 2000, 100, 150, 2000),
+                                   (0, 1999, 3, 2000), (0, 700, 1400, 2001)], ids=str)
+def test_scan_reports_a_bad_table(table):
+    """Entries that a search for a token's sequence passes over, too."""
+    g = torch.Generator().manual_seed(0)
+    T, H, P, N = 2000, 2, 32, 16
+    x, dy = (torch.randn(T, H, P, generator=g).cuda() for _ in range(2))
+    dt, B, C = (torch.randn(T, *s, generator=g).cuda() for s in ((H,), (1, N), (1, N)))
+    A, status = -torch.ones(H, device="cuda"), _word()
+    R.ssu_scan_forward(x, dt, A, B, C, cu_seqlens=_table(*table), status=status)
+    assert int(status) == R.ST_BAD_SEQ
+    status.zero_()
+    R.ssu_scan_backward(dy, x, dt, A, B, C, cu_seqlens=_table(*table), status=status)
+    assert int(status) == R.ST_BAD_SEQ
+    status.zero_()
+    good = _table(0, 0, 1000, 1000, T)
+    R.ssu_scan_forward(x, dt, A, B, C, cu_seqlens=good, status=status)
+    R.ssu_scan_backward(dy, x, dt, A, B, C, cu_seqlens=good, status=status)
+    assert int(status) == 0
