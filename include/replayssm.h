@@ -491,6 +491,8 @@ int replayssm_flush_first_order(int32_t n_rows, const uint8_t* is_flush, int32_t
  *    workspaces of their own.
  *  - Sums over tokens, rows and heads are added in a fixed order: the same
  *    call gives the same bits.
+ *  - An output may share memory with an input only where its description
+ *    says so: workgroups read rows that others have work to do on.
  */
 enum { RSSM_ACT_NONE = 0, RSSM_ACT_SILU = 1 };
 
@@ -521,7 +523,7 @@ typedef struct rssm_conv_dims {
  *     reads slot slot_idx[i] (NULL: i) where has_initial[i] (NULL: all)
  *   final_state [num_slots, W-1, C] or NULL: the last W-1 rows, same slots;
  *     may be initial_state itself
- *   y [tokens, C] io_dtype
+ *   y [tokens, C] io_dtype; sharing memory with x's rows is refused
  */
 int causal_conv_forward(const rssm_conv_dims* dims, const void* x, const float* weight,
                         const float* bias, const int32_t* cu_seqlens,
@@ -531,7 +533,8 @@ int causal_conv_forward(const rssm_conv_dims* dims, const void* x, const float* 
 
 /*
  * causal_conv_backward - gradients of causal_conv_forward's y:
- *   dx [tokens, C] io_dtype; dweight [C, W], dbias [C] (or NULL) float32;
+ *   dx [tokens, C] io_dtype (sharing memory with x's or dy's rows is
+ *   refused); dweight [C, W], dbias [C] (or NULL) float32;
  *   dinitial_state [num_slots, W-1, C] io_dtype or NULL: written for every
  *   sequence's slot, zero where has_initial[i] is 0.
  */

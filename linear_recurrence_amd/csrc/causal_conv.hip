@@ -499,6 +499,19 @@ static bool elt_aligned(const void* p, int32_t dtype) {
   return (reinterpret_cast<uintptr_t>(p) & (dtype == RSSM_F32 ? 3u : 1u)) == 0;
 }
 
+// Whether any of the rows in[0..rows) (stride apart) shares memory with the dense
+// rows out[0..rows), channels of either io_dtype elements: workgroups read up to
+// W-1 rows that another one's results would replace.
+static bool rows_meet(const void* in, long stride, const void* out, const rssm_conv_dims& d) {
+  if (!in || !out || d.tokens == 0) return false;
+  const long es = d.io_dtype == RSSM_F32 ? 4 : 2, len = d.channels * es, step = stride * es;
+  const intptr_t a = reinterpret_cast<intptr_t>(in), b = reinterpret_cast<intptr_t>(out);
+  const intptr_t end = b + d.tokens * len;
+  // the first row that ends behind the output's start
+  const long k = a + len > b ? 0 : (b - a - len) / step + 1;
+  return k < d.tokens && a + k * step < end;
+}
+
 #define RSSM_CONV_PICK(name, d)                                                        \
   ((d).io_dtype == RSSM_F32                                                            \
        ? ((d).width == 2   ? reinterpret_cast<const void*>(&name<float, 2>)            \
@@ -556,6 +569,7 @@ extern "C" int causal_conv_forward(const rssm_conv_dims* dims, const void* x, co
       !elt_aligned(initial_state, d.io_dtype) || !elt_aligned(final_state, d.io_dtype))
     return RSSM_EINVAL;
   ConvArgs a = conv_args(d);
+  if (rows_meet(x, a.x_stride, y, d)) return RSSM_EINVAL;
   a.x = x;
   a.weight = weight;
   a.bias = bias;
@@ -598,6 +612,7 @@ extern "C" int causal_conv_backward(const rssm_conv_dims* dims, const void* dy, 
     return RSSM_EINVAL;
   if (workspace_bytes < causal_conv_backward_workspace(dims)) return RSSM_EINVAL;
   ConvArgs a = conv_args(d);
+  if (rows_meet(x, a.x_stride, dx, d) || rows_meet(dy, a.dy_stride, dx, d)) return RSSM_EINVAL;
   a.x = x;
   a.dy = dy;
   a.weight = weight;

@@ -1,0 +1,39 @@
+"""Overlaps and sizes that the sequence operators refuse on the host, before any
+HIP call.  Only refused calls are made here: the pointers are made up."""
+
+import ctypes
+
+import pytest
+
+import linear_recurrence_amd as R
+from linear_recurrence_amd import sequence as S
+
+EINVAL, ESHAPE = -1, -4
+BASE = 1 << 20
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return R.load()
+
+
+def _conv(lib, x, out, dy=None, x_stride=0, dy_stride=0, tokens=8, channels=40, io=1, **dims):
+    d = ctypes.byref(S.ConvDims(tokens, 1, channels, 4, 1, io, 1, 0, x_stride, dy_stride))
+    p = ctypes.c_void_p(1 << 40)
+    if dy is None:
+        return lib.causal_conv_forward(d, x, p, p, p, None, None, None, None, out, None, None)
+    return lib.causal_conv_backward(d, dy, x, p, p, p, None, None, None, out, p, p, None, p, 1 << 40,
+                                    None, None)
+
+
+@pytest.mark.parametrize("io, es", [(0, 4), (1, 2)])
+def test_conv_refuses_an_output_over_its_input(lib, io, es):
+    row, rows = 40 * es, 8 * 40 * es
+    for at in (0, es, rows - es, es - rows):               # the same, and any overlap at all
+        assert _conv(lib, BASE, BASE + at, io=io) == EINVAL
+        assert _conv(lib, BASE, BASE + at, dy=1 << 30, io=io) == EINVAL
+        assert _conv(lib, 1 << 30, BASE + at, dy=BASE, io=io) == EINVAL
+    # rows of a wide matrix: an output that begins in the last row, or ends in the second
+    wide = dict(x_stride=1000, io=io)
+    assert _conv(lib, BASE, BASE + 7 * 1000 * es + row - es, **wide) == EINVAL
+    assert _conv(lib, BASE, BASE + 1000 * es - rows + es, **wide) == EINVAL
