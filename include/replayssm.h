@@ -491,6 +491,10 @@ int replayssm_flush_first_order(int32_t n_rows, const uint8_t* is_flush, int32_t
  *    workspaces of their own.
  *  - Sums over tokens, rows and heads are added in a fixed order: the same
  *    call gives the same bits.
+ *  - A call whose launches would hold 2^32 threads or more is refused
+ *    (RSSM_ESHAPE): a norm forward from 2^22 rows on (above 8192 elements; 2^26
+ *    up to 1024), a convolution from 2^28 tokens of 512 channels on, a scan
+ *    from 2^34 / (nheads*headdim*dstate) sequences on (backward 2^32 / that).
  *  - An output may share memory with an input only where its description
  *    says so: workgroups read rows that others have work to do on.
  */

@@ -489,9 +489,6 @@ static int conv_check(const rssm_conv_dims* d) {
   if (d->activation != RSSM_ACT_NONE && d->activation != RSSM_ACT_SILU) return RSSM_EINVAL;
   if (!valid_dtype(d->io_dtype)) return RSSM_EDTYPE;
   if (d->width < 2 || d->width > 4 || d->channels > (1 << 24)) return RSSM_ESHAPE;
-  // pointers are aligned to their element type and the grids fit 31 bits
-  if (((long)d->tokens + d->seqs + 1) * ((d->channels + 511) / 512) > 0x7fffffffL)
-    return RSSM_ESHAPE;
   return RSSM_OK;
 }
 
@@ -562,6 +559,9 @@ extern "C" int causal_conv_forward(const rssm_conv_dims* dims, const void* x, co
   if (rc) return rc;
   const rssm_conv_dims& d = *dims;
   if (d.seqs == 0) return d.tokens == 0 ? RSSM_OK : RSSM_EINVAL;
+  const int run = conv_run(d, 512);
+  const long grid = (d.seqs + ((long)d.tokens + run - 1) / run) * ((d.channels + 511) / 512);
+  if (!grid_fits(grid, 64)) return RSSM_ESHAPE;
   if (!weight || (d.tokens > 0 && (!x || !y))) return RSSM_EINVAL;
   if (!cu_seqlens && d.seqs != 1) return RSSM_EINVAL;
   if (x && (d.x_stride != 0 && d.x_stride < d.channels)) return RSSM_EINVAL;
@@ -580,10 +580,8 @@ extern "C" int causal_conv_forward(const rssm_conv_dims* dims, const void* x, co
   a.final_state = final_state;
   a.y = y;
   a.status = status;
-  a.run = conv_run(d, 512);
-  const long tiles = d.seqs + ((long)d.tokens + a.run - 1) / a.run;
-  return launch_kernel(RSSM_CONV_PICK(conv_fwd_kernel, d),
-                       (unsigned)(tiles * ((d.channels + 511) / 512)), 64, 0, stream, a);
+  a.run = run;
+  return launch_kernel(RSSM_CONV_PICK(conv_fwd_kernel, d), (unsigned)grid, 64, 0, stream, a);
 }
 
 extern "C" size_t causal_conv_backward_workspace(const rssm_conv_dims* dims) {
@@ -601,6 +599,10 @@ extern "C" int causal_conv_backward(const rssm_conv_dims* dims, const void* dy, 
   int rc = conv_check(dims);
   if (rc) return rc;
   const rssm_conv_dims& d = *dims;
+  const long parts = bwd_tiles(d), grid = parts * ((d.channels + 64 * kBwdChan - 1) / (64 * kBwdChan));
+  const long cols = (long)(d.width + 1) * d.channels;
+  const long init = dinitial_state ? ((long)d.seqs * ((d.channels + 7) / 8) + 255) / 256 : 0;
+  if (!grid_fits(grid, 64 * kBwdWaves) || !grid_fits((cols + 63) / 64 + init, 256)) return RSSM_ESHAPE;
   if (!weight || !dweight) return RSSM_EINVAL;
   if (d.tokens > 0 && (!x || !dy || !dx || !workspace || d.seqs < 1)) return RSSM_EINVAL;
   if (!cu_seqlens && d.seqs > 1) return RSSM_EINVAL;
@@ -628,16 +630,11 @@ extern "C" int causal_conv_backward(const rssm_conv_dims* dims, const void* dy, 
   a.part = static_cast<float*>(workspace);
   a.status = status;
   a.run = bwd_run(d);
-  a.parts = (int32_t)bwd_tiles(d);
+  a.parts = (int32_t)parts;
   if (a.parts > 0) {
-    rc = launch_kernel(RSSM_CONV_PICK(conv_bwd_kernel, d),
-                       (unsigned)((long)a.parts * ((d.channels + 64 * kBwdChan - 1) / (64 * kBwdChan))),
-                       64 * kBwdWaves, 0,
-                       stream, a);
+    rc = launch_kernel(RSSM_CONV_PICK(conv_bwd_kernel, d), (unsigned)grid, 64 * kBwdWaves, 0, stream, a);
     if (rc) return rc;
   }
-  const long cols = (long)(d.width + 1) * d.channels;
-  const long init = dinitial_state ? ((long)d.seqs * ((d.channels + 7) / 8) + 255) / 256 : 0;
   return launch_kernel(RSSM_CONV_PICK(conv_bwd_join_kernel, d),
                        (unsigned)((cols + 63) / 64 + init), 256, 0, stream, a);
 }
@@ -650,6 +647,12 @@ extern "C" int causal_conv_decode(const rssm_conv_dims* dims, const void* x,
   if (rc) return rc;
   const rssm_conv_dims& d = *dims;
   if (d.tokens == 0) return RSSM_OK;
+  // several rows a wave where that still leaves one for every SIMD (512 rows of
+  // 5376 channels: 11 us with four, 26 with one and element-wise weight loads)
+  const long cblocks = (d.channels + 511) / 512;
+  const int rows = d.tokens * cblocks >= 1024 * kStepRows ? kStepRows : 1;
+  const long grid = ((long)d.tokens + rows - 1) / rows * cblocks;
+  if (!grid_fits(grid, 64)) return RSSM_ESHAPE;
   if (!x || !conv_state || !weight || !new_state || !y) return RSSM_EINVAL;
   if (d.x_stride != 0 && d.x_stride < d.channels) return RSSM_EINVAL;
   if (!elt_aligned(x, d.io_dtype) || !elt_aligned(y, d.io_dtype) ||
@@ -664,13 +667,9 @@ extern "C" int causal_conv_decode(const rssm_conv_dims* dims, const void* x,
   a.final_state = new_state;
   a.y = y;
   a.status = status;
-  // several rows a wave where that still leaves one for every SIMD (512 rows of
-  // 5376 channels: 11 us with four, 26 with one and element-wise weight loads)
-  const long cblocks = (d.channels + 511) / 512;
-  const int rows = d.tokens * cblocks >= 1024 * kStepRows ? kStepRows : 1;
   const bool f32 = d.io_dtype == RSSM_F32;
   const void* fn = d.width == 2   ? (f32 ? pick_step<float, 2>(rows) : pick_step<bf16, 2>(rows))
                    : d.width == 3 ? (f32 ? pick_step<float, 3>(rows) : pick_step<bf16, 3>(rows))
                                   : (f32 ? pick_step<float, 4>(rows) : pick_step<bf16, 4>(rows));
-  return launch_kernel(fn, (unsigned)((d.tokens + rows - 1) / rows * cblocks), 64, 0, stream, a);
+  return launch_kernel(fn, (unsigned)grid, 64, 0, stream, a);
 }

@@ -517,6 +517,7 @@ extern "C" int rms_norm_forward(const rssm_norm_dims* dims, const void* x, const
   a.out = out;
   a.scale = scale;
   const NormShape sh = norm_shape(a.nvec, false, a.rows);
+  if (!grid_fits(a.rows, sh.threads)) return RSSM_ESHAPE;
   const void* fn = f32 ? pick_norm_fwd_kernel<float>(sh) : pick_norm_fwd_kernel<bf16>(sh);
   if (norm_is<1024, 1>(sh))
     fn = f32 ? reinterpret_cast<const void*>(&norm_fwd_kernel<float, 1024, 1>)

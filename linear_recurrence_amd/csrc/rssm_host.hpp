@@ -17,6 +17,9 @@ static inline bool aligned16(const void* p) {
 
 static inline bool valid_dtype(int32_t t) { return t == RSSM_F32 || t == RSSM_BF16; }
 
+// A launch holds fewer than 2^32 threads.
+static inline bool grid_fits(long grid, long threads) { return grid * threads < (1L << 32); }
+
 // Launch with the error code of the launch itself (not a stale one left in
 // the thread's last-error slot by earlier runtime calls).
 template <typename Args>

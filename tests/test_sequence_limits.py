@@ -37,3 +37,20 @@ def test_conv_refuses_an_output_over_its_input(lib, io, es):
     wide = dict(x_stride=1000, io=io)
     assert _conv(lib, BASE, BASE + 7 * 1000 * es + row - es, **wide) == EINVAL
     assert _conv(lib, BASE, BASE + 1000 * es - rows + es, **wide) == EINVAL
+
+
+def test_conv_refuses_grids_past_32_bits(lib):
+    for tokens, channels in ((1 << 30, 1 << 12), ((1 << 31) - 1, 600), ((1 << 31) - 1, 1 << 24)):
+        assert _conv(lib, BASE, BASE, tokens=tokens, channels=channels) == ESHAPE
+        assert _conv(lib, BASE, BASE, dy=BASE, tokens=tokens, channels=channels) == ESHAPE
+    d, p = S.ConvDims(1 << 28, 1, 1 << 10, 4, 1, 1, 1), ctypes.c_void_p(BASE)
+    assert lib.causal_conv_decode(ctypes.byref(d), p, p, p, p, None, p, p, None, None) == ESHAPE
+
+
+@pytest.mark.parametrize("rows, dim", [(1 << 26, 512), (1 << 24, 1032), (1 << 24, 4096), (1 << 24, 8192),
+                                       (1 << 22, 8200), (1 << 22, 32768), ((1 << 31) - 1, 8)])
+def test_norm_refuses_grids_past_32_bits(lib, rows, dim):
+    """One workgroup a row, of 64, 256 or 1024 threads."""
+    p = ctypes.c_void_p(BASE)
+    d = ctypes.byref(S.NormDims(rows, dim, dim, 1, 1, 1, 0, 1e-5))
+    assert lib.rms_norm_forward(d, p, p, None, None, None, p, None, None) == ESHAPE
