@@ -109,6 +109,12 @@ def _rows(t, name, dtype, shape, dev):
     return t.stride(0)
 
 
+def _sizes(t, name):
+    """The library's sizes are 32-bit: ctypes would cut a larger one short."""
+    if max(t.shape, default=0) > 0x7fffffff:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}: sizes are limited to 2^31 - 1")
+
+
 def _first(t, name, ndim):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
@@ -116,6 +122,7 @@ def _first(t, name, ndim):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {ndim} dimensions")
     if t.dtype not in _DT:
         raise ValueError(f"{name} has dtype {t.dtype}, expected {_IO}")
+    _sizes(t, name)
     return t.device, t.dtype
 
 
@@ -136,6 +143,7 @@ def _seqs(cu_seqlens, dev):
         cu_seqlens.dim() == 1 else -1
     if n < 0:
         raise ValueError("cu_seqlens must be a 1-D tensor of sequences + 1 entries")
+    _sizes(cu_seqlens, "cu_seqlens")
     _dense(cu_seqlens, "cu_seqlens", torch.int32, (n + 1,), dev)
     return n
 
@@ -153,6 +161,7 @@ def _scan_dims(x, dt, A, B, C, D, dt_bias, cu_seqlens, slot_idx, has_initial, st
     T, H, P = x.shape
     if not isinstance(B, torch.Tensor) or B.dim() != 3:
         raise ValueError("B must be a GPU tensor of 3 dimensions")
+    _sizes(B, "B")
     G, N = B.shape[1], B.shape[2]
     n = _seqs(cu_seqlens, dev)
     _dense(A, "A", torch.float32, (H,), dev)
@@ -186,6 +195,7 @@ def ssu_scan_forward(x, dt, A, B, C, D=None, z=None, dt_bias=None, cu_seqlens=No
     if pool is not None:
         if not isinstance(pool, torch.Tensor) or pool.dim() != 4 or pool.dtype not in _DT:
             raise ValueError("states must be float32 or bfloat16 GPU tensors [slots, H, P, N]")
+        _sizes(pool, "the state pool")
         shape = (pool.shape[0], H, P, N)
         _dense(initial_state, "initial_state", pool.dtype, shape, dev)
         _dense(final_state, "final_state", pool.dtype, shape, dev)
@@ -227,6 +237,7 @@ def ssu_scan_backward(dy, x, dt, A, B, C, D=None, dt_bias=None, cu_seqlens=None,
                 initial_state.dtype not in _DT:
             raise ValueError("initial_state must be a float32 or bfloat16 GPU tensor "
                              "[slots, H, P, N]")
+        _sizes(initial_state, "initial_state")
         _dense(initial_state, "initial_state", initial_state.dtype,
                (initial_state.shape[0], H, P, N), dev)
         d.num_slots, d.state_dtype = initial_state.shape[0], _DT[initial_state.dtype]
@@ -261,6 +272,7 @@ def _conv_dims(x, weight, bias, cu_seqlens, activation, status):
     T, C = x.shape
     if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
         raise ValueError("weight must be a GPU tensor [channels, width]")
+    _sizes(weight, "weight")
     W = weight.shape[1]
     _dense(weight, "weight", torch.float32, (C, W), dev)
     _dense(bias, "bias", torch.float32, (C,), dev)
@@ -287,6 +299,7 @@ def causal_conv_forward(x, weight, bias=None, cu_seqlens=None, initial_state=Non
         shape = (pool.shape[0] if isinstance(pool, torch.Tensor) and pool.dim() else 0, W - 1, C)
         _dense(initial_state, "initial_state", io, shape, dev)
         _dense(final_state, "final_state", io, shape, dev)
+        _sizes(pool, "the state pool")
         d.num_slots = shape[0]
     _slots(slot_idx, has_initial, None, n, dev)
     lib, (handle, ctx) = _library(), _on(stream, dev)
@@ -313,6 +326,7 @@ def causal_conv_backward(dy, x, weight, bias=None, cu_seqlens=None, initial_stat
         shape = (initial_state.shape[0] if isinstance(initial_state, torch.Tensor) and
                  initial_state.dim() else 0, W - 1, C)
         _dense(initial_state, "initial_state", io, shape, dev)
+        _sizes(initial_state, "initial_state")
         d.num_slots = shape[0]
     _slots(slot_idx, has_initial, None, n, dev)
     lib, (handle, ctx) = _library(), _on(stream, dev)
@@ -350,6 +364,7 @@ def causal_conv_decode(x, conv_state, weight, bias=None, slot_idx=None, new_stat
         new_state = conv_state
     _dense(conv_state, "conv_state", io, shape, dev)
     _dense(new_state, "new_state", io, shape, dev)
+    _sizes(conv_state, "conv_state")
     d.num_slots = shape[0]
     _dense(slot_idx, "slot_idx", torch.int32, (nb,), dev)
     lib, (handle, ctx) = _library(), _on(stream, dev)
@@ -370,6 +385,8 @@ def _norm_dims(x, weight, z, group_size, eps):
     R, M = x.shape
     if weight is None:
         raise ValueError("weight is required")
+    if group_size is not None and not 1 <= group_size <= max(M, 1):
+        raise ValueError(f"group_size is {group_size}, expected a divisor of {M}")
     _dense(weight, "weight", torch.float32, (M,), dev)
     zs = 0 if z is None else _rows(z, "z", io, (R, M), dev)
     return dev, io, NormDims(R, M, M if group_size is None else group_size, _DT[io], _DT[io],

@@ -1,4 +1,5 @@
-"""Outputs beside their inputs in one buffer: near, and sharing nothing."""
+"""Outputs beside their inputs in one buffer (near, and sharing nothing), and
+inputs whose sizes the library's 32-bit fields cannot hold."""
 
 import pytest
 import torch
@@ -42,3 +43,16 @@ def test_conv_output_in_the_gap_of_wide_rows():
         assert torch.equal(R.causal_conv_forward(x, w, y=y), want)
     with pytest.raises(R.RssmError):
         R.causal_conv_forward(x, w, y=flat[1001 - T * C:1001].view(T, C))
+
+
+def test_rows_past_32_bits_are_refused():
+    x = torch.empty((1 << 32) + 4, 1, dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(1, device="cuda")
+    for call in (lambda: R.causal_conv_forward(x, torch.ones(1, 4, device="cuda")),
+                 lambda: R.causal_conv_backward(x, x, torch.ones(1, 4, device="cuda")),
+                 lambda: R.rms_norm_forward(x, w), lambda: R.rms_norm_backward(x, x, w),
+                 lambda: R.rms_norm_forward(x.t(), torch.ones((1 << 32) + 4, device="cuda"))):
+        with pytest.raises(ValueError, match="2\\^31 - 1"):
+            call()
+    with pytest.raises(ValueError, match="group_size"):
+        R.rms_norm_forward(x[:4], w, group_size=(1 << 32) + 1)

@@ -4,6 +4,7 @@ HIP call.  Only refused calls are made here: the pointers are made up."""
 import ctypes
 
 import pytest
+import torch
 
 import linear_recurrence_amd as R
 from linear_recurrence_amd import sequence as S
@@ -54,3 +55,12 @@ def test_norm_refuses_grids_past_32_bits(lib, rows, dim):
     p = ctypes.c_void_p(BASE)
     d = ctypes.byref(S.NormDims(rows, dim, dim, 1, 1, 1, 0, 1e-5))
     assert lib.rms_norm_forward(d, p, p, None, None, None, p, None, None) == ESHAPE
+
+
+def test_the_binding_refuses_sizes_past_32_bits():
+    """2^32 + 4 rows would reach the library as 4."""
+    S._sizes(torch.empty(2 ** 31 - 1, 0, device="meta"), "x")
+    S._sizes(torch.empty((), device="meta"), "x")
+    for shape in ((2 ** 31, 1), (2 ** 32 + 4, 1), (1, 2 ** 32 + 8), (3, 2 ** 31, 4)):
+        with pytest.raises(ValueError, match="2\\^31 - 1"):
+            S._sizes(torch.empty(shape, device="meta"), "x")
