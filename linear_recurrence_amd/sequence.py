@@ -111,7 +111,8 @@ def _rows(t, name, dtype, shape, dev):
 
 def _sizes(t, name):
     """The library's sizes are 32-bit: ctypes would cut a larger one short."""
-    if max(t.shape, default=0) > 0x7fffffff:
+    n = t.numel()
+    if (n > 0x7fffffff or n == 0) and max(t.shape, default=0) > 0x7fffffff:
         raise ValueError(f"{name} has shape {tuple(t.shape)}: sizes are limited to 2^31 - 1")
 
 
@@ -130,9 +131,13 @@ _HERE = contextlib.nullcontext()
 
 
 def _on(stream, dev):
-    """(the stream's handle, a context that allocates on it)"""
+    """(the stream's handle, a context that allocates on it and launches on its
+    device: the default stream's handle is the same on every device)"""
     if stream is None:   # the raw handle: a Stream object costs over a microsecond
-        return torch._C._cuda_getCurrentRawStream(dev.index), _HERE
+        here = torch._C._cuda_getDevice() == dev.index
+        return torch._C._cuda_getCurrentRawStream(dev.index), _HERE if here else torch.cuda.device(dev)
+    if stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, expected {dev}")
     return stream.cuda_stream, torch.cuda.stream(stream)
 
 
@@ -204,15 +209,15 @@ def ssu_scan_forward(x, dt, A, B, C, D=None, z=None, dt_bias=None, cu_seqlens=No
         d.z_stride = _rows(z, "z", io, (T, H, P), dev)
     lib, (handle, ctx) = _library(), _on(stream, dev)
     size = lib.ssu_scan_forward_workspace(ctypes.byref(d))
+    _dense(y, "y", io, (T, H, P), dev)
     with ctx:
         if y is None:
             y = torch.empty((T, H, P), dtype=io, device=dev)
         ws = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
-    _dense(y, "y", io, (T, H, P), dev)
-    _check("ssu_scan_forward", lib.ssu_scan_forward(
-        ctypes.byref(d), _p(x), _p(dt), _p(A), _p(B), _p(C), _p(D), _p(z), _p(dt_bias),
-        _p(cu_seqlens), _p(initial_state), _p(has_initial), _p(slot_idx), _p(final_state), _p(y),
-        _p(ws), size, _p(status), handle))
+        _check("ssu_scan_forward", lib.ssu_scan_forward(
+            ctypes.byref(d), _p(x), _p(dt), _p(A), _p(B), _p(C), _p(D), _p(z), _p(dt_bias),
+            _p(cu_seqlens), _p(initial_state), _p(has_initial), _p(slot_idx), _p(final_state), _p(y),
+            _p(ws), size, _p(status), handle))
     return y
 
 
@@ -256,12 +261,12 @@ def ssu_scan_backward(dy, x, dt, A, B, C, D=None, dt_bias=None, cu_seqlens=None,
                    ddt_bias=None if dt_bias is None else torch.empty(H, dtype=f32, device=dev),
                    dinitial_state=None if initial_state is None else
                    torch.empty((n, H, P, N), dtype=f32, device=dev))
-    _check("ssu_scan_backward", lib.ssu_scan_backward(
-        ctypes.byref(d), _p(dy), _p(x), _p(dt), _p(A), _p(B), _p(C), _p(D), _p(dt_bias),
-        _p(cu_seqlens), _p(initial_state), _p(has_initial), _p(slot_idx), _p(dfinal_state),
-        _p(out["dx"]), _p(out["ddt"]), _p(out["dB"]), _p(out["dC"]), _p(out["dA"]),
-        _p(out["dD"]), _p(out["ddt_bias"]), _p(out["dinitial_state"]), _p(ws), size, _p(status),
-        handle))
+        _check("ssu_scan_backward", lib.ssu_scan_backward(
+            ctypes.byref(d), _p(dy), _p(x), _p(dt), _p(A), _p(B), _p(C), _p(D), _p(dt_bias),
+            _p(cu_seqlens), _p(initial_state), _p(has_initial), _p(slot_idx), _p(dfinal_state),
+            _p(out["dx"]), _p(out["ddt"]), _p(out["dB"]), _p(out["dC"]), _p(out["dA"]),
+            _p(out["dD"]), _p(out["ddt_bias"]), _p(out["dinitial_state"]), _p(ws), size, _p(status),
+            handle))
     return out
 
 
@@ -303,13 +308,13 @@ def causal_conv_forward(x, weight, bias=None, cu_seqlens=None, initial_state=Non
         d.num_slots = shape[0]
     _slots(slot_idx, has_initial, None, n, dev)
     lib, (handle, ctx) = _library(), _on(stream, dev)
-    if y is None:
-        with ctx:
-            y = torch.empty((T, C), dtype=io, device=dev)
     _dense(y, "y", io, (T, C), dev)
-    _check("causal_conv_forward", lib.causal_conv_forward(
-        ctypes.byref(d), _p(x), _p(weight), _p(bias), _p(cu_seqlens), _p(initial_state),
-        _p(has_initial), _p(slot_idx), _p(final_state), _p(y), _p(status), handle))
+    with ctx:
+        if y is None:
+            y = torch.empty((T, C), dtype=io, device=dev)
+        _check("causal_conv_forward", lib.causal_conv_forward(
+            ctypes.byref(d), _p(x), _p(weight), _p(bias), _p(cu_seqlens), _p(initial_state),
+            _p(has_initial), _p(slot_idx), _p(final_state), _p(y), _p(status), handle))
     return y
 
 
@@ -340,10 +345,10 @@ def causal_conv_backward(dy, x, weight, bias=None, cu_seqlens=None, initial_stat
                    dbias=None if bias is None else torch.empty(C, dtype=torch.float32, device=dev),
                    dinitial_state=None if initial_state is None else
                    alloc((d.num_slots, W - 1, C), dtype=io, device=dev))
-    _check("causal_conv_backward", lib.causal_conv_backward(
-        ctypes.byref(d), _p(dy), _p(x), _p(weight), _p(bias), _p(cu_seqlens), _p(initial_state),
-        _p(has_initial), _p(slot_idx), _p(out["dx"]), _p(out["dweight"]), _p(out["dbias"]),
-        _p(out["dinitial_state"]), _p(ws), size, _p(status), handle))
+        _check("causal_conv_backward", lib.causal_conv_backward(
+            ctypes.byref(d), _p(dy), _p(x), _p(weight), _p(bias), _p(cu_seqlens), _p(initial_state),
+            _p(has_initial), _p(slot_idx), _p(out["dx"]), _p(out["dweight"]), _p(out["dbias"]),
+            _p(out["dinitial_state"]), _p(ws), size, _p(status), handle))
     return out
 
 
@@ -368,13 +373,13 @@ def causal_conv_decode(x, conv_state, weight, bias=None, slot_idx=None, new_stat
     d.num_slots = shape[0]
     _dense(slot_idx, "slot_idx", torch.int32, (nb,), dev)
     lib, (handle, ctx) = _library(), _on(stream, dev)
-    if y is None:
-        with ctx:
-            y = torch.empty((nb, C), dtype=io, device=dev)
     _dense(y, "y", io, (nb, C), dev)
-    _check("causal_conv_decode", lib.causal_conv_decode(
-        ctypes.byref(d), _p(x), _p(conv_state), _p(weight), _p(bias), _p(slot_idx),
-        _p(new_state), _p(y), _p(status), handle))
+    with ctx:
+        if y is None:
+            y = torch.empty((nb, C), dtype=io, device=dev)
+        _check("causal_conv_decode", lib.causal_conv_decode(
+            ctypes.byref(d), _p(x), _p(conv_state), _p(weight), _p(bias), _p(slot_idx),
+            _p(new_state), _p(y), _p(status), handle))
     return y
 
 
@@ -427,9 +432,9 @@ def rms_norm_forward(x, weight, z=None, residual=None, group_size=None, eps=1e-5
                                 device=dev)
         if residual is not None and residual_out is None:
             residual_out = torch.empty(shape, dtype=residual.dtype, device=dev)
-    _check("rms_norm_forward", lib.rms_norm_forward(
-        ctypes.byref(d), _p(x), _p(weight), _p(z), _p(residual), _p(residual_out), _p(out),
-        _p(scale), handle))
+        _check("rms_norm_forward", lib.rms_norm_forward(
+            ctypes.byref(d), _p(x), _p(weight), _p(z), _p(residual), _p(residual_out), _p(out),
+            _p(scale), handle))
     return dict(out=out, scale=scale, residual=residual_out)
 
 
@@ -447,7 +452,7 @@ def rms_norm_backward(dy, x, weight, z=None, group_size=None, eps=1e-5, stream=N
         out = dict(dx=torch.empty(shape, dtype=io, device=dev),
                    dweight=torch.empty(d.dim, dtype=torch.float32, device=dev),
                    dz=None if z is None else torch.empty(shape, dtype=io, device=dev))
-    _check("rms_norm_backward", lib.rms_norm_backward(
-        ctypes.byref(d), _p(dy), _p(x), _p(weight), _p(z), _p(out["dx"]), _p(out["dweight"]),
-        _p(out["dz"]), _p(ws), size, handle))
+        _check("rms_norm_backward", lib.rms_norm_backward(
+            ctypes.byref(d), _p(dy), _p(x), _p(weight), _p(z), _p(out["dx"]), _p(out["dweight"]),
+            _p(out["dz"]), _p(ws), size, handle))
     return out

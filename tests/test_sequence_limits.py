@@ -64,3 +64,19 @@ def test_the_binding_refuses_sizes_past_32_bits():
     for shape in ((2 ** 31, 1), (2 ** 32 + 4, 1), (1, 2 ** 32 + 8), (3, 2 ** 31, 4)):
         with pytest.raises(ValueError, match="2\\^31 - 1"):
             S._sizes(torch.empty(shape, device="meta"), "x")
+
+
+def test_launches_go_to_the_tensors_device(monkeypatch):
+    """The default stream's handle is 0 on every device: without the device's
+    context the launch would go to the current one."""
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 100 + i, raising=False)
+    handle, ctx = S._on(None, torch.device("cuda", 0))
+    assert handle == 100 and ctx is S._HERE
+    handle, ctx = S._on(None, torch.device("cuda", 1))
+    assert handle == 101 and isinstance(ctx, torch.cuda.device) and ctx.idx == 1
+
+    class Stream:
+        device, cuda_stream = torch.device("cuda", 1), 7
+    with pytest.raises(ValueError, match="stream is on cuda:1, expected cuda:0"):
+        S._on(Stream(), torch.device("cuda", 0))
