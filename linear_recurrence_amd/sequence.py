@@ -6,7 +6,9 @@ norm, each with its backward pass.  Argument marshalling only, as in the
 decode binding.  Operands may be slices of wider rows (one token's row
 contiguous, any token stride); what is returned is dense.  Workspaces and
 outputs are allocated on the stream the call runs on; a caller whose inputs
-live on another stream orders the two, as for any other work.
+live on another stream orders the two, as for any other work.  The operators are
+not part of torch's automatic differentiation: their backward passes are calls of
+their own, and differentiating through a result raises an error.
 """
 
 import contextlib
@@ -159,6 +161,29 @@ def _slots(slot_idx, has_initial, status, n, dev):
     _dense(status, "status", torch.int32, (1,), dev)
 
 
+class _OwnBackward(torch.autograd.Function):
+    """Passes a result on; raises when a gradient comes back to it, which would
+    otherwise end there without a word."""
+
+    @staticmethod
+    def forward(ctx, name, out, *inputs):
+        ctx.name = name
+        return out
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError(f"{ctx.name} is not differentiable by torch: call its backward pass "
+                           "(in an autograd.Function of your own, for instance)")
+
+
+def _result(name, out, *inputs):
+    if torch.is_grad_enabled():
+        need = [t for t in inputs if t is not None and t.requires_grad]
+        if need:
+            return _OwnBackward.apply(name, out, *need)
+    return out
+
+
 # ------------------------------------------------------------------- the scan
 
 def _scan_dims(x, dt, A, B, C, D, dt_bias, cu_seqlens, slot_idx, has_initial, status, dt_softplus):
@@ -218,7 +243,7 @@ def ssu_scan_forward(x, dt, A, B, C, D=None, z=None, dt_bias=None, cu_seqlens=No
             ctypes.byref(d), _p(x), _p(dt), _p(A), _p(B), _p(C), _p(D), _p(z), _p(dt_bias),
             _p(cu_seqlens), _p(initial_state), _p(has_initial), _p(slot_idx), _p(final_state), _p(y),
             _p(ws), size, _p(status), handle))
-    return y
+    return _result("ssu_scan_forward", y, x, dt, A, B, C, D, z, dt_bias, initial_state)
 
 
 def ssu_scan_backward(dy, x, dt, A, B, C, D=None, dt_bias=None, cu_seqlens=None,
@@ -315,7 +340,7 @@ def causal_conv_forward(x, weight, bias=None, cu_seqlens=None, initial_state=Non
         _check("causal_conv_forward", lib.causal_conv_forward(
             ctypes.byref(d), _p(x), _p(weight), _p(bias), _p(cu_seqlens), _p(initial_state),
             _p(has_initial), _p(slot_idx), _p(final_state), _p(y), _p(status), handle))
-    return y
+    return _result("causal_conv_forward", y, x, weight, bias, initial_state)
 
 
 def causal_conv_backward(dy, x, weight, bias=None, cu_seqlens=None, initial_state=None,
@@ -380,7 +405,7 @@ def causal_conv_decode(x, conv_state, weight, bias=None, slot_idx=None, new_stat
         _check("causal_conv_decode", lib.causal_conv_decode(
             ctypes.byref(d), _p(x), _p(conv_state), _p(weight), _p(bias), _p(slot_idx),
             _p(new_state), _p(y), _p(status), handle))
-    return y
+    return _result("causal_conv_decode", y, x, conv_state, weight, bias)
 
 
 # ------------------------------------------------------------------- the norm
@@ -435,6 +460,12 @@ def rms_norm_forward(x, weight, z=None, residual=None, group_size=None, eps=1e-5
         _check("rms_norm_forward", lib.rms_norm_forward(
             ctypes.byref(d), _p(x), _p(weight), _p(z), _p(residual), _p(residual_out), _p(out),
             _p(scale), handle))
+    if fp8:
+        scale = _result("rms_norm_forward", scale, x, weight, z, residual)
+    else:
+        out = _result("rms_norm_forward", out, x, weight, z, residual)
+    if residual is not None:
+        residual_out = _result("rms_norm_forward", residual_out, x, residual)
     return dict(out=out, scale=scale, residual=residual_out)
 
 
