@@ -58,25 +58,31 @@ class Mamba2Layer:
                 xbc[:, at:at + self.bc].unflatten(1, (self.G, self.N)),
                 xbc[:, at + self.bc:].unflatten(1, (self.G, self.N)))
 
-    def prefill(self, x, residual, cu_seqlens, pools=None, slots=None, fresh=None):
+    def prefill(self, x, residual, cu_seqlens, pools=None, slots=None, has_initial=None, train=False):
         """x [tokens, width] and the fp32 residual stream -> (the layer's output,
         the new residual stream, what the backward pass needs).  The sequences'
         states continue from and go back to their slots of `pools`; those with
-        fresh[i] = 0 start from zeros."""
+        has_initial[i] = 0 start from zeros.  With pools, a backward pass needs
+        train=True, which copies the states that this call replaces."""
         p = self.p
         conv_pool, scan_pool = pools or (None, None)
+        first = {}
+        if pools and train:
+            at = slots.long() if slots is not None else torch.arange(len(cu_seqlens) - 1, device=x.device)
+            first = dict(conv=conv_pool[at], scan=scan_pool[at])
         n1 = R.rms_norm_forward(x, p["norm"], residual=residual)
         row = n1["out"] @ p["w_in"].t()
         z, xbc, dt = self._split(row)
         act = R.causal_conv_forward(xbc, p["conv"], bias=p["conv_bias"], cu_seqlens=cu_seqlens,
-                                    initial_state=conv_pool, has_initial=fresh, slot_idx=slots,
+                                    initial_state=conv_pool, has_initial=has_initial, slot_idx=slots,
                                     final_state=conv_pool)
         xs, B, C = self._heads(act)
         y = R.ssu_scan_forward(xs, dt, p["A"], B, C, D=p["D"], dt_bias=p["dt_bias"],
-                               cu_seqlens=cu_seqlens, initial_state=scan_pool, has_initial=fresh,
+                               cu_seqlens=cu_seqlens, initial_state=scan_pool, has_initial=has_initial,
                                final_state=scan_pool, slot_idx=slots).flatten(1)
         n2 = R.rms_norm_forward(y, p["gate_norm"], z=z, group_size=self.group)["out"]
-        keep = dict(h=n1["residual"], n1=n1["out"], row=row, act=act, y=y, n2=n2, cu=cu_seqlens)
+        keep = dict(h=n1["residual"], n1=n1["out"], row=row, act=act, y=y, n2=n2, cu=cu_seqlens,
+                    first=first, has=has_initial if first else None, whole=not pools or train)
         return n2 @ p["w_out"].t(), n1["residual"], keep
 
     def decode(self, x, residual, pools, slots):
@@ -94,15 +100,20 @@ class Mamba2Layer:
 
     def backward(self, dout, dresidual, k):
         """Gradients of the parameters, and of x (the residual's is the same)."""
+        if not k["whole"]:
+            raise ValueError("the initial states were replaced: prefill with train=True")
         p = self.p
+        first = k["first"]  # by sequence, not by slot
         z, xbc, dt = self._split(k["row"])
         xs, B, C = self._heads(k["act"])
         g = dict(w_out=dout.t() @ k["n2"])
         n2 = R.rms_norm_backward(dout @ p["w_out"], k["y"], p["gate_norm"], z=z, group_size=self.group)
         s = R.ssu_scan_backward(n2["dx"].unflatten(1, (self.H, self.P)), xs, dt, p["A"], B, C, D=p["D"],
-                                dt_bias=p["dt_bias"], cu_seqlens=k["cu"])
+                                dt_bias=p["dt_bias"], cu_seqlens=k["cu"],
+                                initial_state=first.get("scan"), has_initial=k["has"])
         dact = torch.cat([s["dx"].flatten(1), s["dB"].flatten(1), s["dC"].flatten(1)], 1)
-        c = R.causal_conv_backward(dact, xbc, p["conv"], bias=p["conv_bias"], cu_seqlens=k["cu"])
+        c = R.causal_conv_backward(dact, xbc, p["conv"], bias=p["conv_bias"], cu_seqlens=k["cu"],
+                                   initial_state=first.get("conv"), has_initial=k["has"])
         drow = torch.cat([n2["dz"], c["dx"], s["ddt"]], 1)
         # the first norm read the fp32 residual stream
         n1 = R.rms_norm_backward((drow @ p["w_in"]).float(), k["h"], p["norm"])
@@ -126,8 +137,8 @@ def main():
     at = [sum(full[:i]) for i in range(len(lens))]
     prompt = torch.cat([torch.arange(a, a + n) for a, n in zip(at, lens)]).to(dev)
     pools, slots = layer.pools(6), torch.tensor([4, 0, 5, 2], dtype=torch.int32, device=dev)
-    fresh = torch.zeros(len(lens), dtype=torch.uint8, device=dev)
-    layer.prefill(x[prompt], res[prompt], cu(lens), pools, slots, fresh)
+    none = torch.zeros(len(lens), dtype=torch.uint8, device=dev)
+    layer.prefill(x[prompt], res[prompt], cu(lens), pools, slots, none)
     worst = 0.0
     for t in range(4):
         rows = torch.tensor([a + n + t for a, n in zip(at, lens)], device=dev)
