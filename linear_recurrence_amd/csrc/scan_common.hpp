@@ -19,9 +19,6 @@
 
 namespace rssm {
 
-constexpr int kQ = 64;   // tokens of a chunk
-constexpr int kPT = 32;  // state rows of a wave
-
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
@@ -119,26 +116,11 @@ template <> struct Mat<float> {
   }
 };
 
-// A lane's address of a column fragment: K block starting at row k0, the 16
-// columns of a tile that start at c0 and, in a `paired` operand, come in
-// granules of 4 every 8 columns (see tile_col).
+// A lane's address of a column fragment.
 template <typename T, bool PAIRED>
 __device__ static inline const typename Mat<T>::E* cols_at(const typename Mat<T>::E* tile, int ld,
                                                            int k0, int c0, int lane) {
-  const int i = lane & 15, g = lane >> 4;
-  if constexpr (sizeof(typename Mat<T>::E) == 2)
-    return tile + (k0 + 4 * g + (i >> 2)) * ld + c0 + (i & 3) * (PAIRED ? 8 : 4);
-  else
-    return tile + (k0 + 4 * g) * ld + c0 + (PAIRED ? 8 * (i >> 2) + (i & 3) : i);
-}
-
-// Columns of the two tiles of a pair (32 columns) interleave in granules of 4,
-// tile j's index i standing for column 8*(i/4) + 4*j + i%4: a lane that holds
-// rows 4g..4g+3 of both tiles' results then holds 8 neighbours (16 bytes of
-// bf16), as global loads and stores want them.
-__device__ static inline int pair_base(int tile) { return 32 * (tile >> 1) + 4 * (tile & 1); }
-__device__ static inline int tile_col(int tile, int i) {
-  return pair_base(tile) + 8 * (i >> 2) + (i & 3);
+  return tile + cols_offset<sizeof(typename Mat<T>::E), PAIRED>(ld, k0, c0, lane);
 }
 
 // An fp32 operand as kTerms fragments whose sum it is: each product with an
@@ -229,41 +211,6 @@ __device__ static inline float exp2_f32(float v) { return __builtin_amdgcn_exp2f
 
 // log2 of the decay between two tokens, from their sums as (high, low) pairs.
 __device__ static inline float gap2(float2 t, float2 s) { return (t.x - s.x) + (t.y - s.y); }
-
-// Segments: runs of seg tokens (a multiple of kQ) of one sequence, worked on
-// independently.  Segment k of sequence i has the slot start_i/seg + i + k:
-// distinct for all, because a sequence of n tokens spans at least n/seg
-// (rounded up) less one multiples of seg.  At most tokens/seg + seqs slots,
-// so the host needs no lengths.
-struct Segment {
-  int seq, k, tok, len;  // len 0: nothing here, unless `empty`
-  bool first, last, empty, bad;
-};
-__device__ static inline int seg_base(const int32_t* cu, int i, int seg, int tokens) {
-  if (!cu) return 0;
-  const int a = cu[i];
-  return (a < 0 ? 0 : (a > tokens ? tokens : a)) / seg + i;
-}
-__device__ static inline Segment find_segment(const int32_t* cu, int nseq, int tokens, int seg,
-                                              int slot) {
-  int lo = 0, hi = nseq;
-  while (hi - lo > 1) {
-    const int m = (lo + hi) >> 1;
-    if (seg_base(cu, m, seg, tokens) <= slot) lo = m; else hi = m;
-  }
-  const SeqSpan sp = seq_span(cu, lo, nseq, tokens);
-  Segment r;
-  r.seq = lo;
-  r.bad = sp.bad;
-  r.k = slot - seg_base(cu, lo, seg, tokens);
-  const long off = (long)r.k * seg;
-  r.empty = sp.len == 0 && r.k == 0;
-  r.len = r.k < 0 || off >= sp.len ? 0 : (sp.len - off < seg ? (int)(sp.len - off) : seg);
-  r.tok = sp.start + (r.len ? (int)off : 0);
-  r.first = r.k == 0;
-  r.last = off + seg >= sp.len;
-  return r;
-}
 
 struct ScanArgs {
   const void* x;
@@ -447,7 +394,5 @@ __device__ static inline void rank_update(f32x4 (&acc)[NT][2], const typename Ma
     }
   }
 }
-
-static inline long scan_slots(long tokens, long seqs, long seg) { return tokens / seg + seqs; }
 
 }  // namespace rssm

@@ -4,6 +4,7 @@
 #include <type_traits>
 
 #include "rssm_device.hpp"
+#include "seq_index.hpp"
 
 namespace rssm {
 
@@ -149,22 +150,6 @@ __device__ static inline float sigmoid_f32(float v) {
 // gradient would carry whole.
 __device__ static inline float softplus_exact(float v) { return v > 20.f ? v : log1pf(expf(v)); }
 
-// Bounds of sequence i in a packed batch, forced into [0, tokens] so that a
-// malformed table can only give wrong values, never a wrong address.
-struct SeqSpan {
-  int start, len;
-  bool bad;
-};
-__device__ static inline SeqSpan seq_span(const int32_t* cu, int i, int nseq, int tokens) {
-  if (!cu) return {0, tokens, false};
-  const int a = cu[i], b = cu[i + 1];
-  const bool bad = a < 0 || b < a || b > tokens || (i == 0 && a != 0) ||
-                   (i == nseq - 1 && b != tokens);
-  const int s = a < 0 ? 0 : (a > tokens ? tokens : a);
-  const int e = b < s ? s : (b > tokens ? tokens : b);
-  return {s, e - s, bad};
-}
-
 // All of the table, by one workgroup: a kernel whose work is found by searching
 // the table does not meet every entry of one that is not monotone.
 __device__ static inline void check_table(const int32_t* cu, int nseq, int tokens, int32_t* status) {
@@ -172,18 +157,6 @@ __device__ static inline void check_table(const int32_t* cu, int nseq, int token
   bool bad = false;
   for (int i = threadIdx.x; i < nseq; i += blockDim.x) bad |= seq_span(cu, i, nseq, tokens).bad;
   if (bad) atomicOr(status, RSSM_ST_BAD_SEQ);
-}
-
-// The last sequence whose start is at or before token t (binary search over
-// the nseq starts; the table is monotone, or the result is merely arbitrary).
-__device__ static inline int seq_of_token(const int32_t* cu, int nseq, int t) {
-  if (!cu) return 0;
-  int lo = 0, hi = nseq;
-  while (hi - lo > 1) {
-    const int m = (lo + hi) >> 1;
-    if (cu[m] <= t) lo = m; else hi = m;
-  }
-  return lo;
 }
 
 }  // namespace rssm
