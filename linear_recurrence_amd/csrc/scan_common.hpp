@@ -320,11 +320,9 @@ __device__ static inline ChunkDt chunk_dt(const ScanArgs& a, int h, float bias, 
   return c;
 }
 
-// dt and the running sums of dt*A of one chunk and head, a wave each; and the
-// table's check, as the first launch of every call that has one.
+// dt and the running sums of dt*A of one chunk and head, a wave each.
 template <typename T>
 static __global__ void __launch_bounds__(256) scan_decay_kernel(const ScanArgs a) {
-  if (blockIdx.x == 0) check_table(a.cu, a.seqs, a.tokens, a.status);
   const int lane = threadIdx.x & 63, hq = (a.nheads + 3) / 4;
   const long slot = blockIdx.x / hq;
   const int h = (int)(blockIdx.x % hq) * 4 + (threadIdx.x >> 6);

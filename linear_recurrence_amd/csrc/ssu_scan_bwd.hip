@@ -379,10 +379,9 @@ __global__ void __launch_bounds__(64 * bwd_waves(sizeof(typename Mat<T>::E) == 4
   const Segment sg = find_segment(a.cu, a.seqs, a.tokens, kQ, slot);
   const int u0 = hblk * a.upb, u1 = u0 + a.upb < a.upg ? u0 + a.upb : a.upg;
   const int units = a.upg * a.ngroups, per = a.headdim / PB;
-  if (threadIdx.x == 0 && rest == 0 && sg.first && a.status) {
-    if (sg.bad) atomicOr(a.status, RSSM_ST_BAD_SEQ);
-    if (a.init && scan_slot(a, sg.seq) < 0) atomicOr(a.status, RSSM_ST_BAD_SLOT);
-  }
+  if (blockIdx.x == 0) check_table(a.cu, a.seqs, a.tokens, a.status);
+  if (threadIdx.x == 0 && rest == 0 && sg.first && a.status && a.init && scan_slot(a, sg.seq) < 0)
+    atomicOr(a.status, RSSM_ST_BAD_SLOT);
   f32x4* const hp = reinterpret_cast<f32x4*>(b.head_part) + (long)slot * units + grp * a.upg;
   if (sg.len == 0) {
     for (int u = u0 + (int)threadIdx.x; u < u1; u += TH) hp[u] = f32x4{0.f, 0.f, 0.f, 0.f};
