@@ -493,8 +493,10 @@ int replayssm_flush_first_order(int32_t n_rows, const uint8_t* is_flush, int32_t
  *    call gives the same bits.
  *  - A call whose launches would hold 2^32 threads or more is refused
  *    (RSSM_ESHAPE): a norm forward from 2^22 rows on (above 8192 elements; 2^26
- *    up to 1024), a convolution from 2^28 tokens of 512 channels on, a scan
- *    from 2^34 / (nheads*headdim*dstate) sequences on (backward 2^32 / that).
+ *    up to 1024), a convolution's decode step from 2^28 rows of 512 channels, a
+ *    scan from 2^34 / (nheads*headdim*dstate) sequences on (backward 2^32 / that).
+ *  - Sequences of one call that write to a pool (final_state,
+ *    dinitial_state by slot) take slots of their own.
  *  - An output may share memory with an input only where its description
  *    says so: workgroups read rows that others have work to do on.
  */
@@ -589,8 +591,8 @@ typedef struct rssm_norm_dims {
  *     u = h * z * sigmoid(z)    (z NULL: u = h)
  *     y = u * rsqrt(mean over the group of u^2 + eps) * weight
  *   out = y in io_dtype, or the e4m3 values of y / scale with scale =
- *   max|y| / 448 over the row or block (1 where that is 0, and at least the
- *   smallest normal number): scale [rows] or [rows, dim/128] float32.
+ *   max|y| / 448 over the row or block (1 where that is 0 or NaN, whose e4m3
+ *   values are NaN, and at least the smallest normal number): scale [rows] or [rows, dim/128] float32.
  *   residual_out may be residual.
  */
 int rms_norm_forward(const rssm_norm_dims* dims, const void* x, const float* weight,

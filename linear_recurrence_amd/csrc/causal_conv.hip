@@ -7,7 +7,7 @@
 // walks along the tokens with the window in registers: every x row is read
 // once per run of tokens, plus W-1 rows where a run starts.  All of it is
 // memory bound (2 W flops per 4 bytes).  5376 channels, W 4, bf16: 16383 tokens
-// forward 76 us (0.35 GB, 4.6 TB/s), 16384 backward 129 us (0.53 GB, 4.1 TB/s),
+// forward 76 us (0.35 GB, 4.6 TB/s), 16384 backward 124 us (0.53 GB, 4.3 TB/s),
 // 512 decode rows 11 us (44 MB, 4.0 TB/s).
 #include "rssm_host.hpp"
 #include "seq_device.hpp"

@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(64 * scan_waves(sizeof(typename Mat<T>::E) == 
 // and the final one in its pool; otherwise from zero, leaving what the segment
 // adds.  The next chunk's tiles are on their way while one is worked on.
 // Slots without a segment lie in runs, so blocks go to the dies in turn.
-// 16383 tokens of 80 heads: 219 us storing (0.84 GB: 3.8 TB/s), 110 us not.
+// 16383 tokens of 80 heads: 218 us storing (0.84 GB: 3.8 TB/s), 110 us not.
 template <typename T, int N, bool STORE>
 __global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 1 : (N == 256 ? 2 : 3))
     scan_fwd_states_kernel(const ScanArgs a) {
@@ -580,8 +580,12 @@ __global__ void __launch_bounds__(256) scan_combine_kernel(const ScanArgs a) {
 }
 
 // Calls of up to this many tokens take one launch, a chain of two chunks at most;
-// the other way is three launches.  One bf16 sequence, 80 heads, dstate 128: 128
-// tokens 22 us (26 the other way), 256 35 us (33), 512 61 us (56).
+// the other way is three launches.  The lengths are on the device, so the total has
+// to do for the worst that it can stand for, one long sequence.  80 heads, dstate
+// 128, one launch (the other way in brackets), bf16: 128 tokens 25 us (32), 256
+// 41 (39), 512 74 (63); fp32: 42 (49), 75 (64), 148 (101).  1024 bf16 tokens would
+// gain in 16 sequences of 64, 42 us (68), and lose in one of 1009 and 15 of one
+// token, 192 (96).
 constexpr int kShort = 128;
 
 // Tokens of a segment: enough segments to give every one of the 1024 SIMDs two
@@ -709,8 +713,7 @@ extern "C" int ssu_scan_forward(const rssm_scan_dims* dims, const void* x, const
   const long cslots = scan_slots(d.tokens, d.seqs, kQ);
   // Units of a workgroup of the output launch: up to four a wave, which share
   // the chunk's C.B, but so few that there is a workgroup for every compute unit.
-  // 4096 tokens of 80 heads: 16 units 118 us, 8 127; 16383: 16 units 452 us, 8
-  // 456, 32 472.
+  // 16383 tokens of 80 heads: 16 units 613 us, 8 615, 32 655; 4096: 168 us with each.
   a.upg = d.nheads / d.ngroups * (d.headdim == 32 ? 1 : d.headdim / 64);
   a.upb = 16;
   while (a.upb > 4 && cslots * d.ngroups * ((a.upg + a.upb - 1) / a.upb) < 256) a.upb >>= 1;

@@ -28,7 +28,7 @@
 // Every factor that is not an input (S_in, dS, K and e^{a_u-a_t} C_u.B_t) enters
 // its products as three bf16 terms (fp32 inputs: as it is), so nothing is rounded
 // to the io type but the results.  Two terms would be 5% faster (8 x 2048 tokens of
-// 80 heads 1156 us instead of 1240) and leave three times the fp32 sums' own
+// 80 heads: 1156 us instead of 1240 on one card) and leave three times the fp32 sums' own
 // error in dB and dC; one would take dx's error without D to 1.4 times that of
 // rounding it.
 #include "scan_common.hpp"
@@ -492,8 +492,8 @@ __global__ void __launch_bounds__(64 * bwd_waves(sizeof(typename Mat<T>::E) == 4
       for (int j = 0; j < 4; ++j) forget(rc[q][j]);
     // The states' first column tile is on its way during the tokens' products.
     // Unconditional from 64 columns on: behind a condition these loads could not
-    // be told from the x and dy in flight, whose wait then took them in (1165 us
-    // instead of 1088 for 8 x 2048 tokens of 80 heads).
+    // be told from the x and dy in flight, whose wait then took them in (1322 us
+    // instead of 1250 for 8 x 2048 tokens of 80 heads).
     if (NT >= W || wave * NW < NT) {
       load(ls, a.chunk_state, u, wave * NW);
       load(lg, b.grad_state, u, wave * NW);
@@ -891,9 +891,9 @@ static int bwd_seg(const rssm_scan_dims& d) {
 // Units of a workgroup of the main launch: up to sixteen, which share the chunk's
 // C.B and join dB and dC without memory, but so few that there are two
 // workgroups for each place (one a compute unit with eight waves, two with
-// four).  8 x 2048 tokens of 80 heads: 16 units 1059 us, 8 1104, 4 1194; two
+// four).  8 x 2048 tokens of 80 heads: 16 units 1250 us, 8 1291, 4 1393; two
 // uneven sequences of 1291 tokens, 128 heads in 8 groups: two workgroups a place
-// 237 us, one 254, four 259.
+// 264 us, one or four 288.
 static int bwd_units(const rssm_scan_dims& d, int upg) {
   const long blocks = ((long)d.tokens / kQ + d.seqs) * d.ngroups;
   const long least = bwd_waves(d.io_dtype == RSSM_F32, d.dstate) == 8 ? 512 : 1024;
