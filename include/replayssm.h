@@ -676,6 +676,145 @@ int ssu_scan_backward(const rssm_scan_dims* dims, const void* dy, const void* x,
                       float* ddt_bias, float* dinitial_state, void* workspace,
                       size_t workspace_bytes, int32_t* status, hipStream_t stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Operators of linear-attention layers: linear attention with a decay for each
+ * head, the gated delta rule over whole sequences (it fills the pools that the
+ * GDN decode entry points read), and rotary positions.  The conventions of the
+ * sequence operators hold (packed sequences, token strides, workspaces).
+ *
+ * Decays are given as natural logarithms, log g <= 0 as a rule; -infinity
+ * forgets the state.  Value head hv reads key head hv / (v_heads / k_heads).
+ * States are float32 [num_slots, v_heads, dv, dk], as in the GDN pools.
+ */
+enum { RSSM_DECAY_NONE = 0, RSSM_DECAY_HEAD = 1, RSSM_DECAY_TOKEN = 2 };
+
+typedef struct rssm_mixer_dims {
+  int32_t tokens;     /* T (decode: batch rows)                             */
+  int32_t seqs;       /* sequences (ignored by the decode step)             */
+  int32_t k_heads;
+  int32_t v_heads;
+  int32_t dk;         /* K: 64 or 128                                       */
+  int32_t dv;         /* V: 64 or 128 (the gated delta rule: dv == dk)      */
+  int32_t num_slots;  /* first dimension of the state pools                 */
+  int32_t io_dtype;   /* q, k, v, o and their gradients                     */
+  int32_t decay;      /* RSSM_DECAY_*: no decay, log g [v_heads], or        */
+                      /* [tokens, v_heads] (the gated delta rule: the last) */
+  float scale;        /* of the outputs; <= 0 selects 1/sqrt(dk)            */
+  int64_t q_stride;   /* elements between two tokens of q, k [T, HK, K]     */
+  int64_t k_stride;
+  int64_t v_stride;   /* v, do [T, HV, V]                                   */
+  int64_t do_stride;
+} rssm_mixer_dims;
+
+/*
+ * linear_attention_forward - for every sequence i (slot s = slot_idx[i], NULL:
+ * i) and value head, from S = initial_state[s] (zeros where initial_state is
+ * NULL or has_initial[i] is 0), token by token
+ *     S = g*S + outer(v, k);  o = scale * S @ q
+ * and final_state[s] = S (may be initial_state, or NULL).  q, k, v, o [16B]
+ * with token strides that are multiples of 16 bytes; o [tokens, HV, V] dense.
+ * A slot out of range sets RSSM_ST_BAD_SLOT: its sequence starts from zeros and
+ * stores no state.  Tokens are worked on in chunks of 64 of one sequence: a NaN
+ * or infinity in a token's inputs may also show in the up to 63 tokens of its
+ * sequence and chunk before it, and never in another sequence.
+ */
+int linear_attention_forward(const rssm_mixer_dims* dims, const void* q, const void* k,
+                             const void* v, const float* log_decay,
+                             const int32_t* cu_seqlens, const float* initial_state,
+                             const uint8_t* has_initial, const int32_t* slot_idx,
+                             float* final_state, void* o, int32_t* status,
+                             hipStream_t stream);
+
+/*
+ * linear_attention_backward - gradients of linear_attention_forward, given do
+ * [tokens, HV, V] and dfinal_state [seqs, HV, V, K] float32 (the gradient of
+ * each sequence's last state, by sequence and not by slot; NULL: zeros):
+ *   dq, dk [T, HK, K], dv [T, HV, V] io_dtype; dlog_decay float32 in the shape
+ *   of log_decay (NULL without one); dinitial_state [seqs, HV, V, K] float32 by
+ *   sequence, zeros where has_initial[i] is 0 (NULL: not computed).
+ */
+size_t linear_attention_backward_workspace(const rssm_mixer_dims* dims);
+int linear_attention_backward(const rssm_mixer_dims* dims, const void* dout, const void* q,
+                              const void* k, const void* v, const float* log_decay,
+                              const int32_t* cu_seqlens, const float* initial_state,
+                              const uint8_t* has_initial, const int32_t* slot_idx,
+                              const float* dfinal_state, void* dq, void* dk, void* dv,
+                              float* dlog_decay, float* dinitial_state, void* workspace,
+                              size_t workspace_bytes, int32_t* status, hipStream_t stream);
+
+/*
+ * linear_attention_decode - one token of dims->tokens rows: row b's state is
+ * slot slot_idx[b] (NULL: b) of state; the moved-on state goes to the same slot
+ * of new_state (may be state).  A slot out of range sets RSSM_ST_BAD_SLOT, its o
+ * is NaN and no state is written.
+ */
+int linear_attention_decode(const rssm_mixer_dims* dims, const float* state,
+                            const int32_t* slot_idx, const void* q, const void* k,
+                            const void* v, const float* log_decay, float* new_state,
+                            void* o, int32_t* status, hipStream_t stream);
+
+/*
+ * gdn_scan_forward - the recurrence of gdn_standard_decode applied to every
+ * token of packed sequences, with g = exp(log_g):
+ *     S = g*S;  S += beta * outer(v - S@k, k);  o = scale * S@q
+ * log_g, beta [tokens, HV] float32; the rest as linear_attention_forward.
+ */
+size_t gdn_scan_forward_workspace(const rssm_mixer_dims* dims);
+int gdn_scan_forward(const rssm_mixer_dims* dims, const void* q, const void* k,
+                     const void* v, const float* log_g, const float* beta,
+                     const int32_t* cu_seqlens, const float* initial_state,
+                     const uint8_t* has_initial, const int32_t* slot_idx,
+                     float* final_state, void* o, void* workspace,
+                     size_t workspace_bytes, int32_t* status, hipStream_t stream);
+
+/*
+ * gdn_scan_backward - its gradients: dq, dk, dv io_dtype; dlog_g, dbeta
+ * [tokens, HV] float32; dfinal_state and dinitial_state as
+ * linear_attention_backward.
+ */
+size_t gdn_scan_backward_workspace(const rssm_mixer_dims* dims);
+int gdn_scan_backward(const rssm_mixer_dims* dims, const void* dout, const void* q,
+                      const void* k, const void* v, const float* log_g,
+                      const float* beta, const int32_t* cu_seqlens,
+                      const float* initial_state, const uint8_t* has_initial,
+                      const int32_t* slot_idx, const float* dfinal_state, void* dq,
+                      void* dk, void* dv, float* dlog_g, float* dbeta,
+                      float* dinitial_state, void* workspace, size_t workspace_bytes,
+                      int32_t* status, hipStream_t stream);
+
+/*
+ * Rotary positions: the first rotary_dim elements of every head turn in pairs,
+ * pair i by the angle position * freqs[i]; the others are copied.
+ */
+typedef struct rssm_rotary_dims {
+  int32_t tokens;
+  int32_t heads;
+  int32_t dim;          /* elements of a head, up to 1024                   */
+  int32_t rotary_dim;   /* even, 2 to dim                                   */
+  int32_t io_dtype;
+  int32_t interleaved;  /* nonzero: pair i is elements (2i, 2i + 1);        */
+                        /* 0: (i, i + rotary_dim / 2)                       */
+  int32_t pos_int64;    /* nonzero: positions are int64, else int32         */
+  float amplitude;      /* factor of the turned elements                    */
+  int64_t x_stride;     /* elements between two tokens (0: dense)           */
+  int64_t y_stride;
+} rssm_rotary_dims;
+
+/*
+ * rotary_forward - x [tokens, heads, dim], positions [tokens], freqs
+ * [rotary_dim / 2] float32 -> y, which may be x itself (with the same stride)
+ * and otherwise shares no memory with it.  For a pair (a, b) and its angle t,
+ *     (a', b') = amplitude * (a cos t - b sin t, a sin t + b cos t).
+ * The angle and its sine and cosine are formed in 64 bits.
+ *
+ * rotary_backward - the gradient dx of x, given y's gradient dy: the turn back.
+ */
+int rotary_forward(const rssm_rotary_dims* dims, const void* x, const void* positions,
+                   const float* freqs, void* y, hipStream_t stream);
+int rotary_backward(const rssm_rotary_dims* dims, const void* dy, const void* positions,
+                    const float* freqs, void* dx, hipStream_t stream);
+
 /* Human-readable text of a return code (static storage). */
 const char* replayssm_strerror(int code);
 

@@ -25,6 +25,9 @@ __all__ = [
     "check_copy_sources", "library_path", "load",
     "ssu_scan_forward", "ssu_scan_backward", "causal_conv_forward", "causal_conv_backward",
     "causal_conv_decode", "rms_norm_forward", "rms_norm_backward", "ST_BAD_SEQ",
+    "linear_attention_forward", "linear_attention_backward", "linear_attention_decode",
+    "gdn_scan_forward", "gdn_scan_backward", "rotary_forward", "rotary_backward",
+    "rotary_frequencies",
     "RssmError", "ST_BAD_WRITE_POS", "ST_RING_OVERFLOW", "ST_BAD_SLOT",
     "ST_BAD_ROW", "EXPORTS",
 ]
@@ -42,7 +45,10 @@ EXPORTS = ("ssu_standard_decode", "replayssm_decode", "replayssm_ring_reset",
            "ssu_scan_forward", "ssu_scan_forward_workspace", "ssu_scan_backward",
            "ssu_scan_backward_workspace", "causal_conv_forward", "causal_conv_backward",
            "causal_conv_backward_workspace", "causal_conv_decode", "rms_norm_forward",
-           "rms_norm_backward", "rms_norm_backward_workspace")
+           "rms_norm_backward", "rms_norm_backward_workspace", "linear_attention_forward",
+           "linear_attention_backward", "linear_attention_backward_workspace",
+           "linear_attention_decode", "gdn_scan_forward", "gdn_scan_forward_workspace",
+           "gdn_scan_backward", "gdn_scan_backward_workspace", "rotary_forward", "rotary_backward")
 
 _DT = {torch.float32: F32, torch.bfloat16: BF16}
 
@@ -116,6 +122,7 @@ def load():
     lib.replayssm_strerror.restype = ctypes.c_char_p
     lib.replayssm_abi_version.restype = ctypes.c_int
     sequence.bind(lib)
+    mixer.bind(lib)
     _lib = lib
     return lib
 
@@ -589,3 +596,7 @@ from . import sequence  # noqa: E402  (uses the helpers above)
 from .sequence import (  # noqa: E402
     causal_conv_backward, causal_conv_decode, causal_conv_forward, rms_norm_backward,
     rms_norm_forward, ssu_scan_backward, ssu_scan_forward)
+from . import mixer  # noqa: E402
+from .mixer import (  # noqa: E402
+    gdn_scan_backward, gdn_scan_forward, linear_attention_backward, linear_attention_decode,
+    linear_attention_forward, rotary_backward, rotary_forward, rotary_frequencies)

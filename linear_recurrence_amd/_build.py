@@ -18,7 +18,8 @@ OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libreplayssm.so")
 SOURCES = ("mamba2_decode.hip", "mamba2_sr.hip", "mamba2_small.hip", "gdn_decode.hip",
            "gdn_spec.hip", "causal_conv.hip", "rms_norm.hip", "ssu_scan.hip",
-           "ssu_scan_bwd.hip", "metadata.cpp")
+           "ssu_scan_bwd.hip", "mixer_fwd.hip", "mixer_bwd.hip", "mixer_step.hip", "rotary.hip",
+           "metadata.cpp")
 CXX = os.environ.get("CXX", "g++")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -1,0 +1,919 @@
+// Linear attention and the gated delta rule over packed sequences, backward.
+//
+// With the chunk's quantities of mixer_common.hpp, P_ij = scale c_ij q_i.k_j (i >= j),
+// dS' the gradient of the state after the chunk (linear attention: dD itself is dV,
+// D = V, and what has dX in it is left out):
+//   dD = P^T dO + e^{G_Q-G} K dS',  dX = T^T dD,  dV = beta dX
+//   dS = e^{G_Q} dS' + (scale e^G Q)^T dO - (beta e^G K)^T dX
+//   N_ij = scale c_ij dO_i.d_j (i >= j),  L_ij = -beta_i c_ij dX_i.d_j (i > j)
+//   dq = scale e^G dO S^T + N K
+//   dk = e^{G_Q-G} D dS'^T - beta e^G dX S^T + N^T Q + (L + L^T) K
+//   dbeta_i = dX_i.v_i - e^{G_i} dX_i.(S^T k_i) - sum_{j<i} c_ij (k_i.k_j) (dX_i.d_j)
+// and for the decays, with w_ij = (q_i.k_j) N_ij + (k_i.k_j) L_ij (i > j),
+//   dG_i = sum_j w_ij - sum_j w_ji + scale e^{G_i} q_i.(dO_i S^T)
+//          - beta_i e^{G_i} k_i.(dX_i S^T) - take_i,   take = e^{G_Q-G} k.(D dS'^T)
+//   dg_t = sum_{i>=t} dG_i + sum take + e^{G_Q} <S, dS'>    (one chunk's tokens)
+// dX_i.d_i / beta_i would be dbeta in a word, and has no value at beta = 0.
+//
+// Launches: (1) T of every chunk (the delta rule); (2) both recurrences over the
+// chunks, the states and D forward, their gradients and dX backward, which leave
+// every chunk's in the workspace in fp32; (3) the rest, a workgroup for one chunk and
+// key head, which needs nothing from other chunks; (4) decays of a head: its sum.
+//
+// What is not an input enters the products as three bf16 terms, pairs of such factors
+// as the six products that fp32 can hold, because dg and dbeta are fp32 results; N and
+// L, which only dq and dk read, as two (2^-17 of each term; dq and dk are rounded to
+// 2^-9 of themselves).  fp32 inputs stay fp32.
+#include "mixer_common.hpp"
+
+namespace rssm {
+
+struct MixBwdArgs {
+  MixArgs m;
+  const void* dout;
+  const float* dfinal;
+  void* dq;
+  void* dk;
+  void* dv;
+  float* dg;
+  float* dbeta;
+  float* dinit;
+  float* state;  // [chunk slots][v_heads][V][K]: before the chunk
+  float* grad;   // dS', the same
+  float* D;      // [chunk slots][v_heads][64][V]
+  float* dX;     // the same
+  float* part;   // [chunk slots][v_heads]: dg summed over the chunk
+  long do_stride, cslots;
+  int32_t dir_blocks;
+};
+
+template <typename T, int K, bool DELTA>
+struct StatesLds {
+  typedef typename Mat<T>::E E;
+  static constexpr int kFrag = sizeof(typename Mat<T>::Frag), TS = Mat<T>::kTerms;
+  static constexpr int LK = K + Mat<T>::kPad;
+  static constexpr int TF = 6 * TS * 64 * kFrag / 16;  // 16-byte pieces of T or its transpose
+  __attribute__((aligned(16))) E k[kQ * LK];
+  __attribute__((aligned(16))) E q[kQ * LK];
+  __attribute__((aligned(16))) E v[kQ * 64];  // V forward, dO backward
+  __attribute__((aligned(16))) u32x4 t[DELTA ? TF : 1];
+  __attribute__((aligned(16))) u32x4 p[TF];
+  ChunkGates g;
+};
+
+// One of the two recurrences, a workgroup for 64 columns of one value head's state and
+// one sequence (mix_forward_kernel without the outputs; blocks from dir_blocks on:
+// backward, last chunk first).
+template <typename T, int K, bool DELTA>
+__global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 1 : 2)
+    mix_states_kernel(const MixBwdArgs b) {
+  typedef Mat<T> M;
+  typedef typename M::E E;
+  typedef typename M::Frag Frag;
+  typedef StatesLds<T, K, DELTA> L;
+  constexpr int TS = M::kTerms, LK = L::LK, KT = K / 16, KB = K / 32, TF = L::TF;
+  constexpr int QT = DELTA ? (TF + 255) / 256 : 1;
+  __shared__ L s;
+  const MixArgs& a = b.m;
+  int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const bool back = (int)blockIdx.x >= b.dir_blocks;
+  const MixUnit un = mix_unit(a, back ? blockIdx.x - b.dir_blocks : blockIdx.x, a.vpk * a.slices);
+  if (blockIdx.x == 0) check_table(a.cu, a.seqs, a.tokens, a.status);
+  if (!un.live) return;
+  const int hv = un.hk * a.vpk + un.rest / a.slices, v0 = (un.rest % a.slices) * 64;
+  const SeqSpan sp = seq_span(a.cu, un.seq, a.seqs, a.tokens);
+  const int pool = a.init ? mix_slot(a, un.seq) : -1;
+  if (tid == 0 && !back && un.rest == 0 && un.hk == 0 && a.status && a.init && pool < 0)
+    atomicOr(a.status, RSSM_ST_BAD_SLOT);
+  const bool has = pool >= 0 && (!a.has_init || a.has_init[un.seq]);
+  f32x4 S[KT];
+#pragma unroll
+  for (int kt = 0; kt < KT; ++kt) S[kt] = f32x4{0.f, 0.f, 0.f, 0.f};
+  // this lane's first element in state number n
+  const auto place = [&](long n) {
+    return ((n * a.v_heads + hv) * a.dv + v0 + 16 * wave + (lane & 15)) * K + 4 * (lane >> 4);
+  };
+  {
+    const float* src = back ? b.dfinal : (has ? a.init : nullptr);
+    if (src) {
+      src += place(back ? un.seq : pool);
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt) S[kt] = *reinterpret_cast<const f32x4*>(src + 16 * kt);
+    }
+  }
+  const E* const ksrc = static_cast<const E*>(a.k) + (long)un.hk * K;
+  const E* const qsrc = static_cast<const E*>(a.q) + (long)un.hk * K;
+  const E* const vsrc = static_cast<const E*>(back ? b.dout : a.v) + (long)hv * a.dv + v0;
+  const long vstride = back ? b.do_stride : a.v_stride;
+  const long cbase = seg_base(a.cu, un.seq, kQ, a.tokens);
+  const int chunks = (sp.len + kQ - 1) / kQ;
+  TileLoad<T, K, 256> rk, rq;
+  TileLoad<T, 64, 256> rv;
+  u32x4 rt[QT];
+  double rg = 0.0;
+  float rb = 0.f;
+  const auto fetch = [&](int c) {
+    const int rows = sp.len - c * kQ < kQ ? sp.len - c * kQ : kQ;
+    const long t0 = sp.start + (long)c * kQ;
+    rk.fetch(ksrc + t0 * a.k_stride, a.k_stride, rows, tid);
+    if (back) rq.fetch(qsrc + t0 * a.q_stride, a.q_stride, rows, tid);
+    rv.fetch(vsrc + t0 * vstride, vstride, rows, tid);
+    if (DELTA) {
+      const u32x4* src = static_cast<const u32x4*>(a.tinv) + (((cbase + c) * a.v_heads + hv) * 2 + back) * TF;
+#pragma unroll
+      for (int i = 0; i < QT; ++i)
+        if (TF % 256 == 0 || i * 256 + tid < TF) rt[i] = src[i * 256 + tid];
+    }
+    const bool live = lane < rows;
+    rg = gate_log2(a, t0 + lane, hv, live);
+    if (DELTA) rb = live ? a.beta[(t0 + lane) * a.v_heads + hv] : 0.f;
+  };
+  float* const keep = back ? b.grad : b.state;
+  float* const rowmat = back ? b.dX : b.D;
+  if (chunks) fetch(back ? chunks - 1 : 0);
+#pragma unroll 1
+  for (int n = 0; n < chunks; ++n) {
+    const int c = back ? chunks - 1 - n : n;
+    tid = threadIdx.x;
+    forget(tid);
+    lane = tid & 63;
+    const int i16 = lane & 15, g = lane >> 4;
+    const int rows = sp.len - c * kQ < kQ ? sp.len - c * kQ : kQ;
+    const long t0 = sp.start + (long)c * kQ;
+    {
+      float* p = keep + place(cbase + c);
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt) *reinterpret_cast<f32x4*>(p + 16 * kt) = S[kt];
+    }
+    __syncthreads();  // the previous chunk's tiles are no longer read
+    rk.put(s.k, LK, tid);
+    if (back) rq.put(s.q, LK, tid);
+    rv.put(s.v, 64, tid);
+    if (DELTA) {
+#pragma unroll
+      for (int i = 0; i < QT; ++i)
+        if (TF % 256 == 0 || i * 256 + tid < TF) s.t[i * 256 + tid] = rt[i];
+    }
+    if (wave == 3) s.g.set(rg, rb, lane);
+    if (n + 1 < chunks) fetch(back ? c - 1 : c + 1);
+    __syncthreads();
+    if (back) {
+      // P^T by rows j, fragments (0, 1); (0, 0) and (3, 1); (1, 1); (2, 1) and (1, 0)
+      const auto make = [&](int jt, int kb) {
+        f32x4 acc[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) acc[h] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int x = 0; x < KB; ++x) {
+          const Frag kf = M::rows_c(s.k + (16 * jt + i16) * LK + 32 * x + 8 * g);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            if (2 * kb + h >= jt)
+              acc[h] = M::mma(M::rows_c(s.q + (16 * (2 * kb + h) + i16) * LK + 32 * x + 8 * g), kf, acc[h]);
+        }
+        const int j = 16 * jt + i16;
+        const float2 gj = s.g.G[j];
+        float f[8];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int i = 16 * (2 * kb + h) + 4 * g + r;
+            const float w = a.scale * exp2_f32(gap2(s.g.G[i], gj)) * acc[h][r];
+            f[4 * h + r] = i >= j ? w : 0.f;
+          }
+        Split<T, TS> sp3;
+        sp3.set(f);
+        put_split<T, TS>(s.p, up_frag(jt, kb), sp3, lane);
+      };
+      if (wave == 0) {
+        make(0, 1);
+      } else if (wave == 1) {
+        make(0, 0);
+        make(3, 1);
+      } else if (wave == 2) {
+        make(1, 1);
+      } else {
+        make(2, 1);
+        make(1, 0);
+      }
+    }
+    // K S (or K dS'), rows t
+    f32x4 R[4];
+#pragma unroll
+    for (int it = 0; it < 4; ++it) R[it] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (DELTA || back) {
+#pragma unroll
+      for (int x = 0; x < KB; ++x) {
+        float f[8];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          f[r] = S[2 * x][r];
+          f[4 + r] = S[2 * x + 1][r];
+        }
+        Split<T, TS> sf;
+        sf.set(f);
+        Frag kf[4];
+#pragma unroll
+        for (int it = 0; it < 4; ++it) kf[it] = M::rows_d(s.k + (16 * it + i16) * LK + 32 * x + 4 * g);
+#pragma unroll
+        for (int k = TS - 1; k >= 0; --k)
+#pragma unroll
+          for (int it = 0; it < 4; ++it) R[it] = M::mma(kf[it], sf.t[k], R[it]);
+      }
+    }
+    if (back) __syncthreads();  // s.p
+    float d[2][8];  // tokens 32 kb + (4g + r, 16 + 4g + r), this lane's column
+    Frag vf[2];
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+      vf[kb] = M::cols(cols_at<T, false>(s.v, 64, 32 * kb, 16 * wave, lane), 64);
+      M::unpack(vf[kb], d[kb]);
+    }
+    if (back) {  // dD
+#pragma unroll
+      for (int it = 0; it < 4; ++it) {
+        const f32x4 e = *reinterpret_cast<const f32x4*>(&s.g.et[16 * it + 4 * g]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) R[it][r] *= e[r];
+#pragma unroll
+        for (int kb = it / 2; kb < 2; ++kb) {
+          const auto pf = split_at<T, TS>(s.p, up_frag(it, kb), lane);
+          R[it] = pf.a_times(vf[kb], R[it]);
+        }
+      }
+    } else if (DELTA) {  // X
+#pragma unroll
+      for (int it = 0; it < 4; ++it) {
+        const f32x4 e = *reinterpret_cast<const f32x4*>(&s.g.eg[16 * it + 4 * g]);
+        const f32x4 be = *reinterpret_cast<const f32x4*>(&s.g.beta[16 * it + 4 * g]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) R[it][r] = be[r] * fmaf(-e[r], R[it][r], d[it >> 1][4 * (it & 1) + r]);
+      }
+    }
+    if (DELTA) {  // D = T X, or dX = T^T dD
+      f32x4 acc[4];
+      Split<T, TS> xf[2];
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) {
+        float f[8];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          f[r] = R[2 * kb][r];
+          f[4 + r] = R[2 * kb + 1][r];
+        }
+        xf[kb].set(f);
+      }
+#pragma unroll
+      for (int it = 0; it < 4; ++it) acc[it] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (back) {
+#pragma unroll
+        for (int it = 0; it < 4; ++it)
+#pragma unroll
+          for (int kb = it / 2; kb < 2; ++kb)
+            acc[it] = mma_split<T, TS, TS>(split_at<T, TS>(s.t, up_frag(it, kb), lane), xf[kb], acc[it]);
+      } else {
+#pragma unroll
+        for (int it = 0; it < 4; ++it)
+#pragma unroll
+          for (int kb = 0; kb <= it / 2; ++kb)
+            acc[it] = mma_split<T, TS, TS>(split_at<T, TS>(s.t, low_frag(it, kb), lane), xf[kb], acc[it]);
+      }
+      float* p = rowmat + ((cbase + c) * a.v_heads + hv) * (long)(kQ * a.dv) + v0 + 16 * wave + i16;
+#pragma unroll
+      for (int it = 0; it < 4; ++it) {
+        R[it] = acc[it];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) p[(16 * it + 4 * g + r) * a.dv] = acc[it][r];
+      }
+    } else if (back) {  // linear attention: dV
+#pragma unroll
+      for (int it = 0; it < 4; ++it)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int t = 16 * it + 4 * g + r;
+          if (t < rows) Elt<T>::store1(b.dv, ((t0 + t) * a.v_heads + hv) * a.dv + v0 + 16 * wave + i16, R[it][r]);
+        }
+    }
+    if (!back && n + 1 == chunks) break;  // the end is not read
+    const float all = s.g.all;
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) S[kt][r] *= all;
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+      if (32 * kb >= rows) break;
+      float f[8];  // the weighted rows that go with K (D; backward: dX), and with Q (dO)
+      float o[8];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int at = 32 * kb + 16 * h + 4 * g;
+        const f32x4 e = *reinterpret_cast<const f32x4*>(back ? &s.g.eg[at] : &s.g.et[at]);
+        const f32x4 be = *reinterpret_cast<const f32x4*>(&s.g.beta[at]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          o[4 * h + r] = a.scale * e[r] * d[kb][4 * h + r];
+          f[4 * h + r] = back ? -be[r] * e[r] * R[2 * kb + h][r]
+                              : e[r] * (DELTA ? R[2 * kb + h][r] : d[kb][4 * h + r]);
+        }
+      }
+      Split<T, TS> wf;
+      if (DELTA || !back) {
+        wf.set(f);
+#pragma unroll
+        for (int k4 = 0; k4 < KT; k4 += 4) {
+          Frag kf[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) kf[x] = M::cols(cols_at<T, false>(s.k, LK, 32 * kb, 16 * (k4 + x), lane), LK);
+#pragma unroll
+          for (int k = TS - 1; k >= 0; --k)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) S[k4 + x] = M::mma(kf[x], wf.t[k], S[k4 + x]);
+        }
+      }
+      if (back) {
+        wf.set(o);
+#pragma unroll
+        for (int k4 = 0; k4 < KT; k4 += 4) {
+          Frag qf[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) qf[x] = M::cols(cols_at<T, false>(s.q, LK, 32 * kb, 16 * (k4 + x), lane), LK);
+#pragma unroll
+          for (int k = TS - 1; k >= 0; --k)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) S[k4 + x] = M::mma(qf[x], wf.t[k], S[k4 + x]);
+        }
+      }
+    }
+  }
+  if (back && b.dinit) {
+    float* p = b.dinit + place(un.seq);
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt)
+      *reinterpret_cast<f32x4*>(p + 16 * kt) = has ? S[kt] : f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+}
+
+template <typename T, int K, bool DELTA>
+struct MainLds {
+  typedef typename Mat<T>::E E;
+  static constexpr int kFrag = 64 * sizeof(typename Mat<T>::Frag), TS = Mat<T>::kTerms;
+  static constexpr int TO = TS > 2 ? 2 : TS, TD = DELTA ? TS : 1, LK = K + Mat<T>::kPad, W = K / 16;
+  // fragments of 32 columns of dO, D (or V) and dX for the four blocks of 16 tokens
+  static constexpr int kStage = 4 * (1 + TD + (DELTA ? TS : 0)) * kFrag;
+  static constexpr int oD = 4 * kFrag, oX = oD + 4 * TD * kFrag;
+  static constexpr int kTri = 12 * TO * kFrag;  // N, or L: lower and upper triangle
+  static constexpr int kArea = 2 * kStage > (DELTA ? 2 : 1) * kTri ? 2 * kStage : (DELTA ? 2 : 1) * kTri;
+  __attribute__((aligned(16))) E k[kQ * LK];
+  __attribute__((aligned(16))) E q[kQ * LK];
+  __attribute__((aligned(16))) char area[kArea];
+  ChunkGates g;
+  float wrow[10][16], wcol[10][16], brow[10][16];  // by tile i (i + 1) / 2 + j
+  float give[W][kQ], back[W][kQ], take[W][kQ];
+  float xv[kQ], dot[W];
+};
+
+// Everything that stays within a chunk.  A wave owns 16 of the K columns of dq and dk;
+// the columns of V are taken 32 at a time: each wave splits its share of D and dX for
+// all of them, and meanwhile reads its columns of S and dS'.
+template <typename T, int K, bool DELTA>
+__global__ void __launch_bounds__(4 * K) mix_main_kernel(const MixBwdArgs b) {
+  typedef Mat<T> M;
+  typedef typename M::E E;
+  typedef typename M::Frag Frag;
+  typedef MainLds<T, K, DELTA> L;
+  constexpr int TS = L::TS, TO = L::TO, TD = L::TD, LK = L::LK, KB = K / 32, W = L::W, TH = 64 * W;
+  constexpr int JOBS = 8 / W;  // sets of tiles a wave
+  __shared__ L s;
+  const MixArgs& a = b.m;
+  const int tid = threadIdx.x, lane = tid & 63, i16 = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int slot = blockIdx.x / a.k_heads, hk = blockIdx.x % a.k_heads;
+  const Segment sg = find_segment(a.cu, a.seqs, a.tokens, kQ, slot);
+  if (sg.len == 0) {
+    if (b.part && tid < a.vpk) b.part[(long)slot * a.v_heads + hk * a.vpk + tid] = 0.f;
+    return;
+  }
+  const int rows = sg.len;
+  const long t0 = sg.tok;
+  {
+    TileLoad<T, K, TH> x, y;
+    x.fetch(static_cast<const E*>(a.k) + t0 * a.k_stride + (long)hk * K, a.k_stride, rows, tid);
+    y.fetch(static_cast<const E*>(a.q) + t0 * a.q_stride + (long)hk * K, a.q_stride, rows, tid);
+    x.put(s.k, LK, tid);
+    y.put(s.q, LK, tid);
+  }
+  __syncthreads();
+  // This wave's tiles of the 64x64 products: two of one fragment and, in half of the
+  // sets, the only one of another.  Sets below 4 hold rows j, columns i of block (i, j)
+  // (a first operand's rows i), the others rows i, columns j.
+  int bi[JOBS][3], bj[JOBS][3], frag[JOBS][2];
+  bool upper[JOBS], extra[JOBS];
+  f32x4 qk[JOBS][3], kk[JOBS][3];
+#pragma unroll
+  for (int u = 0; u < JOBS; ++u) {
+    const int set = wave + u * W, n = set & 3;
+    upper[u] = set >= 4;
+    extra[u] = n < 2;
+    // lower: (3, 0) (3, 1) (2, 0) (1, 0), then (0, 0) (2, 1)
+    const int it = n < 2 ? 3 : (n == 2 ? 2 : 1), kb = n == 1, ie = n ? 2 : 0, ke = n;
+    frag[u][0] = low_frag(it, kb);  // an upper one's mirror image has the same number
+    frag[u][1] = low_frag(ie, ke & 1);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int other = 2 * kb + h;
+      bi[u][h] = upper[u] ? 3 - other : it;
+      bj[u][h] = upper[u] ? 3 - it : other;
+    }
+    if (upper[u]) {  // columns 2 kb, 2 kb + 1 in order
+      const int x = bi[u][0];
+      bi[u][0] = bi[u][1];
+      bi[u][1] = x;
+    }
+    bi[u][2] = bj[u][2] = upper[u] ? 3 - ie : ie;
+#pragma unroll
+    for (int e = 0; e < 3; ++e) {
+      qk[u][e] = kk[u][e] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (e == 2 && !extra[u]) continue;
+#pragma unroll
+      for (int x = 0; x < KB; ++x) {
+        const int c = 32 * x + 8 * g;
+        const Frag ki = M::rows_c(s.k + (16 * bi[u][e] + i16) * LK + c);
+        const Frag kj = M::rows_c(s.k + (16 * bj[u][e] + i16) * LK + c);
+        const Frag qi = M::rows_c(s.q + (16 * bi[u][e] + i16) * LK + c);
+        if (upper[u]) {
+          qk[u][e] = M::mma(qi, kj, qk[u][e]);
+          if (DELTA) kk[u][e] = M::mma(ki, kj, kk[u][e]);
+        } else {
+          qk[u][e] = M::mma(kj, qi, qk[u][e]);
+          if (DELTA) kk[u][e] = M::mma(kj, ki, kk[u][e]);
+        }
+      }
+    }
+  }
+  f32x4 dq[4], dk[4];  // rows t = 16 t + 4g + r, column 16 wave + i16
+#pragma unroll
+  for (int t = 0; t < 4; ++t) dq[t] = dk[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int kcol = 16 * wave + i16, blocks = a.dv / 32;
+#pragma unroll 1
+  for (int hx = 0; hx < a.vpk; ++hx) {
+    const int hv = hk * a.vpk + hx;
+    const long at = (long)slot * a.v_heads + hv;
+    if (wave == W - 1) {
+      const bool live = lane < rows;
+      s.g.set(gate_log2(a, t0 + lane, hv, live), DELTA && live ? a.beta[(t0 + lane) * a.v_heads + hv] : 0.f,
+              lane);
+    }
+    f32x4 into[4], back[4], out[4], dp[JOBS][3], dx[JOBS][3];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) into[t] = back[t] = out[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int u = 0; u < JOBS; ++u)
+#pragma unroll
+      for (int e = 0; e < 3; ++e) dp[u][e] = dx[u][e] = f32x4{0.f, 0.f, 0.f, 0.f};
+    float xv = 0.f, dot = 0.f;
+    const float beta = DELTA && 16 * (wave & 3) + i16 < rows
+                           ? a.beta[(t0 + 16 * (wave & 3) + i16) * a.v_heads + hv] : 0.f;
+#pragma unroll 1
+    for (int vb = 0; vb < blocks; ++vb) {
+      char* const area = s.area + (vb & 1) * L::kStage;
+      const int vc = 32 * vb + 8 * g;
+      // this wave's columns of the states
+      float fs[8], fg[8];
+      {
+        const float* ps = b.state + (at * a.dv + vc) * K + kcol;
+        const float* pg = b.grad + (at * a.dv + vc) * K + kcol;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          fs[e] = ps[(long)e * K];
+          fg[e] = pg[(long)e * K];
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < JOBS; ++u) {
+        const int set = wave + u * W, tb = set & 3, t = 16 * tb + i16;
+        if (set < 4) {
+          if (DELTA) {
+            float f[8];
+            Vec8<float>::load(b.D, (at * kQ + t) * a.dv + vc, f);
+            Split<T, TS> d;
+            d.set(f);
+            put_split<T, TS>(area + L::oD, tb, d, lane);
+          } else {
+            float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            if (t < rows) Vec8<T>::load(a.v, (t0 + t) * a.v_stride + (long)hv * a.dv + vc, f);
+            Split<T, 1> d;
+            d.set(f);
+            put_split<T, 1>(area + L::oD, tb, d, lane);
+          }
+        } else {
+          float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, f[8], v[8];
+          if (t < rows) Vec8<T>::load(b.dout, (t0 + t) * b.do_stride + (long)hv * a.dv + vc, o);
+          Split<T, 1> d;
+          d.set(o);
+          put_split<T, 1>(area, tb, d, lane);
+          if (DELTA) {
+            Vec8<float>::load(b.dX, (at * kQ + t) * a.dv + vc, f);
+            if (t < rows) {
+              Vec8<T>::load(a.v, (t0 + t) * a.v_stride + (long)hv * a.dv + vc, v);
+              float w[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                xv = fmaf(f[e], v[e], xv);
+                w[e] = beta * f[e];
+              }
+              Vec8<T>::store(b.dv, ((t0 + t) * a.v_heads + hv) * a.dv + vc, w);
+            }
+            Split<T, TS> x;
+            x.set(f);
+            put_split<T, TS>(area + L::oX, tb, x, lane);
+          }
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) dot = fmaf(fs[e], fg[e], dot);
+      Split<T, TS> ss, sd;
+      ss.set(fs);
+      sd.set(fg);
+      __syncthreads();
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const Frag o = frag_at<T>(area, t, lane);
+        into[t] = ss.b_times(o, into[t]);
+        const auto d = split_at<T, TD>(area + L::oD, t, lane);
+        out[t] = mma_split<T, TD, TS>(d, sd, out[t]);
+        if (DELTA) back[t] = mma_split<T, TS, TS>(split_at<T, TS>(area + L::oX, t, lane), ss, back[t]);
+      }
+#pragma unroll
+      for (int u = 0; u < JOBS; ++u)
+#pragma unroll
+        for (int e = 0; e < 3; ++e) {
+          if (e == 2 && !extra[u]) continue;
+          const Frag o = frag_at<T>(area, bi[u][e], lane);
+          const auto d = split_at<T, TD>(area + L::oD, bj[u][e], lane);
+          if (upper[u]) dp[u][e] = d.b_times(o, dp[u][e]);
+          else dp[u][e] = d.a_times(o, dp[u][e]);
+          if (DELTA) {
+            const auto x = split_at<T, TS>(area + L::oX, bi[u][e], lane);
+            if (upper[u]) dx[u][e] = mma_split<T, TS, TD>(x, d, dx[u][e]);
+            else dx[u][e] = mma_split<T, TD, TS>(d, x, dx[u][e]);
+          }
+        }
+    }
+    if (DELTA) {
+      xv += __shfl_xor(xv, 16, 64);
+      xv += __shfl_xor(xv, 32, 64);
+      if (wave >= W - 4 && g == 0) s.xv[16 * (wave & 3) + i16] = xv;
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) dot += __shfl_xor(dot, o, 64);
+    if (lane == 0) s.dot[wave] = dot;
+    __syncthreads();  // the last stage is no longer read
+    // N and L as fragments, and the sums of w's rows and columns
+#pragma unroll
+    for (int u = 0; u < JOBS; ++u) {
+      float fn[2][8], fl[2][8];
+#pragma unroll
+      for (int h = 0; h < 8; ++h) fn[1][h] = fl[1][h] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 3; ++e) {
+        if (e == 2 && !extra[u]) continue;
+        const int I = 16 * bi[u][e], J = 16 * bj[u][e], tile = bi[u][e] * (bi[u][e] + 1) / 2 + bj[u][e];
+        float wr = 0.f, br = 0.f, wc[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int i = I + (upper[u] ? 4 * g + r : i16), j = J + (upper[u] ? i16 : 4 * g + r);
+          const float c = exp2_f32(gap2(s.g.G[i], s.g.G[j]));
+          const float n = i >= j ? a.scale * c * dp[u][e][r] : 0.f;
+          const float m = DELTA && i > j ? c * dx[u][e][r] : 0.f;
+          const float l = DELTA ? -s.g.beta[i] * m : 0.f;
+          float w = i > j ? qk[u][e][r] * n : 0.f;
+          if (DELTA) w = i > j ? fmaf(kk[u][e][r], l, w) : 0.f;
+          const int put = e == 2 ? 1 : 0, h = e == 2 ? (upper[u] ? 4 : 0) : 4 * e;
+          if (e == 2) {
+            fn[put][r] = upper[u] ? 0.f : n;
+            fn[put][4 + r] = upper[u] ? n : 0.f;
+            fl[put][r] = upper[u] ? 0.f : l;
+            fl[put][4 + r] = upper[u] ? l : 0.f;
+          } else {
+            fn[put][h + r] = n;
+            fl[put][h + r] = l;
+          }
+          wr += w;
+          wc[r] = w;
+          if (DELTA && i > j) br = fmaf(kk[u][e][r], m, br);
+        }
+        if (!upper[u]) {  // rows i in the lanes
+#pragma unroll
+          for (int o = 16; o < 64; o <<= 1) {
+            wr += __shfl_xor(wr, o, 64);
+            br += __shfl_xor(br, o, 64);
+          }
+          if (g == 0) {
+            s.wrow[tile][i16] = wr;
+            s.brow[tile][i16] = br;
+          }
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+#pragma unroll
+            for (int o = 1; o < 16; o <<= 1) wc[r] += __shfl_xor(wc[r], o, 64);
+            if (i16 == 0) s.wcol[tile][4 * g + r] = wc[r];
+          }
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        if (e == 1 && !extra[u]) continue;
+        const int n = (upper[u] ? 6 : 0) + frag[u][e];
+        Split<T, TO> x;
+        x.set(fn[e]);
+        put_split<T, TO>(s.area, n, x, lane);
+        if (DELTA) {
+          x.set(fl[e]);
+          put_split<T, TO>(s.area + L::kTri, n, x, lane);
+        }
+      }
+    }
+    __syncthreads();
+    {
+      Frag kf[2], qf[2];
+      float gv[16], bk[16], tk[16];
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) {
+        kf[kb] = M::cols(cols_at<T, false>(s.k, LK, 32 * kb, 16 * wave, lane), LK);
+        qf[kb] = M::cols(cols_at<T, false>(s.q, LK, 32 * kb, 16 * wave, lane), LK);
+        float fk[8], fq[8];
+        M::unpack(kf[kb], fk);
+        M::unpack(qf[kb], fq);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int t = 2 * kb + h;
+          const f32x4 eg = *reinterpret_cast<const f32x4*>(&s.g.eg[16 * t + 4 * g]);
+          const f32x4 et = *reinterpret_cast<const f32x4*>(&s.g.et[16 * t + 4 * g]);
+          const f32x4 be = *reinterpret_cast<const f32x4*>(&s.g.beta[16 * t + 4 * g]);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float x = a.scale * eg[r] * into[t][r], z = et[r] * out[t][r];
+            dq[t][r] += x;
+            dk[t][r] += z;
+            gv[4 * t + r] = x * fq[4 * h + r];
+            tk[4 * t + r] = z * fk[4 * h + r];
+            if (DELTA) {
+              const float y = eg[r] * back[t][r];
+              dk[t][r] = fmaf(-be[r], y, dk[t][r]);
+              bk[4 * t + r] = y * fk[4 * h + r];
+            }
+          }
+        }
+      }
+      // sums over the 16 lanes of a group; item 4 t + r is token 16 t + 4g + r
+      typedef RowReduce<16, 16> Red;
+      Red::run(gv, lane);
+      Red::run(tk, lane);
+      if (DELTA) Red::run(bk, lane);
+      const int item = Red::item(0, lane), tok = 16 * (item >> 2) + 4 * g + (item & 3);
+      s.give[wave][tok] = gv[0];
+      s.take[wave][tok] = tk[0];
+      if (DELTA) s.back[wave][tok] = bk[0];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+#pragma unroll
+        for (int kb = 0; kb <= t / 2; ++kb) {
+          dq[t] = split_at<T, TO>(s.area, low_frag(t, kb), lane).a_times(kf[kb], dq[t]);
+          if (DELTA) dk[t] = split_at<T, TO>(s.area + L::kTri, low_frag(t, kb), lane).a_times(kf[kb], dk[t]);
+        }
+#pragma unroll
+        for (int kb = t / 2; kb < 2; ++kb) {
+          dk[t] = split_at<T, TO>(s.area, 6 + up_frag(t, kb), lane).a_times(qf[kb], dk[t]);
+          if (DELTA) dk[t] = split_at<T, TO>(s.area + L::kTri, 6 + up_frag(t, kb), lane).a_times(kf[kb], dk[t]);
+        }
+      }
+    }
+    __syncthreads();
+    if (wave == 0 && b.dg) {  // one token a lane
+      float give = 0.f, bk = 0.f, take = 0.f, all = 0.f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        give += s.give[w][lane];
+        take += s.take[w][lane];
+        if (DELTA) bk += s.back[w][lane];
+        all += s.dot[w];
+      }
+      float row = 0.f, col = 0.f, br = 0.f;
+      const int blk = lane >> 4;
+      for (int j = 0; j <= blk; ++j) {
+        row += s.wrow[blk * (blk + 1) / 2 + j][i16];
+        if (DELTA) br += s.brow[blk * (blk + 1) / 2 + j][i16];
+      }
+      for (int i = blk; i < 4; ++i) col += s.wcol[i * (i + 1) / 2 + blk][i16];
+      double own = (double)row - col + give - take;
+      if (DELTA) own -= s.g.beta[lane] * bk;
+      double tot = take;
+#pragma unroll
+      for (int o = 32; o > 0; o >>= 1) tot += __shfl_xor(tot, o, 64);
+      tot += (double)s.g.all * all;
+      // sum over i >= t
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const double up = __shfl_down(own, o, 64);
+        if (lane + o < 64) own += up;
+      }
+      double dg = own + tot;
+      if (lane >= rows) dg = 0.0;
+      if (a.decay == RSSM_DECAY_TOKEN) {
+        if (lane < rows) b.dg[(t0 + lane) * a.v_heads + hv] = (float)dg;
+      } else {
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) dg += __shfl_xor(dg, o, 64);
+        if (lane == 0) b.part[at] = (float)dg;
+      }
+      if (DELTA && lane < rows) b.dbeta[(t0 + lane) * a.v_heads + hv] = s.xv[lane] - bk - br;
+    }
+    __syncthreads();  // the next head writes all of it
+  }
+  // to the io type, and 16 bytes at a time to memory
+#pragma unroll
+  for (int t = 0; t < 4; ++t)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int p = (16 * t + 4 * g + r) * LK + kcol;
+      Elt<T>::store1(s.q, p, dq[t][r]);
+      Elt<T>::store1(s.k, p, dk[t][r]);
+    }
+  __syncthreads();
+  constexpr int V = 16 / sizeof(E), PER = K / V;
+  for (int e = tid; e < rows * PER; e += TH) {
+    const int t = e / PER, c = (e % PER) * V;
+    const long o = ((t0 + t) * a.k_heads + hk) * K + c;
+    *reinterpret_cast<u32x4*>(static_cast<E*>(b.dq) + o) = *reinterpret_cast<const u32x4*>(s.q + t * LK + c);
+    *reinterpret_cast<u32x4*>(static_cast<E*>(b.dk) + o) = *reinterpret_cast<const u32x4*>(s.k + t * LK + c);
+  }
+}
+
+// dg of a head's constant decay: its chunks' sums, in a fixed order.
+__global__ void __launch_bounds__(256) mix_decay_sum_kernel(const MixBwdArgs b) {
+  __shared__ double sum[256];
+  double v = 0.0;
+  for (long c = threadIdx.x; c < b.cslots; c += 256) v += b.part[c * b.m.v_heads + blockIdx.x];
+  sum[threadIdx.x] = v;
+  __syncthreads();
+  for (int o = 128; o > 0; o >>= 1) {
+    if ((int)threadIdx.x < o) sum[threadIdx.x] += sum[threadIdx.x + o];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) b.dg[blockIdx.x] = (float)sum[0];
+}
+
+struct BwdLayout {
+  size_t tinv, state, grad, D, dX, part, end;
+};
+static BwdLayout bwd_layout(const rssm_mixer_dims& d, bool delta) {
+  BwdLayout l{};
+  const size_t units = (size_t)scan_slots(d.tokens, d.seqs, kQ) * d.v_heads;
+  size_t at = 0;
+  const auto take = [&](size_t bytes) {
+    const size_t p = at;
+    at += (bytes + 15) / 16 * 16;
+    return p;
+  };
+  l.tinv = take(delta ? units * mix_inverse_bytes(d.io_dtype == RSSM_F32, true) : 0);
+  l.state = take(units * d.dk * d.dv * 4);
+  l.grad = take(units * d.dk * d.dv * 4);
+  l.D = take(delta ? units * kQ * d.dv * 4 : 0);
+  l.dX = take(delta ? units * kQ * d.dv * 4 : 0);
+  l.part = take(units * 4);
+  l.end = at;
+  return l;
+}
+
+enum { kBwdStates, kBwdMain };
+template <typename T, bool DELTA>
+static const void* pick_bwd(int which, int dk) {
+  if (which == kBwdStates)
+    return dk == 64 ? reinterpret_cast<const void*>(&mix_states_kernel<T, 64, DELTA>)
+                    : reinterpret_cast<const void*>(&mix_states_kernel<T, 128, DELTA>);
+  return dk == 64 ? reinterpret_cast<const void*>(&mix_main_kernel<T, 64, DELTA>)
+                  : reinterpret_cast<const void*>(&mix_main_kernel<T, 128, DELTA>);
+}
+
+static size_t mix_backward_bytes(const rssm_mixer_dims* dims, bool delta) {
+  return mix_check(dims, delta) || dims->tokens == 0 ? 0 : bwd_layout(*dims, delta).end;
+}
+
+static int mix_backward(const rssm_mixer_dims* dims, bool delta, MixBwdArgs b, void* workspace,
+                        size_t workspace_bytes, hipStream_t stream) {
+  int rc = mix_check(dims, delta);
+  if (rc) return rc;
+  const rssm_mixer_dims& d = *dims;
+  MixArgs& a = b.m;
+  if (d.seqs == 0) return d.tokens == 0 ? RSSM_OK : RSSM_EINVAL;
+  if (!a.cu && d.seqs != 1) return RSSM_EINVAL;
+  if (d.tokens > 0 && (!a.q || !a.k || !a.v || !b.dout || !b.dq || !b.dk || !b.dv ||
+                       (d.decay && (!a.g || !b.dg)) || (delta && (!a.beta || !b.dbeta))))
+    return RSSM_EINVAL;
+  const void* vec[] = {a.q, a.k, a.v, b.dout, b.dq, b.dk, b.dv, a.init, b.dfinal, b.dinit, workspace};
+  for (const void* p : vec)
+    if (!aligned16(p)) return RSSM_EINVAL;
+  const size_t need = mix_backward_bytes(dims, delta);
+  if (need && (!workspace || workspace_bytes < need)) return RSSM_EINVAL;
+  mix_fill(a, d);
+  b.do_stride = d.do_stride ? d.do_stride : (long)d.v_heads * d.dv;
+  if (!d.decay) b.dg = nullptr;
+  const BwdLayout l = bwd_layout(d, delta);
+  char* const ws = static_cast<char*>(workspace);
+  a.tinv = ws + l.tinv;
+  b.state = reinterpret_cast<float*>(ws + l.state);
+  b.grad = reinterpret_cast<float*>(ws + l.grad);
+  b.D = reinterpret_cast<float*>(ws + l.D);
+  b.dX = reinterpret_cast<float*>(ws + l.dX);
+  b.part = d.decay == RSSM_DECAY_HEAD ? reinterpret_cast<float*>(ws + l.part) : nullptr;
+  const bool f32 = d.io_dtype == RSSM_F32;
+  b.cslots = scan_slots(d.tokens, d.seqs, kQ);
+  const long dir = mix_grid(d.seqs, d.k_heads, (long)a.vpk * a.slices), mgrid = b.cslots * d.k_heads;
+  if (!grid_fits(2 * dir, 256) || !grid_fits(mgrid, 4 * d.dk) ||
+      !grid_fits(b.cslots * ((d.v_heads + 3) / 4), 256))
+    return RSSM_ESHAPE;
+  b.dir_blocks = (int)dir;
+  const auto pick = [&](int which) {
+    return f32 ? (delta ? pick_bwd<float, true>(which, d.dk) : pick_bwd<float, false>(which, d.dk))
+               : (delta ? pick_bwd<bf16, true>(which, d.dk) : pick_bwd<bf16, false>(which, d.dk));
+  };
+  if (d.tokens == 0) {  // no chunks, and no gradient of a decay but zero
+    b.cslots = 0;
+  } else if (delta) {
+    rc = f32 ? launch_inverse<float, true>(a, d.dk, b.cslots, stream)
+             : launch_inverse<bf16, true>(a, d.dk, b.cslots, stream);
+    if (rc) return rc;
+  }
+  rc = launch_kernel(pick(kBwdStates), (unsigned)(2 * dir), 256, 0, stream, b);
+  if (!rc && d.tokens > 0) rc = launch_kernel(pick(kBwdMain), (unsigned)mgrid, 4 * d.dk, 0, stream, b);
+  if (!rc && d.decay == RSSM_DECAY_HEAD && b.dg)
+    rc = launch_kernel(reinterpret_cast<const void*>(&mix_decay_sum_kernel), d.v_heads, 256, 0, stream, b);
+  return rc;
+}
+
+}  // namespace rssm
+
+using namespace rssm;
+
+static MixBwdArgs bwd_args(const void* dout, const void* q, const void* k, const void* v, const float* g,
+                           const int32_t* cu_seqlens, const float* initial_state,
+                           const uint8_t* has_initial, const int32_t* slot_idx,
+                           const float* dfinal_state, void* dq, void* dk, void* dv, float* dg,
+                           float* dinitial_state, int32_t* status) {
+  MixBwdArgs b{};
+  b.m.q = q;
+  b.m.k = k;
+  b.m.v = v;
+  b.m.g = g;
+  b.m.cu = cu_seqlens;
+  b.m.init = initial_state;
+  b.m.has_init = has_initial;
+  b.m.slot_idx = slot_idx;
+  b.m.status = status;
+  b.dout = dout;
+  b.dfinal = dfinal_state;
+  b.dq = dq;
+  b.dk = dk;
+  b.dv = dv;
+  b.dg = dg;
+  b.dinit = dinitial_state;
+  return b;
+}
+
+extern "C" size_t linear_attention_backward_workspace(const rssm_mixer_dims* dims) {
+  return mix_backward_bytes(dims, false);
+}
+
+extern "C" int linear_attention_backward(const rssm_mixer_dims* dims, const void* dout, const void* q,
+                                         const void* k, const void* v, const float* log_decay,
+                                         const int32_t* cu_seqlens, const float* initial_state,
+                                         const uint8_t* has_initial, const int32_t* slot_idx,
+                                         const float* dfinal_state, void* dq, void* dk, void* dv,
+                                         float* dlog_decay, float* dinitial_state, void* workspace,
+                                         size_t workspace_bytes, int32_t* status, hipStream_t stream) {
+  return mix_backward(dims, false,
+                      bwd_args(dout, q, k, v, log_decay, cu_seqlens, initial_state, has_initial, slot_idx,
+                               dfinal_state, dq, dk, dv, dlog_decay, dinitial_state, status),
+                      workspace, workspace_bytes, stream);
+}
+
+extern "C" size_t gdn_scan_backward_workspace(const rssm_mixer_dims* dims) {
+  return mix_backward_bytes(dims, true);
+}
+
+extern "C" int gdn_scan_backward(const rssm_mixer_dims* dims, const void* dout, const void* q, const void* k,
+                                 const void* v, const float* log_g, const float* beta,
+                                 const int32_t* cu_seqlens, const float* initial_state,
+                                 const uint8_t* has_initial, const int32_t* slot_idx,
+                                 const float* dfinal_state, void* dq, void* dk, void* dv, float* dlog_g,
+                                 float* dbeta, float* dinitial_state, void* workspace,
+                                 size_t workspace_bytes, int32_t* status, hipStream_t stream) {
+  MixBwdArgs b = bwd_args(dout, q, k, v, log_g, cu_seqlens, initial_state, has_initial, slot_idx,
+                          dfinal_state, dq, dk, dv, dlog_g, dinitial_state, status);
+  b.m.beta = beta;
+  b.dbeta = dbeta;
+  return mix_backward(dims, true, b, workspace, workspace_bytes, stream);
+}

@@ -1,0 +1,371 @@
+// Shared pieces of linear attention and the gated delta rule over sequences.
+//
+// Per value head, with S [K, V] (the pools hold its transpose), g the decay's
+// logarithm, DELTA the gated delta rule:
+//   S <- e^{g_t} S;  d_t = beta_t (v_t - S^T k_t)  (linear attention: d_t = v_t)
+//   S <- S + k_t d_t^T;  o_t = scale S^T q_t
+// Tokens of a sequence are taken in chunks of 64.  With G the running sum of g in
+// the chunk (inclusive), c_ij = e^{G_i - G_j} and S the state before the chunk,
+//   A_ij = beta_i c_ij k_i.k_j  (i > j),  T = (I + A)^-1
+//   D = T X,  X_i = beta_i (v_i - e^{G_i} S^T k_i)
+//   o_i = scale [ e^{G_i} S^T q_i + sum_{j<=i} c_ij (q_i.k_j) d_j ]
+//   S' = e^{G_Q} S + sum_j e^{G_Q - G_j} k_j d_j^T
+// so all the work is small dense products for the matrix cores (fragments and
+// their orders C and D: scan_common.hpp).
+//
+// A wave owns 16 columns of S as eight (K = 128) or four accumulators, rows in
+// 4g + r: they are the second operand of K S and Q S as they stand, K S's result is
+// that of T X, and its result that of K^T D, so nothing moves between lanes.
+#pragma once
+
+#include "scan_common.hpp"
+
+namespace rssm {
+
+struct MixArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  const float* g;      // [v_heads] or [tokens, v_heads] by decay
+  const float* beta;   // [tokens, v_heads]
+  const int32_t* cu;
+  const float* init;
+  const uint8_t* has_init;
+  const int32_t* slot_idx;
+  float* final_state;
+  void* o;
+  void* tinv;          // [chunk slots][v_heads][6 (12) fragments][terms][64]
+  int32_t* status;
+  long q_stride, k_stride, v_stride;
+  int32_t tokens, seqs, k_heads, v_heads, vpk, dv, num_slots, decay, slices;
+  float scale;
+};
+
+__device__ static inline int mix_slot(const MixArgs& a, int i) {
+  const int s = a.slot_idx ? a.slot_idx[i] : i;
+  return s >= 0 && s < a.num_slots ? s : -1;
+}
+
+// The 64x64 lower triangle as fragments of 16 rows and 32 columns: six are not zero.
+RSSM_HD static inline int low_frag(int it, int kb) { return it < 2 ? it : 2 * it - 2 + kb; }
+// The upper triangle's (a lower one's transpose).
+RSSM_HD static inline int up_frag(int it, int kb) { return low_frag(3 - it, 1 - kb); }
+
+// Products of two split operands: every pair of terms whose weight fp32 can hold.
+template <typename T, int TA, int TB>
+__device__ static inline f32x4 mma_split(const Split<T, TA>& x, const Split<T, TB>& y, f32x4 c) {
+  constexpr int M = TA > TB ? TA : TB;
+#pragma unroll
+  for (int s = M - 1; s >= 0; --s)
+#pragma unroll
+    for (int i = 0; i <= s; ++i)
+      if (i < TA && s - i < TB) c = Mat<T>::mma(x.t[i], y.t[s - i], c);
+  return c;
+}
+
+// A token's decay exponent in log2.  -1e4 already takes any state to zero, and keeps
+// sums of 64 and their differences finite; NaN passes.
+__device__ static inline double gate_log2(const MixArgs& a, long t, int hv, bool live) {
+  float g = 0.f;
+  if (live && a.decay) g = a.decay == RSSM_DECAY_HEAD ? a.g[hv] : a.g[t * a.v_heads + hv];
+  return (double)(g < -1e4f ? -1e4f : g) * 1.4426950408889634074;
+}
+
+// A chunk's decays, one token a lane, as the kernels read them from LDS.
+struct ChunkGates {
+  float2 G[kQ];                                      // log2 of the decay since the chunk began
+  __attribute__((aligned(16))) float eg[kQ];         // e^{G_t}
+  __attribute__((aligned(16))) float et[kQ];         // e^{G_Q - G_t}
+  __attribute__((aligned(16))) float beta[kQ];
+  float all;                                         // e^{G_Q}
+  __device__ inline void set(double log2g, float b, int lane) {
+    const double cum = wave_cumsum(log2g, lane), last = __shfl(cum, 63, 64);
+    const float hi = (float)cum;
+    G[lane] = make_float2(hi, (float)(cum - (double)hi));
+    eg[lane] = exp2_f32(hi);
+    et[lane] = exp2_f32((float)(last - cum));
+    beta[lane] = b;
+    if (lane == 0) all = exp2_f32((float)last);
+  }
+};
+
+// Tiles of a token tile pair on their way from memory: `ROWS` elements wide, 64 tokens.
+template <typename T, int COLS, int THREADS>
+struct TileLoad {
+  typedef typename Mat<T>::E E;
+  static constexpr int V = 16 / sizeof(E), PER = COLS / V, N = kQ * PER / THREADS;
+  static_assert(kQ * PER % THREADS == 0, "whole rounds");
+  u32x4 r[N];
+  __device__ inline void fetch(const E* src, long stride, int rows, int tid) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int e = i * THREADS + tid, row = e / PER;
+      r[i] = u32x4{0, 0, 0, 0};
+      if (row < rows) r[i] = *reinterpret_cast<const u32x4*>(src + row * stride + (e % PER) * V);
+    }
+  }
+  __device__ inline void put(E* tile, int ld, int tid) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int e = i * THREADS + tid;
+      *reinterpret_cast<u32x4*>(tile + (e / PER) * ld + (e % PER) * V) = r[i];
+    }
+  }
+};
+
+// Fragments kept in memory or LDS as lanes hold them.
+template <typename T>
+__device__ static inline typename Mat<T>::Frag frag_at(const void* base, int i, int lane) {
+  typename Mat<T>::Frag f;
+  __builtin_memcpy(&f, __builtin_assume_aligned(static_cast<const char*>(base) + (i * 64 + lane) * sizeof(f), 16),
+                   sizeof(f));
+  return f;
+}
+template <typename T, int TERMS>
+__device__ static inline void put_split(void* base, int i, const Split<T, TERMS>& s, int lane) {
+#pragma unroll
+  for (int k = 0; k < TERMS; ++k)
+    __builtin_memcpy(__builtin_assume_aligned(static_cast<char*>(base) + ((i * TERMS + k) * 64 + lane) * sizeof(s.t[k]), 16),
+                     &s.t[k], sizeof(s.t[k]));
+}
+template <typename T, int TERMS>
+__device__ static inline Split<T, TERMS> split_at(const void* base, int i, int lane) {
+  Split<T, TERMS> s;
+#pragma unroll
+  for (int k = 0; k < TERMS; ++k) s.t[k] = frag_at<T>(base, i * TERMS + k, lane);
+  return s;
+}
+
+template <typename T>
+constexpr int mix_terms() { return Mat<T>::kTerms; }
+
+// Units (a sequence's key head) are dealt to the eight dies in turn, so that a long
+// sequence's heads are spread over them and a key head's workgroups share one L2.
+struct MixUnit {
+  int seq, hk, rest;
+  bool live;
+};
+__device__ static inline MixUnit mix_unit(const MixArgs& a, int id, int per) {
+  const int j = id >> 3, u = (j / per) * 8 + (id & 7);
+  MixUnit m;
+  m.live = u < a.seqs * a.k_heads;
+  m.seq = m.live ? u / a.k_heads : 0;
+  m.hk = m.live ? u % a.k_heads : 0;
+  m.rest = j % per;
+  return m;
+}
+static inline long mix_grid(long seqs, long k_heads, long per) { return (seqs * k_heads + 7) / 8 * 8 * per; }
+
+// 16x16x16 in fp32: operand registers hold four values of k = 4g + e.
+__device__ static inline f32x4 mm16(f32x4 x, f32x4 y, f32x4 c) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(x[e], y[e], c, 0, 0, 0);
+  return c;
+}
+
+// T = (I + A)^-1 of one chunk and value head, a wave each, in fp32: the four 16x16
+// diagonal blocks by substitution (a lane a column), the others from them in order,
+//   T_ij = -T_ii sum_{j<=m<i} A_im T_mj,
+// then split into the products' terms and stored as fragments (lower triangle; BOTH:
+// and the transpose's, for the backward pass).  Each block of A is computed so that a
+// lane holds its row's values: it is a first operand as it stands.
+template <typename T, int K, bool BOTH>
+static __global__ void __launch_bounds__(256) mix_inverse_kernel(const MixArgs a) {
+  typedef Mat<T> M;
+  typedef typename M::Frag Frag;
+  typedef typename M::E E;
+  constexpr int LB = 20, TERMS = M::kTerms, KB = K / 32;
+  __shared__ __attribute__((aligned(16))) float sBlk[4][10][16 * LB];
+  __shared__ float2 sG[4][kQ];
+  __shared__ __attribute__((aligned(16))) float sBeta[4][kQ];
+  const int lane = threadIdx.x & 63, i16 = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int per = (a.v_heads + 3) / 4;
+  const int id = xcd_tile(blockIdx.x, gridDim.x);
+  const int slot = id / per, hv = (id % per) * 4 + wave;
+  const Segment sg = find_segment(a.cu, a.seqs, a.tokens, kQ, slot);
+  if (sg.len == 0 || hv >= a.v_heads) return;
+  const int rows = sg.len, hk = hv / a.vpk;
+  const long t0 = sg.tok;
+  {
+    const bool live = lane < rows;
+    const double cum = wave_cumsum(gate_log2(a, t0 + lane, hv, live), lane);
+    const float hi = (float)cum;
+    sG[wave][lane] = make_float2(hi, (float)(cum - (double)hi));
+    sBeta[wave][lane] = live ? a.beta[(t0 + lane) * a.v_heads + hv] : 0.f;
+  }
+  // k_m.k_i: rows m of block bm, columns i of block bi <= bm is left out
+  f32x4 acc[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int m = 0; m <= i; ++m) acc[i][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const E* const src = static_cast<const E*>(a.k) + t0 * a.k_stride + (long)hk * K;
+#pragma unroll
+  for (int kb = 0; kb < KB; ++kb) {
+    Frag f[4];
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const int t = 16 * b + i16;
+      u32x4 z[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+      if (t < rows) {
+        const E* p = src + t * a.k_stride + 32 * kb + 8 * g;
+        z[0] = *reinterpret_cast<const u32x4*>(p);
+        if (sizeof(E) == 4) z[1] = *reinterpret_cast<const u32x4*>(p + 4);
+      }
+      __builtin_memcpy(&f[b], z, sizeof(Frag));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int m = 0; m <= i; ++m) acc[i][m] = M::mma(f[m], f[i], acc[i][m]);
+  }
+  wave_sync();
+  // A_im in the lane of row i = i16, columns m = 4g + r
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 gi = sG[wave][16 * i + i16];
+    const float bi = sBeta[wave][16 * i + i16];
+#pragma unroll
+    for (int m = 0; m <= i; ++m)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float w = bi * exp2_f32(gap2(gi, sG[wave][16 * m + 4 * g + r])) * acc[i][m][r];
+        acc[i][m][r] = m < i || 4 * g + r < i16 ? w : 0.f;
+      }
+    *reinterpret_cast<f32x4*>(&sBlk[wave][i][i16 * LB + 4 * g]) = acc[i][i];
+  }
+  wave_sync();
+  float x[16];
+  {
+    const float* blk = sBlk[wave][g];  // lane 16 b + c: column c of block b
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float s = i == i16 ? 1.f : 0.f;
+#pragma unroll
+      for (int m4 = 0; m4 < 16; m4 += 4) {
+        if (m4 >= i) break;
+        const f32x4 row = *reinterpret_cast<const f32x4*>(blk + i * LB + m4);
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+          if (m4 + m < i) s = fmaf(-row[m], x[m4 + m], s);
+      }
+      x[i] = s;
+    }
+  }
+  wave_sync();
+#pragma unroll
+  for (int i = 0; i < 16; ++i) sBlk[wave][g][i * LB + i16] = x[i];
+  wave_sync();
+  f32x4 Ad[4], t[4][4];  // t[i][j]: rows 4g + r, column i16
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    Ad[b] = *reinterpret_cast<const f32x4*>(&sBlk[wave][b][i16 * LB + 4 * g]);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) t[b][b][r] = sBlk[wave][b][(4 * g + r) * LB + i16];
+  }
+#pragma unroll
+  for (int dist = 1; dist < 4; ++dist)
+#pragma unroll
+    for (int j = 0; j + dist < 4; ++j) {
+      const int i = j + dist;
+      f32x4 s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int m = j; m < i; ++m) s = mm16(acc[i][m], t[m][j], s);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) s[r] = -s[r];
+      t[i][j] = mm16(Ad[i], s, f32x4{0.f, 0.f, 0.f, 0.f});
+    }
+  // off-diagonal blocks by rows
+#pragma unroll
+  for (int i = 1; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < i; ++j)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) sBlk[wave][4 + i * (i - 1) / 2 + j][(4 * g + r) * LB + i16] = t[i][j][r];
+  wave_sync();
+  char* const out = static_cast<char*>(a.tinv) +
+      ((long)slot * a.v_heads + hv) * ((BOTH ? 12 : 6) * TERMS * 64 * sizeof(Frag));
+#pragma unroll
+  for (int it = 0; it < 4; ++it)
+#pragma unroll
+    for (int kb = 0; kb <= it / 2; ++kb) {
+      float f[8];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int j = 2 * kb + h;
+        f32x4 row = {0.f, 0.f, 0.f, 0.f};
+        if (j == it) row = Ad[it];
+        if (j < it) row = *reinterpret_cast<const f32x4*>(&sBlk[wave][4 + it * (it - 1) / 2 + j][i16 * LB + 4 * g]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) f[4 * h + r] = row[r];
+      }
+      Split<T, TERMS> s;
+      s.set(f);
+      put_split<T, TERMS>(out, low_frag(it, kb), s, lane);
+    }
+  if (BOTH) {
+#pragma unroll
+    for (int jt = 0; jt < 4; ++jt)
+#pragma unroll
+      for (int kb = jt / 2; kb < 2; ++kb) {
+        float f[8];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) f[4 * h + r] = 2 * kb + h >= jt ? t[2 * kb + h][jt][r] : 0.f;
+        Split<T, TERMS> s;
+        s.set(f);
+        put_split<T, TERMS>(out, 6 + up_frag(jt, kb), s, lane);
+      }
+  }
+}
+
+static inline size_t mix_inverse_bytes(bool f32, bool both) {
+  return (size_t)(both ? 12 : 6) * 64 * (f32 ? 32 : 3 * 16);
+}
+
+template <typename T, bool BOTH>
+static inline int launch_inverse(const MixArgs& a, int dk, long cslots, hipStream_t stream) {
+  const void* fn = dk == 64 ? reinterpret_cast<const void*>(&mix_inverse_kernel<T, 64, BOTH>)
+                            : reinterpret_cast<const void*>(&mix_inverse_kernel<T, 128, BOTH>);
+  return launch_kernel(fn, (unsigned)(cslots * ((a.v_heads + 3) / 4)), 256, 0, stream, a);
+}
+
+static inline int mix_check(const rssm_mixer_dims* d, bool delta) {
+  if (!d) return RSSM_EINVAL;
+  if (d->tokens < 0 || d->seqs < 0 || d->k_heads < 1 || d->v_heads < 1 || d->v_heads % d->k_heads ||
+      d->num_slots < 0)
+    return RSSM_EINVAL;
+  if (!valid_dtype(d->io_dtype)) return RSSM_EDTYPE;
+  if (d->decay < RSSM_DECAY_NONE || d->decay > RSSM_DECAY_TOKEN) return RSSM_EINVAL;
+  if (!(d->dk == 64 || d->dk == 128) || !(d->dv == 64 || d->dv == 128)) return RSSM_ESHAPE;
+  if (delta && d->dk != d->dv) return RSSM_ESHAPE;
+  if (d->scale != d->scale) return RSSM_EINVAL;
+  // heads in a row and in a pool slot are indexed in 32 bits
+  if ((long)d->v_heads > (1L << 20)) return RSSM_ESHAPE;
+  const long es = d->io_dtype == RSSM_F32 ? 4 : 2;
+  const long qk = (long)d->k_heads * d->dk, v = (long)d->v_heads * d->dv;
+  const int64_t rows[4] = {d->q_stride, d->k_stride, d->v_stride, d->do_stride};
+  for (int i = 0; i < 4; ++i)
+    if (rows[i] != 0 && (rows[i] < (i < 2 ? qk : v) || rows[i] * es % 16)) return RSSM_EINVAL;
+  return RSSM_OK;
+}
+
+static inline void mix_fill(MixArgs& a, const rssm_mixer_dims& d) {
+  a.q_stride = d.q_stride ? d.q_stride : (long)d.k_heads * d.dk;
+  a.k_stride = d.k_stride ? d.k_stride : (long)d.k_heads * d.dk;
+  a.v_stride = d.v_stride ? d.v_stride : (long)d.v_heads * d.dv;
+  a.tokens = d.tokens;
+  a.seqs = d.seqs;
+  a.k_heads = d.k_heads;
+  a.v_heads = d.v_heads;
+  a.vpk = d.v_heads / d.k_heads;
+  a.dv = d.dv;
+  a.num_slots = d.num_slots;
+  a.decay = d.decay;
+  a.slices = d.dv / 64;
+  a.scale = d.scale > 0.f ? d.scale : 1.f / sqrtf((float)d.dk);
+}
+
+}  // namespace rssm

@@ -1,0 +1,356 @@
+// Linear attention and the gated delta rule over packed sequences, forward (the
+// chunked form: mixer_common.hpp).
+//
+// The delta rule's T of every chunk is independent of the state and comes from a
+// launch in front (mix_inverse_kernel).  Then a workgroup walks the chunks of one
+// sequence and 64 columns of one value head's state, a wave 16 of them, with the
+// state in registers; the next chunk's tiles are on their way while one is worked on.
+//
+// The states, X and D are fp32 values and enter the products that make states as
+// three bf16 terms (24 bits).  What only the output reads goes in as two terms: the
+// decayed q.k, D and S in o's products, 2^-17 of each term where o, rounded to bf16,
+// is off by 2^-9 of itself.  fp32 inputs stay fp32 everywhere.
+#include "mixer_common.hpp"
+
+namespace rssm {
+
+template <typename T>
+constexpr int out_terms() { return Mat<T>::kTerms > 2 ? 2 : Mat<T>::kTerms; }
+
+template <typename T, int TA, int TB>
+__device__ static inline Split<T, TB> cut(const Split<T, TA>& s) {  // the leading terms
+  Split<T, TB> r;
+#pragma unroll
+  for (int k = 0; k < TB; ++k) r.t[k] = s.t[k];
+  return r;
+}
+
+template <typename T, int K, bool DELTA>
+__global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 1 : 2)
+    mix_forward_kernel(const MixArgs a) {
+  typedef Mat<T> M;
+  typedef typename M::E E;
+  typedef typename M::Frag Frag;
+  constexpr int TS = M::kTerms, TO = out_terms<T>();
+  constexpr int LK = K + M::kPad, LV = 64 + M::kPad, KT = K / 16, KB = K / 32;
+  constexpr int TF = 6 * TS * 64 * sizeof(Frag) / 16;  // 16-byte pieces of T
+  constexpr int QT = DELTA ? (TF + 255) / 256 : 1;
+  __shared__ __attribute__((aligned(16))) E sK[kQ * LK];
+  __shared__ __attribute__((aligned(16))) E sQ[kQ * LK];
+  __shared__ __attribute__((aligned(16))) E sV[kQ * LV];
+  __shared__ __attribute__((aligned(16))) u32x4 sT[DELTA ? TF : 1];
+  __shared__ __attribute__((aligned(16))) u32x4 sP[6 * TO * 64 * sizeof(Frag) / 16];
+  __shared__ ChunkGates sg;
+  int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const MixUnit un = mix_unit(a, blockIdx.x, a.vpk * a.slices);
+  if (blockIdx.x == 0) check_table(a.cu, a.seqs, a.tokens, a.status);
+  if (!un.live) return;
+  const int hv = un.hk * a.vpk + un.rest / a.slices, v0 = (un.rest % a.slices) * 64;
+  const SeqSpan sp = seq_span(a.cu, un.seq, a.seqs, a.tokens);
+  const int pool = a.init || a.final_state ? mix_slot(a, un.seq) : -1;
+  if (tid == 0 && un.rest == 0 && un.hk == 0 && a.status && (a.init || a.final_state) && pool < 0)
+    atomicOr(a.status, RSSM_ST_BAD_SLOT);
+  // S: rows k = 16 kt + 4g + r, column v0 + 16 wave + i16
+  f32x4 S[KT];
+#pragma unroll
+  for (int kt = 0; kt < KT; ++kt) S[kt] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const auto place = [&]() {
+    return (((long)pool * a.v_heads + hv) * a.dv + v0 + 16 * wave + (lane & 15)) * K + 4 * (lane >> 4);
+  };
+  if (a.init && pool >= 0 && (!a.has_init || a.has_init[un.seq])) {
+    const float* p = a.init + place();
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt) S[kt] = *reinterpret_cast<const f32x4*>(p + 16 * kt);
+  }
+  const E* const ksrc = static_cast<const E*>(a.k) + (long)un.hk * K;
+  const E* const qsrc = static_cast<const E*>(a.q) + (long)un.hk * K;
+  const E* const vsrc = static_cast<const E*>(a.v) + (long)hv * a.dv + v0;
+  const long cbase = seg_base(a.cu, un.seq, kQ, a.tokens);
+  const int chunks = (sp.len + kQ - 1) / kQ;
+  TileLoad<T, K, 256> rk, rq;
+  TileLoad<T, 64, 256> rv;
+  u32x4 rt[QT];
+  double rg = 0.0;
+  float rb = 0.f;
+  const auto fetch = [&](int c) {
+    const int rows = sp.len - c * kQ < kQ ? sp.len - c * kQ : kQ;
+    const long t0 = sp.start + (long)c * kQ;
+    rk.fetch(ksrc + t0 * a.k_stride, a.k_stride, rows, tid);
+    rq.fetch(qsrc + t0 * a.q_stride, a.q_stride, rows, tid);
+    rv.fetch(vsrc + t0 * a.v_stride, a.v_stride, rows, tid);
+    if (DELTA) {
+      const u32x4* src = static_cast<const u32x4*>(a.tinv) + ((cbase + c) * a.v_heads + hv) * TF;
+#pragma unroll
+      for (int i = 0; i < QT; ++i)
+        if (TF % 256 == 0 || i * 256 + tid < TF) rt[i] = src[i * 256 + tid];
+    }
+    const bool live = lane < rows;
+    rg = gate_log2(a, t0 + lane, hv, live);
+    if (DELTA) rb = live ? a.beta[(t0 + lane) * a.v_heads + hv] : 0.f;
+  };
+  if (chunks) fetch(0);
+#pragma unroll 1
+  for (int c = 0; c < chunks; ++c) {
+    tid = threadIdx.x;
+    forget(tid);
+    lane = tid & 63;
+    const int i16 = lane & 15, g = lane >> 4;
+    const int rows = sp.len - c * kQ < kQ ? sp.len - c * kQ : kQ;
+    const long t0 = sp.start + (long)c * kQ;
+    __syncthreads();  // the previous chunk's tiles are no longer read
+    rk.put(sK, LK, tid);
+    rq.put(sQ, LK, tid);
+    rv.put(sV, LV, tid);
+    if (DELTA) {
+#pragma unroll
+      for (int i = 0; i < QT; ++i)
+        if (TF % 256 == 0 || i * 256 + tid < TF) sT[i * 256 + tid] = rt[i];
+    }
+    if (wave == 3) sg.set(rg, rb, lane);
+    if (c + 1 < chunks) fetch(c + 1);
+    __syncthreads();
+    // scale e^{G_i-G_j} q_i.k_j of the lower triangle: fragments 0 (it 0) and 4 (3, 0);
+    // 5 (3, 1); 1 (1, 0) and 3 (2, 1); 2 (2, 0)
+    {
+      const auto make = [&](int it, int kb) {
+        f32x4 acc[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) acc[h] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int b = 0; b < KB; ++b) {
+          const Frag qf = M::rows_c(sQ + (16 * it + i16) * LK + 32 * b + 8 * g);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            if (2 * kb + h <= it)
+              acc[h] = M::mma(M::rows_c(sK + (16 * (2 * kb + h) + i16) * LK + 32 * b + 8 * g), qf, acc[h]);
+        }
+        const float2 gi = sg.G[16 * it + i16];
+        float f[8];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int j = 16 * (2 * kb + h) + 4 * g + r;
+            const float w = a.scale * exp2_f32(gap2(gi, sg.G[j])) * acc[h][r];
+            f[4 * h + r] = j <= 16 * it + i16 ? w : 0.f;
+          }
+        Split<T, TO> s;
+        s.set(f);
+        put_split<T, TO>(sP, low_frag(it, kb), s, lane);
+      };
+      if (wave == 0) {
+        make(3, 0);
+        make(0, 0);
+      } else if (wave == 1) {
+        make(3, 1);
+      } else if (wave == 2) {
+        make(2, 0);
+      } else {
+        make(1, 0);
+        make(2, 1);
+      }
+    }
+    f32x4 R[4], O[4];  // K S, rows t; (Q S)^T, columns t
+#pragma unroll
+    for (int it = 0; it < 4; ++it) R[it] = O[it] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int b = 0; b < KB; ++b) {
+      float f[8];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        f[r] = S[2 * b][r];
+        f[4 + r] = S[2 * b + 1][r];
+      }
+      Split<T, DELTA ? TS : TO> sf;
+      sf.set(f);
+      const auto so = cut<T, DELTA ? TS : TO, TO>(sf);
+      Frag kf[4], qf[4];
+#pragma unroll
+      for (int it = 0; it < 4; ++it) {
+        if (DELTA) kf[it] = M::rows_d(sK + (16 * it + i16) * LK + 32 * b + 4 * g);
+        qf[it] = M::rows_d(sQ + (16 * it + i16) * LK + 32 * b + 4 * g);
+      }
+      if (DELTA) {
+#pragma unroll
+        for (int k = TS - 1; k >= 0; --k)
+#pragma unroll
+          for (int it = 0; it < 4; ++it) R[it] = M::mma(kf[it], sf.t[k < TS ? k : 0], R[it]);
+      }
+#pragma unroll
+      for (int k = TO - 1; k >= 0; --k)
+#pragma unroll
+        for (int it = 0; it < 4; ++it) O[it] = M::mma(so.t[k], qf[it], O[it]);
+    }
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+      const float e = a.scale * sg.eg[16 * it + i16];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) O[it][r] *= e;
+    }
+    float d[2][8];  // D, token 32 kb + (4g + r, 16 + 4g + r), this lane's column
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+      M::unpack(M::cols(cols_at<T, false>(sV, LV, 32 * kb, 16 * wave, lane), LV), d[kb]);
+      if (DELTA) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const f32x4 e = *reinterpret_cast<const f32x4*>(&sg.eg[32 * kb + 16 * h + 4 * g]);
+          const f32x4 b = *reinterpret_cast<const f32x4*>(&sg.beta[32 * kb + 16 * h + 4 * g]);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) d[kb][4 * h + r] = b[r] * fmaf(-e[r], R[2 * kb + h][r], d[kb][4 * h + r]);
+        }
+      }
+    }
+    if (DELTA) {
+      f32x4 acc[4];
+#pragma unroll
+      for (int it = 0; it < 4; ++it) acc[it] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) {
+        Split<T, TS> xf;
+        xf.set(d[kb]);
+#pragma unroll
+        for (int it = 2 * kb; it < 4; ++it)
+          acc[it] = mma_split<T, TS, TS>(split_at<T, TS>(sT, low_frag(it, kb), lane), xf, acc[it]);
+      }
+#pragma unroll
+      for (int it = 0; it < 4; ++it)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) d[it >> 1][4 * (it & 1) + r] = acc[it][r];
+    }
+    __syncthreads();  // sP
+    // o^T += D^T P^T, and S' = e^{G_Q} S + K^T (e^{G_Q - G} D)
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+      Split<T, DELTA ? TO : 1> df;
+      df.set(d[kb]);
+#pragma unroll
+      for (int it = 2 * kb; it < 4; ++it)
+        O[it] = mma_split<T, DELTA ? TO : 1, TO>(df, split_at<T, TO>(sP, low_frag(it, kb), lane), O[it]);
+    }
+    const float all = sg.all;
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) S[kt][r] *= all;
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+      if (32 * kb >= rows) break;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const f32x4 e = *reinterpret_cast<const f32x4*>(&sg.et[32 * kb + 16 * h + 4 * g]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) d[kb][4 * h + r] *= e[r];
+      }
+      Split<T, TS> wf;
+      wf.set(d[kb]);
+#pragma unroll
+      for (int k4 = 0; k4 < KT; k4 += 4) {
+        Frag kf[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) kf[q] = M::cols(cols_at<T, false>(sK, LK, 32 * kb, 16 * (k4 + q), lane), LK);
+#pragma unroll
+        for (int k = TS - 1; k >= 0; --k)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) S[k4 + q] = M::mma(kf[q], wf.t[k], S[k4 + q]);
+      }
+    }
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+      const int t = 16 * it + i16;
+      if (t >= rows) continue;
+      const long at = ((t0 + t) * a.v_heads + hv) * a.dv + v0 + 16 * wave + 4 * g;
+      const float f[4] = {O[it][0], O[it][1], O[it][2], O[it][3]};
+      *reinterpret_cast<typename M::Four*>(static_cast<E*>(a.o) + at) = M::pack4(f);
+    }
+  }
+  if (a.final_state && pool >= 0) {
+    float* p = a.final_state + place();
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt) *reinterpret_cast<f32x4*>(p + 16 * kt) = S[kt];
+  }
+}
+
+static size_t mix_forward_bytes(const rssm_mixer_dims* dims, bool delta) {
+  if (mix_check(dims, delta) || !delta || dims->tokens == 0) return 0;
+  const bool f32 = dims->io_dtype == RSSM_F32;
+  return (size_t)scan_slots(dims->tokens, dims->seqs, kQ) * dims->v_heads * mix_inverse_bytes(f32, false);
+}
+
+template <typename T, bool DELTA>
+static const void* pick_forward(int dk) {
+  return dk == 64 ? reinterpret_cast<const void*>(&mix_forward_kernel<T, 64, DELTA>)
+                  : reinterpret_cast<const void*>(&mix_forward_kernel<T, 128, DELTA>);
+}
+
+static int mix_forward(const rssm_mixer_dims* dims, bool delta, const void* q, const void* k, const void* v,
+                       const float* g, const float* beta, const int32_t* cu_seqlens,
+                       const float* initial_state, const uint8_t* has_initial, const int32_t* slot_idx,
+                       float* final_state, void* o, void* workspace, size_t workspace_bytes,
+                       int32_t* status, hipStream_t stream) {
+  int rc = mix_check(dims, delta);
+  if (rc) return rc;
+  const rssm_mixer_dims& d = *dims;
+  if (d.seqs == 0) return d.tokens == 0 ? RSSM_OK : RSSM_EINVAL;
+  if (!cu_seqlens && d.seqs != 1) return RSSM_EINVAL;
+  if (d.tokens > 0 && (!q || !k || !v || !o || (d.decay && !g) || (delta && !beta))) return RSSM_EINVAL;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(initial_state) ||
+      !aligned16(final_state) || !aligned16(workspace))
+    return RSSM_EINVAL;
+  const size_t need = mix_forward_bytes(dims, delta);
+  if (need && (!workspace || workspace_bytes < need)) return RSSM_EINVAL;
+  MixArgs a{};
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.g = g;
+  a.beta = beta;
+  a.cu = cu_seqlens;
+  a.init = initial_state;
+  a.has_init = has_initial;
+  a.slot_idx = slot_idx;
+  a.final_state = final_state;
+  a.o = o;
+  a.tinv = workspace;
+  a.status = status;
+  mix_fill(a, d);
+  const bool f32 = d.io_dtype == RSSM_F32;
+  const long cslots = scan_slots(d.tokens, d.seqs, kQ);
+  const long grid = mix_grid(d.seqs, d.k_heads, (long)a.vpk * a.slices);
+  if (!grid_fits(grid, 256) || (delta && !grid_fits(cslots * ((d.v_heads + 3) / 4), 256))) return RSSM_ESHAPE;
+  if (delta && d.tokens > 0) {
+    rc = f32 ? launch_inverse<float, false>(a, d.dk, cslots, stream)
+             : launch_inverse<bf16, false>(a, d.dk, cslots, stream);
+    if (rc) return rc;
+  }
+  const void* fn = f32 ? (delta ? pick_forward<float, true>(d.dk) : pick_forward<float, false>(d.dk))
+                       : (delta ? pick_forward<bf16, true>(d.dk) : pick_forward<bf16, false>(d.dk));
+  return launch_kernel(fn, (unsigned)grid, 256, 0, stream, a);
+}
+
+}  // namespace rssm
+
+using namespace rssm;
+
+extern "C" int linear_attention_forward(const rssm_mixer_dims* dims, const void* q, const void* k,
+                                        const void* v, const float* log_decay, const int32_t* cu_seqlens,
+                                        const float* initial_state, const uint8_t* has_initial,
+                                        const int32_t* slot_idx, float* final_state, void* o,
+                                        int32_t* status, hipStream_t stream) {
+  return mix_forward(dims, false, q, k, v, log_decay, nullptr, cu_seqlens, initial_state, has_initial,
+                     slot_idx, final_state, o, nullptr, 0, status, stream);
+}
+
+extern "C" size_t gdn_scan_forward_workspace(const rssm_mixer_dims* dims) {
+  return mix_forward_bytes(dims, true);
+}
+
+extern "C" int gdn_scan_forward(const rssm_mixer_dims* dims, const void* q, const void* k, const void* v,
+                                const float* log_g, const float* beta, const int32_t* cu_seqlens,
+                                const float* initial_state, const uint8_t* has_initial,
+                                const int32_t* slot_idx, float* final_state, void* o, void* workspace,
+                                size_t workspace_bytes, int32_t* status, hipStream_t stream) {
+  return mix_forward(dims, true, q, k, v, log_g, beta, cu_seqlens, initial_state, has_initial, slot_idx,
+                     final_state, o, workspace, workspace_bytes, status, stream);
+}
