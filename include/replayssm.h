@@ -719,11 +719,13 @@ typedef struct rssm_mixer_dims {
  * or infinity in a token's inputs may also show in the up to 63 tokens of its
  * sequence and chunk before it, and never in another sequence.
  */
+size_t linear_attention_forward_workspace(const rssm_mixer_dims* dims);
 int linear_attention_forward(const rssm_mixer_dims* dims, const void* q, const void* k,
                              const void* v, const float* log_decay,
                              const int32_t* cu_seqlens, const float* initial_state,
                              const uint8_t* has_initial, const int32_t* slot_idx,
-                             float* final_state, void* o, int32_t* status,
+                             float* final_state, void* o, void* workspace,
+                             size_t workspace_bytes, int32_t* status,
                              hipStream_t stream);
 
 /*

@@ -46,7 +46,7 @@ EXPORTS = ("ssu_standard_decode", "replayssm_decode", "replayssm_ring_reset",
            "ssu_scan_backward_workspace", "causal_conv_forward", "causal_conv_backward",
            "causal_conv_backward_workspace", "causal_conv_decode", "rms_norm_forward",
            "rms_norm_backward", "rms_norm_backward_workspace", "linear_attention_forward",
-           "linear_attention_backward", "linear_attention_backward_workspace",
+           "linear_attention_forward_workspace", "linear_attention_backward", "linear_attention_backward_workspace",
            "linear_attention_decode", "gdn_scan_forward", "gdn_scan_forward_workspace",
            "gdn_scan_backward", "gdn_scan_backward_workspace", "rotary_forward", "rotary_backward")
 

@@ -24,337 +24,9 @@
 // as the six products that fp32 can hold, because dg and dbeta are fp32 results; N and
 // L, which only dq and dk read, as two (2^-17 of each term; dq and dk are rounded to
 // 2^-9 of themselves).  fp32 inputs stay fp32.
-#include "mixer_common.hpp"
+#include "mixer_states.hpp"
 
 namespace rssm {
-
-struct MixBwdArgs {
-  MixArgs m;
-  const void* dout;
-  const float* dfinal;
-  void* dq;
-  void* dk;
-  void* dv;
-  float* dg;
-  float* dbeta;
-  float* dinit;
-  float* state;  // [chunk slots][v_heads][V][K]: before the chunk
-  float* grad;   // dS', the same
-  float* D;      // [chunk slots][v_heads][64][V]
-  float* dX;     // the same
-  float* part;   // [chunk slots][v_heads]: dg summed over the chunk
-  long do_stride, cslots;
-  int32_t dir_blocks;
-};
-
-template <typename T, int K, bool DELTA>
-struct StatesLds {
-  typedef typename Mat<T>::E E;
-  static constexpr int kFrag = sizeof(typename Mat<T>::Frag), TS = Mat<T>::kTerms;
-  static constexpr int LK = K + Mat<T>::kPad;
-  static constexpr int TF = 6 * TS * 64 * kFrag / 16;  // 16-byte pieces of T or its transpose
-  __attribute__((aligned(16))) E k[kQ * LK];
-  __attribute__((aligned(16))) E q[kQ * LK];
-  __attribute__((aligned(16))) E v[kQ * 64];  // V forward, dO backward
-  __attribute__((aligned(16))) u32x4 t[DELTA ? TF : 1];
-  __attribute__((aligned(16))) u32x4 p[TF];
-  ChunkGates g;
-};
-
-// One of the two recurrences, a workgroup for 64 columns of one value head's state and
-// one sequence (mix_forward_kernel without the outputs; blocks from dir_blocks on:
-// backward, last chunk first).
-template <typename T, int K, bool DELTA>
-__global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 1 : 2)
-    mix_states_kernel(const MixBwdArgs b) {
-  typedef Mat<T> M;
-  typedef typename M::E E;
-  typedef typename M::Frag Frag;
-  typedef StatesLds<T, K, DELTA> L;
-  constexpr int TS = M::kTerms, LK = L::LK, KT = K / 16, KB = K / 32, TF = L::TF;
-  constexpr int QT = DELTA ? (TF + 255) / 256 : 1;
-  __shared__ L s;
-  const MixArgs& a = b.m;
-  int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const bool back = (int)blockIdx.x >= b.dir_blocks;
-  const MixUnit un = mix_unit(a, back ? blockIdx.x - b.dir_blocks : blockIdx.x, a.vpk * a.slices);
-  if (blockIdx.x == 0) check_table(a.cu, a.seqs, a.tokens, a.status);
-  if (!un.live) return;
-  const int hv = un.hk * a.vpk + un.rest / a.slices, v0 = (un.rest % a.slices) * 64;
-  const SeqSpan sp = seq_span(a.cu, un.seq, a.seqs, a.tokens);
-  const int pool = a.init ? mix_slot(a, un.seq) : -1;
-  if (tid == 0 && !back && un.rest == 0 && un.hk == 0 && a.status && a.init && pool < 0)
-    atomicOr(a.status, RSSM_ST_BAD_SLOT);
-  const bool has = pool >= 0 && (!a.has_init || a.has_init[un.seq]);
-  f32x4 S[KT];
-#pragma unroll
-  for (int kt = 0; kt < KT; ++kt) S[kt] = f32x4{0.f, 0.f, 0.f, 0.f};
-  // this lane's first element in state number n
-  const auto place = [&](long n) {
-    return ((n * a.v_heads + hv) * a.dv + v0 + 16 * wave + (lane & 15)) * K + 4 * (lane >> 4);
-  };
-  {
-    const float* src = back ? b.dfinal : (has ? a.init : nullptr);
-    if (src) {
-      src += place(back ? un.seq : pool);
-#pragma unroll
-      for (int kt = 0; kt < KT; ++kt) S[kt] = *reinterpret_cast<const f32x4*>(src + 16 * kt);
-    }
-  }
-  const E* const ksrc = static_cast<const E*>(a.k) + (long)un.hk * K;
-  const E* const qsrc = static_cast<const E*>(a.q) + (long)un.hk * K;
-  const E* const vsrc = static_cast<const E*>(back ? b.dout : a.v) + (long)hv * a.dv + v0;
-  const long vstride = back ? b.do_stride : a.v_stride;
-  const long cbase = seg_base(a.cu, un.seq, kQ, a.tokens);
-  const int chunks = (sp.len + kQ - 1) / kQ;
-  TileLoad<T, K, 256> rk, rq;
-  TileLoad<T, 64, 256> rv;
-  u32x4 rt[QT];
-  double rg = 0.0;
-  float rb = 0.f;
-  const auto fetch = [&](int c) {
-    const int rows = sp.len - c * kQ < kQ ? sp.len - c * kQ : kQ;
-    const long t0 = sp.start + (long)c * kQ;
-    rk.fetch(ksrc + t0 * a.k_stride, a.k_stride, rows, tid);
-    if (back) rq.fetch(qsrc + t0 * a.q_stride, a.q_stride, rows, tid);
-    rv.fetch(vsrc + t0 * vstride, vstride, rows, tid);
-    if (DELTA) {
-      const u32x4* src = static_cast<const u32x4*>(a.tinv) + (((cbase + c) * a.v_heads + hv) * 2 + back) * TF;
-#pragma unroll
-      for (int i = 0; i < QT; ++i)
-        if (TF % 256 == 0 || i * 256 + tid < TF) rt[i] = src[i * 256 + tid];
-    }
-    const bool live = lane < rows;
-    rg = gate_log2(a, t0 + lane, hv, live);
-    if (DELTA) rb = live ? a.beta[(t0 + lane) * a.v_heads + hv] : 0.f;
-  };
-  float* const keep = back ? b.grad : b.state;
-  float* const rowmat = back ? b.dX : b.D;
-  if (chunks) fetch(back ? chunks - 1 : 0);
-#pragma unroll 1
-  for (int n = 0; n < chunks; ++n) {
-    const int c = back ? chunks - 1 - n : n;
-    tid = threadIdx.x;
-    forget(tid);
-    lane = tid & 63;
-    const int i16 = lane & 15, g = lane >> 4;
-    const int rows = sp.len - c * kQ < kQ ? sp.len - c * kQ : kQ;
-    const long t0 = sp.start + (long)c * kQ;
-    {
-      float* p = keep + place(cbase + c);
-#pragma unroll
-      for (int kt = 0; kt < KT; ++kt) *reinterpret_cast<f32x4*>(p + 16 * kt) = S[kt];
-    }
-    __syncthreads();  // the previous chunk's tiles are no longer read
-    rk.put(s.k, LK, tid);
-    if (back) rq.put(s.q, LK, tid);
-    rv.put(s.v, 64, tid);
-    if (DELTA) {
-#pragma unroll
-      for (int i = 0; i < QT; ++i)
-        if (TF % 256 == 0 || i * 256 + tid < TF) s.t[i * 256 + tid] = rt[i];
-    }
-    if (wave == 3) s.g.set(rg, rb, lane);
-    if (n + 1 < chunks) fetch(back ? c - 1 : c + 1);
-    __syncthreads();
-    if (back) {
-      // P^T by rows j, fragments (0, 1); (0, 0) and (3, 1); (1, 1); (2, 1) and (1, 0)
-      const auto make = [&](int jt, int kb) {
-        f32x4 acc[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) acc[h] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int x = 0; x < KB; ++x) {
-          const Frag kf = M::rows_c(s.k + (16 * jt + i16) * LK + 32 * x + 8 * g);
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            if (2 * kb + h >= jt)
-              acc[h] = M::mma(M::rows_c(s.q + (16 * (2 * kb + h) + i16) * LK + 32 * x + 8 * g), kf, acc[h]);
-        }
-        const int j = 16 * jt + i16;
-        const float2 gj = s.g.G[j];
-        float f[8];
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int i = 16 * (2 * kb + h) + 4 * g + r;
-            const float w = a.scale * exp2_f32(gap2(s.g.G[i], gj)) * acc[h][r];
-            f[4 * h + r] = i >= j ? w : 0.f;
-          }
-        Split<T, TS> sp3;
-        sp3.set(f);
-        put_split<T, TS>(s.p, up_frag(jt, kb), sp3, lane);
-      };
-      if (wave == 0) {
-        make(0, 1);
-      } else if (wave == 1) {
-        make(0, 0);
-        make(3, 1);
-      } else if (wave == 2) {
-        make(1, 1);
-      } else {
-        make(2, 1);
-        make(1, 0);
-      }
-    }
-    // K S (or K dS'), rows t
-    f32x4 R[4];
-#pragma unroll
-    for (int it = 0; it < 4; ++it) R[it] = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (DELTA || back) {
-#pragma unroll
-      for (int x = 0; x < KB; ++x) {
-        float f[8];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          f[r] = S[2 * x][r];
-          f[4 + r] = S[2 * x + 1][r];
-        }
-        Split<T, TS> sf;
-        sf.set(f);
-        Frag kf[4];
-#pragma unroll
-        for (int it = 0; it < 4; ++it) kf[it] = M::rows_d(s.k + (16 * it + i16) * LK + 32 * x + 4 * g);
-#pragma unroll
-        for (int k = TS - 1; k >= 0; --k)
-#pragma unroll
-          for (int it = 0; it < 4; ++it) R[it] = M::mma(kf[it], sf.t[k], R[it]);
-      }
-    }
-    if (back) __syncthreads();  // s.p
-    float d[2][8];  // tokens 32 kb + (4g + r, 16 + 4g + r), this lane's column
-    Frag vf[2];
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
-      vf[kb] = M::cols(cols_at<T, false>(s.v, 64, 32 * kb, 16 * wave, lane), 64);
-      M::unpack(vf[kb], d[kb]);
-    }
-    if (back) {  // dD
-#pragma unroll
-      for (int it = 0; it < 4; ++it) {
-        const f32x4 e = *reinterpret_cast<const f32x4*>(&s.g.et[16 * it + 4 * g]);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) R[it][r] *= e[r];
-#pragma unroll
-        for (int kb = it / 2; kb < 2; ++kb) {
-          const auto pf = split_at<T, TS>(s.p, up_frag(it, kb), lane);
-          R[it] = pf.a_times(vf[kb], R[it]);
-        }
-      }
-    } else if (DELTA) {  // X
-#pragma unroll
-      for (int it = 0; it < 4; ++it) {
-        const f32x4 e = *reinterpret_cast<const f32x4*>(&s.g.eg[16 * it + 4 * g]);
-        const f32x4 be = *reinterpret_cast<const f32x4*>(&s.g.beta[16 * it + 4 * g]);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) R[it][r] = be[r] * fmaf(-e[r], R[it][r], d[it >> 1][4 * (it & 1) + r]);
-      }
-    }
-    if (DELTA) {  // D = T X, or dX = T^T dD
-      f32x4 acc[4];
-      Split<T, TS> xf[2];
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb) {
-        float f[8];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          f[r] = R[2 * kb][r];
-          f[4 + r] = R[2 * kb + 1][r];
-        }
-        xf[kb].set(f);
-      }
-#pragma unroll
-      for (int it = 0; it < 4; ++it) acc[it] = f32x4{0.f, 0.f, 0.f, 0.f};
-      if (back) {
-#pragma unroll
-        for (int it = 0; it < 4; ++it)
-#pragma unroll
-          for (int kb = it / 2; kb < 2; ++kb)
-            acc[it] = mma_split<T, TS, TS>(split_at<T, TS>(s.t, up_frag(it, kb), lane), xf[kb], acc[it]);
-      } else {
-#pragma unroll
-        for (int it = 0; it < 4; ++it)
-#pragma unroll
-          for (int kb = 0; kb <= it / 2; ++kb)
-            acc[it] = mma_split<T, TS, TS>(split_at<T, TS>(s.t, low_frag(it, kb), lane), xf[kb], acc[it]);
-      }
-      float* p = rowmat + ((cbase + c) * a.v_heads + hv) * (long)(kQ * a.dv) + v0 + 16 * wave + i16;
-#pragma unroll
-      for (int it = 0; it < 4; ++it) {
-        R[it] = acc[it];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) p[(16 * it + 4 * g + r) * a.dv] = acc[it][r];
-      }
-    } else if (back) {  // linear attention: dV
-#pragma unroll
-      for (int it = 0; it < 4; ++it)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int t = 16 * it + 4 * g + r;
-          if (t < rows) Elt<T>::store1(b.dv, ((t0 + t) * a.v_heads + hv) * a.dv + v0 + 16 * wave + i16, R[it][r]);
-        }
-    }
-    if (!back && n + 1 == chunks) break;  // the end is not read
-    const float all = s.g.all;
-#pragma unroll
-    for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) S[kt][r] *= all;
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
-      if (32 * kb >= rows) break;
-      float f[8];  // the weighted rows that go with K (D; backward: dX), and with Q (dO)
-      float o[8];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int at = 32 * kb + 16 * h + 4 * g;
-        const f32x4 e = *reinterpret_cast<const f32x4*>(back ? &s.g.eg[at] : &s.g.et[at]);
-        const f32x4 be = *reinterpret_cast<const f32x4*>(&s.g.beta[at]);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          o[4 * h + r] = a.scale * e[r] * d[kb][4 * h + r];
-          f[4 * h + r] = back ? -be[r] * e[r] * R[2 * kb + h][r]
-                              : e[r] * (DELTA ? R[2 * kb + h][r] : d[kb][4 * h + r]);
-        }
-      }
-      Split<T, TS> wf;
-      if (DELTA || !back) {
-        wf.set(f);
-#pragma unroll
-        for (int k4 = 0; k4 < KT; k4 += 4) {
-          Frag kf[4];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) kf[x] = M::cols(cols_at<T, false>(s.k, LK, 32 * kb, 16 * (k4 + x), lane), LK);
-#pragma unroll
-          for (int k = TS - 1; k >= 0; --k)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) S[k4 + x] = M::mma(kf[x], wf.t[k], S[k4 + x]);
-        }
-      }
-      if (back) {
-        wf.set(o);
-#pragma unroll
-        for (int k4 = 0; k4 < KT; k4 += 4) {
-          Frag qf[4];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) qf[x] = M::cols(cols_at<T, false>(s.q, LK, 32 * kb, 16 * (k4 + x), lane), LK);
-#pragma unroll
-          for (int k = TS - 1; k >= 0; --k)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) S[k4 + x] = M::mma(qf[x], wf.t[k], S[k4 + x]);
-        }
-      }
-    }
-  }
-  if (back && b.dinit) {
-    float* p = b.dinit + place(un.seq);
-#pragma unroll
-    for (int kt = 0; kt < KT; ++kt)
-      *reinterpret_cast<f32x4*>(p + 16 * kt) = has ? S[kt] : f32x4{0.f, 0.f, 0.f, 0.f};
-  }
-}
 
 template <typename T, int K, bool DELTA>
 struct MainLds {
@@ -768,23 +440,20 @@ __global__ void __launch_bounds__(256) mix_decay_sum_kernel(const MixBwdArgs b) 
 
 struct BwdLayout {
   size_t tinv, state, grad, D, dX, part, end;
+  SegLayout seg;
 };
 static BwdLayout bwd_layout(const rssm_mixer_dims& d, bool delta) {
   BwdLayout l{};
   const size_t units = (size_t)scan_slots(d.tokens, d.seqs, kQ) * d.v_heads;
-  size_t at = 0;
-  const auto take = [&](size_t bytes) {
-    const size_t p = at;
-    at += (bytes + 15) / 16 * 16;
-    return p;
-  };
+  MixTake take;
   l.tinv = take(delta ? units * mix_inverse_bytes(d.io_dtype == RSSM_F32, true) : 0);
   l.state = take(units * d.dk * d.dv * 4);
   l.grad = take(units * d.dk * d.dv * 4);
   l.D = take(delta ? units * kQ * d.dv * 4 : 0);
   l.dX = take(delta ? units * kQ * d.dv * 4 : 0);
   l.part = take(units * 4);
-  l.end = at;
+  l.seg = seg_layout(d, delta, true, take);
+  l.end = take.at;
   return l;
 }
 
@@ -792,8 +461,8 @@ enum { kBwdStates, kBwdMain };
 template <typename T, bool DELTA>
 static const void* pick_bwd(int which, int dk) {
   if (which == kBwdStates)
-    return dk == 64 ? reinterpret_cast<const void*>(&mix_states_kernel<T, 64, DELTA>)
-                    : reinterpret_cast<const void*>(&mix_states_kernel<T, 128, DELTA>);
+    return dk == 64 ? reinterpret_cast<const void*>(&mix_states_kernel<T, 64, DELTA, true, true>)
+                    : reinterpret_cast<const void*>(&mix_states_kernel<T, 128, DELTA, true, true>);
   return dk == 64 ? reinterpret_cast<const void*>(&mix_main_kernel<T, 64, DELTA>)
                   : reinterpret_cast<const void*>(&mix_main_kernel<T, 128, DELTA>);
 }
@@ -831,8 +500,9 @@ static int mix_backward(const rssm_mixer_dims* dims, bool delta, MixBwdArgs b, v
   b.part = d.decay == RSSM_DECAY_HEAD ? reinterpret_cast<float*>(ws + l.part) : nullptr;
   const bool f32 = d.io_dtype == RSSM_F32;
   b.cslots = scan_slots(d.tokens, d.seqs, kQ);
-  const long dir = mix_grid(d.seqs, d.k_heads, (long)a.vpk * a.slices), mgrid = b.cslots * d.k_heads;
-  if (!grid_fits(2 * dir, 256) || !grid_fits(mgrid, 4 * d.dk) ||
+  seg_fill(a, d, l.seg, workspace);
+  const long dir = mix_grid(a.slots, d.k_heads, (long)a.vpk * a.slices), mgrid = b.cslots * d.k_heads;
+  if (!segments_fit(a, d.dk) || !grid_fits(mgrid, 4 * d.dk) ||
       !grid_fits(b.cslots * ((d.v_heads + 3) / 4), 256))
     return RSSM_ESHAPE;
   b.dir_blocks = (int)dir;
@@ -845,6 +515,13 @@ static int mix_backward(const rssm_mixer_dims* dims, bool delta, MixBwdArgs b, v
   } else if (delta) {
     rc = f32 ? launch_inverse<float, true>(a, d.dk, b.cslots, stream)
              : launch_inverse<bf16, true>(a, d.dk, b.cslots, stream);
+    if (rc) return rc;
+  }
+  if (d.tokens > a.seg) {
+    rc = f32 ? (delta ? launch_segments<float, true, true>(b, d.dk, stream)
+                      : launch_segments<float, false, true>(b, d.dk, stream))
+             : (delta ? launch_segments<bf16, true, true>(b, d.dk, stream)
+                      : launch_segments<bf16, false, true>(b, d.dk, stream));
     if (rc) return rc;
   }
   rc = launch_kernel(pick(kBwdStates), (unsigned)(2 * dir), 256, 0, stream, b);

@@ -36,8 +36,13 @@ struct MixArgs {
   void* o;
   void* tinv;          // [chunk slots][v_heads][6 (12) fragments][terms][64]
   int32_t* status;
+  float* seg_state;    // [segment slots][v_heads][V][K]
+  float* seg_grad;     // the same
+  float* seg_decay;    // [segment slots][v_heads]
+  void* trans;         // [segment slots][v_heads][K K / 512 (twice) fragments][terms][64]
   long q_stride, k_stride, v_stride;
   int32_t tokens, seqs, k_heads, v_heads, vpk, dv, num_slots, decay, slices;
+  int32_t seg, slots;  // tokens of a segment, segment slots
   float scale;
 };
 
@@ -71,6 +76,31 @@ __device__ static inline double gate_log2(const MixArgs& a, long t, int hv, bool
   return (double)(g < -1e4f ? -1e4f : g) * 1.4426950408889634074;
 }
 
+// Inclusive sum over the wave's lanes in double, by lane shifts within the vector unit:
+// it stands on every chunk's path, and through LDS it took six round trips.
+template <int CTRL, int ROWS>
+__device__ static inline double dpp_moved(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROWS, 0xF, true);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, ROWS, 0xF, true);
+  return __builtin_bit_cast(double, (uint64_t)lo | ((uint64_t)hi << 32));
+}
+__device__ static inline double lane_sums(double v) {
+  v += dpp_moved<0x111, 0xF>(v);  // from 1, 2, 4 and 8 lanes below in the row of 16
+  v += dpp_moved<0x112, 0xF>(v);
+  v += dpp_moved<0x114, 0xF>(v);
+  v += dpp_moved<0x118, 0xF>(v);
+  v += dpp_moved<0x142, 0xA>(v);  // a row's last lane to the next row
+  v += dpp_moved<0x143, 0xC>(v);  // lane 31 to the upper half
+  return v;
+}
+__device__ static inline double last_lane(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, 63);
+  const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), 63);
+  return __builtin_bit_cast(double, (uint64_t)lo | ((uint64_t)hi << 32));
+}
+
 // A chunk's decays, one token a lane, as the kernels read them from LDS.
 struct ChunkGates {
   float2 G[kQ];                                      // log2 of the decay since the chunk began
@@ -79,7 +109,7 @@ struct ChunkGates {
   __attribute__((aligned(16))) float beta[kQ];
   float all;                                         // e^{G_Q}
   __device__ inline void set(double log2g, float b, int lane) {
-    const double cum = wave_cumsum(log2g, lane), last = __shfl(cum, 63, 64);
+    const double cum = lane_sums(log2g), last = last_lane(cum);
     const float hi = (float)cum;
     G[lane] = make_float2(hi, (float)(cum - (double)hi));
     eg[lane] = exp2_f32(hi);
@@ -139,22 +169,22 @@ __device__ static inline Split<T, TERMS> split_at(const void* base, int i, int l
 template <typename T>
 constexpr int mix_terms() { return Mat<T>::kTerms; }
 
-// Units (a sequence's key head) are dealt to the eight dies in turn, so that a long
+// Units (a segment's key head) are dealt to the eight dies in turn, so that a long
 // sequence's heads are spread over them and a key head's workgroups share one L2.
 struct MixUnit {
-  int seq, hk, rest;
+  int slot, hk, rest;
   bool live;
 };
 __device__ static inline MixUnit mix_unit(const MixArgs& a, int id, int per) {
   const int j = id >> 3, u = (j / per) * 8 + (id & 7);
   MixUnit m;
-  m.live = u < a.seqs * a.k_heads;
-  m.seq = m.live ? u / a.k_heads : 0;
+  m.live = u < a.slots * a.k_heads;
+  m.slot = m.live ? u / a.k_heads : 0;
   m.hk = m.live ? u % a.k_heads : 0;
   m.rest = j % per;
   return m;
 }
-static inline long mix_grid(long seqs, long k_heads, long per) { return (seqs * k_heads + 7) / 8 * 8 * per; }
+static inline long mix_grid(long slots, long k_heads, long per) { return (slots * k_heads + 7) / 8 * 8 * per; }
 
 // 16x16x16 in fp32: operand registers hold four values of k = 4g + e.
 __device__ static inline f32x4 mm16(f32x4 x, f32x4 y, f32x4 c) {
@@ -189,7 +219,7 @@ static __global__ void __launch_bounds__(256) mix_inverse_kernel(const MixArgs a
   const long t0 = sg.tok;
   {
     const bool live = lane < rows;
-    const double cum = wave_cumsum(gate_log2(a, t0 + lane, hv, live), lane);
+    const double cum = lane_sums(gate_log2(a, t0 + lane, hv, live));
     const float hi = (float)cum;
     sG[wave][lane] = make_float2(hi, (float)(cum - (double)hi));
     sBeta[wave][lane] = live ? a.beta[(t0 + lane) * a.v_heads + hv] : 0.f;
@@ -366,6 +396,52 @@ static inline void mix_fill(MixArgs& a, const rssm_mixer_dims& d) {
   a.decay = d.decay;
   a.slices = d.dv / 64;
   a.scale = d.scale > 0.f ? d.scale : 1.f / sqrtf((float)d.dk);
+}
+
+// Tokens of a segment.  A sequence longer than this is worked on in segments: what each
+// adds from zero and (the delta rule) the matrix that its start goes through, then
+// their combination, then all segments at once.  That is up to three times the
+// recurrence's work for one sequence, and worth it where few sequences leave the
+// compute units idle: so long that a workgroup for every 64 columns and segment fills
+// them twice.
+static inline int mix_seg(const rssm_mixer_dims& d) {
+  const long chunks = (d.tokens + kQ - 1) / kQ, columns = (long)d.v_heads * (d.dv / 64);
+  long seg = (chunks * columns + 511) / 512;
+  if (seg < 8) seg = 8;
+  return (int)(seg > (1 << 20) ? (1 << 20) : seg) * kQ;
+}
+
+// Parts of a workspace, in order; every one a multiple of 16 bytes.
+struct MixTake {
+  size_t at = 0;
+  size_t operator()(size_t bytes) {
+    const size_t p = at;
+    at += (bytes + 15) / 16 * 16;
+    return p;
+  }
+};
+struct SegLayout {
+  size_t state, grad, decay, trans;
+};
+static inline SegLayout seg_layout(const rssm_mixer_dims& d, bool delta, bool both, MixTake& take) {
+  SegLayout l{};
+  if (d.tokens <= mix_seg(d)) return l;
+  const size_t units = (size_t)scan_slots(d.tokens, d.seqs, mix_seg(d)) * d.v_heads;
+  const size_t st = units * d.dk * d.dv * 4;
+  l.state = take(st);
+  l.grad = take(both ? st : 0);
+  l.decay = take(delta ? 0 : units * 4);
+  l.trans = take(delta ? units * d.dk * d.dk / 512 * (both ? 2 : 1) * 64 * (d.io_dtype == RSSM_F32 ? 32 : 48) : 0);
+  return l;
+}
+static inline void seg_fill(MixArgs& a, const rssm_mixer_dims& d, const SegLayout& l, void* workspace) {
+  char* const ws = static_cast<char*>(workspace);
+  a.seg = mix_seg(d);
+  a.slots = (int)scan_slots(d.tokens, d.seqs, a.seg);
+  a.seg_state = reinterpret_cast<float*>(ws + l.state);
+  a.seg_grad = reinterpret_cast<float*>(ws + l.grad);
+  a.seg_decay = reinterpret_cast<float*>(ws + l.decay);
+  a.trans = ws + l.trans;
 }
 
 }  // namespace rssm

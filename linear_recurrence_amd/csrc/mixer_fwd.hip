@@ -10,7 +10,7 @@
 // three bf16 terms (24 bits).  What only the output reads goes in as two terms: the
 // decayed q.k, D and S in o's products, 2^-17 of each term where o, rounded to bf16,
 // is off by 2^-9 of itself.  fp32 inputs stay fp32 everywhere.
-#include "mixer_common.hpp"
+#include "mixer_states.hpp"
 
 namespace rssm {
 
@@ -47,26 +47,31 @@ __global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 1 : 2)
   if (blockIdx.x == 0) check_table(a.cu, a.seqs, a.tokens, a.status);
   if (!un.live) return;
   const int hv = un.hk * a.vpk + un.rest / a.slices, v0 = (un.rest % a.slices) * 64;
-  const SeqSpan sp = seq_span(a.cu, un.seq, a.seqs, a.tokens);
-  const int pool = a.init || a.final_state ? mix_slot(a, un.seq) : -1;
-  if (tid == 0 && un.rest == 0 && un.hk == 0 && a.status && (a.init || a.final_state) && pool < 0)
+  const Segment sp = find_segment(a.cu, a.seqs, a.tokens, a.seg, un.slot);
+  if (sp.len == 0 && !sp.empty) return;
+  const int pool = a.init || a.final_state ? mix_slot(a, sp.seq) : -1;
+  if (tid == 0 && sp.first && un.rest == 0 && un.hk == 0 && a.status && (a.init || a.final_state) && pool < 0)
     atomicOr(a.status, RSSM_ST_BAD_SLOT);
   // S: rows k = 16 kt + 4g + r, column v0 + 16 wave + i16
   f32x4 S[KT];
 #pragma unroll
   for (int kt = 0; kt < KT; ++kt) S[kt] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const auto place = [&]() {
-    return (((long)pool * a.v_heads + hv) * a.dv + v0 + 16 * wave + (lane & 15)) * K + 4 * (lane >> 4);
+  const auto place = [&](long n) {
+    return ((n * a.v_heads + hv) * a.dv + v0 + 16 * wave + (lane & 15)) * K + 4 * (lane >> 4);
   };
-  if (a.init && pool >= 0 && (!a.has_init || a.has_init[un.seq])) {
-    const float* p = a.init + place();
+  // The pool is read here only by a sequence of one segment, whose wave also writes it:
+  // a longer one's first segment takes the copy that the combining launch left, since
+  // its last segment may already have stored the final state over the initial one.
+  const bool whole = sp.first && sp.last;
+  if (!whole || (a.init && pool >= 0 && (!a.has_init || a.has_init[sp.seq]))) {
+    const float* p = whole ? a.init + place(pool) : a.seg_state + place(un.slot);
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt) S[kt] = *reinterpret_cast<const f32x4*>(p + 16 * kt);
   }
   const E* const ksrc = static_cast<const E*>(a.k) + (long)un.hk * K;
   const E* const qsrc = static_cast<const E*>(a.q) + (long)un.hk * K;
   const E* const vsrc = static_cast<const E*>(a.v) + (long)hv * a.dv + v0;
-  const long cbase = seg_base(a.cu, un.seq, kQ, a.tokens);
+  const long cbase = seg_base(a.cu, sp.seq, kQ, a.tokens) + (long)sp.k * (a.seg / kQ);
   const int chunks = (sp.len + kQ - 1) / kQ;
   TileLoad<T, K, 256> rk, rq;
   TileLoad<T, 64, 256> rv;
@@ -75,7 +80,7 @@ __global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 1 : 2)
   float rb = 0.f;
   const auto fetch = [&](int c) {
     const int rows = sp.len - c * kQ < kQ ? sp.len - c * kQ : kQ;
-    const long t0 = sp.start + (long)c * kQ;
+    const long t0 = sp.tok + (long)c * kQ;
     rk.fetch(ksrc + t0 * a.k_stride, a.k_stride, rows, tid);
     rq.fetch(qsrc + t0 * a.q_stride, a.q_stride, rows, tid);
     rv.fetch(vsrc + t0 * a.v_stride, a.v_stride, rows, tid);
@@ -97,7 +102,7 @@ __global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 1 : 2)
     lane = tid & 63;
     const int i16 = lane & 15, g = lane >> 4;
     const int rows = sp.len - c * kQ < kQ ? sp.len - c * kQ : kQ;
-    const long t0 = sp.start + (long)c * kQ;
+    const long t0 = sp.tok + (long)c * kQ;
     __syncthreads();  // the previous chunk's tiles are no longer read
     rk.put(sK, LK, tid);
     rq.put(sQ, LK, tid);
@@ -265,17 +270,28 @@ __global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 1 : 2)
       *reinterpret_cast<typename M::Four*>(static_cast<E*>(a.o) + at) = M::pack4(f);
     }
   }
-  if (a.final_state && pool >= 0) {
-    float* p = a.final_state + place();
+  if (sp.last && a.final_state && pool >= 0) {
+    float* p = a.final_state + place(pool);
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt) *reinterpret_cast<f32x4*>(p + 16 * kt) = S[kt];
   }
 }
 
+struct FwdLayout {
+  size_t tinv, end;
+  SegLayout seg;
+};
+static FwdLayout fwd_layout(const rssm_mixer_dims& d, bool delta) {
+  FwdLayout l{};
+  MixTake take;
+  const size_t units = (size_t)scan_slots(d.tokens, d.seqs, kQ) * d.v_heads;
+  l.tinv = take(delta ? units * mix_inverse_bytes(d.io_dtype == RSSM_F32, false) : 0);
+  l.seg = seg_layout(d, delta, false, take);
+  l.end = take.at;
+  return l;
+}
 static size_t mix_forward_bytes(const rssm_mixer_dims* dims, bool delta) {
-  if (mix_check(dims, delta) || !delta || dims->tokens == 0) return 0;
-  const bool f32 = dims->io_dtype == RSSM_F32;
-  return (size_t)scan_slots(dims->tokens, dims->seqs, kQ) * dims->v_heads * mix_inverse_bytes(f32, false);
+  return mix_check(dims, delta) || dims->tokens == 0 ? 0 : fwd_layout(*dims, delta).end;
 }
 
 template <typename T, bool DELTA>
@@ -312,16 +328,28 @@ static int mix_forward(const rssm_mixer_dims* dims, bool delta, const void* q, c
   a.slot_idx = slot_idx;
   a.final_state = final_state;
   a.o = o;
-  a.tinv = workspace;
   a.status = status;
   mix_fill(a, d);
   const bool f32 = d.io_dtype == RSSM_F32;
+  const FwdLayout l = fwd_layout(d, delta);
+  a.tinv = static_cast<char*>(workspace) + l.tinv;
+  seg_fill(a, d, l.seg, workspace);
+  a.seg_grad = nullptr;  // no gradients to combine
   const long cslots = scan_slots(d.tokens, d.seqs, kQ);
-  const long grid = mix_grid(d.seqs, d.k_heads, (long)a.vpk * a.slices);
-  if (!grid_fits(grid, 256) || (delta && !grid_fits(cslots * ((d.v_heads + 3) / 4), 256))) return RSSM_ESHAPE;
+  const long grid = mix_grid(a.slots, d.k_heads, (long)a.vpk * a.slices);
+  if (!segments_fit(a, d.dk) || (delta && !grid_fits(cslots * ((d.v_heads + 3) / 4), 256))) return RSSM_ESHAPE;
   if (delta && d.tokens > 0) {
     rc = f32 ? launch_inverse<float, false>(a, d.dk, cslots, stream)
              : launch_inverse<bf16, false>(a, d.dk, cslots, stream);
+    if (rc) return rc;
+  }
+  if (d.tokens > a.seg) {
+    MixBwdArgs b{};
+    b.m = a;
+    rc = f32 ? (delta ? launch_segments<float, true, false>(b, d.dk, stream)
+                      : launch_segments<float, false, false>(b, d.dk, stream))
+             : (delta ? launch_segments<bf16, true, false>(b, d.dk, stream)
+                      : launch_segments<bf16, false, false>(b, d.dk, stream));
     if (rc) return rc;
   }
   const void* fn = f32 ? (delta ? pick_forward<float, true>(d.dk) : pick_forward<float, false>(d.dk))
@@ -333,13 +361,18 @@ static int mix_forward(const rssm_mixer_dims* dims, bool delta, const void* q, c
 
 using namespace rssm;
 
+extern "C" size_t linear_attention_forward_workspace(const rssm_mixer_dims* dims) {
+  return mix_forward_bytes(dims, false);
+}
+
 extern "C" int linear_attention_forward(const rssm_mixer_dims* dims, const void* q, const void* k,
                                         const void* v, const float* log_decay, const int32_t* cu_seqlens,
                                         const float* initial_state, const uint8_t* has_initial,
                                         const int32_t* slot_idx, float* final_state, void* o,
-                                        int32_t* status, hipStream_t stream) {
+                                        void* workspace, size_t workspace_bytes, int32_t* status,
+                                        hipStream_t stream) {
   return mix_forward(dims, false, q, k, v, log_decay, nullptr, cu_seqlens, initial_state, has_initial,
-                     slot_idx, final_state, o, nullptr, 0, status, stream);
+                     slot_idx, final_state, o, workspace, workspace_bytes, status, stream);
 }
 
 extern "C" size_t gdn_scan_forward_workspace(const rssm_mixer_dims* dims) {

@@ -41,7 +41,7 @@ def bind(lib):
     global _lib
     P, Z = ctypes.c_void_p, ctypes.c_size_t
     for name, dims, n_ptr, ws in (
-            ("linear_attention_forward", MixerDims, 10, False),
+            ("linear_attention_forward", MixerDims, 11, True),
             ("linear_attention_backward", MixerDims, 16, True),
             ("linear_attention_decode", MixerDims, 8, False),
             ("gdn_scan_forward", MixerDims, 12, True), ("gdn_scan_backward", MixerDims, 18, True),
@@ -114,18 +114,17 @@ def _forward(delta, q, k, v, decay, beta, scale, cu_seqlens, initial_state, has_
     _slots(slot_idx, has_initial, status, n, dev)
     _pools(d, dev, ("initial_state", initial_state), ("final_state", final_state))
     lib, (handle, ctx) = _library(), _on(stream, dev)
+    size = getattr(lib, name + "_workspace")(ctypes.byref(d))
     shape = (T, d.v_heads, d.dv)
     _dense(o, "o", io, shape, dev)
     with ctx:
         if o is None:
             o = torch.empty(shape, dtype=io, device=dev)
-        args = [ctypes.byref(d), _p(q), _p(k), _p(v), _p(decay)]
-        rest = [_p(cu_seqlens), _p(initial_state), _p(has_initial), _p(slot_idx), _p(final_state), _p(o)]
-        if delta:
-            size = lib.gdn_scan_forward_workspace(ctypes.byref(d))
-            ws = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
-            args, rest = args + [_p(beta)], rest + [_p(ws), size]
-        _check(name, getattr(lib, name)(*args, *rest, _p(status), handle))
+        ws = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
+        _check(name, getattr(lib, name)(
+            ctypes.byref(d), _p(q), _p(k), _p(v), _p(decay), *([_p(beta)] if delta else []), _p(cu_seqlens),
+            _p(initial_state), _p(has_initial), _p(slot_idx), _p(final_state), _p(o), _p(ws), size, _p(status),
+            handle))
     return _result(name, o, q, k, v, decay, beta, initial_state)
 
 

@@ -198,6 +198,20 @@ def test_delta_rule(lens, shape, io):
     _both(lens, shape, True, io)
 
 
+@pytest.mark.parametrize("io", [F32, BF16])
+@pytest.mark.parametrize("shape", [dict(delta=False, **LINEAR[0]), dict(delta=False, **LINEAR[1]),
+                                   dict(delta=True, **DELTA[0]), dict(delta=True, **DELTA[1])],
+                         ids=lambda s: ("delta" if s["delta"] else "linear") + _ID(**s))
+@pytest.mark.parametrize("lens", [[1300], [513, 2, 0, 1025, 512]], ids=str)
+def test_segments(lens, shape, io):
+    """Sequences of more than 512 tokens are worked on in segments; the pool that they
+    start from may be the one that they store to."""
+    m = Mix(lens, io=io, seed=23, **shape)
+    pool = m.pool.clone()
+    m.check_forward(m.forward(initial_state=pool, final_state=pool), pool)
+    m.check_backward(m.backward())
+
+
 @pytest.mark.parametrize("delta", [False, True])
 @pytest.mark.parametrize("io", [F32, BF16])
 def test_bare(io, delta):

@@ -17,7 +17,7 @@ OK, EINVAL, EDTYPE, ESHAPE = 0, -1, -2, -4
 BIG = 1 << 45
 
 NAMES = dict(
-    linear_attention_forward="q k v g cu init has slot final o",
+    linear_attention_forward="q k v g cu init has slot final o ws",
     linear_attention_backward="do q k v g cu init has slot dfinal gq gk gv gg dinit ws",
     linear_attention_decode="state slot q k v g new o",
     gdn_scan_forward="q k v g beta cu init has slot final o ws",
@@ -72,8 +72,9 @@ def test_mixer_refusals(lib, fn):
         assert _mix(lib, fn, tokens=0, seqs=0) == OK
         assert _mix(lib, fn, seqs=1 << 24) == ESHAPE   # 2^32 threads and more
     if "ws" in names:
-        assert _mix(lib, fn, ws=64) == EINVAL
-        assert _mix(lib, fn, wsp=None) == EINVAL
+        long = dict(tokens=1 << 15)
+        assert _mix(lib, fn, ws=64, **long) == EINVAL
+        assert _mix(lib, fn, wsp=None, **long) == EINVAL
         assert _mix(lib, fn, wsp=V(0x1008)) == EINVAL
         assert getattr(lib, fn + "_workspace")(None) == 0
 
@@ -83,6 +84,9 @@ def test_mixer_workspace_sizes(lib):
     d = S.MixerDims(1 << 20, 4, 16, 32, 128, 128, 4, 1, 2, 0.0)
     for fn in ("gdn_scan_backward", "linear_attention_backward", "gdn_scan_forward"):
         assert getattr(lib, fn + "_workspace")(ctypes.byref(d)) > 1 << 32
+    # one segment needs none; a longer call the segments' states
+    assert lib.linear_attention_forward_workspace(ctypes.byref(S.MixerDims(64, 1, 4, 4, 64, 64, 1, 1, 2))) == 0
+    assert lib.linear_attention_forward_workspace(ctypes.byref(d)) > 1 << 22
     assert lib.gdn_scan_forward_workspace(ctypes.byref(S.MixerDims(8, 1, 4, 4, 48, 48, 1, 1, 2))) == 0
     assert lib.gdn_scan_forward_workspace(ctypes.byref(S.MixerDims(0, 3, 4, 4, 64, 64, 1, 1, 2))) == 0
 
