@@ -72,8 +72,10 @@ __global__ void __launch_bounds__(4 * K) mix_main_kernel(const MixBwdArgs b) {
   const long t0 = sg.tok;
   {
     TileLoad<T, K, TH> x, y;
-    x.fetch(static_cast<const E*>(a.k) + t0 * a.k_stride + (long)hk * K, a.k_stride, rows, tid);
-    y.fetch(static_cast<const E*>(a.q) + t0 * a.q_stride + (long)hk * K, a.q_stride, rows, tid);
+    x.start(static_cast<const E*>(a.k) + t0 * a.k_stride + (long)hk * K, a.k_stride, tid);
+    y.start(static_cast<const E*>(a.q) + t0 * a.q_stride + (long)hk * K, a.q_stride, tid);
+    x.fetch(rows, tid);
+    y.fetch(rows, tid);
     x.put(s.k, LK, tid);
     y.put(s.q, LK, tid);
   }
@@ -134,9 +136,10 @@ __global__ void __launch_bounds__(4 * K) mix_main_kernel(const MixBwdArgs b) {
     const int hv = hk * a.vpk + hx;
     const long at = (long)slot * a.v_heads + hv;
     if (wave == W - 1) {
-      const bool live = lane < rows;
-      s.g.set(gate_log2(a, t0 + lane, hv, live), DELTA && live ? a.beta[(t0 + lane) * a.v_heads + hv] : 0.f,
-              lane);
+      GateLoad ld;
+      ld.start(a, t0, hv, lane, DELTA);
+      ld.fetch(rows, lane);
+      s.g.set(ld.rg, ld.rb, lane);
     }
     f32x4 into[4], back[4], out[4], dp[JOBS][3], dx[JOBS][3];
 #pragma unroll

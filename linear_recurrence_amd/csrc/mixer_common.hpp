@@ -68,13 +68,36 @@ __device__ static inline f32x4 mma_split(const Split<T, TA>& x, const Split<T, T
   return c;
 }
 
-// A token's decay exponent in log2.  -1e4 already takes any state to zero, and keeps
-// sums of 64 and their differences finite; NaN passes.
-__device__ static inline double gate_log2(const MixArgs& a, long t, int hv, bool live) {
-  float g = 0.f;
-  if (live && a.decay) g = a.decay == RSSM_DECAY_HEAD ? a.g[hv] : a.g[t * a.v_heads + hv];
+// A decay exponent in log2.  -1e4 already takes any state to zero, and keeps sums of 64
+// and their differences finite; NaN passes.
+__device__ static inline double gate_log2(float g) {
   return (double)(g < -1e4f ? -1e4f : g) * 1.4426950408889634074;
 }
+// log g and beta of the chunk's tokens, one a lane, on their way from memory.
+struct GateLoad {
+  const float *g, *b;
+  long step_g;
+  float rg, rb;
+  int mode;
+  __device__ inline void start(const MixArgs& a, long t0, int hv, int lane, bool delta) {
+    mode = a.decay;
+    step_g = a.v_heads;
+    const long at = (t0 + lane) * a.v_heads + hv;
+    g = mode == RSSM_DECAY_TOKEN ? a.g + at : (mode == RSSM_DECAY_HEAD ? a.g + hv : nullptr);
+    b = delta ? a.beta + at : nullptr;
+  }
+  __device__ inline void step(int chunks) {
+    if (mode == RSSM_DECAY_TOKEN) g += chunks * kQ * step_g;
+    if (b) b += chunks * kQ * step_g;
+  }
+  __device__ inline void fetch(int rows, int lane) {
+    rg = rb = 0.f;
+    if (lane < rows) {
+      if (mode) rg = *g;
+      if (b) rb = *b;
+    }
+  }
+};
 
 // Inclusive sum over the wave's lanes in double, by lane shifts within the vector unit:
 // it stands on every chunk's path, and through LDS it took six round trips.
@@ -108,8 +131,8 @@ struct ChunkGates {
   __attribute__((aligned(16))) float et[kQ];         // e^{G_Q - G_t}
   __attribute__((aligned(16))) float beta[kQ];
   float all;                                         // e^{G_Q}
-  __device__ inline void set(double log2g, float b, int lane) {
-    const double cum = lane_sums(log2g), last = last_lane(cum);
+  __device__ inline void set(float log_g, float b, int lane) {
+    const double cum = lane_sums(gate_log2(log_g)), last = last_lane(cum);
     const float hi = (float)cum;
     G[lane] = make_float2(hi, (float)(cum - (double)hi));
     eg[lane] = exp2_f32(hi);
@@ -119,27 +142,37 @@ struct ChunkGates {
   }
 };
 
-// Tiles of a token tile pair on their way from memory: `ROWS` elements wide, 64 tokens.
+// A tile of 64 tokens' rows on its way from memory to LDS, chunk after chunk: a thread
+// keeps one address, from which its pieces are whole rows apart.
 template <typename T, int COLS, int THREADS>
 struct TileLoad {
   typedef typename Mat<T>::E E;
-  static constexpr int V = 16 / sizeof(E), PER = COLS / V, N = kQ * PER / THREADS;
-  static_assert(kQ * PER % THREADS == 0, "whole rounds");
+  static constexpr int V = 16 / sizeof(E), PER = COLS / V, N = kQ * PER / THREADS, R = THREADS / PER;
+  static_assert(kQ * PER % THREADS == 0 && THREADS % PER == 0, "whole rounds");
+  const E* p;
+  long stride;
   u32x4 r[N];
-  __device__ inline void fetch(const E* src, long stride, int rows, int tid) {
+  __device__ inline void start(const E* src, long s, int tid) {
+    stride = s;
+    p = src + (tid / PER) * s + (tid % PER) * V;
+  }
+  __device__ inline void step(int chunks) { p += chunks * kQ * stride; }
+  __device__ inline void fetch(int rows, int tid) {
+    if (rows == kQ) {  // the same for the whole workgroup: no conditions in between
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int e = i * THREADS + tid, row = e / PER;
-      r[i] = u32x4{0, 0, 0, 0};
-      if (row < rows) r[i] = *reinterpret_cast<const u32x4*>(src + row * stride + (e % PER) * V);
+      for (int i = 0; i < N; ++i) r[i] = *reinterpret_cast<const u32x4*>(p + i * (R * stride));
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        r[i] = u32x4{0, 0, 0, 0};
+        if (tid / PER + i * R < rows) r[i] = *reinterpret_cast<const u32x4*>(p + i * (R * stride));
+      }
     }
   }
   __device__ inline void put(E* tile, int ld, int tid) const {
+    E* const to = tile + (tid / PER) * ld + (tid % PER) * V;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int e = i * THREADS + tid;
-      *reinterpret_cast<u32x4*>(tile + (e / PER) * ld + (e % PER) * V) = r[i];
-    }
+    for (int i = 0; i < N; ++i) *reinterpret_cast<u32x4*>(to + i * R * ld) = r[i];
   }
 };
 
@@ -218,11 +251,13 @@ static __global__ void __launch_bounds__(256) mix_inverse_kernel(const MixArgs a
   const int rows = sg.len, hk = hv / a.vpk;
   const long t0 = sg.tok;
   {
-    const bool live = lane < rows;
-    const double cum = lane_sums(gate_log2(a, t0 + lane, hv, live));
+    GateLoad ld;
+    ld.start(a, t0, hv, lane, true);
+    ld.fetch(rows, lane);
+    const double cum = lane_sums(gate_log2(ld.rg));
     const float hi = (float)cum;
     sG[wave][lane] = make_float2(hi, (float)(cum - (double)hi));
-    sBeta[wave][lane] = live ? a.beta[(t0 + lane) * a.v_heads + hv] : 0.f;
+    sBeta[wave][lane] = ld.rb;
   }
   // k_m.k_i: rows m of block bm, columns i of block bi <= bm is left out
   f32x4 acc[4][4];

@@ -41,7 +41,7 @@ __global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 1 : 2)
   __shared__ __attribute__((aligned(16))) u32x4 sT[DELTA ? TF : 1];
   __shared__ __attribute__((aligned(16))) u32x4 sP[6 * TO * 64 * sizeof(Frag) / 16];
   __shared__ ChunkGates sg;
-  int tid = threadIdx.x, lane = tid & 63;
+  const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const MixUnit un = mix_unit(a, blockIdx.x, a.vpk * a.slices);
   if (blockIdx.x == 0) check_table(a.cu, a.seqs, a.tokens, a.status);
@@ -68,41 +68,41 @@ __global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 1 : 2)
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt) S[kt] = *reinterpret_cast<const f32x4*>(p + 16 * kt);
   }
-  const E* const ksrc = static_cast<const E*>(a.k) + (long)un.hk * K;
-  const E* const qsrc = static_cast<const E*>(a.q) + (long)un.hk * K;
-  const E* const vsrc = static_cast<const E*>(a.v) + (long)hv * a.dv + v0;
   const long cbase = seg_base(a.cu, sp.seq, kQ, a.tokens) + (long)sp.k * (a.seg / kQ);
   const int chunks = (sp.len + kQ - 1) / kQ;
+  const int i16 = lane & 15, g = lane >> 4;
   TileLoad<T, K, 256> rk, rq;
   TileLoad<T, 64, 256> rv;
+  GateLoad rg;
   u32x4 rt[QT];
-  double rg = 0.0;
-  float rb = 0.f;
+  const u32x4* tsrc = static_cast<const u32x4*>(a.tinv) + (cbase * a.v_heads + hv) * TF + tid;
+  rk.start(static_cast<const E*>(a.k) + sp.tok * a.k_stride + (long)un.hk * K, a.k_stride, tid);
+  rq.start(static_cast<const E*>(a.q) + sp.tok * a.q_stride + (long)un.hk * K, a.q_stride, tid);
+  rv.start(static_cast<const E*>(a.v) + sp.tok * a.v_stride + (long)hv * a.dv + v0, a.v_stride, tid);
+  rg.start(a, sp.tok, hv, lane, DELTA);
+  E* out = static_cast<E*>(a.o) + ((long)(sp.tok + i16) * a.v_heads + hv) * a.dv + v0 + 16 * wave + 4 * g;
+  const long orow = (long)a.v_heads * a.dv;
   const auto fetch = [&](int c) {
     const int rows = sp.len - c * kQ < kQ ? sp.len - c * kQ : kQ;
-    const long t0 = sp.tok + (long)c * kQ;
-    rk.fetch(ksrc + t0 * a.k_stride, a.k_stride, rows, tid);
-    rq.fetch(qsrc + t0 * a.q_stride, a.q_stride, rows, tid);
-    rv.fetch(vsrc + t0 * a.v_stride, a.v_stride, rows, tid);
+    rk.fetch(rows, tid);
+    rq.fetch(rows, tid);
+    rv.fetch(rows, tid);
+    rg.fetch(rows, lane);
     if (DELTA) {
-      const u32x4* src = static_cast<const u32x4*>(a.tinv) + ((cbase + c) * a.v_heads + hv) * TF;
 #pragma unroll
       for (int i = 0; i < QT; ++i)
-        if (TF % 256 == 0 || i * 256 + tid < TF) rt[i] = src[i * 256 + tid];
+        if (TF % 256 == 0 || i * 256 + tid < TF) rt[i] = tsrc[i * 256];
     }
-    const bool live = lane < rows;
-    rg = gate_log2(a, t0 + lane, hv, live);
-    if (DELTA) rb = live ? a.beta[(t0 + lane) * a.v_heads + hv] : 0.f;
+    rk.step(1);
+    rq.step(1);
+    rv.step(1);
+    rg.step(1);
+    tsrc += (long)a.v_heads * TF;
   };
   if (chunks) fetch(0);
 #pragma unroll 1
   for (int c = 0; c < chunks; ++c) {
-    tid = threadIdx.x;
-    forget(tid);
-    lane = tid & 63;
-    const int i16 = lane & 15, g = lane >> 4;
     const int rows = sp.len - c * kQ < kQ ? sp.len - c * kQ : kQ;
-    const long t0 = sp.tok + (long)c * kQ;
     __syncthreads();  // the previous chunk's tiles are no longer read
     rk.put(sK, LK, tid);
     rq.put(sQ, LK, tid);
@@ -112,53 +112,14 @@ __global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 1 : 2)
       for (int i = 0; i < QT; ++i)
         if (TF % 256 == 0 || i * 256 + tid < TF) sT[i * 256 + tid] = rt[i];
     }
-    if (wave == 3) sg.set(rg, rb, lane);
+    if (wave == 3) sg.set(rg.rg, rg.rb, lane);
     if (c + 1 < chunks) fetch(c + 1);
     __syncthreads();
-    // scale e^{G_i-G_j} q_i.k_j of the lower triangle: fragments 0 (it 0) and 4 (3, 0);
-    // 5 (3, 1); 1 (1, 0) and 3 (2, 1); 2 (2, 0)
-    {
-      const auto make = [&](int it, int kb) {
-        f32x4 acc[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) acc[h] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int b = 0; b < KB; ++b) {
-          const Frag qf = M::rows_c(sQ + (16 * it + i16) * LK + 32 * b + 8 * g);
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            if (2 * kb + h <= it)
-              acc[h] = M::mma(M::rows_c(sK + (16 * (2 * kb + h) + i16) * LK + 32 * b + 8 * g), qf, acc[h]);
-        }
-        const float2 gi = sg.G[16 * it + i16];
-        float f[8];
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int j = 16 * (2 * kb + h) + 4 * g + r;
-            const float w = a.scale * exp2_f32(gap2(gi, sg.G[j])) * acc[h][r];
-            f[4 * h + r] = j <= 16 * it + i16 ? w : 0.f;
-          }
-        Split<T, TO> s;
-        s.set(f);
-        put_split<T, TO>(sP, low_frag(it, kb), s, lane);
-      };
-      if (wave == 0) {
-        make(3, 0);
-        make(0, 0);
-      } else if (wave == 1) {
-        make(3, 1);
-      } else if (wave == 2) {
-        make(2, 0);
-      } else {
-        make(1, 0);
-        make(2, 1);
-      }
-    }
     f32x4 R[4], O[4];  // K S, rows t; (Q S)^T, columns t
+    f32x4 P[3];        // this wave's tiles of k_j.q_i, rows j
 #pragma unroll
     for (int it = 0; it < 4; ++it) R[it] = O[it] = f32x4{0.f, 0.f, 0.f, 0.f};
+    P[0] = P[1] = P[2] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int b = 0; b < KB; ++b) {
       float f[8];
@@ -173,19 +134,59 @@ __global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 1 : 2)
       Frag kf[4], qf[4];
 #pragma unroll
       for (int it = 0; it < 4; ++it) {
-        if (DELTA) kf[it] = M::rows_d(sK + (16 * it + i16) * LK + 32 * b + 4 * g);
+        kf[it] = M::rows_d(sK + (16 * it + i16) * LK + 32 * b + 4 * g);
         qf[it] = M::rows_d(sQ + (16 * it + i16) * LK + 32 * b + 4 * g);
       }
-      if (DELTA) {
+      if constexpr (DELTA) {
 #pragma unroll
         for (int k = TS - 1; k >= 0; --k)
 #pragma unroll
-          for (int it = 0; it < 4; ++it) R[it] = M::mma(kf[it], sf.t[k < TS ? k : 0], R[it]);
+          for (int it = 0; it < 4; ++it) R[it] = M::mma(kf[it], sf.t[k], R[it]);
       }
 #pragma unroll
       for (int k = TO - 1; k >= 0; --k)
 #pragma unroll
         for (int it = 0; it < 4; ++it) O[it] = M::mma(so.t[k], qf[it], O[it]);
+      if (wave == 0) {
+        P[0] = M::mma(kf[0], qf[3], P[0]);
+        P[1] = M::mma(kf[1], qf[3], P[1]);
+        P[2] = M::mma(kf[0], qf[0], P[2]);
+      } else if (wave == 1) {
+        P[0] = M::mma(kf[2], qf[3], P[0]);
+        P[1] = M::mma(kf[3], qf[3], P[1]);
+      } else if (wave == 2) {
+        P[0] = M::mma(kf[0], qf[2], P[0]);
+        P[1] = M::mma(kf[1], qf[2], P[1]);
+      } else {
+        P[0] = M::mma(kf[0], qf[1], P[0]);
+        P[1] = M::mma(kf[1], qf[1], P[1]);
+        P[2] = M::mma(kf[2], qf[2], P[2]);
+      }
+    }
+    {
+      // scale e^{G_i-G_j} q_i.k_j of the lower triangle as fragments: (3, 0) and (0, 0);
+      // (3, 1); (2, 0); (1, 0) and (2, 1)
+      const int it = wave < 2 ? 3 : (wave == 2 ? 2 : 1), kb = wave == 1, ie = wave ? 2 : 0, ke = wave != 0;
+      const auto weigh = [&](int i, int j, const f32x4& p, float* f) {  // of one tile
+        const float2 gi = sg.G[16 * i + i16];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float w = a.scale * exp2_f32(gap2(gi, sg.G[16 * j + 4 * g + r])) * p[r];
+          f[r] = j < i || 4 * g + r <= i16 ? w : 0.f;
+        }
+      };
+      float f[8];
+      Split<T, TO> s;
+      weigh(it, 2 * kb, P[0], f);
+      weigh(it, 2 * kb + 1, P[1], f + 4);
+      s.set(f);
+      put_split<T, TO>(sP, low_frag(it, kb), s, lane);
+      if (wave == 0 || wave == 3) {
+        weigh(ie, 2 * ke, P[2], f);
+        f[4] = f[5] = f[6] = f[7] = 0.f;
+        s.set(f);
+        put_split<T, TO>(sP, low_frag(ie, ke), s, lane);
+      }
     }
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
@@ -263,12 +264,10 @@ __global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 1 : 2)
     }
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
-      const int t = 16 * it + i16;
-      if (t >= rows) continue;
-      const long at = ((t0 + t) * a.v_heads + hv) * a.dv + v0 + 16 * wave + 4 * g;
       const float f[4] = {O[it][0], O[it][1], O[it][2], O[it][3]};
-      *reinterpret_cast<typename M::Four*>(static_cast<E*>(a.o) + at) = M::pack4(f);
+      if (16 * it + i16 < rows) *reinterpret_cast<typename M::Four*>(out + 16 * it * orow) = M::pack4(f);
     }
+    out += kQ * orow;
   }
   if (sp.last && a.final_state && pool >= 0) {
     float* p = a.final_state + place(pool);

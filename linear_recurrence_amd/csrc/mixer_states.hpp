@@ -60,7 +60,7 @@ static __global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 
   constexpr int QT = DELTA ? (TF + 255) / 256 : 1;
   __shared__ L s;
   const MixArgs& a = b.m;
-  int tid = threadIdx.x, lane = tid & 63;
+  const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const bool back = BOTH && (int)blockIdx.x >= b.dir_blocks && (int)blockIdx.x < 2 * b.dir_blocks;
   const bool trans = !STORE && DELTA && (int)blockIdx.x >= (BOTH ? 2 : 1) * b.dir_blocks;
@@ -101,32 +101,37 @@ static __global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 
         S[kt][r] = 16 * kt + 4 * (lane >> 4) + r == v0 + 16 * wave + (lane & 15) ? 1.f : 0.f;
   }
   float total = 1.f;
-  const E* const ksrc = static_cast<const E*>(a.k) + (long)un.hk * K;
-  const E* const qsrc = static_cast<const E*>(a.q) + (long)un.hk * K;
-  const E* const vsrc = static_cast<const E*>(back ? b.dout : a.v) + (long)hv * a.dv + v0;
   const long vstride = back ? b.do_stride : a.v_stride;
   const long cbase = seg_base(a.cu, sg.seq, kQ, a.tokens) + (long)sg.k * (a.seg / kQ);
-  const int chunks = (sg.len + kQ - 1) / kQ;
+  const int chunks = (sg.len + kQ - 1) / kQ, way = back ? -1 : 1;
+  const int i16 = lane & 15, g = lane >> 4;
+  const long first = chunks && back ? chunks - 1 : 0, tok = sg.tok + first * kQ;
   TileLoad<T, K, 256> rk, rq;
   TileLoad<T, 64, 256> rv;
+  GateLoad rg;
   u32x4 rt[QT];
-  double rg = 0.0;
-  float rb = 0.f;
+  const u32x4* tsrc = static_cast<const u32x4*>(a.tinv) +
+      (((cbase + first) * a.v_heads + hv) * (BOTH ? 2 : 1) + back) * TF + tid;
+  rk.start(static_cast<const E*>(a.k) + tok * a.k_stride + (long)un.hk * K, a.k_stride, tid);
+  if (BOTH) rq.start(static_cast<const E*>(a.q) + tok * a.q_stride + (long)un.hk * K, a.q_stride, tid);
+  rv.start(static_cast<const E*>(back ? b.dout : a.v) + tok * vstride + (long)hv * a.dv + v0, vstride, tid);
+  rg.start(a, tok, hv, lane, DELTA);
   const auto fetch = [&](int c) {
     const int rows = sg.len - c * kQ < kQ ? sg.len - c * kQ : kQ;
-    const long t0 = sg.tok + (long)c * kQ;
-    rk.fetch(ksrc + t0 * a.k_stride, a.k_stride, rows, tid);
-    if (back) rq.fetch(qsrc + t0 * a.q_stride, a.q_stride, rows, tid);
-    rv.fetch(vsrc + t0 * vstride, vstride, trans ? 0 : rows, tid);
+    rk.fetch(rows, tid);
+    if (back) rq.fetch(rows, tid);
+    rv.fetch(trans ? 0 : rows, tid);
+    rg.fetch(rows, lane);
     if (DELTA) {
-      const u32x4* src = static_cast<const u32x4*>(a.tinv) + (((cbase + c) * a.v_heads + hv) * (BOTH ? 2 : 1) + back) * TF;
 #pragma unroll
       for (int i = 0; i < QT; ++i)
-        if (TF % 256 == 0 || i * 256 + tid < TF) rt[i] = src[i * 256 + tid];
+        if (TF % 256 == 0 || i * 256 + tid < TF) rt[i] = tsrc[i * 256];
     }
-    const bool live = lane < rows;
-    rg = gate_log2(a, t0 + lane, hv, live);
-    if (DELTA) rb = live ? a.beta[(t0 + lane) * a.v_heads + hv] : 0.f;
+    rk.step(way);
+    if (BOTH) rq.step(way);
+    rv.step(way);
+    rg.step(way);
+    tsrc += way * (long)a.v_heads * ((BOTH ? 2 : 1) * TF);
   };
   float* const keep = back ? b.grad : b.state;
   float* const rowmat = back ? b.dX : b.D;
@@ -134,10 +139,6 @@ static __global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 
 #pragma unroll 1
   for (int n = 0; n < chunks; ++n) {
     const int c = back ? chunks - 1 - n : n;
-    tid = threadIdx.x;
-    forget(tid);
-    lane = tid & 63;
-    const int i16 = lane & 15, g = lane >> 4;
     const int rows = sg.len - c * kQ < kQ ? sg.len - c * kQ : kQ;
     const long t0 = sg.tok + (long)c * kQ;
     if (STORE) {
@@ -154,7 +155,7 @@ static __global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 
       for (int i = 0; i < QT; ++i)
         if (TF % 256 == 0 || i * 256 + tid < TF) s.t[i * 256 + tid] = rt[i];
     }
-    if (wave == 3) s.g.set(rg, rb, lane);
+    if (wave == 3) s.g.set(rg.rg, rg.rb, lane);
     if (n + 1 < chunks) fetch(back ? c - 1 : c + 1);
     __syncthreads();
     if (back) {
@@ -362,7 +363,6 @@ static __global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 
     if constexpr (DELTA) {
     // fragments (rows kt, columns jb) of the matrix, then (rows jt, columns kb) of its transpose
     constexpr int NF = KT * KB, LM = K + 4;
-    const int i16 = lane & 15, g = lane >> 4;
     char* const out = static_cast<char*>(a.trans) +
         ((long)un.slot * a.v_heads + hv) * ((BOTH ? 2 : 1) * NF * TS * 64 * sizeof(Frag));
     if (BOTH) {
