@@ -32,14 +32,14 @@ template <typename T, int K, bool DELTA>
 struct MainLds {
   typedef typename Mat<T>::E E;
   static constexpr int kFrag = 64 * sizeof(typename Mat<T>::Frag), TS = Mat<T>::kTerms;
-  static constexpr int TO = TS > 2 ? 2 : TS, TD = DELTA ? TS : 1, LK = K + Mat<T>::kPad, W = K / 16;
+  static constexpr int TO = TS > 2 ? 2 : TS, TD = DELTA ? TS : 1, W = K / 16;
   // fragments of 32 columns of dO, D (or V) and dX for the four blocks of 16 tokens
   static constexpr int kStage = 4 * (1 + TD + (DELTA ? TS : 0)) * kFrag;
   static constexpr int oD = 4 * kFrag, oX = oD + 4 * TD * kFrag;
   static constexpr int kTri = 12 * TO * kFrag;  // N, or L: lower and upper triangle
   static constexpr int kArea = 2 * kStage > (DELTA ? 2 : 1) * kTri ? 2 * kStage : (DELTA ? 2 : 1) * kTri;
-  __attribute__((aligned(16))) E k[kQ * LK];
-  __attribute__((aligned(16))) E q[kQ * LK];
+  __attribute__((aligned(16))) E k[Tile<T, K>::SIZE];
+  __attribute__((aligned(16))) E q[Tile<T, K>::SIZE];
   __attribute__((aligned(16))) char area[kArea];
   ChunkGates g;
   float wrow[10][16], wcol[10][16], brow[10][16];  // by tile i (i + 1) / 2 + j
@@ -56,7 +56,8 @@ __global__ void __launch_bounds__(4 * K) mix_main_kernel(const MixBwdArgs b) {
   typedef typename M::E E;
   typedef typename M::Frag Frag;
   typedef MainLds<T, K, DELTA> L;
-  constexpr int TS = L::TS, TO = L::TO, TD = L::TD, LK = L::LK, KB = K / 32, W = L::W, TH = 64 * W;
+  typedef Tile<T, K> TK;
+  constexpr int TS = L::TS, TO = L::TO, TD = L::TD, KB = K / 32, W = L::W, TH = 64 * W;
   constexpr int JOBS = 8 / W;  // sets of tiles a wave
   __shared__ L s;
   const MixArgs& a = b.m;
@@ -76,8 +77,8 @@ __global__ void __launch_bounds__(4 * K) mix_main_kernel(const MixBwdArgs b) {
     y.start(static_cast<const E*>(a.q) + t0 * a.q_stride + (long)hk * K, a.q_stride, tid);
     x.fetch(rows, tid);
     y.fetch(rows, tid);
-    x.put(s.k, LK, tid);
-    y.put(s.q, LK, tid);
+    x.put(s.k, rows, tid);
+    y.put(s.q, rows, tid);
   }
   __syncthreads();
   // This wave's tiles of the 64x64 products: two of one fragment and, in half of the
@@ -113,10 +114,9 @@ __global__ void __launch_bounds__(4 * K) mix_main_kernel(const MixBwdArgs b) {
       if (e == 2 && !extra[u]) continue;
 #pragma unroll
       for (int x = 0; x < KB; ++x) {
-        const int c = 32 * x + 8 * g;
-        const Frag ki = M::rows_c(s.k + (16 * bi[u][e] + i16) * LK + c);
-        const Frag kj = M::rows_c(s.k + (16 * bj[u][e] + i16) * LK + c);
-        const Frag qi = M::rows_c(s.q + (16 * bi[u][e] + i16) * LK + c);
+        const Frag ki = TK::rows_c(s.k, bi[u][e], 32 * x, lane);
+        const Frag kj = TK::rows_c(s.k, bj[u][e], 32 * x, lane);
+        const Frag qi = TK::rows_c(s.q, bi[u][e], 32 * x, lane);
         if (upper[u]) {
           qk[u][e] = M::mma(qi, kj, qk[u][e]);
           if (DELTA) kk[u][e] = M::mma(ki, kj, kk[u][e]);
@@ -130,6 +130,7 @@ __global__ void __launch_bounds__(4 * K) mix_main_kernel(const MixBwdArgs b) {
   f32x4 dq[4], dk[4];  // rows t = 16 t + 4g + r, column 16 wave + i16
 #pragma unroll
   for (int t = 0; t < 4; ++t) dq[t] = dk[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const Minus minus;
   const int kcol = 16 * wave + i16, blocks = a.dv / 32;
 #pragma unroll 1
   for (int hx = 0; hx < a.vpk; ++hx) {
@@ -137,9 +138,9 @@ __global__ void __launch_bounds__(4 * K) mix_main_kernel(const MixBwdArgs b) {
     const long at = (long)slot * a.v_heads + hv;
     if (wave == W - 1) {
       GateLoad ld;
-      ld.start(a, t0, hv, lane, DELTA);
+      ld.start(a, t0, hv, DELTA);
       ld.fetch(rows, lane);
-      s.g.set(ld.rg, ld.rb, lane);
+      s.g.set(ld.log_g(rows, lane), ld.beta(rows, lane), lane);
     }
     f32x4 into[4], back[4], out[4], dp[JOBS][3], dx[JOBS][3];
 #pragma unroll
@@ -173,21 +174,18 @@ __global__ void __launch_bounds__(4 * K) mix_main_kernel(const MixBwdArgs b) {
           if (DELTA) {
             float f[8];
             Vec8<float>::load(b.D, (at * kQ + t) * a.dv + vc, f);
-            Split<T, TS> d;
-            d.set(f);
+            const auto d = split<T, TS>(f, minus);
             put_split<T, TS>(area + L::oD, tb, d, lane);
           } else {
             float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
             if (t < rows) Vec8<T>::load(a.v, (t0 + t) * a.v_stride + (long)hv * a.dv + vc, f);
-            Split<T, 1> d;
-            d.set(f);
+            const auto d = split<T, 1>(f, minus);
             put_split<T, 1>(area + L::oD, tb, d, lane);
           }
         } else {
           float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, f[8], v[8];
           if (t < rows) Vec8<T>::load(b.dout, (t0 + t) * b.do_stride + (long)hv * a.dv + vc, o);
-          Split<T, 1> d;
-          d.set(o);
+          const auto d = split<T, 1>(o, minus);
           put_split<T, 1>(area, tb, d, lane);
           if (DELTA) {
             Vec8<float>::load(b.dX, (at * kQ + t) * a.dv + vc, f);
@@ -201,26 +199,19 @@ __global__ void __launch_bounds__(4 * K) mix_main_kernel(const MixBwdArgs b) {
               }
               Vec8<T>::store(b.dv, ((t0 + t) * a.v_heads + hv) * a.dv + vc, w);
             }
-            Split<T, TS> x;
-            x.set(f);
+            const auto x = split<T, TS>(f, minus);
             put_split<T, TS>(area + L::oX, tb, x, lane);
           }
         }
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) dot = fmaf(fs[e], fg[e], dot);
-      Split<T, TS> ss, sd;
-      ss.set(fs);
-      sd.set(fg);
+      const auto ss = split<T, TS>(fs, minus), sd = split<T, TS>(fg, minus);
       __syncthreads();
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const Frag o = frag_at<T>(area, t, lane);
-        into[t] = ss.b_times(o, into[t]);
-        const auto d = split_at<T, TD>(area + L::oD, t, lane);
-        out[t] = mma_split<T, TD, TS>(d, sd, out[t]);
-        if (DELTA) back[t] = mma_split<T, TS, TS>(split_at<T, TS>(area + L::oX, t, lane), ss, back[t]);
-      }
+      mma_many<T, 1, TS, 4>([&](int t, int) { return frag_at<T>(area, t, lane); }, ss, into);
+      mma_many<T, TD, TS, 4>([&](int t, int k) { return frag_at<T>(area + L::oD, t * TD + k, lane); }, sd, out);
+      if (DELTA)
+        mma_many<T, TS, TS, 4>([&](int t, int k) { return frag_at<T>(area + L::oX, t * TS + k, lane); }, ss, back);
 #pragma unroll
       for (int u = 0; u < JOBS; ++u)
 #pragma unroll
@@ -302,12 +293,10 @@ __global__ void __launch_bounds__(4 * K) mix_main_kernel(const MixBwdArgs b) {
       for (int e = 0; e < 2; ++e) {
         if (e == 1 && !extra[u]) continue;
         const int n = (upper[u] ? 6 : 0) + frag[u][e];
-        Split<T, TO> x;
-        x.set(fn[e]);
+        const auto x = split<T, TO>(fn[e], minus);
         put_split<T, TO>(s.area, n, x, lane);
         if (DELTA) {
-          x.set(fl[e]);
-          put_split<T, TO>(s.area + L::kTri, n, x, lane);
+          put_split<T, TO>(s.area + L::kTri, n, split<T, TO>(fl[e], minus), lane);
         }
       }
     }
@@ -317,8 +306,8 @@ __global__ void __launch_bounds__(4 * K) mix_main_kernel(const MixBwdArgs b) {
       float gv[16], bk[16], tk[16];
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb) {
-        kf[kb] = M::cols(cols_at<T, false>(s.k, LK, 32 * kb, 16 * wave, lane), LK);
-        qf[kb] = M::cols(cols_at<T, false>(s.q, LK, 32 * kb, 16 * wave, lane), LK);
+        kf[kb] = TK::cols(s.k, 32 * kb, 16 * wave, lane);
+        qf[kb] = TK::cols(s.q, 32 * kb, 16 * wave, lane);
         float fk[8], fq[8];
         M::unpack(kf[kb], fk);
         M::unpack(qf[kb], fq);
@@ -413,7 +402,7 @@ __global__ void __launch_bounds__(4 * K) mix_main_kernel(const MixBwdArgs b) {
   for (int t = 0; t < 4; ++t)
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const int p = (16 * t + 4 * g + r) * LK + kcol;
+      const int p = TK::at(16 * t + 4 * g + r, kcol);
       Elt<T>::store1(s.q, p, dq[t][r]);
       Elt<T>::store1(s.k, p, dk[t][r]);
     }
@@ -422,8 +411,8 @@ __global__ void __launch_bounds__(4 * K) mix_main_kernel(const MixBwdArgs b) {
   for (int e = tid; e < rows * PER; e += TH) {
     const int t = e / PER, c = (e % PER) * V;
     const long o = ((t0 + t) * a.k_heads + hk) * K + c;
-    *reinterpret_cast<u32x4*>(static_cast<E*>(b.dq) + o) = *reinterpret_cast<const u32x4*>(s.q + t * LK + c);
-    *reinterpret_cast<u32x4*>(static_cast<E*>(b.dk) + o) = *reinterpret_cast<const u32x4*>(s.k + t * LK + c);
+    *reinterpret_cast<u32x4*>(static_cast<E*>(b.dq) + o) = *reinterpret_cast<const u32x4*>(s.q + TK::at(t, c));
+    *reinterpret_cast<u32x4*>(static_cast<E*>(b.dk) + o) = *reinterpret_cast<const u32x4*>(s.k + TK::at(t, c));
   }
 }
 
@@ -460,14 +449,24 @@ static BwdLayout bwd_layout(const rssm_mixer_dims& d, bool delta) {
   return l;
 }
 
-enum { kBwdStates, kBwdMain };
-template <typename T, bool DELTA>
-static const void* pick_bwd(int which, int dk) {
-  if (which == kBwdStates)
-    return dk == 64 ? reinterpret_cast<const void*>(&mix_states_kernel<T, 64, DELTA, true, true>)
-                    : reinterpret_cast<const void*>(&mix_states_kernel<T, 128, DELTA, true, true>);
-  return dk == 64 ? reinterpret_cast<const void*>(&mix_main_kernel<T, 64, DELTA>)
-                  : reinterpret_cast<const void*>(&mix_main_kernel<T, 128, DELTA>);
+template <typename T>
+static const void* pick_states(const rssm_mixer_dims& d, bool delta) {
+  if (delta)
+    return d.dk == 64 ? reinterpret_cast<const void*>(&mix_states_kernel<T, 64, 64, true, true, true>)
+                      : reinterpret_cast<const void*>(&mix_states_kernel<T, 128, 128, true, true, true>);
+  if (d.dk == 64)
+    return d.dv == 64 ? reinterpret_cast<const void*>(&mix_states_kernel<T, 64, 64, false, true, true>)
+                      : reinterpret_cast<const void*>(&mix_states_kernel<T, 64, 128, false, true, true>);
+  return d.dv == 64 ? reinterpret_cast<const void*>(&mix_states_kernel<T, 128, 64, false, true, true>)
+                    : reinterpret_cast<const void*>(&mix_states_kernel<T, 128, 128, false, true, true>);
+}
+template <typename T>
+static const void* pick_main(const rssm_mixer_dims& d, bool delta) {
+  if (delta)
+    return d.dk == 64 ? reinterpret_cast<const void*>(&mix_main_kernel<T, 64, true>)
+                      : reinterpret_cast<const void*>(&mix_main_kernel<T, 128, true>);
+  return d.dk == 64 ? reinterpret_cast<const void*>(&mix_main_kernel<T, 64, false>)
+                    : reinterpret_cast<const void*>(&mix_main_kernel<T, 128, false>);
 }
 
 static size_t mix_backward_bytes(const rssm_mixer_dims* dims, bool delta) {
@@ -504,15 +503,11 @@ static int mix_backward(const rssm_mixer_dims* dims, bool delta, MixBwdArgs b, v
   const bool f32 = d.io_dtype == RSSM_F32;
   b.cslots = scan_slots(d.tokens, d.seqs, kQ);
   seg_fill(a, d, l.seg, workspace);
-  const long dir = mix_grid(a.slots, d.k_heads, (long)a.vpk * a.slices), mgrid = b.cslots * d.k_heads;
+  const long dir = mix_grid(a.slots, d.k_heads, a.vpk), mgrid = b.cslots * d.k_heads;
   if (!segments_fit(a, d.dk) || !grid_fits(mgrid, 4 * d.dk) ||
       !grid_fits(b.cslots * ((d.v_heads + 3) / 4), 256))
     return RSSM_ESHAPE;
   b.dir_blocks = (int)dir;
-  const auto pick = [&](int which) {
-    return f32 ? (delta ? pick_bwd<float, true>(which, d.dk) : pick_bwd<float, false>(which, d.dk))
-               : (delta ? pick_bwd<bf16, true>(which, d.dk) : pick_bwd<bf16, false>(which, d.dk));
-  };
   if (d.tokens == 0) {  // no chunks, and no gradient of a decay but zero
     b.cslots = 0;
   } else if (delta) {
@@ -521,14 +516,15 @@ static int mix_backward(const rssm_mixer_dims* dims, bool delta, MixBwdArgs b, v
     if (rc) return rc;
   }
   if (d.tokens > a.seg) {
-    rc = f32 ? (delta ? launch_segments<float, true, true>(b, d.dk, stream)
-                      : launch_segments<float, false, true>(b, d.dk, stream))
-             : (delta ? launch_segments<bf16, true, true>(b, d.dk, stream)
-                      : launch_segments<bf16, false, true>(b, d.dk, stream));
+    rc = f32 ? launch_segments<float, true>(b, d.dk, delta, stream)
+             : launch_segments<bf16, true>(b, d.dk, delta, stream);
     if (rc) return rc;
   }
-  rc = launch_kernel(pick(kBwdStates), (unsigned)(2 * dir), 256, 0, stream, b);
-  if (!rc && d.tokens > 0) rc = launch_kernel(pick(kBwdMain), (unsigned)mgrid, 4 * d.dk, 0, stream, b);
+  rc = launch_kernel(f32 ? pick_states<float>(d, delta) : pick_states<bf16>(d, delta), (unsigned)(2 * dir),
+                     4 * d.dv, 0, stream, b);
+  if (!rc && d.tokens > 0)
+    rc = launch_kernel(f32 ? pick_main<float>(d, delta) : pick_main<bf16>(d, delta), (unsigned)mgrid, 4 * d.dk, 0,
+                       stream, b);
   if (!rc && d.decay == RSSM_DECAY_HEAD && b.dg)
     rc = launch_kernel(reinterpret_cast<const void*>(&mix_decay_sum_kernel), d.v_heads, 256, 0, stream, b);
   return rc;

@@ -41,7 +41,7 @@ struct MixArgs {
   float* seg_decay;    // [segment slots][v_heads]
   void* trans;         // [segment slots][v_heads][K K / 512 (twice) fragments][terms][64]
   long q_stride, k_stride, v_stride;
-  int32_t tokens, seqs, k_heads, v_heads, vpk, dv, num_slots, decay, slices;
+  int32_t tokens, seqs, k_heads, v_heads, vpk, dv, num_slots, decay;
   int32_t seg, slots;  // tokens of a segment, segment slots
   float scale;
 };
@@ -51,20 +51,71 @@ __device__ static inline int mix_slot(const MixArgs& a, int i) {
   return s >= 0 && s < a.num_slots ? s : -1;
 }
 
+// (-1, 0) and (0, -1) as pairs of bf16, in registers that the compiler knows nothing
+// about: as constants of a two-product instruction they come out as other values.
+struct Minus {
+  uint32_t lo = 0x0000bf80u, hi = 0xbf800000u;
+  __device__ inline Minus() { asm volatile("" : "+v"(lo), "+v"(hi)); }
+};
+
+// Split::set with half the instructions for what a term leaves: x - bf16(x) is exact, and
+// one two-product with (-1, 0) forms it from the packed pair (0 times an infinity next to
+// it is NaN: the eight values are factors of the same sums).  The terms were most of the
+// vector unit's work, which stands beside the products'.
+template <typename T, int TERMS>
+__device__ static inline Split<T, TERMS> split(const float* f, const Minus& m) {
+  Split<T, TERMS> s;
+  if constexpr (TERMS == 1) {
+    s.t[0] = Mat<T>::pack(f);
+  } else {
+    float r[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) r[e] = f[e];
+#pragma unroll
+    for (int k = 0; k < TERMS; ++k) {
+      s.t[k] = Mat<T>::pack(r);
+      if (k + 1 == TERMS) break;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t pair = s.t[k][q];
+        const bf16x2_t h = __builtin_bit_cast(bf16x2_t, pair);
+        r[2 * q] = __builtin_amdgcn_fdot2_f32_bf16(h, __builtin_bit_cast(bf16x2_t, m.lo), r[2 * q], false);
+        r[2 * q + 1] = __builtin_amdgcn_fdot2_f32_bf16(h, __builtin_bit_cast(bf16x2_t, m.hi), r[2 * q + 1], false);
+      }
+    }
+  }
+  return s;
+}
+
 // The 64x64 lower triangle as fragments of 16 rows and 32 columns: six are not zero.
 RSSM_HD static inline int low_frag(int it, int kb) { return it < 2 ? it : 2 * it - 2 + kb; }
 // The upper triangle's (a lower one's transpose).
 RSSM_HD static inline int up_frag(int it, int kb) { return low_frag(3 - it, 1 - kb); }
 
-// Products of two split operands: every pair of terms whose weight fp32 can hold.
-template <typename T, int TA, int TB>
-__device__ static inline f32x4 mma_split(const Split<T, TA>& x, const Split<T, TB>& y, f32x4 c) {
+// N results at once of a split operand (a fragment for each: load(n, term)) and another
+// that they share: every pair of terms whose weight fp32 can hold.  Neighbouring
+// products do not wait for each other, as a result's own terms would.  SWAP: the shared
+// one is the first operand.
+template <typename T, int TA, int TB, int N, bool SWAP = false, typename Load>
+__device__ static inline void mma_many(const Load& load, const Split<T, TB>& y, f32x4* acc) {
   constexpr int M = TA > TB ? TA : TB;
 #pragma unroll
-  for (int s = M - 1; s >= 0; --s)
+  for (int i = TA - 1; i >= 0; --i) {
+    typename Mat<T>::Frag x[N];
 #pragma unroll
-    for (int i = 0; i <= s; ++i)
-      if (i < TA && s - i < TB) c = Mat<T>::mma(x.t[i], y.t[s - i], c);
+    for (int n = 0; n < N; ++n) x[n] = load(n, i);
+#pragma unroll
+    for (int j = TB - 1; j >= 0; --j) {
+      if (i + j >= M) continue;
+#pragma unroll
+      for (int n = 0; n < N; ++n)
+        acc[n] = SWAP ? Mat<T>::mma(y.t[j], x[n], acc[n]) : Mat<T>::mma(x[n], y.t[j], acc[n]);
+    }
+  }
+}
+template <typename T, int TA, int TB>
+__device__ static inline f32x4 mma_split(const Split<T, TA>& x, const Split<T, TB>& y, f32x4 c) {
+  mma_many<T, TA, TB, 1>([&](int, int i) { return x.t[i]; }, y, &c);
   return c;
 }
 
@@ -73,30 +124,34 @@ __device__ static inline f32x4 mma_split(const Split<T, TA>& x, const Split<T, T
 __device__ static inline double gate_log2(float g) {
   return (double)(g < -1e4f ? -1e4f : g) * 1.4426950408889634074;
 }
-// log g and beta of the chunk's tokens, one a lane, on their way from memory.
+// log g and beta of the chunk's tokens, one a lane, on their way from memory.  Loads
+// without conditions (a lane without a token takes the first one's, and drops it): in
+// branches, each would be waited for before the next is issued.
 struct GateLoad {
-  const float *g, *b;
-  long step_g;
+  const float *g, *b;  // of the chunk's first token
+  long step_g;         // floats between two tokens' log g
+  int heads;
   float rg, rb;
-  int mode;
-  __device__ inline void start(const MixArgs& a, long t0, int hv, int lane, bool delta) {
-    mode = a.decay;
-    step_g = a.v_heads;
-    const long at = (t0 + lane) * a.v_heads + hv;
-    g = mode == RSSM_DECAY_TOKEN ? a.g + at : (mode == RSSM_DECAY_HEAD ? a.g + hv : nullptr);
-    b = delta ? a.beta + at : nullptr;
+  bool have_g, have_b;
+  __device__ inline void start(const MixArgs& a, long t0, int hv, bool delta) {
+    heads = a.v_heads;
+    step_g = a.decay == RSSM_DECAY_TOKEN ? heads : 0;
+    have_g = a.decay != RSSM_DECAY_NONE;
+    have_b = delta;
+    g = have_g ? a.g + hv + t0 * step_g : reinterpret_cast<const float*>(a.k);
+    b = delta ? a.beta + t0 * heads + hv : g;
   }
   __device__ inline void step(int chunks) {
-    if (mode == RSSM_DECAY_TOKEN) g += chunks * kQ * step_g;
-    if (b) b += chunks * kQ * step_g;
+    g += chunks * kQ * step_g;
+    if (have_b) b += (long)chunks * kQ * heads;
   }
   __device__ inline void fetch(int rows, int lane) {
-    rg = rb = 0.f;
-    if (lane < rows) {
-      if (mode) rg = *g;
-      if (b) rb = *b;
-    }
+    const long t = lane < rows ? lane : 0;
+    rg = g[t * step_g];
+    rb = have_b ? b[t * heads] : 0.f;
   }
+  __device__ inline float log_g(int rows, int lane) const { return have_g && lane < rows ? rg : 0.f; }
+  __device__ inline float beta(int rows, int lane) const { return lane < rows ? rb : 0.f; }
 };
 
 // Inclusive sum over the wave's lanes in double, by lane shifts within the vector unit:
@@ -142,37 +197,99 @@ struct ChunkGates {
   }
 };
 
-// A tile of 64 tokens' rows on its way from memory to LDS, chunk after chunk: a thread
-// keeps one address, from which its pieces are whole rows apart.
+// A tile of 64 tokens' rows in LDS.  bf16: 16-byte pieces of a row change places by
+// the row, so that the 16 rows of a fragment and the eight rows of half a transposing
+// read lie in different banks without padding.  fp32: padded rows.
+template <typename T, int COLS>
+struct Tile {
+  typedef typename Mat<T>::E E;
+  typedef typename Mat<T>::Frag Frag;
+  static constexpr bool kSwap = sizeof(E) == 2;
+  static constexpr int LD = kSwap ? COLS : COLS + Mat<T>::kPad, SIZE = kQ * LD;
+  __device__ static inline int place(int row) {
+    return COLS == 64 ? ((row >> 1 & 3) << 1) | (row >> 3 & 1) : ((row & 7) << 1) | (row >> 3 & 1);
+  }
+  __device__ static inline int at(int row, int col) {
+    return kSwap ? row * LD + (((col >> 3) ^ place(row)) << 3) + (col & 7) : row * LD + col;
+  }
+  // fragments of rows 16 it + l%16, 32 columns from c, in order C and in order D
+  __device__ static inline Frag rows_c(const E* p, int it, int c, int lane) {
+    return Mat<T>::rows_c(p + at(16 * it + (lane & 15), c + 8 * (lane >> 4)));
+  }
+  __device__ static inline Frag rows_d(const E* p, int it, int c, int lane) {
+    const int row = 16 * it + (lane & 15), col = c + 4 * (lane >> 4);
+    if constexpr (kSwap) {
+      const u32x2 a = *reinterpret_cast<const u32x2*>(p + at(row, col));
+      const u32x2 b = *reinterpret_cast<const u32x2*>(p + at(row, col + 16));
+      return Frag{a[0], a[1], b[0], b[1]};
+    } else {
+      return Mat<T>::rows_d(p + at(row, col));
+    }
+  }
+  // of 32 rows from k0, columns c .. c + 15
+  __device__ static inline Frag cols(const E* p, int k0, int c, int lane) {
+    const int i = lane & 15, g = lane >> 4;
+    if constexpr (kSwap) return Mat<T>::cols(p + at(k0 + 4 * g + (i >> 2), c + 4 * (i & 3)), LD);
+    else return Mat<T>::cols(p + at(k0 + 4 * g, c + i), LD);
+  }
+};
+
+// Such a tile on its way from memory, chunk after chunk: a thread keeps one address,
+// from which its pieces are whole rows (multiples of 16) apart.  Loads without
+// conditions: a piece behind the last row takes the first one's, and is put as zero.
+// (Behind a condition each load was waited for before the next: 73 us instead of XX for
+// the delta rule's 4096 tokens.)
 template <typename T, int COLS, int THREADS>
 struct TileLoad {
   typedef typename Mat<T>::E E;
   static constexpr int V = 16 / sizeof(E), PER = COLS / V, N = kQ * PER / THREADS, R = THREADS / PER;
   static_assert(kQ * PER % THREADS == 0 && THREADS % PER == 0, "whole rounds");
-  const E* p;
+  static_assert(sizeof(E) == 4 || R % 16 == 0, "a thread's pieces keep their place");
+  const E *p, *p0;  // of this thread's first row, and of the chunk's
   long stride;
   u32x4 r[N];
   __device__ inline void start(const E* src, long s, int tid) {
     stride = s;
+    p0 = src;
     p = src + (tid / PER) * s + (tid % PER) * V;
   }
-  __device__ inline void step(int chunks) { p += chunks * kQ * stride; }
-  __device__ inline void fetch(int rows, int tid) {
-    if (rows == kQ) {  // the same for the whole workgroup: no conditions in between
-#pragma unroll
-      for (int i = 0; i < N; ++i) r[i] = *reinterpret_cast<const u32x4*>(p + i * (R * stride));
-    } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        r[i] = u32x4{0, 0, 0, 0};
-        if (tid / PER + i * R < rows) r[i] = *reinterpret_cast<const u32x4*>(p + i * (R * stride));
-      }
-    }
+  __device__ inline void step(int chunks) {
+    p += chunks * kQ * stride;
+    p0 += chunks * kQ * stride;
   }
-  __device__ inline void put(E* tile, int ld, int tid) const {
-    E* const to = tile + (tid / PER) * ld + (tid % PER) * V;
+  __device__ inline void fetch(int rows, int tid) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) *reinterpret_cast<u32x4*>(to + i * R * ld) = r[i];
+    for (int i = 0; i < N; ++i)
+      r[i] = *reinterpret_cast<const u32x4*>(tid / PER + i * R < rows ? p + i * (R * stride) : p0);
+  }
+  __device__ inline void put(E* tile, int rows, int tid) {
+    if (rows < kQ) {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (tid / PER + i * R >= rows) r[i] = u32x4{0, 0, 0, 0};
+    }
+    E* const to = tile + Tile<T, COLS>::at(tid / PER, (tid % PER) * V);
+#pragma unroll
+    for (int i = 0; i < N; ++i) *reinterpret_cast<u32x4*>(to + i * R * Tile<T, COLS>::LD) = r[i];
+  }
+};
+
+// The fragments of T in the same way; the last piece may be taken twice.
+template <int PIECES, int THREADS>
+struct FragLoad {
+  static constexpr int N = (PIECES + THREADS - 1) / THREADS;
+  const u32x4* p;
+  u32x4 r[N];
+  __device__ static inline int at(int i, int tid) {
+    return PIECES % THREADS == 0 || i * THREADS + tid < PIECES ? i * THREADS + tid : PIECES - 1;
+  }
+  __device__ inline void fetch(int tid) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) r[i] = p[at(i, tid)];
+  }
+  __device__ inline void put(u32x4* to, int tid) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) to[at(i, tid)] = r[i];
   }
 };
 
@@ -252,12 +369,12 @@ static __global__ void __launch_bounds__(256) mix_inverse_kernel(const MixArgs a
   const long t0 = sg.tok;
   {
     GateLoad ld;
-    ld.start(a, t0, hv, lane, true);
+    ld.start(a, t0, hv, true);
     ld.fetch(rows, lane);
-    const double cum = lane_sums(gate_log2(ld.rg));
+    const double cum = lane_sums(gate_log2(ld.log_g(rows, lane)));
     const float hi = (float)cum;
     sG[wave][lane] = make_float2(hi, (float)(cum - (double)hi));
-    sBeta[wave][lane] = ld.rb;
+    sBeta[wave][lane] = ld.beta(rows, lane);
   }
   // k_m.k_i: rows m of block bm, columns i of block bi <= bm is left out
   f32x4 acc[4][4];
@@ -349,6 +466,7 @@ static __global__ void __launch_bounds__(256) mix_inverse_kernel(const MixArgs a
 #pragma unroll
       for (int r = 0; r < 4; ++r) sBlk[wave][4 + i * (i - 1) / 2 + j][(4 * g + r) * LB + i16] = t[i][j][r];
   wave_sync();
+  const Minus minus;
   char* const out = static_cast<char*>(a.tinv) +
       ((long)slot * a.v_heads + hv) * ((BOTH ? 12 : 6) * TERMS * 64 * sizeof(Frag));
 #pragma unroll
@@ -365,8 +483,7 @@ static __global__ void __launch_bounds__(256) mix_inverse_kernel(const MixArgs a
 #pragma unroll
         for (int r = 0; r < 4; ++r) f[4 * h + r] = row[r];
       }
-      Split<T, TERMS> s;
-      s.set(f);
+      const auto s = split<T, TERMS>(f, minus);
       put_split<T, TERMS>(out, low_frag(it, kb), s, lane);
     }
   if (BOTH) {
@@ -379,8 +496,7 @@ static __global__ void __launch_bounds__(256) mix_inverse_kernel(const MixArgs a
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int r = 0; r < 4; ++r) f[4 * h + r] = 2 * kb + h >= jt ? t[2 * kb + h][jt][r] : 0.f;
-        Split<T, TERMS> s;
-        s.set(f);
+        const auto s = split<T, TERMS>(f, minus);
         put_split<T, TERMS>(out, 6 + up_frag(jt, kb), s, lane);
       }
   }
@@ -429,7 +545,6 @@ static inline void mix_fill(MixArgs& a, const rssm_mixer_dims& d) {
   a.dv = d.dv;
   a.num_slots = d.num_slots;
   a.decay = d.decay;
-  a.slices = d.dv / 64;
   a.scale = d.scale > 0.f ? d.scale : 1.f / sqrtf((float)d.dk);
 }
 

@@ -3,8 +3,8 @@
 //
 // The delta rule's T of every chunk is independent of the state and comes from a
 // launch in front (mix_inverse_kernel).  Then a workgroup walks the chunks of one
-// sequence and 64 columns of one value head's state, a wave 16 of them, with the
-// state in registers; the next chunk's tiles are on their way while one is worked on.
+// sequence (or a segment of one) and value head with the state in registers; the next
+// chunk's tiles are on their way while one is worked on.
 //
 // The states, X and D are fp32 values and enter the products that make states as
 // three bf16 terms (24 bits).  What only the output reads goes in as two terms: the
@@ -25,40 +25,56 @@ __device__ static inline Split<T, TB> cut(const Split<T, TA>& s) {  // the leadi
   return r;
 }
 
-template <typename T, int K, bool DELTA>
-__global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 1 : 2)
-    mix_forward_kernel(const MixArgs a) {
+template <typename T, int K, int V, bool DELTA>
+struct ForwardLds {
+  typedef typename Mat<T>::E E;
+  static constexpr int kFrag = sizeof(typename Mat<T>::Frag);
+  static constexpr int TF = 6 * Mat<T>::kTerms * 64 * kFrag / 16;  // 16-byte pieces of T
+  // fp32: nothing is left of 160 KB for the outputs
+  static constexpr int kOut = sizeof(E) == 4 ? Tile<T, V>::SIZE / 4 : 1;
+  __attribute__((aligned(16))) E k[2][Tile<T, K>::SIZE];
+  __attribute__((aligned(16))) E q[Tile<T, K>::SIZE];
+  __attribute__((aligned(16))) E v[Tile<T, V>::SIZE];
+  __attribute__((aligned(16))) u32x4 t[DELTA ? TF : 1];
+  __attribute__((aligned(16))) u32x4 p[6 * out_terms<T>() * 64 * kFrag / 16];
+  __attribute__((aligned(16))) E o[Tile<T, V>::SIZE / kOut];
+  ChunkGates g[2];
+};
+
+// A workgroup for one value head and segment, a wave for 16 columns of its state.  Two
+// barriers a chunk: behind the first its tiles are in LDS and the next chunk's loads
+// start; at the second the tiles of q, v and T are no longer read, and take the next
+// chunk's (K, read to the end, has two).  The outputs cross LDS and go to memory behind
+// the next barrier, a row's neighbours together: as the lanes hold them, 32 bytes of a
+// row a wave, their stores took a fifth of the time.
+template <typename T, int K, int V, bool DELTA>
+__global__ void __launch_bounds__(4 * V, 2) mix_forward_kernel(const MixArgs a) {
   typedef Mat<T> M;
   typedef typename M::E E;
   typedef typename M::Frag Frag;
-  constexpr int TS = M::kTerms, TO = out_terms<T>();
-  constexpr int LK = K + M::kPad, LV = 64 + M::kPad, KT = K / 16, KB = K / 32;
-  constexpr int TF = 6 * TS * 64 * sizeof(Frag) / 16;  // 16-byte pieces of T
-  constexpr int QT = DELTA ? (TF + 255) / 256 : 1;
-  __shared__ __attribute__((aligned(16))) E sK[kQ * LK];
-  __shared__ __attribute__((aligned(16))) E sQ[kQ * LK];
-  __shared__ __attribute__((aligned(16))) E sV[kQ * LV];
-  __shared__ __attribute__((aligned(16))) u32x4 sT[DELTA ? TF : 1];
-  __shared__ __attribute__((aligned(16))) u32x4 sP[6 * TO * 64 * sizeof(Frag) / 16];
-  __shared__ ChunkGates sg;
-  const int tid = threadIdx.x, lane = tid & 63;
+  typedef ForwardLds<T, K, V, DELTA> L;
+  typedef Tile<T, K> TK;
+  typedef Tile<T, V> TV;
+  constexpr bool kBf16 = sizeof(E) == 2;
+  constexpr int TS = M::kTerms, TO = out_terms<T>(), W = V / 16, TH = 64 * W;
+  constexpr int KT = K / 16, KB = K / 32, TF = L::TF;
+  __shared__ L s;
+  const int tid = threadIdx.x, lane = tid & 63, i16 = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const MixUnit un = mix_unit(a, blockIdx.x, a.vpk * a.slices);
+  const MixUnit un = mix_unit(a, blockIdx.x, a.vpk);
   if (blockIdx.x == 0) check_table(a.cu, a.seqs, a.tokens, a.status);
   if (!un.live) return;
-  const int hv = un.hk * a.vpk + un.rest / a.slices, v0 = (un.rest % a.slices) * 64;
+  const int hv = un.hk * a.vpk + un.rest;
   const Segment sp = find_segment(a.cu, a.seqs, a.tokens, a.seg, un.slot);
   if (sp.len == 0 && !sp.empty) return;
   const int pool = a.init || a.final_state ? mix_slot(a, sp.seq) : -1;
   if (tid == 0 && sp.first && un.rest == 0 && un.hk == 0 && a.status && (a.init || a.final_state) && pool < 0)
     atomicOr(a.status, RSSM_ST_BAD_SLOT);
-  // S: rows k = 16 kt + 4g + r, column v0 + 16 wave + i16
+  // S: rows k = 16 kt + 4g + r, column 16 wave + i16
   f32x4 S[KT];
 #pragma unroll
   for (int kt = 0; kt < KT; ++kt) S[kt] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const auto place = [&](long n) {
-    return ((n * a.v_heads + hv) * a.dv + v0 + 16 * wave + (lane & 15)) * K + 4 * (lane >> 4);
-  };
+  const auto place = [&](long n) { return ((n * a.v_heads + hv) * V + 16 * wave + i16) * K + 4 * g; };
   // The pool is read here only by a sequence of one segment, whose wave also writes it:
   // a longer one's first segment takes the copy that the combining launch left, since
   // its last segment may already have stored the final state over the initial one.
@@ -70,56 +86,75 @@ __global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 1 : 2)
   }
   const long cbase = seg_base(a.cu, sp.seq, kQ, a.tokens) + (long)sp.k * (a.seg / kQ);
   const int chunks = (sp.len + kQ - 1) / kQ;
-  const int i16 = lane & 15, g = lane >> 4;
-  TileLoad<T, K, 256> rk, rq;
-  TileLoad<T, 64, 256> rv;
+  TileLoad<T, K, TH> rk, rq;
+  TileLoad<T, V, TH> rv;
   GateLoad rg;
-  u32x4 rt[QT];
-  const u32x4* tsrc = static_cast<const u32x4*>(a.tinv) + (cbase * a.v_heads + hv) * TF + tid;
+  FragLoad<TF, TH> rt;
+  rt.p = static_cast<const u32x4*>(a.tinv) + (cbase * a.v_heads + hv) * TF;
   rk.start(static_cast<const E*>(a.k) + sp.tok * a.k_stride + (long)un.hk * K, a.k_stride, tid);
   rq.start(static_cast<const E*>(a.q) + sp.tok * a.q_stride + (long)un.hk * K, a.q_stride, tid);
-  rv.start(static_cast<const E*>(a.v) + sp.tok * a.v_stride + (long)hv * a.dv + v0, a.v_stride, tid);
-  rg.start(a, sp.tok, hv, lane, DELTA);
-  E* out = static_cast<E*>(a.o) + ((long)(sp.tok + i16) * a.v_heads + hv) * a.dv + v0 + 16 * wave + 4 * g;
-  const long orow = (long)a.v_heads * a.dv;
+  rv.start(static_cast<const E*>(a.v) + sp.tok * a.v_stride + (long)hv * V, a.v_stride, tid);
+  rg.start(a, sp.tok, hv, DELTA);
+  const long orow = (long)a.v_heads * V;
+  E* out = static_cast<E*>(a.o) + ((long)sp.tok * a.v_heads + hv) * V;
+  if (kBf16) out += tid / TileLoad<T, V, TH>::PER * orow + tid % TileLoad<T, V, TH>::PER * 8;
+  else out += i16 * orow + 16 * wave + 4 * g;
+  // 16 bytes of every R-th row of the chunk before
+  const auto store = [&](int rows) {
+    constexpr int PER = TileLoad<T, V, TH>::PER, R = TileLoad<T, V, TH>::R;
+#pragma unroll
+    for (int i = 0; i < kQ / R; ++i)
+      if (tid / PER + i * R < rows)
+        *reinterpret_cast<u32x4*>(out + i * R * orow) =
+            *reinterpret_cast<const u32x4*>(s.o + TV::at(tid / PER + i * R, tid % PER * 8));
+    out += kQ * orow;
+  };
+  const Minus minus;
+  const auto rows_of = [&](int c) { return sp.len - c * kQ < kQ ? sp.len - c * kQ : kQ; };
   const auto fetch = [&](int c) {
-    const int rows = sp.len - c * kQ < kQ ? sp.len - c * kQ : kQ;
+    const int rows = rows_of(c);
     rk.fetch(rows, tid);
     rq.fetch(rows, tid);
     rv.fetch(rows, tid);
     rg.fetch(rows, lane);
-    if (DELTA) {
-#pragma unroll
-      for (int i = 0; i < QT; ++i)
-        if (TF % 256 == 0 || i * 256 + tid < TF) rt[i] = tsrc[i * 256];
-    }
+    if (DELTA) rt.fetch(tid);
     rk.step(1);
     rq.step(1);
     rv.step(1);
     rg.step(1);
-    tsrc += (long)a.v_heads * TF;
+    rt.p += (long)a.v_heads * TF;
   };
-  if (chunks) fetch(0);
+  const auto put = [&](int c) {
+    const int rows = rows_of(c);
+    rk.put(s.k[c & 1], rows, tid);
+    rq.put(s.q, rows, tid);
+    rv.put(s.v, rows, tid);
+    if (DELTA) rt.put(s.t, tid);
+    if (wave == W - 1) s.g[c & 1].set(rg.log_g(rows, lane), rg.beta(rows, lane), lane);
+  };
+  if (chunks) {
+    fetch(0);
+    put(0);
+  }
+  // The state has arrived: waited for at its first use, in the loop, it would have every
+  // chunk wait for the next one's loads too (16383 tokens: 363 us instead of XXX).
+#pragma unroll
+  for (int kt = 0; kt < KT; ++kt) forget(S[kt]);
 #pragma unroll 1
   for (int c = 0; c < chunks; ++c) {
-    const int rows = sp.len - c * kQ < kQ ? sp.len - c * kQ : kQ;
-    __syncthreads();  // the previous chunk's tiles are no longer read
-    rk.put(sK, LK, tid);
-    rq.put(sQ, LK, tid);
-    rv.put(sV, LV, tid);
-    if (DELTA) {
-#pragma unroll
-      for (int i = 0; i < QT; ++i)
-        if (TF % 256 == 0 || i * 256 + tid < TF) sT[i * 256 + tid] = rt[i];
-    }
-    if (wave == 3) sg.set(rg.rg, rg.rb, lane);
-    if (c + 1 < chunks) fetch(c + 1);
+    const int rows = rows_of(c);
+    const E* const sK = s.k[c & 1];
+    const ChunkGates& sg = s.g[c & 1];
     __syncthreads();
+    if (c + 1 < chunks) fetch(c + 1);
+    if (kBf16 && c) store(kQ);
     f32x4 R[4], O[4];  // K S, rows t; (Q S)^T, columns t
-    f32x4 P[3];        // this wave's tiles of k_j.q_i, rows j
+    f32x4 P[2];        // this wave's tiles of k_j.q_i, rows j
 #pragma unroll
     for (int it = 0; it < 4; ++it) R[it] = O[it] = f32x4{0.f, 0.f, 0.f, 0.f};
-    P[0] = P[1] = P[2] = f32x4{0.f, 0.f, 0.f, 0.f};
+    P[0] = P[1] = f32x4{0.f, 0.f, 0.f, 0.f};
+    f32x4 P2[2];
+    P2[0] = P2[1] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int b = 0; b < KB; ++b) {
       float f[8];
@@ -128,14 +163,13 @@ __global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 1 : 2)
         f[r] = S[2 * b][r];
         f[4 + r] = S[2 * b + 1][r];
       }
-      Split<T, DELTA ? TS : TO> sf;
-      sf.set(f);
+      const auto sf = split<T, DELTA ? TS : TO>(f, minus);
       const auto so = cut<T, DELTA ? TS : TO, TO>(sf);
       Frag kf[4], qf[4];
 #pragma unroll
       for (int it = 0; it < 4; ++it) {
-        kf[it] = M::rows_d(sK + (16 * it + i16) * LK + 32 * b + 4 * g);
-        qf[it] = M::rows_d(sQ + (16 * it + i16) * LK + 32 * b + 4 * g);
+        kf[it] = TK::rows_d(sK, it, 32 * b, lane);
+        qf[it] = TK::rows_d(s.q, it, 32 * b, lane);
       }
       if constexpr (DELTA) {
 #pragma unroll
@@ -147,46 +181,38 @@ __global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 1 : 2)
       for (int k = TO - 1; k >= 0; --k)
 #pragma unroll
         for (int it = 0; it < 4; ++it) O[it] = M::mma(so.t[k], qf[it], O[it]);
-      if (wave == 0) {
-        P[0] = M::mma(kf[0], qf[3], P[0]);
-        P[1] = M::mma(kf[1], qf[3], P[1]);
-        P[2] = M::mma(kf[0], qf[0], P[2]);
-      } else if (wave == 1) {
-        P[0] = M::mma(kf[2], qf[3], P[0]);
-        P[1] = M::mma(kf[3], qf[3], P[1]);
-      } else if (wave == 2) {
-        P[0] = M::mma(kf[0], qf[2], P[0]);
-        P[1] = M::mma(kf[1], qf[2], P[1]);
-      } else {
-        P[0] = M::mma(kf[0], qf[1], P[0]);
-        P[1] = M::mma(kf[1], qf[1], P[1]);
-        P[2] = M::mma(kf[2], qf[2], P[2]);
+    }
+    // k_j.q_i of the lower triangle's six fragments: a wave each (of four waves, two have a
+    // second one)
+    const int pi = wave < 2 ? 3 : (wave == 2 || wave == 5 ? 2 : (wave == 3 ? 1 : 0)), pk = wave == 1 || wave == 5;
+    if (wave < 6) {
+#pragma unroll
+      for (int b = 0; b < KB; ++b) {
+        const Frag qf = TK::rows_c(s.q, pi, 32 * b, lane);
+        P[0] = M::mma(TK::rows_c(sK, 2 * pk, 32 * b, lane), qf, P[0]);
+        P[1] = M::mma(TK::rows_c(sK, 2 * pk + 1, 32 * b, lane), qf, P[1]);
+        if (W == 4 && wave < 2)
+          P2[0] = M::mma(TK::rows_c(sK, 2 * wave, 32 * b, lane), TK::rows_c(s.q, 2 * wave, 32 * b, lane), P2[0]);
       }
     }
     {
-      // scale e^{G_i-G_j} q_i.k_j of the lower triangle as fragments: (3, 0) and (0, 0);
-      // (3, 1); (2, 0); (1, 0) and (2, 1)
-      const int it = wave < 2 ? 3 : (wave == 2 ? 2 : 1), kb = wave == 1, ie = wave ? 2 : 0, ke = wave != 0;
+      // scale e^{G_i-G_j} q_i.k_j as a fragment
       const auto weigh = [&](int i, int j, const f32x4& p, float* f) {  // of one tile
         const float2 gi = sg.G[16 * i + i16];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const float w = a.scale * exp2_f32(gap2(gi, sg.G[16 * j + 4 * g + r])) * p[r];
-          f[r] = j < i || 4 * g + r <= i16 ? w : 0.f;
+          f[r] = j < i || (j == i && 4 * g + r <= i16) ? w : 0.f;
         }
       };
-      float f[8];
-      Split<T, TO> s;
-      weigh(it, 2 * kb, P[0], f);
-      weigh(it, 2 * kb + 1, P[1], f + 4);
-      s.set(f);
-      put_split<T, TO>(sP, low_frag(it, kb), s, lane);
-      if (wave == 0 || wave == 3) {
-        weigh(ie, 2 * ke, P[2], f);
-        f[4] = f[5] = f[6] = f[7] = 0.f;
-        s.set(f);
-        put_split<T, TO>(sP, low_frag(ie, ke), s, lane);
-      }
+      const auto make = [&](int it, int kb, const f32x4* p) {
+        float f[8];
+        weigh(it, 2 * kb, p[0], f);
+        weigh(it, 2 * kb + 1, p[1], f + 4);
+        put_split<T, TO>(s.p, low_frag(it, kb), split<T, TO>(f, minus), lane);
+      };
+      if (wave < 6) make(pi, pk, P);
+      if (W == 4 && wave < 2) make(wave ? 2 : 0, wave, P2);
     }
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
@@ -197,7 +223,7 @@ __global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 1 : 2)
     float d[2][8];  // D, token 32 kb + (4g + r, 16 + 4g + r), this lane's column
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
-      M::unpack(M::cols(cols_at<T, false>(sV, LV, 32 * kb, 16 * wave, lane), LV), d[kb]);
+      M::unpack(TV::cols(s.v, 32 * kb, 16 * wave, lane), d[kb]);
       if (DELTA) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -214,26 +240,25 @@ __global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 1 : 2)
       for (int it = 0; it < 4; ++it) acc[it] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb) {
-        Split<T, TS> xf;
-        xf.set(d[kb]);
-#pragma unroll
-        for (int it = 2 * kb; it < 4; ++it)
-          acc[it] = mma_split<T, TS, TS>(split_at<T, TS>(sT, low_frag(it, kb), lane), xf, acc[it]);
+        const auto xf = split<T, TS>(d[kb], minus);
+        const auto tf = [&](int n, int k) { return frag_at<T>(s.t, low_frag(2 * kb + n, kb) * TS + k, lane); };
+        if (kb == 0) mma_many<T, TS, TS, 4>(tf, xf, acc);
+        else mma_many<T, TS, TS, 2>(tf, xf, acc + 2);
       }
 #pragma unroll
       for (int it = 0; it < 4; ++it)
 #pragma unroll
         for (int r = 0; r < 4; ++r) d[it >> 1][4 * (it & 1) + r] = acc[it][r];
     }
-    __syncthreads();  // sP
+    __syncthreads();  // P; and q, v and T are no longer read
+    if (c + 1 < chunks) put(c + 1);
     // o^T += D^T P^T, and S' = e^{G_Q} S + K^T (e^{G_Q - G} D)
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
-      Split<T, DELTA ? TO : 1> df;
-      df.set(d[kb]);
-#pragma unroll
-      for (int it = 2 * kb; it < 4; ++it)
-        O[it] = mma_split<T, DELTA ? TO : 1, TO>(df, split_at<T, TO>(sP, low_frag(it, kb), lane), O[it]);
+      const auto df = split<T, DELTA ? TO : 1>(d[kb], minus);
+      const auto pf = [&](int n, int k) { return frag_at<T>(s.p, low_frag(2 * kb + n, kb) * TO + k, lane); };
+      if (kb == 0) mma_many<T, TO, DELTA ? TO : 1, 4, true>(pf, df, O);
+      else mma_many<T, TO, DELTA ? TO : 1, 2, true>(pf, df, O + 2);
     }
     const float all = sg.all;
 #pragma unroll
@@ -249,13 +274,12 @@ __global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 1 : 2)
 #pragma unroll
         for (int r = 0; r < 4; ++r) d[kb][4 * h + r] *= e[r];
       }
-      Split<T, TS> wf;
-      wf.set(d[kb]);
+      const auto wf = split<T, TS>(d[kb], minus);
 #pragma unroll
       for (int k4 = 0; k4 < KT; k4 += 4) {
         Frag kf[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) kf[q] = M::cols(cols_at<T, false>(sK, LK, 32 * kb, 16 * (k4 + q), lane), LK);
+        for (int q = 0; q < 4; ++q) kf[q] = TK::cols(sK, 32 * kb, 16 * (k4 + q), lane);
 #pragma unroll
         for (int k = TS - 1; k >= 0; --k)
 #pragma unroll
@@ -265,9 +289,16 @@ __global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 1 : 2)
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
       const float f[4] = {O[it][0], O[it][1], O[it][2], O[it][3]};
-      if (16 * it + i16 < rows) *reinterpret_cast<typename M::Four*>(out + 16 * it * orow) = M::pack4(f);
+      if (kBf16)
+        *reinterpret_cast<typename M::Four*>(s.o + TV::at(16 * it + i16, 16 * wave + 4 * g)) = M::pack4(f);
+      else if (16 * it + i16 < rows)
+        *reinterpret_cast<typename M::Four*>(out + 16 * it * orow) = M::pack4(f);
     }
-    out += kQ * orow;
+    if (!kBf16) out += kQ * orow;
+  }
+  if (kBf16 && chunks) {
+    __syncthreads();
+    store(sp.len - (chunks - 1) * kQ);
   }
   if (sp.last && a.final_state && pool >= 0) {
     float* p = a.final_state + place(pool);
@@ -293,10 +324,16 @@ static size_t mix_forward_bytes(const rssm_mixer_dims* dims, bool delta) {
   return mix_check(dims, delta) || dims->tokens == 0 ? 0 : fwd_layout(*dims, delta).end;
 }
 
-template <typename T, bool DELTA>
-static const void* pick_forward(int dk) {
-  return dk == 64 ? reinterpret_cast<const void*>(&mix_forward_kernel<T, 64, DELTA>)
-                  : reinterpret_cast<const void*>(&mix_forward_kernel<T, 128, DELTA>);
+template <typename T>
+static const void* pick_forward(const rssm_mixer_dims& d, bool delta) {
+  if (delta)
+    return d.dk == 64 ? reinterpret_cast<const void*>(&mix_forward_kernel<T, 64, 64, true>)
+                      : reinterpret_cast<const void*>(&mix_forward_kernel<T, 128, 128, true>);
+  if (d.dk == 64)
+    return d.dv == 64 ? reinterpret_cast<const void*>(&mix_forward_kernel<T, 64, 64, false>)
+                      : reinterpret_cast<const void*>(&mix_forward_kernel<T, 64, 128, false>);
+  return d.dv == 64 ? reinterpret_cast<const void*>(&mix_forward_kernel<T, 128, 64, false>)
+                    : reinterpret_cast<const void*>(&mix_forward_kernel<T, 128, 128, false>);
 }
 
 static int mix_forward(const rssm_mixer_dims* dims, bool delta, const void* q, const void* k, const void* v,
@@ -335,7 +372,7 @@ static int mix_forward(const rssm_mixer_dims* dims, bool delta, const void* q, c
   seg_fill(a, d, l.seg, workspace);
   a.seg_grad = nullptr;  // no gradients to combine
   const long cslots = scan_slots(d.tokens, d.seqs, kQ);
-  const long grid = mix_grid(a.slots, d.k_heads, (long)a.vpk * a.slices);
+  const long grid = mix_grid(a.slots, d.k_heads, a.vpk);
   if (!segments_fit(a, d.dk) || (delta && !grid_fits(cslots * ((d.v_heads + 3) / 4), 256))) return RSSM_ESHAPE;
   if (delta && d.tokens > 0) {
     rc = f32 ? launch_inverse<float, false>(a, d.dk, cslots, stream)
@@ -345,15 +382,12 @@ static int mix_forward(const rssm_mixer_dims* dims, bool delta, const void* q, c
   if (d.tokens > a.seg) {
     MixBwdArgs b{};
     b.m = a;
-    rc = f32 ? (delta ? launch_segments<float, true, false>(b, d.dk, stream)
-                      : launch_segments<float, false, false>(b, d.dk, stream))
-             : (delta ? launch_segments<bf16, true, false>(b, d.dk, stream)
-                      : launch_segments<bf16, false, false>(b, d.dk, stream));
+    rc = f32 ? launch_segments<float, false>(b, d.dk, delta, stream)
+             : launch_segments<bf16, false>(b, d.dk, delta, stream);
     if (rc) return rc;
   }
-  const void* fn = f32 ? (delta ? pick_forward<float, true>(d.dk) : pick_forward<float, false>(d.dk))
-                       : (delta ? pick_forward<bf16, true>(d.dk) : pick_forward<bf16, false>(d.dk));
-  return launch_kernel(fn, (unsigned)grid, 256, 0, stream, a);
+  return launch_kernel(f32 ? pick_forward<float>(d, delta) : pick_forward<bf16>(d, delta), (unsigned)grid,
+                       4 * d.dv, 0, stream, a);
 }
 
 }  // namespace rssm

@@ -27,48 +27,49 @@ struct MixBwdArgs {
   int32_t elems;       // of a state
 };
 
-template <typename T, int K, bool DELTA, bool BOTH>
+template <typename T, int K, int V, bool DELTA, bool BOTH>
 struct StatesLds {
   typedef typename Mat<T>::E E;
   static constexpr int kFrag = sizeof(typename Mat<T>::Frag), TS = Mat<T>::kTerms;
-  static constexpr int LK = K + Mat<T>::kPad;
   static constexpr int TF = 6 * TS * 64 * kFrag / 16;  // 16-byte pieces of T or its transpose
-  __attribute__((aligned(16))) E k[kQ * LK];
-  __attribute__((aligned(16))) E v[kQ * 64];  // V forward, dO backward
-  __attribute__((aligned(16))) u32x4 t[DELTA ? TF : 1];
-  __attribute__((aligned(16))) E q[BOTH ? kQ * LK : 1];
+  // fp32 with both directions' tiles twice would not fit 160 KB
+  static constexpr int B = BOTH && sizeof(E) == 4 ? 1 : 2;
+  __attribute__((aligned(16))) E k[B][Tile<T, K>::SIZE];
+  __attribute__((aligned(16))) E v[B][Tile<T, V>::SIZE];  // V forward, dO backward
+  __attribute__((aligned(16))) u32x4 t[DELTA ? B : 1][DELTA ? TF : 1];
+  __attribute__((aligned(16))) E q[BOTH ? B : 1][BOTH ? Tile<T, K>::SIZE : 1];
   __attribute__((aligned(16))) u32x4 p[BOTH ? TF : 1];
-  ChunkGates g;
+  ChunkGates g[B];
 };
 
-// One of the two recurrences over the chunks of a segment, a workgroup for 64 columns of
-// one value head's state (mix_forward_kernel without the outputs).  Blocks: forward;
-// BOTH: backward, last chunk first; the delta rule's transition.
+// One of the two recurrences over the chunks of a segment, a workgroup for one value
+// head's state (mix_forward_kernel without the outputs).  Blocks: forward; BOTH:
+// backward, last chunk first; the delta rule's transition.
 // STORE: from the segment's start, leaving the states before all chunks, D and dX (or
 // dV) and the gradient of the initial state.  Otherwise from zero, leaving what the
 // segment adds and, as columns that start from the identity without V, the matrix that
 // its starting state is multiplied by, as first operands: rows of it and (BOTH) of its
 // transpose, which gradients go through.
-template <typename T, int K, bool DELTA, bool STORE, bool BOTH>
-static __global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 1 : 2)
-    mix_states_kernel(const MixBwdArgs b) {
+template <typename T, int K, int V, bool DELTA, bool STORE, bool BOTH>
+static __global__ void __launch_bounds__(4 * V, 2) mix_states_kernel(const MixBwdArgs b) {
   typedef Mat<T> M;
   typedef typename M::E E;
   typedef typename M::Frag Frag;
-  typedef StatesLds<T, K, DELTA, BOTH> L;
-  constexpr int TS = M::kTerms, LK = L::LK, KT = K / 16, KB = K / 32, TF = L::TF;
-  constexpr int QT = DELTA ? (TF + 255) / 256 : 1;
+  typedef StatesLds<T, K, V, DELTA, BOTH> L;
+  typedef Tile<T, K> TK;
+  typedef Tile<T, V> TV;
+  static_assert(!DELTA || K == V, "the transition's columns are as many as V's");
+  constexpr int TS = M::kTerms, KT = K / 16, KB = K / 32, TF = L::TF, W = V / 16, TH = 64 * W, B = L::B;
   __shared__ L s;
   const MixArgs& a = b.m;
-  const int tid = threadIdx.x, lane = tid & 63;
+  const int tid = threadIdx.x, lane = tid & 63, i16 = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const bool back = BOTH && (int)blockIdx.x >= b.dir_blocks && (int)blockIdx.x < 2 * b.dir_blocks;
   const bool trans = !STORE && DELTA && (int)blockIdx.x >= (BOTH ? 2 : 1) * b.dir_blocks;
-  const int slices = trans ? K / 64 : a.slices;
-  const MixUnit un = mix_unit(a, blockIdx.x - (trans ? (BOTH ? 2 : 1) : back) * b.dir_blocks, a.vpk * slices);
+  const MixUnit un = mix_unit(a, blockIdx.x - (trans ? (BOTH ? 2 : 1) : back) * b.dir_blocks, a.vpk);
   if (STORE && blockIdx.x == 0) check_table(a.cu, a.seqs, a.tokens, a.status);
   if (!un.live) return;
-  const int hv = un.hk * a.vpk + un.rest / slices, v0 = (un.rest % slices) * 64;
+  const int hv = un.hk * a.vpk + un.rest;
   const Segment sg = find_segment(a.cu, a.seqs, a.tokens, a.seg, un.slot);
   if (sg.len == 0 && !(STORE && sg.empty)) return;
   const bool whole = sg.first && sg.last;
@@ -82,9 +83,7 @@ static __global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 
 #pragma unroll
   for (int kt = 0; kt < KT; ++kt) S[kt] = f32x4{0.f, 0.f, 0.f, 0.f};
   // this lane's first element in state number n
-  const auto place = [&](long n) {
-    return ((n * a.v_heads + hv) * a.dv + v0 + 16 * wave + (lane & 15)) * K + 4 * (lane >> 4);
-  };
+  const auto place = [&](long n) { return ((n * a.v_heads + hv) * V + 16 * wave + i16) * K + 4 * g; };
   if (STORE) {
     const float* src = back ? b.dfinal : (has ? a.init : nullptr);
     if (!whole) src = back ? a.seg_grad : a.seg_state;
@@ -97,112 +96,75 @@ static __global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        S[kt][r] = 16 * kt + 4 * (lane >> 4) + r == v0 + 16 * wave + (lane & 15) ? 1.f : 0.f;
+      for (int r = 0; r < 4; ++r) S[kt][r] = 16 * kt + 4 * g + r == 16 * wave + i16 ? 1.f : 0.f;
   }
   float total = 1.f;
   const long vstride = back ? b.do_stride : a.v_stride;
   const long cbase = seg_base(a.cu, sg.seq, kQ, a.tokens) + (long)sg.k * (a.seg / kQ);
   const int chunks = (sg.len + kQ - 1) / kQ, way = back ? -1 : 1;
-  const int i16 = lane & 15, g = lane >> 4;
   const long first = chunks && back ? chunks - 1 : 0, tok = sg.tok + first * kQ;
-  TileLoad<T, K, 256> rk, rq;
-  TileLoad<T, 64, 256> rv;
+  TileLoad<T, K, TH> rk, rq;
+  TileLoad<T, V, TH> rv;
   GateLoad rg;
-  u32x4 rt[QT];
-  const u32x4* tsrc = static_cast<const u32x4*>(a.tinv) +
-      (((cbase + first) * a.v_heads + hv) * (BOTH ? 2 : 1) + back) * TF + tid;
+  FragLoad<TF, TH> rt;
+  rt.p = static_cast<const u32x4*>(a.tinv) + (((cbase + first) * a.v_heads + hv) * (BOTH ? 2 : 1) + back) * TF;
   rk.start(static_cast<const E*>(a.k) + tok * a.k_stride + (long)un.hk * K, a.k_stride, tid);
   if (BOTH) rq.start(static_cast<const E*>(a.q) + tok * a.q_stride + (long)un.hk * K, a.q_stride, tid);
-  rv.start(static_cast<const E*>(back ? b.dout : a.v) + tok * vstride + (long)hv * a.dv + v0, vstride, tid);
-  rg.start(a, tok, hv, lane, DELTA);
+  rv.start(static_cast<const E*>(back ? b.dout : a.v) + tok * vstride + (long)hv * V, vstride, tid);
+  rg.start(a, tok, hv, DELTA);
+  const Minus minus;
+  const auto rows_of = [&](int c) { return sg.len - c * kQ < kQ ? sg.len - c * kQ : kQ; };
   const auto fetch = [&](int c) {
-    const int rows = sg.len - c * kQ < kQ ? sg.len - c * kQ : kQ;
+    const int rows = rows_of(c);
     rk.fetch(rows, tid);
     if (back) rq.fetch(rows, tid);
-    rv.fetch(trans ? 0 : rows, tid);
+    rv.fetch(rows, tid);
     rg.fetch(rows, lane);
-    if (DELTA) {
-#pragma unroll
-      for (int i = 0; i < QT; ++i)
-        if (TF % 256 == 0 || i * 256 + tid < TF) rt[i] = tsrc[i * 256];
-    }
+    if (DELTA) rt.fetch(tid);
     rk.step(way);
     if (BOTH) rq.step(way);
     rv.step(way);
     rg.step(way);
-    tsrc += way * (long)a.v_heads * ((BOTH ? 2 : 1) * TF);
+    rt.p += way * (long)a.v_heads * ((BOTH ? 2 : 1) * TF);
+  };
+  const auto put = [&](int n) {
+    const int rows = rows_of(back ? chunks - 1 - n : n);
+    rk.put(s.k[n % B], rows, tid);
+    if (back) rq.put(s.q[BOTH ? n % B : 0], rows, tid);
+    rv.put(s.v[n % B], trans ? 0 : rows, tid);
+    if (DELTA) rt.put(s.t[DELTA ? n % B : 0], tid);
+    if (wave == W - 1) s.g[n % B].set(rg.log_g(rows, lane), rg.beta(rows, lane), lane);
   };
   float* const keep = back ? b.grad : b.state;
   float* const rowmat = back ? b.dX : b.D;
-  if (chunks) fetch(back ? chunks - 1 : 0);
+  if (chunks) {
+    fetch(back ? chunks - 1 : 0);
+    put(0);
+  }
+#pragma unroll
+  for (int kt = 0; kt < KT; ++kt) forget(S[kt]);  // has arrived: see mix_forward_kernel
 #pragma unroll 1
   for (int n = 0; n < chunks; ++n) {
-    const int c = back ? chunks - 1 - n : n;
-    const int rows = sg.len - c * kQ < kQ ? sg.len - c * kQ : kQ;
+    const int c = back ? chunks - 1 - n : n, rows = rows_of(c);
     const long t0 = sg.tok + (long)c * kQ;
+    const E *const sK = s.k[n % B], *const sQ = s.q[BOTH ? n % B : 0], *const sV = s.v[n % B];
+    const u32x4* const sT = s.t[DELTA ? n % B : 0];
+    const ChunkGates& gt = s.g[n % B];
     if (STORE) {
       float* p = keep + place(cbase + c);
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt) *reinterpret_cast<f32x4*>(p + 16 * kt) = S[kt];
     }
-    __syncthreads();  // the previous chunk's tiles are no longer read
-    rk.put(s.k, LK, tid);
-    if (back) rq.put(s.q, LK, tid);
-    rv.put(s.v, 64, tid);
-    if (DELTA) {
-#pragma unroll
-      for (int i = 0; i < QT; ++i)
-        if (TF % 256 == 0 || i * 256 + tid < TF) s.t[i * 256 + tid] = rt[i];
-    }
-    if (wave == 3) s.g.set(rg.rg, rg.rb, lane);
-    if (n + 1 < chunks) fetch(back ? c - 1 : c + 1);
     __syncthreads();
-    if (back) {
-      // P^T by rows j, fragments (0, 1); (0, 0) and (3, 1); (1, 1); (2, 1) and (1, 0)
-      const auto make = [&](int jt, int kb) {
-        f32x4 acc[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) acc[h] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int x = 0; x < KB; ++x) {
-          const Frag kf = M::rows_c(s.k + (16 * jt + i16) * LK + 32 * x + 8 * g);
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            if (2 * kb + h >= jt)
-              acc[h] = M::mma(M::rows_c(s.q + (16 * (2 * kb + h) + i16) * LK + 32 * x + 8 * g), kf, acc[h]);
-        }
-        const int j = 16 * jt + i16;
-        const float2 gj = s.g.G[j];
-        float f[8];
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int i = 16 * (2 * kb + h) + 4 * g + r;
-            const float w = a.scale * exp2_f32(gap2(s.g.G[i], gj)) * acc[h][r];
-            f[4 * h + r] = i >= j ? w : 0.f;
-          }
-        Split<T, TS> sp3;
-        sp3.set(f);
-        put_split<T, TS>(s.p, up_frag(jt, kb), sp3, lane);
-      };
-      if (wave == 0) {
-        make(0, 1);
-      } else if (wave == 1) {
-        make(0, 0);
-        make(3, 1);
-      } else if (wave == 2) {
-        make(1, 1);
-      } else {
-        make(2, 1);
-        make(1, 0);
-      }
-    }
-    // K S (or K dS'), rows t
-    f32x4 R[4];
+    if (n + 1 < chunks) fetch(back ? c - 1 : c + 1);
+    // K S (or K dS'), rows t; backward: this wave's tiles of q_i.k_j, rows i
+    f32x4 R[4], P[2], P2[2];
 #pragma unroll
     for (int it = 0; it < 4; ++it) R[it] = f32x4{0.f, 0.f, 0.f, 0.f};
+    P[0] = P[1] = P2[0] = P2[1] = f32x4{0.f, 0.f, 0.f, 0.f};
+    // P^T by rows j: fragments (0, 1), (0, 0), (1, 1), (2, 1), then (3, 1) and (1, 0)
+    const int jt = wave < 2 ? 0 : (wave == 2 ? 1 : (wave == 3 ? 2 : (wave == 4 ? 3 : 1)));
+    const int kp = wave == 0 || wave == 2 || wave == 3 || wave == 4;
     if (DELTA || back) {
 #pragma unroll
       for (int x = 0; x < KB; ++x) {
@@ -212,42 +174,70 @@ static __global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 
           f[r] = S[2 * x][r];
           f[4 + r] = S[2 * x + 1][r];
         }
-        Split<T, TS> sf;
-        sf.set(f);
+        const auto sf = split<T, TS>(f, minus);
         Frag kf[4];
 #pragma unroll
-        for (int it = 0; it < 4; ++it) kf[it] = M::rows_d(s.k + (16 * it + i16) * LK + 32 * x + 4 * g);
+        for (int it = 0; it < 4; ++it) kf[it] = TK::rows_d(sK, it, 32 * x, lane);
 #pragma unroll
         for (int k = TS - 1; k >= 0; --k)
 #pragma unroll
           for (int it = 0; it < 4; ++it) R[it] = M::mma(kf[it], sf.t[k], R[it]);
+        if (back && wave < 6) {
+          const Frag kj = TK::rows_d(sK, jt, 32 * x, lane);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            if (2 * kp + h >= jt) P[h] = M::mma(TK::rows_d(sQ, 2 * kp + h, 32 * x, lane), kj, P[h]);
+          if (W == 4 && wave < 2) {  // (1, 0) and (3, 1): one tile each
+            const int j2 = wave ? 3 : 1;
+            P2[1] = M::mma(TK::rows_d(sQ, j2, 32 * x, lane), TK::rows_d(sK, j2, 32 * x, lane), P2[1]);
+          }
+        }
       }
     }
-    if (back) __syncthreads();  // s.p
+    if (back) {
+      const auto make = [&](int jb, int kb, const f32x4* acc) {
+        const int j = 16 * jb + i16;
+        const float2 gj = gt.G[j];
+        float f[8];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int i = 16 * (2 * kb + h) + 4 * g + r;
+            const float w = a.scale * exp2_f32(gap2(gt.G[i], gj)) * acc[h][r];
+            f[4 * h + r] = i >= j ? w : 0.f;
+          }
+        const auto x = split<T, TS>(f, minus);
+        put_split<T, TS>(s.p, up_frag(jb, kb), x, lane);
+      };
+      if (wave < 6) make(jt, kp, P);
+      if (W == 4 && wave < 2) make(wave ? 3 : 1, wave, P2);
+      __syncthreads();
+    }
     float d[2][8];  // tokens 32 kb + (4g + r, 16 + 4g + r), this lane's column
     Frag vf[2];
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
-      vf[kb] = M::cols(cols_at<T, false>(s.v, 64, 32 * kb, 16 * wave, lane), 64);
+      vf[kb] = TV::cols(sV, 32 * kb, 16 * wave, lane);
       M::unpack(vf[kb], d[kb]);
     }
     if (back) {  // dD
 #pragma unroll
       for (int it = 0; it < 4; ++it) {
-        const f32x4 e = *reinterpret_cast<const f32x4*>(&s.g.et[16 * it + 4 * g]);
+        const f32x4 e = *reinterpret_cast<const f32x4*>(&gt.et[16 * it + 4 * g]);
 #pragma unroll
         for (int r = 0; r < 4; ++r) R[it][r] *= e[r];
-#pragma unroll
-        for (int kb = it / 2; kb < 2; ++kb) {
-          const auto pf = split_at<T, TS>(s.p, up_frag(it, kb), lane);
-          R[it] = pf.a_times(vf[kb], R[it]);
-        }
       }
+      Split<T, 1> o0, o1;
+      o0.t[0] = vf[0];
+      o1.t[0] = vf[1];
+      mma_many<T, TS, 1, 2>([&](int n, int k) { return frag_at<T>(s.p, up_frag(n, 0) * TS + k, lane); }, o0, R);
+      mma_many<T, TS, 1, 4>([&](int n, int k) { return frag_at<T>(s.p, up_frag(n, 1) * TS + k, lane); }, o1, R);
     } else if (DELTA) {  // X
 #pragma unroll
       for (int it = 0; it < 4; ++it) {
-        const f32x4 e = *reinterpret_cast<const f32x4*>(&s.g.eg[16 * it + 4 * g]);
-        const f32x4 be = *reinterpret_cast<const f32x4*>(&s.g.beta[16 * it + 4 * g]);
+        const f32x4 e = *reinterpret_cast<const f32x4*>(&gt.eg[16 * it + 4 * g]);
+        const f32x4 be = *reinterpret_cast<const f32x4*>(&gt.beta[16 * it + 4 * g]);
 #pragma unroll
         for (int r = 0; r < 4; ++r) R[it][r] = be[r] * fmaf(-e[r], R[it][r], d[it >> 1][4 * (it & 1) + r]);
       }
@@ -263,31 +253,26 @@ static __global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 
           f[r] = R[2 * kb][r];
           f[4 + r] = R[2 * kb + 1][r];
         }
-        xf[kb].set(f);
+        xf[kb] = split<T, TS>(f, minus);
       }
 #pragma unroll
       for (int it = 0; it < 4; ++it) acc[it] = f32x4{0.f, 0.f, 0.f, 0.f};
       if (back) {
-#pragma unroll
-        for (int it = 0; it < 4; ++it)
-#pragma unroll
-          for (int kb = it / 2; kb < 2; ++kb)
-            acc[it] = mma_split<T, TS, TS>(split_at<T, TS>(s.t, up_frag(it, kb), lane), xf[kb], acc[it]);
+        mma_many<T, TS, TS, 2>([&](int n, int k) { return frag_at<T>(sT, up_frag(n, 0) * TS + k, lane); }, xf[0], acc);
+        mma_many<T, TS, TS, 4>([&](int n, int k) { return frag_at<T>(sT, up_frag(n, 1) * TS + k, lane); }, xf[1], acc);
       } else {
-#pragma unroll
-        for (int it = 0; it < 4; ++it)
-#pragma unroll
-          for (int kb = 0; kb <= it / 2; ++kb)
-            acc[it] = mma_split<T, TS, TS>(split_at<T, TS>(s.t, low_frag(it, kb), lane), xf[kb], acc[it]);
+        mma_many<T, TS, TS, 4>([&](int n, int k) { return frag_at<T>(sT, low_frag(n, 0) * TS + k, lane); }, xf[0], acc);
+        mma_many<T, TS, TS, 2>([&](int n, int k) { return frag_at<T>(sT, low_frag(2 + n, 1) * TS + k, lane); }, xf[1],
+                               acc + 2);
       }
 #pragma unroll
       for (int it = 0; it < 4; ++it) R[it] = acc[it];
       if (STORE) {
-        float* p = rowmat + ((cbase + c) * a.v_heads + hv) * (long)(kQ * a.dv) + v0 + 16 * wave + i16;
+        float* p = rowmat + ((cbase + c) * a.v_heads + hv) * (long)(kQ * V) + 16 * wave + i16;
 #pragma unroll
         for (int it = 0; it < 4; ++it)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) p[(16 * it + 4 * g + r) * a.dv] = acc[it][r];
+          for (int r = 0; r < 4; ++r) p[(16 * it + 4 * g + r) * V] = acc[it][r];
       }
     } else if (STORE && back) {  // linear attention: dV
 #pragma unroll
@@ -295,11 +280,12 @@ static __global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int t = 16 * it + 4 * g + r;
-          if (t < rows) Elt<T>::store1(b.dv, ((t0 + t) * a.v_heads + hv) * a.dv + v0 + 16 * wave + i16, R[it][r]);
+          if (t < rows) Elt<T>::store1(b.dv, ((t0 + t) * a.v_heads + hv) * V + 16 * wave + i16, R[it][r]);
         }
     }
     if (STORE && !back && n + 1 == chunks) break;  // the end is not read
-    const float all = s.g.all;
+    if (B == 2 && n + 1 < chunks) put(n + 1);
+    const float all = gt.all;
     total *= all;
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt)
@@ -313,8 +299,8 @@ static __global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int at = 32 * kb + 16 * h + 4 * g;
-        const f32x4 e = *reinterpret_cast<const f32x4*>(back ? &s.g.eg[at] : &s.g.et[at]);
-        const f32x4 be = *reinterpret_cast<const f32x4*>(&s.g.beta[at]);
+        const f32x4 e = *reinterpret_cast<const f32x4*>(back ? &gt.eg[at] : &gt.et[at]);
+        const f32x4 be = *reinterpret_cast<const f32x4*>(&gt.beta[at]);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           o[4 * h + r] = a.scale * e[r] * d[kb][4 * h + r];
@@ -324,12 +310,12 @@ static __global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 
       }
       Split<T, TS> wf;
       if (DELTA || !back) {
-        wf.set(f);
+        wf = split<T, TS>(f, minus);
 #pragma unroll
         for (int k4 = 0; k4 < KT; k4 += 4) {
           Frag kf[4];
 #pragma unroll
-          for (int x = 0; x < 4; ++x) kf[x] = M::cols(cols_at<T, false>(s.k, LK, 32 * kb, 16 * (k4 + x), lane), LK);
+          for (int x = 0; x < 4; ++x) kf[x] = TK::cols(sK, 32 * kb, 16 * (k4 + x), lane);
 #pragma unroll
           for (int k = TS - 1; k >= 0; --k)
 #pragma unroll
@@ -337,18 +323,22 @@ static __global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 
         }
       }
       if (back) {
-        wf.set(o);
+        wf = split<T, TS>(o, minus);
 #pragma unroll
         for (int k4 = 0; k4 < KT; k4 += 4) {
           Frag qf[4];
 #pragma unroll
-          for (int x = 0; x < 4; ++x) qf[x] = M::cols(cols_at<T, false>(s.q, LK, 32 * kb, 16 * (k4 + x), lane), LK);
+          for (int x = 0; x < 4; ++x) qf[x] = TK::cols(sQ, 32 * kb, 16 * (k4 + x), lane);
 #pragma unroll
           for (int k = TS - 1; k >= 0; --k)
 #pragma unroll
             for (int x = 0; x < 4; ++x) S[k4 + x] = M::mma(qf[x], wf.t[k], S[k4 + x]);
         }
       }
+    }
+    if (B == 1) {
+      __syncthreads();  // the tiles are no longer read
+      if (n + 1 < chunks) put(n + 1);
     }
   }
   if (!STORE) {
@@ -357,7 +347,7 @@ static __global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt) *reinterpret_cast<f32x4*>(p + 16 * kt) = S[kt];
       // once, so that the same call gives the same bits: forward but for a last segment
-      if (!DELTA && tid == 0 && v0 == 0 && back == sg.last) a.seg_decay[(long)un.slot * a.v_heads + hv] = total;
+      if (!DELTA && tid == 0 && back == sg.last) a.seg_decay[(long)un.slot * a.v_heads + hv] = total;
       return;
     }
     if constexpr (DELTA) {
@@ -374,26 +364,23 @@ static __global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 
           f[r] = S[2 * kb][r];
           f[4 + r] = S[2 * kb + 1][r];
         }
-        Split<T, TS> x;
-        x.set(f);
-        put_split<T, TS>(out, NF + (v0 / 16 + wave) * KB + kb, x, lane);
+        const auto x = split<T, TS>(f, minus);
+        put_split<T, TS>(out, NF + wave * KB + kb, x, lane);
       }
     }
-    float* const sm = reinterpret_cast<float*>(&s);  // [64 columns][LM]
-    static_assert(sizeof(L) >= 64 * LM * 4, "the matrix's columns fit");
+    float* const sm = reinterpret_cast<float*>(&s);  // [K columns][LM]
+    static_assert(sizeof(L) >= K * LM * 4, "the matrix's columns fit");
     __syncthreads();
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt) *reinterpret_cast<f32x4*>(sm + (16 * wave + i16) * LM + 16 * kt + 4 * g) = S[kt];
     __syncthreads();
 #pragma unroll
-    for (int n = 0; n < KT / 2; ++n) {
-      const int id = wave * (KT / 2) + n, kt = id >> 1, jl = id & 1;
+    for (int jb = 0; jb < KB; ++jb) {  // a wave for 16 rows
       float f[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = sm[(32 * jl + 4 * g + (e < 4 ? e : 12 + e)) * LM + 16 * kt + i16];
-      Split<T, TS> x;
-      x.set(f);
-      put_split<T, TS>(out, kt * KB + v0 / 32 + jl, x, lane);
+      for (int e = 0; e < 8; ++e) f[e] = sm[(32 * jb + 4 * g + (e < 4 ? e : 12 + e)) * LM + 16 * wave + i16];
+      const auto x = split<T, TS>(f, minus);
+      put_split<T, TS>(out, wave * KB + jb, x, lane);
     }
     }
     return;
@@ -408,49 +395,65 @@ static __global__ void __launch_bounds__(256, sizeof(typename Mat<T>::E) == 4 ? 
 
 // Each sequence's segments in order (backward: from the last): what a segment adds is
 // replaced by the state (the gradient) it starts from, S <- M S + N.  The delta rule:
-// a wave for 16 columns, as in the recurrence.
+// a wave for 16 columns, as in the recurrence, 64 columns a workgroup; the matrix of a
+// segment is on its way while the one before is worked on.
 template <typename T, int K>
-static __global__ void __launch_bounds__(256) mix_combine_kernel(const MixBwdArgs b) {
+static __global__ void __launch_bounds__(256, 1) mix_combine_kernel(const MixBwdArgs b) {
   typedef Mat<T> M;
   typedef typename M::Frag Frag;
   constexpr int TS = M::kTerms, KT = K / 16, KB = K / 32, NF = KT * KB;
+  constexpr int PIECES = NF * TS * 64 * sizeof(Frag) / 16, N = PIECES / 256;
+  __shared__ __attribute__((aligned(16))) u32x4 sM[PIECES];
   const MixArgs& a = b.m;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const bool back = (int)blockIdx.x >= b.dir_blocks, both = a.seg_grad != nullptr;
   const int id = back ? blockIdx.x - b.dir_blocks : blockIdx.x;
-  const int hv = id / a.slices % a.v_heads, v0 = id % a.slices * 64, seq = id / a.slices / a.v_heads;
+  const int hv = id / (K / 64) % a.v_heads, v0 = id % (K / 64) * 64, seq = id / (K / 64) / a.v_heads;
   const SeqSpan sp = seq_span(a.cu, seq, a.seqs, a.tokens);
   const int segs = (sp.len + a.seg - 1) / a.seg;
   if (segs <= 1) return;
   const auto place = [&](long n) {
-    return ((n * a.v_heads + hv) * a.dv + v0 + 16 * wave + (lane & 15)) * K + 4 * (lane >> 4);
+    return ((n * a.v_heads + hv) * K + v0 + 16 * wave + (lane & 15)) * K + 4 * (lane >> 4);
   };
-  f32x4 S[KT];
-#pragma unroll
-  for (int kt = 0; kt < KT; ++kt) S[kt] = f32x4{0.f, 0.f, 0.f, 0.f};
   const int pool = a.init ? mix_slot(a, seq) : -1;
   const bool has = pool >= 0 && (!a.has_init || a.has_init[seq]);
-  const float* src = back ? b.dfinal : (has ? a.init : nullptr);
-  if (src) {
-    src += place(back ? seq : pool);
-#pragma unroll
-    for (int kt = 0; kt < KT; ++kt) S[kt] = *reinterpret_cast<const f32x4*>(src + 16 * kt);
-  }
   const long base = seg_base(a.cu, seq, a.seg, a.tokens);
-#pragma unroll 1
-  for (int n = 0; n < segs; ++n) {
+  const Minus minus;
+  u32x4 rm[N];
+  f32x4 add[KT], S[KT];
+  const auto fetch = [&](int n) {  // what segment n adds, and its matrix
     const long slot = base + (back ? segs - 1 - n : n);
-    float* const p = (back ? a.seg_grad : a.seg_state) + place(slot);
-    f32x4 add[KT];
-    if (n + 1 < segs) {
+    const u32x4* const m = static_cast<const u32x4*>(a.trans) +
+        ((slot * a.v_heads + hv) * (both ? 2 : 1) + back) * PIECES + tid;
 #pragma unroll
-      for (int kt = 0; kt < KT; ++kt) add[kt] = *reinterpret_cast<const f32x4*>(p + 16 * kt);
+    for (int i = 0; i < N; ++i) rm[i] = m[i * 256];
+    const float* const p = (back ? a.seg_grad : a.seg_state) + place(slot);
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt) add[kt] = *reinterpret_cast<const f32x4*>(p + 16 * kt);
+  };
+  fetch(0);
+  const float* src = back ? b.dfinal : (has ? a.init : nullptr);
+  if (src) src += place(back ? seq : pool);
+#pragma unroll
+  for (int kt = 0; kt < KT; ++kt)
+    S[kt] = src ? *reinterpret_cast<const f32x4*>(src + 16 * kt) : f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+  for (int n = 0;; ++n) {
+    const long slot = base + (back ? segs - 1 - n : n);
+    f32x4 acc[KT];
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt) acc[kt] = add[kt];
+    if (n + 1 < segs) {
+      __syncthreads();  // the last matrix is no longer read
+#pragma unroll
+      for (int i = 0; i < N; ++i) sM[i * 256 + tid] = rm[i];
+      if (n + 2 < segs) fetch(n + 1);
+      __syncthreads();
     }
+    float* const p = (back ? a.seg_grad : a.seg_state) + place(slot);
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt) *reinterpret_cast<f32x4*>(p + 16 * kt) = S[kt];
     if (n + 1 == segs) break;
-    const char* const tr = static_cast<const char*>(a.trans) +
-        ((slot * a.v_heads + hv) * (both ? 2 : 1) + back) * (NF * TS * 64 * sizeof(Frag));
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb) {
       float f[8];
@@ -459,14 +462,14 @@ static __global__ void __launch_bounds__(256) mix_combine_kernel(const MixBwdArg
         f[r] = S[2 * kb][r];
         f[4 + r] = S[2 * kb + 1][r];
       }
-      Split<T, TS> x;
-      x.set(f);
+      const auto x = split<T, TS>(f, minus);
 #pragma unroll
-      for (int kt = 0; kt < KT; ++kt)
-        add[kt] = mma_split<T, TS, TS>(split_at<T, TS>(tr, kt * KB + kb, lane), x, add[kt]);
+      for (int k4 = 0; k4 < KT; k4 += 4)
+        mma_many<T, TS, TS, 4>([&](int n, int k) { return frag_at<T>(sM, ((k4 + n) * KB + kb) * TS + k, lane); }, x,
+                               acc + k4);
     }
 #pragma unroll
-    for (int kt = 0; kt < KT; ++kt) S[kt] = add[kt];
+    for (int kt = 0; kt < KT; ++kt) S[kt] = acc[kt];
   }
 }
 
@@ -517,32 +520,39 @@ static __global__ void __launch_bounds__(256) mix_combine_decay_kernel(const Mix
 
 // Whether those launches hold fewer than 2^32 threads each.
 static inline bool segments_fit(const MixArgs& a, int dk) {
-  const long dir = mix_grid(a.slots, a.k_heads, (long)a.vpk * a.slices);
-  const long tr = mix_grid(a.slots, a.k_heads, (long)a.vpk * (dk / 64));
-  return grid_fits(2 * dir + tr, 256) && grid_fits(2L * a.seqs * a.v_heads * (dk * a.dv / 1024), 256);
+  const long dir = mix_grid(a.slots, a.k_heads, a.vpk);
+  return grid_fits(3 * dir, 512) && grid_fits(2L * a.seqs * a.v_heads * (dk * a.dv / 1024), 256);
+}
+
+template <typename T, bool BOTH>
+static const void* pick_segments(int dk, int dv, bool delta) {
+  if (delta)
+    return dk == 64 ? reinterpret_cast<const void*>(&mix_states_kernel<T, 64, 64, true, false, BOTH>)
+                    : reinterpret_cast<const void*>(&mix_states_kernel<T, 128, 128, true, false, BOTH>);
+  if (dk == 64)
+    return dv == 64 ? reinterpret_cast<const void*>(&mix_states_kernel<T, 64, 64, false, false, BOTH>)
+                    : reinterpret_cast<const void*>(&mix_states_kernel<T, 64, 128, false, false, BOTH>);
+  return dv == 64 ? reinterpret_cast<const void*>(&mix_states_kernel<T, 128, 64, false, false, BOTH>)
+                  : reinterpret_cast<const void*>(&mix_states_kernel<T, 128, 128, false, false, BOTH>);
 }
 
 // The launches in front of a call whose tokens may take several segments.
-template <typename T, bool DELTA, bool BOTH>
-static int launch_segments(MixBwdArgs b, int dk, hipStream_t stream) {
+template <typename T, bool BOTH>
+static int launch_segments(MixBwdArgs b, int dk, bool delta, hipStream_t stream) {
   const MixArgs& a = b.m;
-  const long dir = mix_grid(a.slots, a.k_heads, (long)a.vpk * a.slices);
-  const long tr = DELTA ? mix_grid(a.slots, a.k_heads, (long)a.vpk * (dk / 64)) : 0;
-  const long cdir = DELTA ? (long)a.seqs * a.v_heads * a.slices : (long)a.seqs * a.v_heads * (dk * a.dv / 1024);
-  const long grid = (BOTH ? 2 : 1) * dir + tr, cgrid = (BOTH ? 2 : 1) * cdir;
+  const long dir = mix_grid(a.slots, a.k_heads, a.vpk);
+  const long cdir = (long)a.seqs * a.v_heads * (delta ? dk / 64 : dk * a.dv / 1024);
   b.dir_blocks = (int)dir;
   b.elems = dk * a.dv;
-  const void* fn = dk == 64 ? reinterpret_cast<const void*>(&mix_states_kernel<T, 64, DELTA, false, BOTH>)
-                            : reinterpret_cast<const void*>(&mix_states_kernel<T, 128, DELTA, false, BOTH>);
-  const int rc = launch_kernel(fn, (unsigned)grid, 256, 0, stream, b);
+  const int rc = launch_kernel(pick_segments<T, BOTH>(dk, a.dv, delta), (unsigned)(((BOTH ? 2 : 1) + delta) * dir),
+                               4 * a.dv, 0, stream, b);
   if (rc) return rc;
   b.dir_blocks = (int)cdir;
-  if (DELTA)
+  const void* fn = reinterpret_cast<const void*>(&mix_combine_decay_kernel);
+  if (delta)
     fn = dk == 64 ? reinterpret_cast<const void*>(&mix_combine_kernel<T, 64>)
                   : reinterpret_cast<const void*>(&mix_combine_kernel<T, 128>);
-  else
-    fn = reinterpret_cast<const void*>(&mix_combine_decay_kernel);
-  return launch_kernel(fn, (unsigned)cgrid, 256, 0, stream, b);
+  return launch_kernel(fn, (unsigned)((BOTH ? 2 : 1) * cdir), 256, 0, stream, b);
 }
 
 }  // namespace rssm
