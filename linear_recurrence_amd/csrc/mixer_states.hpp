@@ -33,7 +33,7 @@ struct StatesLds {
   static constexpr int kFrag = sizeof(typename Mat<T>::Frag), TS = Mat<T>::kTerms;
   static constexpr int TF = 6 * TS * 64 * kFrag / 16;  // 16-byte pieces of T or its transpose
   // fp32 with both directions' tiles twice would not fit 160 KB
-  static constexpr int B = BOTH && sizeof(E) == 4 ? 1 : 2;
+  static constexpr int B = BOTH && sizeof(E) == 2 ? 2 : 1;
   __attribute__((aligned(16))) E k[B][Tile<T, K>::SIZE];
   __attribute__((aligned(16))) E v[B][Tile<T, V>::SIZE];  // V forward, dO backward
   __attribute__((aligned(16))) u32x4 t[DELTA ? B : 1][DELTA ? TF : 1];
@@ -51,7 +51,7 @@ struct StatesLds {
 // its starting state is multiplied by, as first operands: rows of it and (BOTH) of its
 // transpose, which gradients go through.
 template <typename T, int K, int V, bool DELTA, bool STORE, bool BOTH>
-static __global__ void __launch_bounds__(4 * V, 2) mix_states_kernel(const MixBwdArgs b) {
+static __global__ void __launch_bounds__(4 * V, BOTH || sizeof(typename Mat<T>::E) == 4 ? 2 : 4) mix_states_kernel(const MixBwdArgs b) {
   typedef Mat<T> M;
   typedef typename M::E E;
   typedef typename M::Frag Frag;
@@ -60,7 +60,12 @@ static __global__ void __launch_bounds__(4 * V, 2) mix_states_kernel(const MixBw
   typedef Tile<T, V> TV;
   static_assert(!DELTA || K == V, "the transition's columns are as many as V's");
   constexpr int TS = M::kTerms, KT = K / 16, KB = K / 32, TF = L::TF, W = V / 16, TH = 64 * W, B = L::B;
-  __shared__ L s;
+  constexpr bool kAhead = BOTH || !DELTA || sizeof(E) == 4;
+  __shared__ union {
+    L t;
+    float m[STORE || !DELTA ? 1 : K * (K + 4)];
+  } u;
+  L& s = u.t;
   const MixArgs& a = b.m;
   const int tid = threadIdx.x, lane = tid & 63, i16 = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -156,7 +161,7 @@ static __global__ void __launch_bounds__(4 * V, 2) mix_states_kernel(const MixBw
       for (int kt = 0; kt < KT; ++kt) *reinterpret_cast<f32x4*>(p + 16 * kt) = S[kt];
     }
     __syncthreads();
-    if (n + 1 < chunks) fetch(back ? c - 1 : c + 1);
+    if (kAhead && n + 1 < chunks) fetch(back ? c - 1 : c + 1);
     // K S (or K dS'), rows t; backward: this wave's tiles of q_i.k_j, rows i
     f32x4 R[4], P[2], P2[2];
 #pragma unroll
@@ -338,7 +343,10 @@ static __global__ void __launch_bounds__(4 * V, 2) mix_states_kernel(const MixBw
     }
     if (B == 1) {
       __syncthreads();  // the tiles are no longer read
-      if (n + 1 < chunks) put(n + 1);
+      if (n + 1 < chunks) {
+        if (!kAhead) fetch(back ? c - 1 : c + 1);
+        put(n + 1);
+      }
     }
   }
   if (!STORE) {
@@ -368,8 +376,7 @@ static __global__ void __launch_bounds__(4 * V, 2) mix_states_kernel(const MixBw
         put_split<T, TS>(out, NF + wave * KB + kb, x, lane);
       }
     }
-    float* const sm = reinterpret_cast<float*>(&s);  // [K columns][LM]
-    static_assert(sizeof(L) >= K * LM * 4, "the matrix's columns fit");
+    float* const sm = u.m;  // [K columns][LM]
     __syncthreads();
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt) *reinterpret_cast<f32x4*>(sm + (16 * wave + i16) * LM + 16 * kt + 4 * g) = S[kt];
