@@ -36,11 +36,11 @@ struct MainLds {
   // fragments of 32 columns of dO, D (or V) and dX for the four blocks of 16 tokens
   static constexpr int kStage = 4 * (1 + TD + (DELTA ? TS : 0)) * kFrag;
   static constexpr int oD = 4 * kFrag, oX = oD + 4 * TD * kFrag;
-  static constexpr int kTri = 12 * TO * kFrag;  // N, or L: lower and upper triangle
-  static constexpr int kArea = 2 * kStage > (DELTA ? 2 : 1) * kTri ? 2 * kStage : (DELTA ? 2 : 1) * kTri;
+  static constexpr int kTri = TO * Tile<T, 64>::SIZE;  // N, or L, as terms
+  static constexpr int kTris = (DELTA ? 2 : 1) * kTri * (int)sizeof(E);
   __attribute__((aligned(16))) E k[Tile<T, K>::SIZE];
   __attribute__((aligned(16))) E q[Tile<T, K>::SIZE];
-  __attribute__((aligned(16))) char area[kArea];
+  __attribute__((aligned(16))) char area[2 * kStage > kTris ? 2 * kStage : kTris];
   ChunkGates g;
   float wrow[10][16], wcol[10][16], brow[10][16];  // by tile i (i + 1) / 2 + j
   float give[W][kQ], back[W][kQ], take[W][kQ];
@@ -49,19 +49,31 @@ struct MainLds {
 
 // Everything that stays within a chunk.  A wave owns 16 of the K columns of dq and dk;
 // the columns of V are taken 32 at a time: each wave splits its share of D and dX for
-// all of them, and meanwhile reads its columns of S and dS'.
+// all of them and its own columns of S and dS', whose loads (the next 32 columns', or
+// the next head's) are on their way during the products.  The 64x64 products dO D^T and
+// dX D^T are held by tiles, and cross LDS once as rows of N and L, which then are read
+// by rows and, transposing, by columns.
 template <typename T, int K, bool DELTA>
-__global__ void __launch_bounds__(4 * K) mix_main_kernel(const MixBwdArgs b) {
+__global__ void __launch_bounds__(4 * K, 2) mix_main_kernel(const MixBwdArgs b) {
   typedef Mat<T> M;
   typedef typename M::E E;
   typedef typename M::Frag Frag;
   typedef MainLds<T, K, DELTA> L;
   typedef Tile<T, K> TK;
+  typedef Tile<T, 64> TN;
   constexpr int TS = L::TS, TO = L::TO, TD = L::TD, KB = K / 32, W = L::W, TH = 64 * W;
-  constexpr int JOBS = 8 / W;  // sets of tiles a wave
+  constexpr int JOBS = (10 + W - 1) / W;  // 16x16 tiles of the lower triangle a wave
+  constexpr int SETS = 8 / W;             // blocks of rows that a wave splits: of D (V), of dX and dO
   __shared__ L s;
   const MixArgs& a = b.m;
-  const int tid = threadIdx.x, lane = tid & 63, i16 = lane & 15, g = lane >> 4;
+  const int tid = threadIdx.x;
+  int lane = tid & 63, i16 = lane & 15, g = lane >> 4;
+  // what is worked out from the lane is worked out again, not kept through the loops
+  const auto again = [&]() {
+    forget(lane);
+    i16 = lane & 15;
+    g = lane >> 4;
+  };
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int slot = blockIdx.x / a.k_heads, hk = blockIdx.x % a.k_heads;
   const Segment sg = find_segment(a.cu, a.seqs, a.tokens, kQ, slot);
@@ -80,153 +92,101 @@ __global__ void __launch_bounds__(4 * K) mix_main_kernel(const MixBwdArgs b) {
     x.put(s.k, rows, tid);
     y.put(s.q, rows, tid);
   }
-  __syncthreads();
-  // This wave's tiles of the 64x64 products: two of one fragment and, in half of the
-  // sets, the only one of another.  Sets below 4 hold rows j, columns i of block (i, j)
-  // (a first operand's rows i), the others rows i, columns j.
-  int bi[JOBS][3], bj[JOBS][3], frag[JOBS][2];
-  bool upper[JOBS], extra[JOBS];
-  f32x4 qk[JOBS][3], kk[JOBS][3];
-#pragma unroll
-  for (int u = 0; u < JOBS; ++u) {
-    const int set = wave + u * W, n = set & 3;
-    upper[u] = set >= 4;
-    extra[u] = n < 2;
-    // lower: (3, 0) (3, 1) (2, 0) (1, 0), then (0, 0) (2, 1)
-    const int it = n < 2 ? 3 : (n == 2 ? 2 : 1), kb = n == 1, ie = n ? 2 : 0, ke = n;
-    frag[u][0] = low_frag(it, kb);  // an upper one's mirror image has the same number
-    frag[u][1] = low_frag(ie, ke & 1);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int other = 2 * kb + h;
-      bi[u][h] = upper[u] ? 3 - other : it;
-      bj[u][h] = upper[u] ? 3 - it : other;
-    }
-    if (upper[u]) {  // columns 2 kb, 2 kb + 1 in order
-      const int x = bi[u][0];
-      bi[u][0] = bi[u][1];
-      bi[u][1] = x;
-    }
-    bi[u][2] = bj[u][2] = upper[u] ? 3 - ie : ie;
-#pragma unroll
-    for (int e = 0; e < 3; ++e) {
-      qk[u][e] = kk[u][e] = f32x4{0.f, 0.f, 0.f, 0.f};
-      if (e == 2 && !extra[u]) continue;
-#pragma unroll
-      for (int x = 0; x < KB; ++x) {
-        const Frag ki = TK::rows_c(s.k, bi[u][e], 32 * x, lane);
-        const Frag kj = TK::rows_c(s.k, bj[u][e], 32 * x, lane);
-        const Frag qi = TK::rows_c(s.q, bi[u][e], 32 * x, lane);
-        if (upper[u]) {
-          qk[u][e] = M::mma(qi, kj, qk[u][e]);
-          if (DELTA) kk[u][e] = M::mma(ki, kj, kk[u][e]);
-        } else {
-          qk[u][e] = M::mma(kj, qi, qk[u][e]);
-          if (DELTA) kk[u][e] = M::mma(kj, ki, kk[u][e]);
-        }
-      }
-    }
-  }
   f32x4 dq[4], dk[4];  // rows t = 16 t + 4g + r, column 16 wave + i16
 #pragma unroll
   for (int t = 0; t < 4; ++t) dq[t] = dk[t] = f32x4{0.f, 0.f, 0.f, 0.f};
   const Minus minus;
-  const int kcol = 16 * wave + i16, blocks = a.dv / 32;
+  const int blocks = a.dv / 32;
+  // What the next 32 columns of V need, on its way: this wave's columns of the states, and
+  // its rows (set 0: D, or V of linear attention; set 1: dX, dO and V)
+  float fs[8], fg[8];
+  RawK<float, 8> rx[SETS];
+  RawK<T, 8> ro[SETS], rv;
+  const auto fetch = [&](int hx, int vb) {
+    const int kcol = 16 * wave + i16, trow = 16 * (wave & 3) + i16;
+    const long tok = t0 + (trow < rows ? trow : 0);
+    const long hv = hk * a.vpk + hx, at = (long)slot * a.v_heads + hv;
+    const int vc = 32 * vb + 8 * g;
+    const float* ps = b.state + (at * a.dv + vc) * K + kcol;
+    const float* pg = b.grad + (at * a.dv + vc) * K + kcol;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      fs[e] = ps[e * K];
+      fg[e] = pg[e * K];
+    }
+#pragma unroll
+    for (int u = 0; u < SETS; ++u) {
+      const bool second = W == 4 ? u == 1 : wave >= 4;
+      if (DELTA) rx[u].load(second ? b.dX : b.D, (at * kQ + trow) * a.dv + vc, 8);
+      ro[u].load(second ? b.dout : a.v, tok * (second ? b.do_stride : a.v_stride) + hv * a.dv + vc, 8);
+    }
+    if (DELTA) rv.load(a.v, tok * a.v_stride + hv * a.dv + vc, 8);
+  };
+  fetch(0, 0);
 #pragma unroll 1
   for (int hx = 0; hx < a.vpk; ++hx) {
     const int hv = hk * a.vpk + hx;
     const long at = (long)slot * a.v_heads + hv;
-    if (wave == W - 1) {
-      GateLoad ld;
-      ld.start(a, t0, hv, DELTA);
-      ld.fetch(rows, lane);
-      s.g.set(ld.log_g(rows, lane), ld.beta(rows, lane), lane);
-    }
-    f32x4 into[4], back[4], out[4], dp[JOBS][3], dx[JOBS][3];
+    GateLoad ld;
+    ld.start(a, t0, hv, DELTA);
+    ld.fetch(rows, lane);
+    const int brow = 16 * (wave & 3) + i16;
+    const float beta = DELTA ? a.beta[(t0 + (brow < rows ? brow : 0)) * a.v_heads + hv] : 0.f;
+    f32x4 into[4], back[4], out[4], dp[JOBS], dx[JOBS];
 #pragma unroll
     for (int t = 0; t < 4; ++t) into[t] = back[t] = out[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int u = 0; u < JOBS; ++u)
-#pragma unroll
-      for (int e = 0; e < 3; ++e) dp[u][e] = dx[u][e] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int u = 0; u < JOBS; ++u) dp[u] = dx[u] = f32x4{0.f, 0.f, 0.f, 0.f};
     float xv = 0.f, dot = 0.f;
-    const float beta = DELTA && 16 * (wave & 3) + i16 < rows
-                           ? a.beta[(t0 + 16 * (wave & 3) + i16) * a.v_heads + hv] : 0.f;
 #pragma unroll 1
     for (int vb = 0; vb < blocks; ++vb) {
+      again();
       char* const area = s.area + (vb & 1) * L::kStage;
-      const int vc = 32 * vb + 8 * g;
-      // this wave's columns of the states
-      float fs[8], fg[8];
-      {
-        const float* ps = b.state + (at * a.dv + vc) * K + kcol;
-        const float* pg = b.grad + (at * a.dv + vc) * K + kcol;
+      const int vc = 32 * vb + 8 * g, trow = 16 * (wave & 3) + i16;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          fs[e] = ps[(long)e * K];
-          fg[e] = pg[(long)e * K];
-        }
-      }
+      for (int u = 0; u < SETS; ++u) {
+        const bool second = W == 4 ? u == 1 : wave >= 4;
+        const int tb = wave & 3;
+        float o[8], f[8];
+        ro[u].get(o);
 #pragma unroll
-      for (int u = 0; u < JOBS; ++u) {
-        const int set = wave + u * W, tb = set & 3, t = 16 * tb + i16;
-        if (set < 4) {
-          if (DELTA) {
-            float f[8];
-            Vec8<float>::load(b.D, (at * kQ + t) * a.dv + vc, f);
-            const auto d = split<T, TS>(f, minus);
-            put_split<T, TS>(area + L::oD, tb, d, lane);
-          } else {
-            float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            if (t < rows) Vec8<T>::load(a.v, (t0 + t) * a.v_stride + (long)hv * a.dv + vc, f);
-            const auto d = split<T, 1>(f, minus);
-            put_split<T, 1>(area + L::oD, tb, d, lane);
+        for (int e = 0; e < 8; ++e) o[e] = trow < rows ? o[e] : 0.f;
+        if (DELTA) rx[u].get(f);
+        if (second || !DELTA)
+          put_split<T, 1>(area + (second ? 0 : L::oD), tb, split<T, 1>(o, minus), lane);
+        if (DELTA) put_split<T, TS>(area + (second ? L::oX : L::oD), tb, split<T, TS>(f, minus), lane);
+        if (DELTA && second && trow < rows) {
+          float v[8], w[8];
+          rv.get(v);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            xv = fmaf(f[e], v[e], xv);
+            w[e] = beta * f[e];
           }
-        } else {
-          float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, f[8], v[8];
-          if (t < rows) Vec8<T>::load(b.dout, (t0 + t) * b.do_stride + (long)hv * a.dv + vc, o);
-          const auto d = split<T, 1>(o, minus);
-          put_split<T, 1>(area, tb, d, lane);
-          if (DELTA) {
-            Vec8<float>::load(b.dX, (at * kQ + t) * a.dv + vc, f);
-            if (t < rows) {
-              Vec8<T>::load(a.v, (t0 + t) * a.v_stride + (long)hv * a.dv + vc, v);
-              float w[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                xv = fmaf(f[e], v[e], xv);
-                w[e] = beta * f[e];
-              }
-              Vec8<T>::store(b.dv, ((t0 + t) * a.v_heads + hv) * a.dv + vc, w);
-            }
-            const auto x = split<T, TS>(f, minus);
-            put_split<T, TS>(area + L::oX, tb, x, lane);
-          }
+          Vec8<T>::store(b.dv, ((t0 + trow) * a.v_heads + hv) * a.dv + vc, w);
         }
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) dot = fmaf(fs[e], fg[e], dot);
       const auto ss = split<T, TS>(fs, minus), sd = split<T, TS>(fg, minus);
+      if (vb + 1 < blocks) fetch(hx, vb + 1);
+      else if (hx + 1 < a.vpk) fetch(hx + 1, 0);
       __syncthreads();
+      again();
       mma_many<T, 1, TS, 4>([&](int t, int) { return frag_at<T>(area, t, lane); }, ss, into);
       mma_many<T, TD, TS, 4>([&](int t, int k) { return frag_at<T>(area + L::oD, t * TD + k, lane); }, sd, out);
       if (DELTA)
         mma_many<T, TS, TS, 4>([&](int t, int k) { return frag_at<T>(area + L::oX, t * TS + k, lane); }, ss, back);
+      // rows j, columns i of tile (i, j)
 #pragma unroll
-      for (int u = 0; u < JOBS; ++u)
-#pragma unroll
-        for (int e = 0; e < 3; ++e) {
-          if (e == 2 && !extra[u]) continue;
-          const Frag o = frag_at<T>(area, bi[u][e], lane);
-          const auto d = split_at<T, TD>(area + L::oD, bj[u][e], lane);
-          if (upper[u]) dp[u][e] = d.b_times(o, dp[u][e]);
-          else dp[u][e] = d.a_times(o, dp[u][e]);
-          if (DELTA) {
-            const auto x = split_at<T, TS>(area + L::oX, bi[u][e], lane);
-            if (upper[u]) dx[u][e] = mma_split<T, TS, TD>(x, d, dx[u][e]);
-            else dx[u][e] = mma_split<T, TD, TS>(d, x, dx[u][e]);
-          }
+      for (int u = 0; u < JOBS; ++u) {
+        const int n = wave + u * W, ti = n < 1 ? 0 : (n < 3 ? 1 : (n < 6 ? 2 : 3)), tj = n - ti * (ti + 1) / 2;
+        if (n < 10) {
+          const auto d = split_at<T, TD>(area + L::oD, tj, lane);
+          dp[u] = d.a_times(frag_at<T>(area, ti, lane), dp[u]);
+          if (DELTA) dx[u] = mma_split<T, TD, TS>(d, split_at<T, TS>(area + L::oX, ti, lane), dx[u]);
         }
+      }
     }
     if (DELTA) {
       xv += __shfl_xor(xv, 16, 64);
@@ -236,71 +196,82 @@ __global__ void __launch_bounds__(4 * K) mix_main_kernel(const MixBwdArgs b) {
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) dot += __shfl_xor(dot, o, 64);
     if (lane == 0) s.dot[wave] = dot;
-    __syncthreads();  // the last stage is no longer read
-    // N and L as fragments, and the sums of w's rows and columns
+    if (wave == W - 1) s.g.set(ld.log_g(rows, lane), ld.beta(rows, lane), lane);
+    __syncthreads();  // the stages are no longer read
+    again();
+    // N and L by rows i, and the sums of w's rows and columns
+    E* const sN = reinterpret_cast<E*>(s.area);
+    E* const sL = sN + L::kTri;
 #pragma unroll
     for (int u = 0; u < JOBS; ++u) {
-      float fn[2][8], fl[2][8];
+      const int tile = wave + u * W, ti = tile < 1 ? 0 : (tile < 3 ? 1 : (tile < 6 ? 2 : 3)),
+                tj = tile - ti * (ti + 1) / 2;
+      if (tile < 10) {
+        f32x4 qk = {0.f, 0.f, 0.f, 0.f}, kk = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int h = 0; h < 8; ++h) fn[1][h] = fl[1][h] = 0.f;
-#pragma unroll
-      for (int e = 0; e < 3; ++e) {
-        if (e == 2 && !extra[u]) continue;
-        const int I = 16 * bi[u][e], J = 16 * bj[u][e], tile = bi[u][e] * (bi[u][e] + 1) / 2 + bj[u][e];
-        float wr = 0.f, br = 0.f, wc[4];
+        for (int x = 0; x < KB; ++x) {
+          const Frag kj = TK::rows_c(s.k, tj, 32 * x, lane);
+          qk = M::mma(kj, TK::rows_c(s.q, ti, 32 * x, lane), qk);
+          if (DELTA) kk = M::mma(kj, TK::rows_c(s.k, ti, 32 * x, lane), kk);
+        }
+        const int i = 16 * ti + i16;
+        const float2 gi = s.g.G[i];
+        const float be = s.g.beta[i];
+        float n[4], l[4], wc[4], wr = 0.f, br = 0.f;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const int i = I + (upper[u] ? 4 * g + r : i16), j = J + (upper[u] ? i16 : 4 * g + r);
-          const float c = exp2_f32(gap2(s.g.G[i], s.g.G[j]));
-          const float n = i >= j ? a.scale * c * dp[u][e][r] : 0.f;
-          const float m = DELTA && i > j ? c * dx[u][e][r] : 0.f;
-          const float l = DELTA ? -s.g.beta[i] * m : 0.f;
-          float w = i > j ? qk[u][e][r] * n : 0.f;
-          if (DELTA) w = i > j ? fmaf(kk[u][e][r], l, w) : 0.f;
-          const int put = e == 2 ? 1 : 0, h = e == 2 ? (upper[u] ? 4 : 0) : 4 * e;
-          if (e == 2) {
-            fn[put][r] = upper[u] ? 0.f : n;
-            fn[put][4 + r] = upper[u] ? n : 0.f;
-            fl[put][r] = upper[u] ? 0.f : l;
-            fl[put][4 + r] = upper[u] ? l : 0.f;
-          } else {
-            fn[put][h + r] = n;
-            fl[put][h + r] = l;
+          const int j = 16 * tj + 4 * g + r;
+          const float c = exp2_f32(gap2(gi, s.g.G[j]));
+          n[r] = i >= j ? a.scale * c * dp[u][r] : 0.f;
+          wc[r] = i > j ? qk[r] * n[r] : 0.f;
+          if (DELTA) {
+            const float m = i > j ? c * dx[u][r] : 0.f;
+            l[r] = -be * m;
+            wc[r] = i > j ? fmaf(kk[r], l[r], wc[r]) : 0.f;
+            br = i > j ? fmaf(kk[r], m, br) : br;
           }
-          wr += w;
-          wc[r] = w;
-          if (DELTA && i > j) br = fmaf(kk[u][e][r], m, br);
+          wr += wc[r];
         }
-        if (!upper[u]) {  // rows i in the lanes
 #pragma unroll
-          for (int o = 16; o < 64; o <<= 1) {
-            wr += __shfl_xor(wr, o, 64);
-            br += __shfl_xor(br, o, 64);
-          }
-          if (g == 0) {
-            s.wrow[tile][i16] = wr;
-            s.brow[tile][i16] = br;
-          }
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-#pragma unroll
-            for (int o = 1; o < 16; o <<= 1) wc[r] += __shfl_xor(wc[r], o, 64);
-            if (i16 == 0) s.wcol[tile][4 * g + r] = wc[r];
-          }
+        for (int o = 16; o < 64; o <<= 1) {
+          wr += __shfl_xor(wr, o, 64);
+          if (DELTA) br += __shfl_xor(br, o, 64);
         }
-      }
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        if (e == 1 && !extra[u]) continue;
-        const int n = (upper[u] ? 6 : 0) + frag[u][e];
-        const auto x = split<T, TO>(fn[e], minus);
-        put_split<T, TO>(s.area, n, x, lane);
-        if (DELTA) {
-          put_split<T, TO>(s.area + L::kTri, n, split<T, TO>(fl[e], minus), lane);
+        if (g == 0) {
+          s.wrow[tile][i16] = wr;
+          if (DELTA) s.brow[tile][i16] = br;
         }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+#pragma unroll
+          for (int o = 1; o < 16; o <<= 1) wc[r] += __shfl_xor(wc[r], o, 64);
+          if (i16 == 0) s.wcol[tile][4 * g + r] = wc[r];
+        }
+        // four neighbours of row i, a term at a time; above the diagonal zeros
+        const auto put4 = [&](E* plane, float* v) {
+#pragma unroll
+          for (int k = 0; k < TO; ++k) {
+            const auto p = M::pack4(v);
+            *reinterpret_cast<typename M::Four*>(plane + k * TN::SIZE + TN::at(i, 16 * tj + 4 * g)) = p;
+            if (k + 1 < TO) {
+              float f[4];
+              M::unpack4(p, f);
+#pragma unroll
+              for (int r = 0; r < 4; ++r) v[r] -= f[r];
+            }
+            if (ti != tj) {
+              const float z[4] = {0.f, 0.f, 0.f, 0.f};
+              *reinterpret_cast<typename M::Four*>(plane + k * TN::SIZE + TN::at(16 * tj + i16, 16 * ti + 4 * g)) =
+                  M::pack4(z);
+            }
+          }
+        };
+        put4(sN, n);
+        if (DELTA) put4(sL, l);
       }
     }
     __syncthreads();
+    again();
     {
       Frag kf[2], qf[2];
       float gv[16], bk[16], tk[16];
@@ -337,23 +308,26 @@ __global__ void __launch_bounds__(4 * K) mix_main_kernel(const MixBwdArgs b) {
       Red::run(gv, lane);
       Red::run(tk, lane);
       if (DELTA) Red::run(bk, lane);
-      const int item = Red::item(0, lane), tok = 16 * (item >> 2) + 4 * g + (item & 3);
-      s.give[wave][tok] = gv[0];
-      s.take[wave][tok] = tk[0];
-      if (DELTA) s.back[wave][tok] = bk[0];
+      const int item = Red::item(0, lane), t16 = 16 * (item >> 2) + 4 * g + (item & 3);
+      s.give[wave][t16] = gv[0];
+      s.take[wave][t16] = tk[0];
+      if (DELTA) s.back[wave][t16] = bk[0];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
+      for (int k = TO - 1; k >= 0; --k)
 #pragma unroll
-        for (int kb = 0; kb <= t / 2; ++kb) {
-          dq[t] = split_at<T, TO>(s.area, low_frag(t, kb), lane).a_times(kf[kb], dq[t]);
-          if (DELTA) dk[t] = split_at<T, TO>(s.area + L::kTri, low_frag(t, kb), lane).a_times(kf[kb], dk[t]);
-        }
+        for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-        for (int kb = t / 2; kb < 2; ++kb) {
-          dk[t] = split_at<T, TO>(s.area, 6 + up_frag(t, kb), lane).a_times(qf[kb], dk[t]);
-          if (DELTA) dk[t] = split_at<T, TO>(s.area + L::kTri, 6 + up_frag(t, kb), lane).a_times(kf[kb], dk[t]);
-        }
-      }
+          for (int t = 0; t < 4; ++t) {
+            const E *const pn = sN + k * TN::SIZE, *const pl = sL + k * TN::SIZE;
+            if (kb <= t / 2) {
+              dq[t] = M::mma(TN::rows_d(pn, t, 32 * kb, lane), kf[kb], dq[t]);
+              if (DELTA) dk[t] = M::mma(TN::rows_d(pl, t, 32 * kb, lane), kf[kb], dk[t]);
+            }
+            if (kb >= t / 2) {
+              dk[t] = M::mma(TN::cols(pn, 32 * kb, 16 * t, lane), qf[kb], dk[t]);
+              if (DELTA) dk[t] = M::mma(TN::cols(pl, 32 * kb, 16 * t, lane), kf[kb], dk[t]);
+            }
+          }
     }
     __syncthreads();
     if (wave == 0 && b.dg) {  // one token a lane
@@ -402,7 +376,7 @@ __global__ void __launch_bounds__(4 * K) mix_main_kernel(const MixBwdArgs b) {
   for (int t = 0; t < 4; ++t)
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const int p = TK::at(16 * t + 4 * g + r, kcol);
+      const int p = TK::at(16 * t + 4 * g + r, 16 * wave + i16);
       Elt<T>::store1(s.q, p, dq[t][r]);
       Elt<T>::store1(s.k, p, dk[t][r]);
     }
