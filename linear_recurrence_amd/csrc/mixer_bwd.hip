@@ -102,18 +102,19 @@ __global__ void __launch_bounds__(4 * K, 2) mix_main_kernel(const MixBwdArgs b) 
   float fs[8], fg[8];
   RawK<float, 8> rx[SETS];
   RawK<T, 8> ro[SETS], rv;
-  const auto fetch = [&](int hx, int vb) {
-    const int kcol = 16 * wave + i16, trow = 16 * (wave & 3) + i16;
-    const long tok = t0 + (trow < rows ? trow : 0);
-    const long hv = hk * a.vpk + hx, at = (long)slot * a.v_heads + hv;
-    const int vc = 32 * vb + 8 * g;
-    const float* ps = b.state + (at * a.dv + vc) * K + kcol;
-    const float* pg = b.grad + (at * a.dv + vc) * K + kcol;
+  const auto fetch_states = [&](int hx, int vb) {
+    const long at = (long)slot * a.v_heads + hk * a.vpk + hx;
+    const long p = (at * a.dv + 32 * vb + 8 * g) * K + 16 * wave + i16;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      fs[e] = ps[e * K];
-      fg[e] = pg[e * K];
+      fs[e] = b.state[p + e * K];
+      fg[e] = b.grad[p + e * K];
     }
+  };
+  const auto fetch_rows = [&](int hx, int vb) {
+    const int trow = 16 * (wave & 3) + i16, vc = 32 * vb + 8 * g;
+    const long hv = hk * a.vpk + hx, at = (long)slot * a.v_heads + hv;
+    const long tok = t0 + (trow < rows ? trow : 0);
 #pragma unroll
     for (int u = 0; u < SETS; ++u) {
       const bool second = W == 4 ? u == 1 : wave >= 4;
@@ -122,7 +123,8 @@ __global__ void __launch_bounds__(4 * K, 2) mix_main_kernel(const MixBwdArgs b) 
     }
     if (DELTA) rv.load(a.v, tok * a.v_stride + hv * a.dv + vc, 8);
   };
-  fetch(0, 0);
+  fetch_states(0, 0);
+  fetch_rows(0, 0);
 #pragma unroll 1
   for (int hx = 0; hx < a.vpk; ++hx) {
     const int hv = hk * a.vpk + hx;
@@ -143,6 +145,12 @@ __global__ void __launch_bounds__(4 * K, 2) mix_main_kernel(const MixBwdArgs b) 
       again();
       char* const area = s.area + (vb & 1) * L::kStage;
       const int vc = 32 * vb + 8 * g, trow = 16 * (wave & 3) + i16;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) dot = fmaf(fs[e], fg[e], dot);
+      const auto ss = split<T, TS>(fs, minus), sd = split<T, TS>(fg, minus);
+      const int hn = vb + 1 < blocks ? hx : hx + 1, vn = vb + 1 < blocks ? vb + 1 : 0;
+      const bool more = hn < a.vpk;  // (behind the last there is the first again)
+      fetch_states(more ? hn : 0, vn);
 #pragma unroll
       for (int u = 0; u < SETS; ++u) {
         const bool second = W == 4 ? u == 1 : wave >= 4;
@@ -166,11 +174,7 @@ __global__ void __launch_bounds__(4 * K, 2) mix_main_kernel(const MixBwdArgs b) 
           Vec8<T>::store(b.dv, ((t0 + trow) * a.v_heads + hv) * a.dv + vc, w);
         }
       }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) dot = fmaf(fs[e], fg[e], dot);
-      const auto ss = split<T, TS>(fs, minus), sd = split<T, TS>(fg, minus);
-      if (vb + 1 < blocks) fetch(hx, vb + 1);
-      else if (hx + 1 < a.vpk) fetch(hx + 1, 0);
+      fetch_rows(more ? hn : 0, vn);
       __syncthreads();
       again();
       mma_many<T, 1, TS, 4>([&](int t, int) { return frag_at<T>(area, t, lane); }, ss, into);
@@ -193,8 +197,9 @@ __global__ void __launch_bounds__(4 * K, 2) mix_main_kernel(const MixBwdArgs b) 
       xv += __shfl_xor(xv, 32, 64);
       if (wave >= W - 4 && g == 0) s.xv[16 * (wave & 3) + i16] = xv;
     }
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) dot += __shfl_xor(dot, o, 64);
+    dot = row16_sum(dot);
+    dot += __shfl_xor(dot, 16, 64);
+    dot += __shfl_xor(dot, 32, 64);
     if (lane == 0) s.dot[wave] = dot;
     if (wave == W - 1) s.g.set(ld.log_g(rows, lane), ld.beta(rows, lane), lane);
     __syncthreads();  // the stages are no longer read
@@ -243,9 +248,8 @@ __global__ void __launch_bounds__(4 * K, 2) mix_main_kernel(const MixBwdArgs b) 
         }
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-#pragma unroll
-          for (int o = 1; o < 16; o <<= 1) wc[r] += __shfl_xor(wc[r], o, 64);
-          if (i16 == 0) s.wcol[tile][4 * g + r] = wc[r];
+          wc[r] = row16_sum(wc[r]);
+          if (i16 == r) s.wcol[tile][4 * g + r] = wc[r];
         }
         // four neighbours of row i, a term at a time; above the diagonal zeros
         const auto put4 = [&](E* plane, float* v) {
@@ -304,11 +308,10 @@ __global__ void __launch_bounds__(4 * K, 2) mix_main_kernel(const MixBwdArgs b) 
         }
       }
       // sums over the 16 lanes of a group; item 4 t + r is token 16 t + 4g + r
-      typedef RowReduce<16, 16> Red;
-      Red::run(gv, lane);
-      Red::run(tk, lane);
-      if (DELTA) Red::run(bk, lane);
-      const int item = Red::item(0, lane), t16 = 16 * (item >> 2) + 4 * g + (item & 3);
+      row16_sums<0>(gv, lane);
+      row16_sums<0>(tk, lane);
+      if (DELTA) row16_sums<0>(bk, lane);
+      const int t16 = 16 * (i16 >> 2) + 4 * g + (i16 & 3);
       s.give[wave][t16] = gv[0];
       s.take[wave][t16] = tk[0];
       if (DELTA) s.back[wave][t16] = bk[0];
@@ -348,23 +351,14 @@ __global__ void __launch_bounds__(4 * K, 2) mix_main_kernel(const MixBwdArgs b) 
       for (int i = blk; i < 4; ++i) col += s.wcol[i * (i + 1) / 2 + blk][i16];
       double own = (double)row - col + give - take;
       if (DELTA) own -= s.g.beta[lane] * bk;
-      double tot = take;
-#pragma unroll
-      for (int o = 32; o > 0; o >>= 1) tot += __shfl_xor(tot, o, 64);
-      tot += (double)s.g.all * all;
-      // sum over i >= t
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const double up = __shfl_down(own, o, 64);
-        if (lane + o < 64) own += up;
-      }
-      double dg = own + tot;
+      const double tot = last_lane(lane_sums(take)) + (double)s.g.all * all;
+      const double before = lane_sums(own);  // in double: a difference of sums will do
+      double dg = last_lane(before) - before + own + tot;
       if (lane >= rows) dg = 0.0;
       if (a.decay == RSSM_DECAY_TOKEN) {
         if (lane < rows) b.dg[(t0 + lane) * a.v_heads + hv] = (float)dg;
       } else {
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) dg += __shfl_xor(dg, o, 64);
+        dg = last_lane(lane_sums(dg));
         if (lane == 0) b.part[at] = (float)dg;
       }
       if (DELTA && lane < rows) b.dbeta[(t0 + lane) * a.v_heads + hv] = s.xv[lane] - bk - br;

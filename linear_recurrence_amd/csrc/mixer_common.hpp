@@ -179,6 +179,36 @@ __device__ static inline double last_lane(double v) {
   return __builtin_bit_cast(double, (uint64_t)lo | ((uint64_t)hi << 32));
 }
 
+// fp32 lane shifts within rows of 16, for sums over the 16 lanes of a group.
+template <int CTRL>
+__device__ static inline float dpp_f32(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, true));
+}
+// Every lane gets its group's sum.
+__device__ static inline float row16_sum(float v) {
+  v += dpp_f32<0x128>(v);  // 8 lanes round
+  v += dpp_f32<0x141>(v);  // mirrored in halves
+  v += dpp_f32<0x4E>(v);   // the other pair of a quad
+  v += dpp_f32<0xB1>(v);   // the other lane of a pair
+  return v;
+}
+// Sixteen such sums at once: lane l%16 gets item l%16's.  At each level a lane keeps half
+// of its items and takes the partner's sums of them: 15 shifts instead of 64.
+template <int LEVEL>
+__device__ static inline void row16_sums(float (&v)[16], int lane) {
+  if constexpr (LEVEL < 4) {
+    constexpr int bit = 8 >> LEVEL, half = 8 >> LEVEL;
+    constexpr int ctrl = LEVEL == 0 ? 0x128 : (LEVEL == 1 ? 0x141 : (LEVEL == 2 ? 0x4E : 0xB1));
+    const bool up = (lane & bit) != 0;
+#pragma unroll
+    for (int j = 0; j < half; ++j) {
+      const float send = up ? v[j] : v[j + half], keep = up ? v[j + half] : v[j];
+      v[j] = keep + dpp_f32<ctrl>(send);
+    }
+    row16_sums<LEVEL + 1>(v, lane);
+  }
+}
+
 // A chunk's decays, one token a lane, as the kernels read them from LDS.
 struct ChunkGates {
   float2 G[kQ];                                      // log2 of the decay since the chunk began
