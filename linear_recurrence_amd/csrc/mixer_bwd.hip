@@ -44,7 +44,7 @@ struct MainLds {
   ChunkGates g;
   float wrow[10][16], wcol[10][16], brow[10][16];  // by tile i (i + 1) / 2 + j
   float give[W][kQ], back[W][kQ], take[W][kQ];
-  float xv[kQ], dot[W];
+  float xv[kQ], dot[W], own[kQ], took[kQ], all;
 };
 
 // Everything that stays within a chunk.  A wave owns 16 of the K columns of dq and dk;
@@ -83,14 +83,12 @@ __global__ void __launch_bounds__(4 * K, 2) mix_main_kernel(const MixBwdArgs b) 
   }
   const int rows = sg.len;
   const long t0 = sg.tok;
+  TileLoad<T, K, TH> x, y;
   {
-    TileLoad<T, K, TH> x, y;
     x.start(static_cast<const E*>(a.k) + t0 * a.k_stride + (long)hk * K, a.k_stride, tid);
     y.start(static_cast<const E*>(a.q) + t0 * a.q_stride + (long)hk * K, a.q_stride, tid);
     x.fetch(rows, tid);
     y.fetch(rows, tid);
-    x.put(s.k, rows, tid);
-    y.put(s.q, rows, tid);
   }
   f32x4 dq[4], dk[4];  // rows t = 16 t + 4g + r, column 16 wave + i16
 #pragma unroll
@@ -125,6 +123,8 @@ __global__ void __launch_bounds__(4 * K, 2) mix_main_kernel(const MixBwdArgs b) 
   };
   fetch_states(0, 0);
   fetch_rows(0, 0);
+  x.put(s.k, rows, tid);
+  y.put(s.q, rows, tid);
 #pragma unroll 1
   for (int hx = 0; hx < a.vpk; ++hx) {
     const int hv = hk * a.vpk + hx;
@@ -333,26 +333,40 @@ __global__ void __launch_bounds__(4 * K, 2) mix_main_kernel(const MixBwdArgs b) 
           }
     }
     __syncthreads();
-    if (wave == 0 && b.dg) {  // one token a lane
-      float give = 0.f, bk = 0.f, take = 0.f, all = 0.f;
+    again();
+    // the parts of each token's sums: eight lanes a token (its waves', then its tiles')
+    if (b.dg) {
 #pragma unroll
-      for (int w = 0; w < W; ++w) {
-        give += s.give[w][lane];
-        take += s.take[w][lane];
-        if (DELTA) bk += s.back[w][lane];
-        all += s.dot[w];
+      for (int u = 0; u < SETS; ++u) {
+        const int p = lane & 7, t = 8 * (wave + u * W) + (lane >> 3), blk = t >> 4, r = t & 15;
+        float give = p < W ? s.give[p][t] : 0.f, take = p < W ? s.take[p][t] : 0.f;
+        float bk = DELTA && p < W ? s.back[p][t] : 0.f, all = p < W ? s.dot[p] : 0.f;
+        float row = p <= blk ? s.wrow[blk * (blk + 1) / 2 + p][r] : 0.f;
+        float br = DELTA && p <= blk ? s.brow[blk * (blk + 1) / 2 + p][r] : 0.f;
+        row -= p >= blk && p < 4 ? s.wcol[p * (p + 1) / 2 + blk][r] : 0.f;
+        const auto sum8 = [](float v) {
+          v += dpp_f32<0x141>(v);
+          v += dpp_f32<0x4E>(v);
+          return v + dpp_f32<0xB1>(v);
+        };
+        row += give - take;
+        if (DELTA) row = fmaf(-s.g.beta[t], bk, row);
+        row = sum8(row);
+        take = sum8(take);
+        all = sum8(all);
+        if (DELTA) bk = sum8(bk), br = sum8(br);
+        if (p == 0) {
+          s.own[t] = row;
+          s.took[t] = take;
+          if (t == 0) s.all = all;
+          if (DELTA && t < rows) b.dbeta[(t0 + t) * a.v_heads + hv] = s.xv[t] - bk - br;
+        }
       }
-      float row = 0.f, col = 0.f, br = 0.f;
-      const int blk = lane >> 4;
-      for (int j = 0; j <= blk; ++j) {
-        row += s.wrow[blk * (blk + 1) / 2 + j][i16];
-        if (DELTA) br += s.brow[blk * (blk + 1) / 2 + j][i16];
-      }
-      for (int i = blk; i < 4; ++i) col += s.wcol[i * (i + 1) / 2 + blk][i16];
-      double own = (double)row - col + give - take;
-      if (DELTA) own -= s.g.beta[lane] * bk;
-      const double tot = last_lane(lane_sums(take)) + (double)s.g.all * all;
-      const double before = lane_sums(own);  // in double: a difference of sums will do
+    }
+    __syncthreads();  // the next head writes all but what follows needs
+    if (wave == 0 && b.dg) {  // one token a lane: the sums over i >= t, in double
+      const double own = s.own[lane], tot = last_lane(lane_sums((double)s.took[lane])) + (double)s.g.all * s.all;
+      const double before = lane_sums(own);  // a difference of sums will do in double
       double dg = last_lane(before) - before + own + tot;
       if (lane >= rows) dg = 0.0;
       if (a.decay == RSSM_DECAY_TOKEN) {
@@ -361,9 +375,7 @@ __global__ void __launch_bounds__(4 * K, 2) mix_main_kernel(const MixBwdArgs b) 
         dg = last_lane(lane_sums(dg));
         if (lane == 0) b.part[at] = (float)dg;
       }
-      if (DELTA && lane < rows) b.dbeta[(t0 + lane) * a.v_heads + hv] = s.xv[lane] - bk - br;
     }
-    __syncthreads();  // the next head writes all of it
   }
   // to the io type, and 16 bytes at a time to memory
 #pragma unroll

@@ -401,82 +401,106 @@ static __global__ void __launch_bounds__(4 * V, BOTH || sizeof(typename Mat<T>::
 }
 
 // Each sequence's segments in order (backward: from the last): what a segment adds is
-// replaced by the state (the gradient) it starts from, S <- M S + N.  The delta rule:
-// a wave for 16 columns, as in the recurrence, 64 columns a workgroup; the matrix of a
-// segment is on its way while the one before is worked on.
+// replaced by the state (the gradient) it starts from, S <- M S + N.  The delta rule: a
+// workgroup for 32 columns, a wave for 32 rows of them: it reads its rows of M alone, the
+// next segment's as this one's are used up, and S is passed on through LDS as terms, with
+// one barrier a segment.  (With all rows of 16 columns a wave and M through LDS a segment
+// took 6 us instead of XX.)
 template <typename T, int K>
-static __global__ void __launch_bounds__(256, 1) mix_combine_kernel(const MixBwdArgs b) {
+static __global__ void __launch_bounds__(2 * K) mix_combine_kernel(const MixBwdArgs b) {
   typedef Mat<T> M;
   typedef typename M::Frag Frag;
-  constexpr int TS = M::kTerms, KT = K / 16, KB = K / 32, NF = KT * KB;
-  constexpr int PIECES = NF * TS * 64 * sizeof(Frag) / 16, N = PIECES / 256;
-  __shared__ __attribute__((aligned(16))) u32x4 sM[PIECES];
+  constexpr int TS = M::kTerms, KB = K / 32, NF = 2 * KB * KB;
+  __shared__ __attribute__((aligned(16))) Frag sS[2][KB * 2 * TS * 64];
   const MixArgs& a = b.m;
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lane = threadIdx.x & 63, i16 = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const bool back = (int)blockIdx.x >= b.dir_blocks, both = a.seg_grad != nullptr;
   const int id = back ? blockIdx.x - b.dir_blocks : blockIdx.x;
-  const int hv = id / (K / 64) % a.v_heads, v0 = id % (K / 64) * 64, seq = id / (K / 64) / a.v_heads;
+  const int hv = id / KB % a.v_heads, c0 = id % KB * 32, seq = id / KB / a.v_heads;
   const SeqSpan sp = seq_span(a.cu, seq, a.seqs, a.tokens);
   const int segs = (sp.len + a.seg - 1) / a.seg;
   if (segs <= 1) return;
-  const auto place = [&](long n) {
-    return ((n * a.v_heads + hv) * K + v0 + 16 * wave + (lane & 15)) * K + 4 * (lane >> 4);
+  // this lane's first element: rows 32 wave + 16 h + 4g, column c0 + 16 ct + i16
+  const auto place = [&](long n, int h, int ct) {
+    return ((n * a.v_heads + hv) * K + c0 + 16 * ct + i16) * K + 32 * wave + 16 * h + 4 * g;
   };
   const int pool = a.init ? mix_slot(a, seq) : -1;
   const bool has = pool >= 0 && (!a.has_init || a.has_init[seq]);
   const long base = seg_base(a.cu, seq, a.seg, a.tokens);
+  const auto slot_of = [&](int n) { return base + (back ? segs - 1 - n : n); };
+  float* const mat = back ? a.seg_grad : a.seg_state;
   const Minus minus;
-  u32x4 rm[N];
-  f32x4 add[KT], S[KT];
-  const auto fetch = [&](int n) {  // what segment n adds, and its matrix
-    const long slot = base + (back ? segs - 1 - n : n);
-    const u32x4* const m = static_cast<const u32x4*>(a.trans) +
-        ((slot * a.v_heads + hv) * (both ? 2 : 1) + back) * PIECES + tid;
+  Frag m[KB][2][TS];
+  f32x4 S[2][2], add[2][2];  // [h][ct]
+  const auto fetch_m = [&](int n, int kb) {
+    const char* const p = static_cast<const char*>(a.trans) +
+        ((slot_of(n) * a.v_heads + hv) * (both ? 2 : 1) + back) * (NF * TS * 64 * sizeof(Frag));
 #pragma unroll
-    for (int i = 0; i < N; ++i) rm[i] = m[i * 256];
-    const float* const p = (back ? a.seg_grad : a.seg_state) + place(slot);
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int kt = 0; kt < KT; ++kt) add[kt] = *reinterpret_cast<const f32x4*>(p + 16 * kt);
+      for (int k = 0; k < TS; ++k) m[kb][h][k] = frag_at<T>(p, ((2 * wave + h) * KB + kb) * TS + k, lane);
   };
-  fetch(0);
-  const float* src = back ? b.dfinal : (has ? a.init : nullptr);
-  if (src) src += place(back ? seq : pool);
+  const auto fetch_add = [&](int n) {
 #pragma unroll
-  for (int kt = 0; kt < KT; ++kt)
-    S[kt] = src ? *reinterpret_cast<const f32x4*>(src + 16 * kt) : f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int ct = 0; ct < 2; ++ct) add[h][ct] = *reinterpret_cast<const f32x4*>(mat + place(slot_of(n), h, ct));
+  };
+#pragma unroll
+  for (int kb = 0; kb < KB; ++kb) fetch_m(0, kb);
+  fetch_add(0);
+  const float* src = back ? b.dfinal : (has ? a.init : nullptr);
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int ct = 0; ct < 2; ++ct)
+      S[h][ct] = src ? *reinterpret_cast<const f32x4*>(src + place(back ? seq : pool, h, ct)) : f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
   for (int n = 0;; ++n) {
-    const long slot = base + (back ? segs - 1 - n : n);
-    f32x4 acc[KT];
+    const long slot = slot_of(n);
 #pragma unroll
-    for (int kt = 0; kt < KT; ++kt) acc[kt] = add[kt];
-    if (n + 1 < segs) {
-      __syncthreads();  // the last matrix is no longer read
-#pragma unroll
-      for (int i = 0; i < N; ++i) sM[i * 256 + tid] = rm[i];
-      if (n + 2 < segs) fetch(n + 1);
-      __syncthreads();
-    }
-    float* const p = (back ? a.seg_grad : a.seg_state) + place(slot);
-#pragma unroll
-    for (int kt = 0; kt < KT; ++kt) *reinterpret_cast<f32x4*>(p + 16 * kt) = S[kt];
-    if (n + 1 == segs) break;
-#pragma unroll
-    for (int kb = 0; kb < KB; ++kb) {
+    for (int ct = 0; ct < 2; ++ct) {
       float f[8];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        f[r] = S[2 * kb][r];
-        f[4 + r] = S[2 * kb + 1][r];
+        f[r] = S[0][ct][r];
+        f[4 + r] = S[1][ct][r];
       }
-      const auto x = split<T, TS>(f, minus);
+      put_split<T, TS>(sS[n & 1], wave * 2 + ct, split<T, TS>(f, minus), lane);
+    }
+    f32x4 acc[2][2];
 #pragma unroll
-      for (int k4 = 0; k4 < KT; k4 += 4)
-        mma_many<T, TS, TS, 4>([&](int n, int k) { return frag_at<T>(sM, ((k4 + n) * KB + kb) * TS + k, lane); }, x,
-                               acc + k4);
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int ct = 0; ct < 2; ++ct) acc[h][ct] = add[h][ct];
+    const int next = n + 2 < segs ? n + 1 : n;  // (at the end: the same again)
+    fetch_add(next);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int ct = 0; ct < 2; ++ct) *reinterpret_cast<f32x4*>(mat + place(slot, h, ct)) = S[h][ct];
+    if (n + 1 == segs) break;
+    __syncthreads();
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+      Split<T, TS> x[2];
+#pragma unroll
+      for (int ct = 0; ct < 2; ++ct) x[ct] = split_at<T, TS>(sS[n & 1], kb * 2 + ct, lane);
+#pragma unroll
+      for (int s = TS - 1; s >= 0; --s)
+#pragma unroll
+        for (int i = 0; i <= s; ++i)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int ct = 0; ct < 2; ++ct) acc[h][ct] = M::mma(m[kb][h][i], x[ct].t[s - i], acc[h][ct]);
+      fetch_m(next, kb);
     }
 #pragma unroll
-    for (int kt = 0; kt < KT; ++kt) S[kt] = acc[kt];
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int ct = 0; ct < 2; ++ct) S[h][ct] = acc[h][ct];
   }
 }
 
@@ -548,7 +572,7 @@ template <typename T, bool BOTH>
 static int launch_segments(MixBwdArgs b, int dk, bool delta, hipStream_t stream) {
   const MixArgs& a = b.m;
   const long dir = mix_grid(a.slots, a.k_heads, a.vpk);
-  const long cdir = (long)a.seqs * a.v_heads * (delta ? dk / 64 : dk * a.dv / 1024);
+  const long cdir = (long)a.seqs * a.v_heads * (delta ? dk / 32 : dk * a.dv / 1024);
   b.dir_blocks = (int)dir;
   b.elems = dk * a.dv;
   const int rc = launch_kernel(pick_segments<T, BOTH>(dk, a.dv, delta), (unsigned)(((BOTH ? 2 : 1) + delta) * dir),
@@ -559,7 +583,7 @@ static int launch_segments(MixBwdArgs b, int dk, bool delta, hipStream_t stream)
   if (delta)
     fn = dk == 64 ? reinterpret_cast<const void*>(&mix_combine_kernel<T, 64>)
                   : reinterpret_cast<const void*>(&mix_combine_kernel<T, 128>);
-  return launch_kernel(fn, (unsigned)((BOTH ? 2 : 1) * cdir), 256, 0, stream, b);
+  return launch_kernel(fn, (unsigned)((BOTH ? 2 : 1) * cdir), delta ? 2 * dk : 256, 0, stream, b);
 }
 
 }  // namespace rssm
