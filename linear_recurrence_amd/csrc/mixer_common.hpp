@@ -227,9 +227,15 @@ struct ChunkGates {
   }
 };
 
-// A tile of 64 tokens' rows in LDS.  bf16: 16-byte pieces of a row change places by
-// the row, so that the 16 rows of a fragment and the eight rows of half a transposing
-// read lie in different banks without padding.  fp32: padded rows.
+// Row i of a state's 16-row tile kt: two tiles share 32 rows in turns of four, so that a
+// lane's rows 4g + r of both are eight neighbours, which fragments of K and Q in order C
+// hold too: one 16-byte read each.  (In order D, two reads of 8 bytes, the compiler paired
+// reads of different fragments and moved their halves together again.)
+RSSM_HD static inline int mix_row(int kt, int i) { return 32 * (kt >> 1) + 8 * (i >> 2) + 4 * (kt & 1) + (i & 3); }
+
+// A tile of 64 tokens' rows in LDS.  bf16: 16-byte pieces of a row change places by the
+// row, so that the 16 rows of a fragment, and the four rows that 16 lanes of a
+// transposing read take, lie in different banks without padding.  fp32: padded rows.
 template <typename T, int COLS>
 struct Tile {
   typedef typename Mat<T>::E E;
@@ -237,7 +243,7 @@ struct Tile {
   static constexpr bool kSwap = sizeof(E) == 2;
   static constexpr int LD = kSwap ? COLS : COLS + Mat<T>::kPad, SIZE = kQ * LD;
   __device__ static inline int place(int row) {
-    return COLS == 64 ? ((row >> 1 & 3) << 1) | (row >> 3 & 1) : ((row & 7) << 1) | (row >> 3 & 1);
+    return COLS == 64 ? ((row >> 1 & 1) << 2) | (row >> 2 & 3) : ((row & 3) << 2) | (row >> 2 & 3);
   }
   __device__ static inline int at(int row, int col) {
     return kSwap ? row * LD + (((col >> 3) ^ place(row)) << 3) + (col & 7) : row * LD + col;
@@ -255,6 +261,12 @@ struct Tile {
     } else {
       return Mat<T>::rows_d(p + at(row, col));
     }
+  }
+  // of 32 rows from k0, the columns of a state's tile kt (see mix_row)
+  __device__ static inline Frag cols_of(const E* p, int k0, int kt, int lane) {
+    const int i = lane & 15, g = lane >> 4, c = 32 * (kt >> 1) + 4 * (kt & 1);
+    if constexpr (kSwap) return Mat<T>::cols(p + at(k0 + 4 * g + (i >> 2), c + 8 * (i & 3)), LD);
+    else return Mat<T>::cols(p + at(k0 + 4 * g, c + 8 * (i >> 2) + (i & 3)), LD);
   }
   // of 32 rows from k0, columns c .. c + 15
   __device__ static inline Frag cols(const E* p, int k0, int c, int lane) {

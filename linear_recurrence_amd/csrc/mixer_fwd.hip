@@ -70,11 +70,11 @@ __global__ void __launch_bounds__(4 * V, 2) mix_forward_kernel(const MixArgs a) 
   const int pool = a.init || a.final_state ? mix_slot(a, sp.seq) : -1;
   if (tid == 0 && sp.first && un.rest == 0 && un.hk == 0 && a.status && (a.init || a.final_state) && pool < 0)
     atomicOr(a.status, RSSM_ST_BAD_SLOT);
-  // S: rows k = 16 kt + 4g + r, column 16 wave + i16
+  // S: rows mix_row(kt, 4g + r), column 16 wave + i16
   f32x4 S[KT];
 #pragma unroll
   for (int kt = 0; kt < KT; ++kt) S[kt] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const auto place = [&](long n) { return ((n * a.v_heads + hv) * V + 16 * wave + i16) * K + 4 * g; };
+  const auto place = [&](long n) { return ((n * a.v_heads + hv) * V + 16 * wave + i16) * K + 8 * g; };
   // The pool is read here only by a sequence of one segment, whose wave also writes it:
   // a longer one's first segment takes the copy that the combining launch left, since
   // its last segment may already have stored the final state over the initial one.
@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(4 * V, 2) mix_forward_kernel(const MixArgs a) 
   if (!whole || (a.init && pool >= 0 && (!a.has_init || a.has_init[sp.seq]))) {
     const float* p = whole ? a.init + place(pool) : a.seg_state + place(un.slot);
 #pragma unroll
-    for (int kt = 0; kt < KT; ++kt) S[kt] = *reinterpret_cast<const f32x4*>(p + 16 * kt);
+    for (int kt = 0; kt < KT; ++kt) S[kt] = *reinterpret_cast<const f32x4*>(p + mix_row(kt, 0));
   }
   const long cbase = seg_base(a.cu, sp.seq, kQ, a.tokens) + (long)sp.k * (a.seg / kQ);
   const int chunks = (sp.len + kQ - 1) / kQ;
@@ -168,8 +168,8 @@ __global__ void __launch_bounds__(4 * V, 2) mix_forward_kernel(const MixArgs a) 
       Frag kf[4], qf[4];
 #pragma unroll
       for (int it = 0; it < 4; ++it) {
-        kf[it] = TK::rows_d(sK, it, 32 * b, lane);
-        qf[it] = TK::rows_d(s.q, it, 32 * b, lane);
+        kf[it] = TK::rows_c(sK, it, 32 * b, lane);
+        qf[it] = TK::rows_c(s.q, it, 32 * b, lane);
       }
       if constexpr (DELTA) {
 #pragma unroll
@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(4 * V, 2) mix_forward_kernel(const MixArgs a) 
       for (int k4 = 0; k4 < KT; k4 += 4) {
         Frag kf[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) kf[q] = TK::cols(sK, 32 * kb, 16 * (k4 + q), lane);
+        for (int q = 0; q < 4; ++q) kf[q] = TK::cols_of(sK, 32 * kb, k4 + q, lane);
 #pragma unroll
         for (int k = TS - 1; k >= 0; --k)
 #pragma unroll
@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(4 * V, 2) mix_forward_kernel(const MixArgs a) 
   if (sp.last && a.final_state && pool >= 0) {
     float* p = a.final_state + place(pool);
 #pragma unroll
-    for (int kt = 0; kt < KT; ++kt) *reinterpret_cast<f32x4*>(p + 16 * kt) = S[kt];
+    for (int kt = 0; kt < KT; ++kt) *reinterpret_cast<f32x4*>(p + mix_row(kt, 0)) = S[kt];
   }
 }
 

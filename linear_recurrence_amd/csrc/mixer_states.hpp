@@ -88,20 +88,20 @@ static __global__ void __launch_bounds__(4 * V, BOTH || sizeof(typename Mat<T>::
 #pragma unroll
   for (int kt = 0; kt < KT; ++kt) S[kt] = f32x4{0.f, 0.f, 0.f, 0.f};
   // this lane's first element in state number n
-  const auto place = [&](long n) { return ((n * a.v_heads + hv) * V + 16 * wave + i16) * K + 4 * g; };
+  const auto place = [&](long n) { return ((n * a.v_heads + hv) * V + 16 * wave + i16) * K + 8 * g; };
   if (STORE) {
     const float* src = back ? b.dfinal : (has ? a.init : nullptr);
     if (!whole) src = back ? a.seg_grad : a.seg_state;
     if (src) {
       src += place(!whole ? un.slot : (back ? sg.seq : pool));
 #pragma unroll
-      for (int kt = 0; kt < KT; ++kt) S[kt] = *reinterpret_cast<const f32x4*>(src + 16 * kt);
+      for (int kt = 0; kt < KT; ++kt) S[kt] = *reinterpret_cast<const f32x4*>(src + mix_row(kt, 0));
     }
   } else if (trans) {
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) S[kt][r] = 16 * kt + 4 * g + r == 16 * wave + i16 ? 1.f : 0.f;
+      for (int r = 0; r < 4; ++r) S[kt][r] = mix_row(kt, 4 * g + r) == mix_row(wave, i16) ? 1.f : 0.f;
   }
   float total = 1.f;
   const long vstride = back ? b.do_stride : a.v_stride;
@@ -158,7 +158,7 @@ static __global__ void __launch_bounds__(4 * V, BOTH || sizeof(typename Mat<T>::
     if (STORE) {
       float* p = keep + place(cbase + c);
 #pragma unroll
-      for (int kt = 0; kt < KT; ++kt) *reinterpret_cast<f32x4*>(p + 16 * kt) = S[kt];
+      for (int kt = 0; kt < KT; ++kt) *reinterpret_cast<f32x4*>(p + mix_row(kt, 0)) = S[kt];
     }
     __syncthreads();
     if (kAhead && n + 1 < chunks) fetch(back ? c - 1 : c + 1);
@@ -182,19 +182,19 @@ static __global__ void __launch_bounds__(4 * V, BOTH || sizeof(typename Mat<T>::
         const auto sf = split<T, TS>(f, minus);
         Frag kf[4];
 #pragma unroll
-        for (int it = 0; it < 4; ++it) kf[it] = TK::rows_d(sK, it, 32 * x, lane);
+        for (int it = 0; it < 4; ++it) kf[it] = TK::rows_c(sK, it, 32 * x, lane);
 #pragma unroll
         for (int k = TS - 1; k >= 0; --k)
 #pragma unroll
           for (int it = 0; it < 4; ++it) R[it] = M::mma(kf[it], sf.t[k], R[it]);
         if (back && wave < 6) {
-          const Frag kj = TK::rows_d(sK, jt, 32 * x, lane);
+          const Frag kj = TK::rows_c(sK, jt, 32 * x, lane);
 #pragma unroll
           for (int h = 0; h < 2; ++h)
-            if (2 * kp + h >= jt) P[h] = M::mma(TK::rows_d(sQ, 2 * kp + h, 32 * x, lane), kj, P[h]);
+            if (2 * kp + h >= jt) P[h] = M::mma(TK::rows_c(sQ, 2 * kp + h, 32 * x, lane), kj, P[h]);
           if (W == 4 && wave < 2) {  // (1, 0) and (3, 1): one tile each
             const int j2 = wave ? 3 : 1;
-            P2[1] = M::mma(TK::rows_d(sQ, j2, 32 * x, lane), TK::rows_d(sK, j2, 32 * x, lane), P2[1]);
+            P2[1] = M::mma(TK::rows_c(sQ, j2, 32 * x, lane), TK::rows_c(sK, j2, 32 * x, lane), P2[1]);
           }
         }
       }
@@ -320,7 +320,7 @@ static __global__ void __launch_bounds__(4 * V, BOTH || sizeof(typename Mat<T>::
         for (int k4 = 0; k4 < KT; k4 += 4) {
           Frag kf[4];
 #pragma unroll
-          for (int x = 0; x < 4; ++x) kf[x] = TK::cols(sK, 32 * kb, 16 * (k4 + x), lane);
+          for (int x = 0; x < 4; ++x) kf[x] = TK::cols_of(sK, 32 * kb, k4 + x, lane);
 #pragma unroll
           for (int k = TS - 1; k >= 0; --k)
 #pragma unroll
@@ -333,7 +333,7 @@ static __global__ void __launch_bounds__(4 * V, BOTH || sizeof(typename Mat<T>::
         for (int k4 = 0; k4 < KT; k4 += 4) {
           Frag qf[4];
 #pragma unroll
-          for (int x = 0; x < 4; ++x) qf[x] = TK::cols(sQ, 32 * kb, 16 * (k4 + x), lane);
+          for (int x = 0; x < 4; ++x) qf[x] = TK::cols_of(sQ, 32 * kb, k4 + x, lane);
 #pragma unroll
           for (int k = TS - 1; k >= 0; --k)
 #pragma unroll
@@ -353,7 +353,7 @@ static __global__ void __launch_bounds__(4 * V, BOTH || sizeof(typename Mat<T>::
     if (!trans) {
       float* p = (back ? a.seg_grad : a.seg_state) + place(un.slot);
 #pragma unroll
-      for (int kt = 0; kt < KT; ++kt) *reinterpret_cast<f32x4*>(p + 16 * kt) = S[kt];
+      for (int kt = 0; kt < KT; ++kt) *reinterpret_cast<f32x4*>(p + mix_row(kt, 0)) = S[kt];
       // once, so that the same call gives the same bits: forward but for a last segment
       if (!DELTA && tid == 0 && back == sg.last) a.seg_decay[(long)un.slot * a.v_heads + hv] = total;
       return;
@@ -379,13 +379,13 @@ static __global__ void __launch_bounds__(4 * V, BOTH || sizeof(typename Mat<T>::
     float* const sm = u.m;  // [K columns][LM]
     __syncthreads();
 #pragma unroll
-    for (int kt = 0; kt < KT; ++kt) *reinterpret_cast<f32x4*>(sm + (16 * wave + i16) * LM + 16 * kt + 4 * g) = S[kt];
+    for (int kt = 0; kt < KT; ++kt) *reinterpret_cast<f32x4*>(sm + mix_row(wave, i16) * LM + mix_row(kt, 4 * g)) = S[kt];
     __syncthreads();
 #pragma unroll
     for (int jb = 0; jb < KB; ++jb) {  // a wave for 16 rows
       float f[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = sm[(32 * jb + 4 * g + (e < 4 ? e : 12 + e)) * LM + 16 * wave + i16];
+      for (int e = 0; e < 8; ++e) f[e] = sm[(32 * jb + 8 * g + e) * LM + mix_row(wave, i16)];
       const auto x = split<T, TS>(f, minus);
       put_split<T, TS>(out, wave * KB + jb, x, lane);
     }
@@ -396,7 +396,7 @@ static __global__ void __launch_bounds__(4 * V, BOTH || sizeof(typename Mat<T>::
     float* p = b.dinit + place(sg.seq);
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt)
-      *reinterpret_cast<f32x4*>(p + 16 * kt) = has ? S[kt] : f32x4{0.f, 0.f, 0.f, 0.f};
+      *reinterpret_cast<f32x4*>(p + mix_row(kt, 0)) = has ? S[kt] : f32x4{0.f, 0.f, 0.f, 0.f};
   }
 }
 
@@ -421,9 +421,9 @@ static __global__ void __launch_bounds__(2 * K) mix_combine_kernel(const MixBwdA
   const SeqSpan sp = seq_span(a.cu, seq, a.seqs, a.tokens);
   const int segs = (sp.len + a.seg - 1) / a.seg;
   if (segs <= 1) return;
-  // this lane's first element: rows 32 wave + 16 h + 4g, column c0 + 16 ct + i16
+  // this lane's first element: rows 32 wave + 8 g + 4 h, column c0 + 16 ct + i16
   const auto place = [&](long n, int h, int ct) {
-    return ((n * a.v_heads + hv) * K + c0 + 16 * ct + i16) * K + 32 * wave + 16 * h + 4 * g;
+    return ((n * a.v_heads + hv) * K + c0 + 16 * ct + i16) * K + 32 * wave + 8 * g + 4 * h;
   };
   const int pool = a.init ? mix_slot(a, seq) : -1;
   const bool has = pool >= 0 && (!a.has_init || a.has_init[seq]);
