@@ -39,6 +39,7 @@ struct MixArgs {
   float* seg_state;    // [segment slots][v_heads][V][K]
   float* seg_grad;     // the same
   float* seg_decay;    // [segment slots][v_heads]
+  const int32_t* order;  // [segment slots]: the longest first, or null
   void* trans;         // [segment slots][v_heads][K K / 512 (twice) fragments][terms][64]
   long q_stride, k_stride, v_stride;
   int32_t tokens, seqs, k_heads, v_heads, vpk, dv, num_slots, decay;
@@ -372,6 +373,7 @@ __device__ static inline MixUnit mix_unit(const MixArgs& a, int id, int per) {
   MixUnit m;
   m.live = u < a.slots * a.k_heads;
   m.slot = m.live ? u / a.k_heads : 0;
+  if (m.live && a.order) m.slot = a.order[m.slot];
   m.hk = m.live ? u % a.k_heads : 0;
   m.rest = j % per;
   return m;
@@ -613,7 +615,7 @@ struct MixTake {
   }
 };
 struct SegLayout {
-  size_t state, grad, decay, trans;
+  size_t state, grad, decay, trans, order;
 };
 static inline SegLayout seg_layout(const rssm_mixer_dims& d, bool delta, bool both, MixTake& take) {
   SegLayout l{};
@@ -623,6 +625,7 @@ static inline SegLayout seg_layout(const rssm_mixer_dims& d, bool delta, bool bo
   l.state = take(st);
   l.grad = take(both ? st : 0);
   l.decay = take(delta ? 0 : units * 4);
+  l.order = take(units / d.v_heads * 4);
   l.trans = take(delta ? units * d.dk * d.dk / 512 * (both ? 2 : 1) * 64 * (d.io_dtype == RSSM_F32 ? 32 : 48) : 0);
   return l;
 }
@@ -634,6 +637,7 @@ static inline void seg_fill(MixArgs& a, const rssm_mixer_dims& d, const SegLayou
   a.seg_grad = reinterpret_cast<float*>(ws + l.grad);
   a.seg_decay = reinterpret_cast<float*>(ws + l.decay);
   a.trans = ws + l.trans;
+  a.order = d.tokens > a.seg ? reinterpret_cast<const int32_t*>(ws + l.order) : nullptr;
 }
 
 }  // namespace rssm

@@ -22,6 +22,7 @@ struct MixBwdArgs {
   float* D;      // [chunk slots][v_heads][64][V]
   float* dX;     // the same
   float* part;   // [chunk slots][v_heads]: dg summed over the chunk
+  int32_t* new_order;  // of the first launch (MixArgs::order)
   long do_stride, cslots;
   int32_t dir_blocks;  // blocks of one direction
   int32_t elems;       // of a state
@@ -41,6 +42,32 @@ struct StatesLds {
   __attribute__((aligned(16))) u32x4 p[BOTH ? TF : 1];
   ChunkGates g[B];
 };
+
+// The segment slots by length, the longest first and those without a segment last, by one
+// workgroup (64 classes of length; the order within one does not matter to any result):
+// uneven sequences otherwise leave the longest to the end (16383 tokens of 13 sequences,
+// delta rule: the outputs' launch 315 us instead of 376).
+__device__ static inline void order_segments(const MixArgs& a, int32_t* order) {
+  __shared__ int count[65];
+  for (int i = threadIdx.x; i < 65; i += blockDim.x) count[i] = 0;
+  __syncthreads();
+  const auto rank = [&](int slot) {
+    const Segment sg = find_segment(a.cu, a.seqs, a.tokens, a.seg, slot);
+    return sg.len == 0 ? 64 : 63 - (int)((sg.len - 1L) * 64 / a.seg);
+  };
+  for (int i = threadIdx.x; i < a.slots; i += blockDim.x) atomicAdd(&count[rank(i)], 1);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    int at = 0;
+    for (int i = 0; i < 65; ++i) {
+      const int n = count[i];
+      count[i] = at;
+      at += n;
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < a.slots; i += blockDim.x) order[atomicAdd(&count[rank(i)], 1)] = i;
+}
 
 // One of the two recurrences over the chunks of a segment, a workgroup for one value
 // head's state (mix_forward_kernel without the outputs).  Blocks: forward; BOTH:
@@ -69,6 +96,10 @@ static __global__ void __launch_bounds__(4 * V, BOTH || sizeof(typename Mat<T>::
   const MixArgs& a = b.m;
   const int tid = threadIdx.x, lane = tid & 63, i16 = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  if (!STORE && blockIdx.x + 1 == gridDim.x) {
+    order_segments(a, b.new_order);
+    return;
+  }
   const bool back = BOTH && (int)blockIdx.x >= b.dir_blocks && (int)blockIdx.x < 2 * b.dir_blocks;
   const bool trans = !STORE && DELTA && (int)blockIdx.x >= (BOTH ? 2 : 1) * b.dir_blocks;
   const MixUnit un = mix_unit(a, blockIdx.x - (trans ? (BOTH ? 2 : 1) : back) * b.dir_blocks, a.vpk);
@@ -575,8 +606,11 @@ static int launch_segments(MixBwdArgs b, int dk, bool delta, hipStream_t stream)
   const long cdir = (long)a.seqs * a.v_heads * (delta ? dk / 32 : dk * a.dv / 1024);
   b.dir_blocks = (int)dir;
   b.elems = dk * a.dv;
-  const int rc = launch_kernel(pick_segments<T, BOTH>(dk, a.dv, delta), (unsigned)(((BOTH ? 2 : 1) + delta) * dir),
-                               4 * a.dv, 0, stream, b);
+  MixBwdArgs first = b;  // its own units are in no order yet: the last block makes it
+  first.new_order = const_cast<int32_t*>(b.m.order);
+  first.m.order = nullptr;
+  const int rc = launch_kernel(pick_segments<T, BOTH>(dk, a.dv, delta),
+                               (unsigned)(((BOTH ? 2 : 1) + delta) * dir + 1), 4 * a.dv, 0, stream, first);
   if (rc) return rc;
   b.dir_blocks = (int)cdir;
   const void* fn = reinterpret_cast<const void*>(&mix_combine_decay_kernel);
