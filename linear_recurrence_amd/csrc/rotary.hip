@@ -4,7 +4,8 @@
 // tokens and a range of heads.  First a thread for each (token, pair) forms the
 // angle in turns, its fraction, sine and cosine in double (at position 2^20 an fp32
 // angle would be off by 0.06), once for all heads; then a thread keeps the sines of
-// eight pairs of one token in registers and walks the heads.
+// its pairs of one token in registers and walks the heads with two loads on their way.  Elements that
+// only pass take the same way, so that lanes that turn and lanes that copy load together.
 #include <math.h>
 
 #include "rssm_host.hpp"
@@ -20,7 +21,7 @@ struct RotaryArgs {
   long x_stride, y_stride;
   int32_t tokens, heads, dim, half, interleaved, pos_int64, inverse;
   int32_t tok, hpg, groups;  // tokens a workgroup, heads a group, groups of heads
-  int32_t turn, items;       // vectors of 8 pairs a head; and of 8 copied elements
+  int32_t turn, items;       // a head's items of pairs; those and the items of copied elements
   float amplitude;
 };
 
@@ -45,58 +46,64 @@ __global__ void __launch_bounds__(256) rotary_kernel(const RotaryArgs a) {
     sT[e] = make_float2((float)(amp * c), (float)(a.inverse ? -amp * s : amp * s));
   }
   __syncthreads();
+  // A thread's item: one vector of 8 elements (INTER: 4 pairs, or copies), or two (8 pairs,
+  // one element of each in either; or copies).
+  constexpr int NV = INTER ? 1 : 2, NP = INTER ? 4 : 8, U = 2 / NV;
   const int step = 256 / a.items, hh = tid / a.items, it = tid - hh * a.items;
   if (hh >= step) return;
   const bool turns = it < a.turn;
-  const int i0 = 8 * (turns ? it : it - a.turn);
-  const int n = turns ? (a.half - i0 < 8 ? a.half - i0 : 8)
-                      : (a.dim - 2 * a.half - i0 < 8 ? a.dim - 2 * a.half - i0 : 8);
+  int off[NV], n[NV];
+  const int i0 = NP * it;  // the first pair
+  if (turns) {
+    const int m = a.half - i0 < NP ? a.half - i0 : NP;
+    off[0] = INTER ? 2 * i0 : i0;
+    n[0] = INTER ? 2 * m : m;
+    if (!INTER) off[NV - 1] = a.half + i0, n[NV - 1] = m;
+  } else {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      off[v] = 2 * a.half + 8 * (NV * (it - a.turn) + v);
+      n[v] = a.dim - off[v] < 0 ? 0 : (a.dim - off[v] < 8 ? a.dim - off[v] : 8);
+    }
+  }
   for (int t = 0; t < toks; ++t) {
     const long xr = (t0 + t) * a.x_stride, yr = (t0 + t) * a.y_stride;
-    if (!turns) {
-      for (int h = h0 + hh; h < h1; h += step) {
-        const long at = (long)h * a.dim + 2 * a.half + i0;
-        float f[8];
-        load8<T>(a.x, xr + at, n, f);
-        store8<T>(a.y, yr + at, n, f);
-      }
-      continue;
-    }
-    float co[8], si[8];
+    float co[NP], si[NP];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float2 w = k < n ? sT[t * a.half + i0 + k] : make_float2(0.f, 0.f);
+    for (int k = 0; k < NP; ++k) {
+      const float2 w = turns && i0 + k < a.half ? sT[t * a.half + i0 + k] : make_float2(0.f, 0.f);
       co[k] = w.x;
       si[k] = w.y;
     }
-    for (int h = h0 + hh; h < h1; h += step) {
-      const long at = (long)h * a.dim;
-      float u[8], v[8];  // the pairs, or (interleaved) their 16 elements in order
-      if (INTER) {
-        const int m = 2 * n;
-        load8<T>(a.x, xr + at + 2 * i0, m < 8 ? m : 8, u);
-        load8<T>(a.x, xr + at + 2 * i0 + 8, m < 8 ? 0 : m - 8, v);
+    const auto load = [&](int h, float (*f)[8]) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          float* const p = k < 4 ? u + 2 * k : v + 2 * (k - 4);
-          const float p0 = p[0], p1 = p[1];
-          p[0] = fmaf(p0, co[k], -p1 * si[k]);
-          p[1] = fmaf(p0, si[k], p1 * co[k]);
-        }
-        store8<T>(a.y, yr + at + 2 * i0, m < 8 ? m : 8, u);
-        store8<T>(a.y, yr + at + 2 * i0 + 8, m < 8 ? 0 : m - 8, v);
-      } else {
-        load8<T>(a.x, xr + at + i0, n, u);
-        load8<T>(a.x, xr + at + a.half + i0, n, v);
+      for (int v = 0; v < NV; ++v) load8<T>(a.x, xr + (long)h * a.dim + off[v], n[v], f[v]);
+    };
+    const auto finish = [&](int h, float (*f)[8]) {
+      if (turns) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float p0 = u[k], p1 = v[k];
-          u[k] = fmaf(p0, co[k], -p1 * si[k]);
-          v[k] = fmaf(p0, si[k], p1 * co[k]);
+        for (int k = 0; k < NP; ++k) {
+          float& x0 = INTER ? f[0][2 * k] : f[0][k];
+          float& x1 = INTER ? f[0][2 * k + 1] : f[NV - 1][k];
+          const float p0 = x0, p1 = x1;
+          x0 = fmaf(p0, co[k], -p1 * si[k]);
+          x1 = fmaf(p0, si[k], p1 * co[k]);
         }
-        store8<T>(a.y, yr + at + i0, n, u);
-        store8<T>(a.y, yr + at + a.half + i0, n, v);
       }
+#pragma unroll
+      for (int v = 0; v < NV; ++v) store8<T>(a.y, yr + (long)h * a.dim + off[v], n[v], f[v]);
+    };
+    int h = h0 + hh;
+    float f[U][NV][8];
+    for (; h + (U - 1) * step < h1; h += U * step) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) load(h + u * step, f[u]);
+#pragma unroll
+      for (int u = 0; u < U; ++u) finish(h + u * step, f[u]);
+    }
+    if (U > 1 && h < h1) {
+      load(h, f[0]);
+      finish(h, f[0]);
     }
   }
 }
@@ -144,8 +151,9 @@ static int rotary(const rssm_rotary_dims* dims, const void* x, const void* posit
   a.pos_int64 = d.pos_int64;
   a.inverse = inverse;
   a.amplitude = d.amplitude;
-  a.turn = (a.half + 7) / 8;
-  a.items = a.turn + (same ? 0 : (d.dim - d.rotary_dim + 7) / 8);
+  const int rest = same ? 0 : d.dim - d.rotary_dim;
+  a.turn = d.interleaved ? (a.half + 3) / 4 : (a.half + 7) / 8;
+  a.items = a.turn + (d.interleaved ? (rest + 7) / 8 : (rest + 15) / 16);
   // Tokens enough for a thread each in the table, while there are 1024 workgroups;
   // then the heads are split until there are, down to one round of the threads.
   a.tok = 256 / a.half < 1 ? 1 : 256 / a.half;
