@@ -100,6 +100,7 @@ __global__ void __launch_bounds__(4 * K, 2) mix_main_kernel(const MixBwdArgs b) 
   float fs[8], fg[8];
   RawK<float, 8> rx[SETS];
   RawK<T, 8> ro[SETS], rv;
+  float rb = 0.f;  // beta of this lane's row
   const auto fetch_states = [&](int hx, int vb) {
     const long at = (long)slot * a.v_heads + hk * a.vpk + hx;
     const long p = (at * a.dv + 32 * vb + 8 * g) * K + 16 * wave + i16;
@@ -120,11 +121,28 @@ __global__ void __launch_bounds__(4 * K, 2) mix_main_kernel(const MixBwdArgs b) 
       ro[u].load(second ? b.dout : a.v, tok * (second ? b.do_stride : a.v_stride) + hv * a.dv + vc, 8);
     }
     if (DELTA) rv.load(a.v, tok * a.v_stride + hv * a.dv + vc, 8);
+    if (DELTA) rb = a.beta[tok * a.v_heads + hv];
   };
   fetch_states(0, 0);
   fetch_rows(0, 0);
   x.put(s.k, rows, tid);
   y.put(s.q, rows, tid);
+  // q_i.k_j and k_i.k_j of this wave's tiles (i, j), rows j, columns i: the same for all heads
+  f32x4 qk[JOBS], kk[JOBS];
+  __syncthreads();
+#pragma unroll
+  for (int u = 0; u < JOBS; ++u) {
+    const int n = wave + u * W, ti = n < 1 ? 0 : (n < 3 ? 1 : (n < 6 ? 2 : 3)), tj = n - ti * (ti + 1) / 2;
+    qk[u] = kk[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (n < 10) {
+#pragma unroll
+      for (int x = 0; x < KB; ++x) {
+        const Frag kj = TK::rows_c(s.k, tj, 32 * x, lane);
+        qk[u] = M::mma(kj, TK::rows_c(s.q, ti, 32 * x, lane), qk[u]);
+        if (DELTA) kk[u] = M::mma(kj, TK::rows_c(s.k, ti, 32 * x, lane), kk[u]);
+      }
+    }
+  }
 #pragma unroll 1
   for (int hx = 0; hx < a.vpk; ++hx) {
     const int hv = hk * a.vpk + hx;
@@ -132,8 +150,6 @@ __global__ void __launch_bounds__(4 * K, 2) mix_main_kernel(const MixBwdArgs b) 
     GateLoad ld;
     ld.start(a, t0, hv, DELTA);
     ld.fetch(rows, lane);
-    const int brow = 16 * (wave & 3) + i16;
-    const float beta = DELTA ? a.beta[(t0 + (brow < rows ? brow : 0)) * a.v_heads + hv] : 0.f;
     f32x4 into[4], back[4], out[4], dp[JOBS], dx[JOBS];
 #pragma unroll
     for (int t = 0; t < 4; ++t) into[t] = back[t] = out[t] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -169,7 +185,7 @@ __global__ void __launch_bounds__(4 * K, 2) mix_main_kernel(const MixBwdArgs b) 
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             xv = fmaf(f[e], v[e], xv);
-            w[e] = beta * f[e];
+            w[e] = rb * f[e];
           }
           Vec8<T>::store(b.dv, ((t0 + trow) * a.v_heads + hv) * a.dv + vc, w);
         }
@@ -193,13 +209,10 @@ __global__ void __launch_bounds__(4 * K, 2) mix_main_kernel(const MixBwdArgs b) 
       }
     }
     if (DELTA) {
-      xv += __shfl_xor(xv, 16, 64);
-      xv += __shfl_xor(xv, 32, 64);
+      xv = groups_sum(xv);
       if (wave >= W - 4 && g == 0) s.xv[16 * (wave & 3) + i16] = xv;
     }
-    dot = row16_sum(dot);
-    dot += __shfl_xor(dot, 16, 64);
-    dot += __shfl_xor(dot, 32, 64);
+    dot = groups_sum(row16_sum(dot));
     if (lane == 0) s.dot[wave] = dot;
     if (wave == W - 1) s.g.set(ld.log_g(rows, lane), ld.beta(rows, lane), lane);
     __syncthreads();  // the stages are no longer read
@@ -212,13 +225,6 @@ __global__ void __launch_bounds__(4 * K, 2) mix_main_kernel(const MixBwdArgs b) 
       const int tile = wave + u * W, ti = tile < 1 ? 0 : (tile < 3 ? 1 : (tile < 6 ? 2 : 3)),
                 tj = tile - ti * (ti + 1) / 2;
       if (tile < 10) {
-        f32x4 qk = {0.f, 0.f, 0.f, 0.f}, kk = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int x = 0; x < KB; ++x) {
-          const Frag kj = TK::rows_c(s.k, tj, 32 * x, lane);
-          qk = M::mma(kj, TK::rows_c(s.q, ti, 32 * x, lane), qk);
-          if (DELTA) kk = M::mma(kj, TK::rows_c(s.k, ti, 32 * x, lane), kk);
-        }
         const int i = 16 * ti + i16;
         const float2 gi = s.g.G[i];
         const float be = s.g.beta[i];
@@ -228,20 +234,17 @@ __global__ void __launch_bounds__(4 * K, 2) mix_main_kernel(const MixBwdArgs b) 
           const int j = 16 * tj + 4 * g + r;
           const float c = exp2_f32(gap2(gi, s.g.G[j]));
           n[r] = i >= j ? a.scale * c * dp[u][r] : 0.f;
-          wc[r] = i > j ? qk[r] * n[r] : 0.f;
+          wc[r] = i > j ? qk[u][r] * n[r] : 0.f;
           if (DELTA) {
             const float m = i > j ? c * dx[u][r] : 0.f;
             l[r] = -be * m;
-            wc[r] = i > j ? fmaf(kk[r], l[r], wc[r]) : 0.f;
-            br = i > j ? fmaf(kk[r], m, br) : br;
+            wc[r] = i > j ? fmaf(kk[u][r], l[r], wc[r]) : 0.f;
+            br = i > j ? fmaf(kk[u][r], m, br) : br;
           }
           wr += wc[r];
         }
-#pragma unroll
-        for (int o = 16; o < 64; o <<= 1) {
-          wr += __shfl_xor(wr, o, 64);
-          if (DELTA) br += __shfl_xor(br, o, 64);
-        }
+        wr = groups_sum(wr);
+        if (DELTA) br = groups_sum(br);
         if (g == 0) {
           s.wrow[tile][i16] = wr;
           if (DELTA) s.brow[tile][i16] = br;
@@ -364,7 +367,7 @@ __global__ void __launch_bounds__(4 * K, 2) mix_main_kernel(const MixBwdArgs b) 
       }
     }
     __syncthreads();  // the next head writes all but what follows needs
-    if (wave == 0 && b.dg) {  // one token a lane: the sums over i >= t, in double
+    if (wave == W / 2 && b.dg) {  // a wave with the fewest tiles; one token a lane: the sums over i >= t, in double
       const double own = s.own[lane], tot = last_lane(lane_sums((double)s.took[lane])) + (double)s.g.all * s.all;
       const double before = lane_sums(own);  // a difference of sums will do in double
       double dg = last_lane(before) - before + own + tot;

@@ -193,7 +193,14 @@ __device__ static inline float row16_sum(float v) {
   v += dpp_f32<0xB1>(v);   // the other lane of a pair
   return v;
 }
-// Sixteen such sums at once: lane l%16 gets item l%16's.  At each level a lane keeps half
+// The sum over the four groups of 16 lanes, in every lane.
+__device__ static inline float groups_sum(float v) {
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+// Sixteen sums over a group at once: lane l%16 gets item l%16's.  At each level a lane keeps half
 // of its items and takes the partner's sums of them: 15 shifts instead of 64.
 template <int LEVEL>
 __device__ static inline void row16_sums(float (&v)[16], int lane) {
