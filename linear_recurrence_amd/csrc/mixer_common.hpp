@@ -286,9 +286,8 @@ struct Tile {
 
 // Such a tile on its way from memory, chunk after chunk: a thread keeps one address,
 // from which its pieces are whole rows (multiples of 16) apart.  Loads without
-// conditions: a piece behind the last row takes the first one's, and is put as zero.
-// (Behind a condition each load was waited for before the next: 73 us instead of XX for
-// the delta rule's 4096 tokens.)
+// conditions, so that all are issued at once: a piece behind the last row takes the first
+// one's, and is put as zero.
 template <typename T, int COLS, int THREADS>
 struct TileLoad {
   typedef typename Mat<T>::E E;
@@ -399,7 +398,9 @@ __device__ static inline f32x4 mm16(f32x4 x, f32x4 y, f32x4 c) {
 //   T_ij = -T_ii sum_{j<=m<i} A_im T_mj,
 // then split into the products' terms and stored as fragments (lower triangle; BOTH:
 // and the transpose's, for the backward pass).  Each block of A is computed so that a
-// lane holds its row's values: it is a first operand as it stands.
+// lane holds its row's values: it is a first operand as it stands.  The substitutions'
+// chains bound it: 2048 matrices (4096 tokens of 32 heads) take 22 us, and in front of a
+// backward pass 4096 with their transposes 40 us, of it 150 MB written.
 template <typename T, int K, bool BOTH>
 static __global__ void __launch_bounds__(256) mix_inverse_kernel(const MixArgs a) {
   typedef Mat<T> M;
@@ -573,6 +574,7 @@ static inline int mix_check(const rssm_mixer_dims* d, bool delta) {
   if (d->decay < RSSM_DECAY_NONE || d->decay > RSSM_DECAY_TOKEN) return RSSM_EINVAL;
   if (!(d->dk == 64 || d->dk == 128) || !(d->dv == 64 || d->dv == 128)) return RSSM_ESHAPE;
   if (delta && d->dk != d->dv) return RSSM_ESHAPE;
+  if (delta && d->decay != RSSM_DECAY_TOKEN) return RSSM_EINVAL;
   if (d->scale != d->scale) return RSSM_EINVAL;
   // heads in a row and in a pool slot are indexed in 32 bits
   if ((long)d->v_heads > (1L << 20)) return RSSM_ESHAPE;
@@ -604,7 +606,9 @@ static inline void mix_fill(MixArgs& a, const rssm_mixer_dims& d) {
 // their combination, then all segments at once.  That is up to three times the
 // recurrence's work for one sequence, and worth it where few sequences leave the
 // compute units idle: so long that a workgroup for every 64 columns and segment fills
-// them twice.
+// them twice (one prompt of 4096 tokens, delta rule: 188 us; not cut it would walk 64
+// chunks with 32 workgroups).  Half as long, where the batch's mean length is, was slower
+// for 13 uneven sequences: 564 us instead of 528, and 259 instead of 243 without the rule.
 static inline int mix_seg(const rssm_mixer_dims& d) {
   const long chunks = (d.tokens + kQ - 1) / kQ, columns = (long)d.v_heads * (d.dv / 64);
   long seg = (chunks * columns + 511) / 512;

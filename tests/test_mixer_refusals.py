@@ -157,3 +157,13 @@ def test_rotary_frequencies():
                 dict(rotary_dim=2, scaling="ntk"), dict(rotary_dim=8, scaling="bands", original_length=64, low=4.0)):
         with pytest.raises(ValueError):
             R.rotary_frequencies(**bad, device="cpu")
+
+
+@pytest.mark.parametrize("fn", ["gdn_scan_forward", "gdn_scan_backward"])
+@pytest.mark.parametrize("decay", [0, 1])
+def test_the_delta_rule_has_a_gate_for_every_token(lib, fn, decay):
+    """With another kind of decay the gradient of beta was left unwritten."""
+    assert _mix(lib, fn, decay=decay) == EINVAL
+    d = S.MixerDims(tokens=8, seqs=2, k_heads=2, v_heads=4, dk=64, dv=64, num_slots=2, io_dtype=1, decay=decay,
+                    scale=0.5)
+    assert getattr(lib, fn + "_workspace")(ctypes.byref(d)) == 0
