@@ -52,7 +52,9 @@ struct MainLds {
 // all of them and its own columns of S and dS', whose loads (the next 32 columns', or
 // the next head's) are on their way during the products.  The 64x64 products dO D^T and
 // dX D^T are held by tiles, and cross LDS once as rows of N and L, which then are read
-// by rows and, transposing, by columns.
+// by rows and, transposing, by columns.  8 x 1024 tokens of 32 value heads of the delta
+// rule take 400 us: 0.8 GB are read, 170 us at a copy's rate; the rest are products, splits
+// and barriers of one workgroup a compute unit (registers), which overlap little.
 template <typename T, int K, bool DELTA>
 __global__ void __launch_bounds__(4 * K, 2) mix_main_kernel(const MixBwdArgs b) {
   typedef Mat<T> M;

@@ -482,6 +482,74 @@ def test_offsets_past_32_bits():
     assert torch.equal(pool[at], small)
 
 
+@pytest.mark.parametrize("delta", [False, True])
+def test_segments_bits_streams_and_graphs(delta):
+    """The same with sequences of several segments, whose order of work is made by
+    atomic counters: two calls at once on two streams, and a captured pass replayed
+    between others, give the same bits."""
+    m = Mix([700, 64, 0, 1300, 1, 513, 520, 2], HK=2, HV=8, K=64, V=64, delta=delta,
+            decay="token" if delta else "head", seed=23)
+
+    def both(stream=None):
+        final = torch.zeros_like(m.pool)
+        o = m.forward(final_state=final, stream=stream)
+        g = m.backward(stream=stream)
+        return [o, final] + [t for t in g.values() if t is not None]
+    want = both()
+    m.check_forward(want[0], want[1])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        here = both()
+        with torch.cuda.stream(side):
+            there = both(stream=side)
+        torch.cuda.synchronize()
+        for a, b, c in zip(want, here, there):
+            assert torch.equal(a, b) and torch.equal(a, c)
+    graph = torch.cuda.CUDAGraph()
+    v, cu = m.v.clone(), m.cu.clone()
+    with torch.cuda.graph(graph):
+        got = both()
+    for i in range(3):
+        m.v.copy_(v * (i + 1))
+        if i == 2:      # other lengths in the same graph: the order of work follows
+            m.cu.copy_(torch.tensor([0, 1, 2000, 2001, 2001, 2500, 2900, 3099, 3100], dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        kept = [t.clone() for t in got]
+        for a, b in zip(both(), kept):
+            assert torch.equal(a, b)
+    m.cu.copy_(cu)
+
+
+@pytest.mark.parametrize("delta", [False, True])
+def test_segments_and_a_bad_table(delta):
+    """A table that is not one is reported, and the rows of sequences that it gives
+    right have the values they have without it."""
+    m = Mix([600, 700, 40], delta=delta, initial=False, seed=29)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    want = m.forward()
+    for bad in ([0, 600, 500, 1340], [0, 600, 1300, 1400], [-3, 600, 1300, 1340], [0, 600, 2 ** 31 - 1, 1340]):
+        cu = torch.tensor(bad, dtype=torch.int32, device="cuda")
+        for call in (lambda: m.forward(cu_seqlens=cu, status=status), lambda: m.backward(cu_seqlens=cu, status=status)):
+            status.zero_()
+            call()
+            assert int(status) & R.ST_BAD_SEQ, bad
+    # the last row behind the last sequence keeps what was there
+    cu = torch.tensor([0, 600, 1300, 1339], dtype=torch.int32, device="cuda")
+    o = torch.full_like(want, 5.0)
+    m.forward(cu_seqlens=cu, o=o)
+    assert torch.equal(o[:1300], want[:1300]) and (o[1339] == 5.0).all()
+
+
+def test_one_key_head_for_all():
+    """Sixteen value heads on one key head, whose gradients add up over them."""
+    for delta in (False, True):
+        m = Mix([150, 20], HK=1, HV=16, K=64, V=64, delta=delta, decay="token", seed=31)
+        m.check_forward(m.forward(), None)
+        m.check_backward(m.backward())
+
+
 # ------------------------------------------------------------------- positions
 
 ROT = [(1, 1, 64, 64), (7, 3, 40, 40), (5, 2, 128, 14), (9, 5, 24, 2), (300, 4, 128, 128), (3, 2, 1024, 1024),
