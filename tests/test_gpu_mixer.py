@@ -542,6 +542,16 @@ def test_segments_and_a_bad_table(delta):
     assert torch.equal(o[:1300], want[:1300]) and (o[1339] == 5.0).all()
 
 
+@pytest.mark.parametrize("io", [F32, BF16])
+@pytest.mark.parametrize("delta", [False, True])
+def test_many_heads(delta, io):
+    """More heads and sequences than compute units: a workgroup then takes all 128
+    columns of a head forward, and otherwise half of them."""
+    m = Mix([70, 3, 66, 1, 5], HK=16, HV=32, K=128, V=128, delta=delta, io=io, seed=37)
+    final = torch.full_like(m.pool, 7.0)
+    m.check_forward(m.forward(final_state=final), final)
+
+
 def test_one_key_head_for_all():
     """Sixteen value heads on one key head, whose gradients add up over them."""
     for delta in (False, True):
