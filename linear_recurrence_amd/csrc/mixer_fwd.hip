@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(4 * V, 2) mix_forward_kernel(const MixArgs a) 
   __shared__ L s;
   const int tid = threadIdx.x, lane = tid & 63, i16 = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int parts = a.dv / V;
+  const int dv = V == 128 ? V : a.dv, parts = dv / V;
   const MixUnit un = mix_unit(a, blockIdx.x, a.vpk * parts);
   if (blockIdx.x == 0) check_table(a.cu, a.seqs, a.tokens, a.status);
   if (!un.live) return;
@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(4 * V, 2) mix_forward_kernel(const MixArgs a) 
   f32x4 S[KT];
 #pragma unroll
   for (int kt = 0; kt < KT; ++kt) S[kt] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const auto place = [&](long n) { return ((n * a.v_heads + hv) * a.dv + v0 + 16 * wave + i16) * K + 8 * g; };
+  const auto place = [&](long n) { return ((n * a.v_heads + hv) * dv + v0 + 16 * wave + i16) * K + 8 * g; };
   // The pool is read here only by a sequence of one segment, whose wave also writes it:
   // a longer one's first segment takes the copy that the combining launch left, since
   // its last segment may already have stored the final state over the initial one.
@@ -98,10 +98,10 @@ __global__ void __launch_bounds__(4 * V, 2) mix_forward_kernel(const MixArgs a) 
   rt.p = static_cast<const u32x4*>(a.tinv) + (cbase * a.v_heads + hv) * TF;
   rk.start(static_cast<const E*>(a.k) + sp.tok * a.k_stride + (long)un.hk * K, a.k_stride, tid);
   rq.start(static_cast<const E*>(a.q) + sp.tok * a.q_stride + (long)un.hk * K, a.q_stride, tid);
-  rv.start(static_cast<const E*>(a.v) + sp.tok * a.v_stride + (long)hv * a.dv + v0, a.v_stride, tid);
+  rv.start(static_cast<const E*>(a.v) + sp.tok * a.v_stride + (long)hv * dv + v0, a.v_stride, tid);
   rg.start(a, sp.tok, hv, DELTA);
-  const long orow = (long)a.v_heads * a.dv;
-  E* out = static_cast<E*>(a.o) + ((long)sp.tok * a.v_heads + hv) * a.dv + v0;
+  const long orow = (long)a.v_heads * dv;
+  E* out = static_cast<E*>(a.o) + ((long)sp.tok * a.v_heads + hv) * dv + v0;
   if (kBf16) out += tid / TileLoad<T, V, TH>::PER * orow + tid % TileLoad<T, V, TH>::PER * 8;
   else out += i16 * orow + 16 * wave + 4 * g;
   // 16 bytes of every R-th row of the chunk before
