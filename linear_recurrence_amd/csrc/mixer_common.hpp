@@ -365,9 +365,6 @@ __device__ static inline Split<T, TERMS> split_at(const void* base, int i, int l
   return s;
 }
 
-template <typename T>
-constexpr int mix_terms() { return Mat<T>::kTerms; }
-
 // Units (a segment's key head) are dealt to the eight dies in turn, so that a long
 // sequence's heads are spread over them and a key head's workgroups share one L2.
 struct MixUnit {

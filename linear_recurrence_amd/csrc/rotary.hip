@@ -4,8 +4,9 @@
 // tokens and a range of heads.  First a thread for each (token, pair) forms the
 // angle in turns, its fraction, sine and cosine in double (at position 2^20 an fp32
 // angle would be off by 0.06), once for all heads; then a thread keeps the sines of
-// its pairs of one token in registers and walks the heads with two loads on their way.  Elements that
-// only pass take the same way, so that lanes that turn and lanes that copy load together.
+// its pairs of one token in registers and walks the heads with two loads on their way.
+// Elements that only pass take the same way, so that lanes that turn and lanes that copy
+// load together.
 // 16383 tokens of 64 heads of 128: 109 us, 4.9 TB/s; 8192 of 48 heads, half of each
 // interleaved: 44 us, 4.6 TB/s (63 with the copying lanes in a branch of their own).
 #include <math.h>
