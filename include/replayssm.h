@@ -736,7 +736,8 @@ int linear_attention_forward(const rssm_mixer_dims* dims, const void* q, const v
  *   of log_decay (NULL without one); dinitial_state [seqs, HV, V, K] float32 by
  *   sequence, zeros where has_initial[i] is 0 (NULL: not computed).
  * The workspace holds both directions' states of every 64 tokens: 8 dk dv bytes
- * for each of them and value head, and (the gated delta rule) 512 dv more.
+ * for each of them and value head, and (the gated delta rule) about 512 dv and
+ * 36 KB more.
  */
 size_t linear_attention_backward_workspace(const rssm_mixer_dims* dims);
 int linear_attention_backward(const rssm_mixer_dims* dims, const void* dout, const void* q,
