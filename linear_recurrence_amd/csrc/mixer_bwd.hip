@@ -80,7 +80,8 @@ __global__ void __launch_bounds__(4 * K, 2) mix_main_kernel(const MixBwdArgs b) 
   const int slot = blockIdx.x / a.k_heads, hk = blockIdx.x % a.k_heads;
   const Segment sg = find_segment(a.cu, a.seqs, a.tokens, kQ, slot);
   if (sg.len == 0) {
-    if (b.part && tid < a.vpk) b.part[(long)slot * a.v_heads + hk * a.vpk + tid] = 0.f;
+    if (b.part)  // (the value heads of a key head may be more than the threads)
+      for (int i = tid; i < a.vpk; i += TH) b.part[(long)slot * a.v_heads + hk * a.vpk + i] = 0.f;
     return;
   }
   const int rows = sg.len;
