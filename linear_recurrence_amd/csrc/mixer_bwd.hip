@@ -415,6 +415,9 @@ __global__ void __launch_bounds__(256) mix_decay_sum_kernel(const MixBwdArgs b) 
   }
   if (threadIdx.x == 0) b.dg[blockIdx.x] = (float)sum[0];
 }
+static int launch_decay_sum(const MixBwdArgs& b, hipStream_t stream) {
+  return launch_kernel(reinterpret_cast<const void*>(&mix_decay_sum_kernel), b.m.v_heads, 256, 0, stream, b);
+}
 
 struct BwdLayout {
   size_t tinv, state, grad, D, dX, part, end;
@@ -465,7 +468,13 @@ static int mix_backward(const rssm_mixer_dims* dims, bool delta, MixBwdArgs b, v
   if (rc) return rc;
   const rssm_mixer_dims& d = *dims;
   MixArgs& a = b.m;
-  if (d.seqs == 0) return d.tokens == 0 ? RSSM_OK : RSSM_EINVAL;
+  if (d.seqs == 0 && d.tokens) return RSSM_EINVAL;
+  if (d.decay == RSSM_DECAY_HEAD && !b.dg) return RSSM_EINVAL;
+  if (d.seqs == 0) {  // nothing is written but a decay's gradient that has no token's shape
+    if (d.decay != RSSM_DECAY_HEAD) return RSSM_OK;
+    a.v_heads = d.v_heads;
+    return launch_decay_sum(b, stream);
+  }
   if (!a.cu && d.seqs != 1) return RSSM_EINVAL;
   if (d.tokens > 0 && (!a.q || !a.k || !a.v || !b.dout || !b.dq || !b.dk || !b.dv ||
                        (d.decay && (!a.g || !b.dg)) || (delta && (!a.beta || !b.dbeta))))
@@ -511,8 +520,7 @@ static int mix_backward(const rssm_mixer_dims* dims, bool delta, MixBwdArgs b, v
   if (!rc && d.tokens > 0)
     rc = launch_kernel(f32 ? pick_main<float>(d, delta) : pick_main<bf16>(d, delta), (unsigned)mgrid, 4 * d.dk, 0,
                        stream, b);
-  if (!rc && d.decay == RSSM_DECAY_HEAD && b.dg)
-    rc = launch_kernel(reinterpret_cast<const void*>(&mix_decay_sum_kernel), d.v_heads, 256, 0, stream, b);
+  if (!rc && d.decay == RSSM_DECAY_HEAD) rc = launch_decay_sum(b, stream);
   return rc;
 }
 
