@@ -735,9 +735,12 @@ int linear_attention_forward(const rssm_mixer_dims* dims, const void* q, const v
  *   dq, dk [T, HK, K], dv [T, HV, V] io_dtype; dlog_decay float32 in the shape
  *   of log_decay (NULL without one); dinitial_state [seqs, HV, V, K] float32 by
  *   sequence, zeros where has_initial[i] is 0 (NULL: not computed).
- * The workspace holds both directions' states of every 64 tokens: 8 dk dv bytes
- * for each of them and value head, and (the gated delta rule) about 512 dv and
- * 36 KB more.
+ * Workspaces, for each value head.  A chunk is up to 64 tokens of one sequence: at
+ * most tokens / 64 + seqs of them.  Backward, each: 8 dk dv bytes, and for the
+ * delta rule 512 dv and 36 KB (fp32: 24 KB) more.  Delta rule forward, each: 18 KB
+ * (fp32: 12 KB).  Calls of more than 512 tokens, for segments of long sequences, at
+ * most 4 tokens / 512 of them: 4 dk dv bytes forward and 8 dk dv backward each, and
+ * for the delta rule 6 dk dk forward and 12 dk dk backward (fp32: 4 and 8).
  */
 size_t linear_attention_backward_workspace(const rssm_mixer_dims* dims);
 int linear_attention_backward(const rssm_mixer_dims* dims, const void* dout, const void* q,

@@ -36,14 +36,14 @@ struct MixArgs {
   void* o;
   void* tinv;          // [chunk slots][v_heads][6 (12) fragments][terms][64]
   int32_t* status;
-  float* seg_state;    // [segment slots][v_heads][V][K]
+  float* seg_state;    // [places][v_heads][V][K] (long_base: seq_index.hpp)
   float* seg_grad;     // the same
-  float* seg_decay;    // [segment slots][v_heads]
+  float* seg_decay;    // [places][v_heads]
   const int32_t* order;  // [segment slots]: the longest first, or null
-  void* trans;         // [segment slots][v_heads][K K / 512 (twice) fragments][terms][64]
+  void* trans;         // [places][v_heads][K K / 512 (twice) fragments][terms][64]
   long q_stride, k_stride, v_stride;
   int32_t tokens, seqs, k_heads, v_heads, vpk, dv, num_slots, decay;
-  int32_t seg, slots;  // tokens of a segment, segment slots
+  int32_t seg, slots, few;  // tokens of a segment, segment slots, long_few
   float scale;
 };
 
@@ -628,12 +628,12 @@ struct SegLayout {
 static inline SegLayout seg_layout(const rssm_mixer_dims& d, bool delta, bool both, MixTake& take) {
   SegLayout l{};
   if (d.tokens <= mix_seg(d)) return l;
-  const size_t units = (size_t)scan_slots(d.tokens, d.seqs, mix_seg(d)) * d.v_heads;
+  const size_t units = (size_t)long_places(d.tokens, d.seqs, mix_seg(d)) * d.v_heads;
   const size_t st = units * d.dk * d.dv * 4;
   l.state = take(st);
   l.grad = take(both ? st : 0);
   l.decay = take(delta ? 0 : units * 4);
-  l.order = take(units / d.v_heads * 4);
+  l.order = take((size_t)scan_slots(d.tokens, d.seqs, mix_seg(d)) * 4);
   l.trans = take(delta ? units * d.dk * d.dk / 512 * (both ? 2 : 1) * 64 * (d.io_dtype == RSSM_F32 ? 32 : 48) : 0);
   return l;
 }
@@ -641,6 +641,7 @@ static inline void seg_fill(MixArgs& a, const rssm_mixer_dims& d, const SegLayou
   char* const ws = static_cast<char*>(workspace);
   a.seg = mix_seg(d);
   a.slots = (int)scan_slots(d.tokens, d.seqs, a.seg);
+  a.few = long_few(d.tokens, d.seqs, a.seg);
   a.seg_state = reinterpret_cast<float*>(ws + l.state);
   a.seg_grad = reinterpret_cast<float*>(ws + l.grad);
   a.seg_decay = reinterpret_cast<float*>(ws + l.decay);

@@ -75,7 +75,8 @@ __global__ void __launch_bounds__(4 * V, 2) mix_forward_kernel(const MixArgs a) 
   // its last segment may already have stored the final state over the initial one.
   const bool whole = sp.first && sp.last;
   if (!whole || (a.init && pool >= 0 && (!a.has_init || a.has_init[sp.seq]))) {
-    const float* p = whole ? a.init + place(pool) : a.seg_state + place(un.slot);
+    const float* p = whole ? a.init + place(pool)
+                           : a.seg_state + place(long_base(a.cu, sp.seq, a.seg, a.tokens, a.few) + sp.k);
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt) S[kt] = *reinterpret_cast<const f32x4*>(p + mix_row(kt, 0));
   }

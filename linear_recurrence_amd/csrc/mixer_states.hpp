@@ -22,7 +22,8 @@ struct MixBwdArgs {
   float* D;      // [chunk slots][v_heads][64][V]
   float* dX;     // the same
   float* part;   // [chunk slots][v_heads]: dg summed over the chunk
-  int32_t* new_order;  // of the first launch (MixArgs::order)
+  int32_t* new_order;  // of the first launch (MixArgs::order), of all_slots segments
+  int32_t all_slots;
   long do_stride, cslots;
   int32_t dir_blocks;  // blocks of one direction
   int32_t elems;       // of a state
@@ -47,7 +48,7 @@ struct StatesLds {
 // workgroup (64 classes of length; the order within one does not matter to any result):
 // uneven sequences otherwise leave the longest to the end (16383 tokens of 13 sequences,
 // delta rule: the outputs' launch 315 us instead of 376).
-__device__ static inline void order_segments(const MixArgs& a, int32_t* order) {
+__device__ static inline void order_segments(const MixArgs& a, int slots, int32_t* order) {
   __shared__ int count[65];
   for (int i = threadIdx.x; i < 65; i += blockDim.x) count[i] = 0;
   __syncthreads();
@@ -55,7 +56,7 @@ __device__ static inline void order_segments(const MixArgs& a, int32_t* order) {
     const Segment sg = find_segment(a.cu, a.seqs, a.tokens, a.seg, slot);
     return sg.len == 0 ? 64 : 63 - (int)((sg.len - 1L) * 64 / a.seg);
   };
-  for (int i = threadIdx.x; i < a.slots; i += blockDim.x) atomicAdd(&count[rank(i)], 1);
+  for (int i = threadIdx.x; i < slots; i += blockDim.x) atomicAdd(&count[rank(i)], 1);
   __syncthreads();
   if (threadIdx.x == 0) {
     int at = 0;
@@ -66,7 +67,7 @@ __device__ static inline void order_segments(const MixArgs& a, int32_t* order) {
     }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < a.slots; i += blockDim.x) order[atomicAdd(&count[rank(i)], 1)] = i;
+  for (int i = threadIdx.x; i < slots; i += blockDim.x) order[atomicAdd(&count[rank(i)], 1)] = i;
 }
 
 // One of the two recurrences over the chunks of a segment, a workgroup for one value
@@ -101,7 +102,7 @@ static __global__ void __launch_bounds__(4 * V, BOTH || sizeof(typename Mat<T>::
   const int tid = threadIdx.x, lane = tid & 63, i16 = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   if (!STORE && blockIdx.x + 1 == gridDim.x) {
-    order_segments(a, b.new_order);
+    order_segments(a, b.all_slots, b.new_order);
     return;
   }
   // Batches without a sequence of several segments: found by one look at the table (the
@@ -115,9 +116,11 @@ static __global__ void __launch_bounds__(4 * V, BOTH || sizeof(typename Mat<T>::
   if (STORE && blockIdx.x == 0) check_table(a.cu, a.seqs, a.tokens, a.status);
   if (!un.live) return;
   const int hv = un.hk * a.vpk + un.rest;
-  const Segment sg = find_segment(a.cu, a.seqs, a.tokens, a.seg, un.slot);
+  const Segment sg = STORE ? find_segment(a.cu, a.seqs, a.tokens, a.seg, un.slot)
+                           : find_long(a.cu, a.seqs, a.tokens, a.seg, a.few, un.slot);
   if (sg.len == 0 && !(STORE && sg.empty)) return;
   const bool whole = sg.first && sg.last;
+  const long kept = STORE ? long_base(a.cu, sg.seq, a.seg, a.tokens, a.few) + sg.k : un.slot;  // (not of a whole one)
   // what no other segment starts from (the matrix of a last one: only gradients)
   if (!STORE && (whole || (trans ? sg.last && !BOTH : (back ? sg.first : sg.last)))) return;
   const int pool = STORE && a.init ? mix_slot(a, sg.seq) : -1;
@@ -133,7 +136,7 @@ static __global__ void __launch_bounds__(4 * V, BOTH || sizeof(typename Mat<T>::
     const float* src = back ? b.dfinal : (has ? a.init : nullptr);
     if (!whole) src = back ? a.seg_grad : a.seg_state;
     if (src) {
-      src += place(!whole ? un.slot : (back ? sg.seq : pool));
+      src += place(!whole ? kept : (back ? sg.seq : pool));
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt) S[kt] = *reinterpret_cast<const f32x4*>(src + mix_row(kt, 0));
     }
@@ -391,18 +394,18 @@ static __global__ void __launch_bounds__(4 * V, BOTH || sizeof(typename Mat<T>::
   }
   if (!STORE) {
     if (!trans) {
-      float* p = (back ? a.seg_grad : a.seg_state) + place(un.slot);
+      float* p = (back ? a.seg_grad : a.seg_state) + place(kept);
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt) *reinterpret_cast<f32x4*>(p + mix_row(kt, 0)) = S[kt];
       // once, so that the same call gives the same bits: forward but for a last segment
-      if (!DELTA && tid == 0 && back == sg.last) a.seg_decay[(long)un.slot * a.v_heads + hv] = total;
+      if (!DELTA && tid == 0 && back == sg.last) a.seg_decay[kept * a.v_heads + hv] = total;
       return;
     }
     if constexpr (DELTA) {
     // fragments (rows kt, columns jb) of the matrix, then (rows jt, columns kb) of its transpose
     constexpr int NF = KT * KB, LM = K + 4;
     char* const out = static_cast<char*>(a.trans) +
-        ((long)un.slot * a.v_heads + hv) * ((BOTH ? 2 : 1) * NF * TS * 64 * sizeof(Frag));
+        (kept * a.v_heads + hv) * ((BOTH ? 2 : 1) * NF * TS * 64 * sizeof(Frag));
     if (BOTH) {
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb) {
@@ -440,6 +443,14 @@ static __global__ void __launch_bounds__(4 * V, BOTH || sizeof(typename Mat<T>::
   }
 }
 
+// The sequence that a combining workgroup takes: the n-th, or, where most are short, the
+// one whose segments begin at place n; -1: none.
+__device__ static inline int combine_seq(const MixArgs& a, int n) {
+  if (a.few) return n;
+  const Segment sg = find_long(a.cu, a.seqs, a.tokens, a.seg, false, n);
+  return sg.len && sg.first ? sg.seq : -1;
+}
+
 // Each sequence's segments in order (backward: from the last): what a segment adds is
 // replaced by the state (the gradient) it starts from, S <- M S + N.  The delta rule: a
 // workgroup for 32 columns, a wave for 32 rows of them: it reads its rows of M alone, the
@@ -457,7 +468,8 @@ static __global__ void __launch_bounds__(2 * K) mix_combine_kernel(const MixBwdA
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const bool back = (int)blockIdx.x >= b.dir_blocks, both = a.seg_grad != nullptr;
   const int id = back ? blockIdx.x - b.dir_blocks : blockIdx.x;
-  const int hv = id / KB % a.v_heads, c0 = id % KB * 32, seq = id / KB / a.v_heads;
+  const int hv = id / KB % a.v_heads, c0 = id % KB * 32, seq = combine_seq(a, id / KB / a.v_heads);
+  if (seq < 0) return;
   const SeqSpan sp = seq_span(a.cu, seq, a.seqs, a.tokens);
   const int segs = (sp.len + a.seg - 1) / a.seg;
   if (segs <= 1) return;
@@ -467,7 +479,7 @@ static __global__ void __launch_bounds__(2 * K) mix_combine_kernel(const MixBwdA
   };
   const int pool = a.init ? mix_slot(a, seq) : -1;
   const bool has = pool >= 0 && (!a.has_init || a.has_init[seq]);
-  const long base = seg_base(a.cu, seq, a.seg, a.tokens);
+  const long base = long_base(a.cu, seq, a.seg, a.tokens, a.few);
   const auto slot_of = [&](int n) { return base + (back ? segs - 1 - n : n); };
   float* const mat = back ? a.seg_grad : a.seg_state;
   const Minus minus;
@@ -550,7 +562,9 @@ static __global__ void __launch_bounds__(256) mix_combine_decay_kernel(const Mix
   const bool back = (int)blockIdx.x >= b.dir_blocks;
   const int id = back ? blockIdx.x - b.dir_blocks : blockIdx.x;
   const int elems = b.elems, per = elems / 1024;
-  const int e = (id % per * 256 + (int)threadIdx.x) * 4, hv = id / per % a.v_heads, seq = id / per / a.v_heads;
+  const int e = (id % per * 256 + (int)threadIdx.x) * 4, hv = id / per % a.v_heads;
+  const int seq = combine_seq(a, id / per / a.v_heads);
+  if (seq < 0) return;
   const SeqSpan sp = seq_span(a.cu, seq, a.seqs, a.tokens);
   const int segs = (sp.len + a.seg - 1) / a.seg;
   if (segs <= 1) return;
@@ -559,7 +573,7 @@ static __global__ void __launch_bounds__(256) mix_combine_decay_kernel(const Mix
   const float* src = back ? b.dfinal : (has ? a.init : nullptr);
   f32x4 S = {0.f, 0.f, 0.f, 0.f};
   if (src) S = *reinterpret_cast<const f32x4*>(src + ((long)(back ? seq : pool) * a.v_heads + hv) * elems + e);
-  const long base = seg_base(a.cu, seq, a.seg, a.tokens);
+  const long base = long_base(a.cu, seq, a.seg, a.tokens, a.few);
   float* const mat = back ? a.seg_grad : a.seg_state;
   // eight segments' loads at a time: one after another they would take a memory
   // latency each
@@ -591,8 +605,8 @@ static __global__ void __launch_bounds__(256) mix_combine_decay_kernel(const Mix
 
 // Whether those launches hold fewer than 2^32 threads each.
 static inline bool segments_fit(const MixArgs& a, int dk) {
-  const long dir = mix_grid(a.slots, a.k_heads, a.vpk);
-  return grid_fits(3 * dir + 1, 512) && grid_fits(2L * a.seqs * a.v_heads * (dk * a.dv / 1024), 256);
+  const long dir = mix_grid(a.slots, a.k_heads, a.vpk), seqs = a.few ? a.seqs : long_places(a.tokens, a.seqs, a.seg);
+  return grid_fits(3 * dir + 1, 512) && grid_fits(2 * seqs * a.v_heads * (dk * a.dv / 1024), 256);
 }
 
 template <typename T, bool BOTH>
@@ -611,13 +625,15 @@ static const void* pick_segments(int dk, int dv, bool delta) {
 template <typename T, bool BOTH>
 static int launch_segments(MixBwdArgs b, int dk, bool delta, hipStream_t stream) {
   const MixArgs& a = b.m;
-  const long dir = mix_grid(a.slots, a.k_heads, a.vpk);
-  const long cdir = (long)a.seqs * a.v_heads * (delta ? dk / 32 : dk * a.dv / 1024);
+  const long places = long_places(a.tokens, a.seqs, a.seg), dir = mix_grid(places, a.k_heads, a.vpk);
+  const long cdir = (a.few ? a.seqs : places) * a.v_heads * (delta ? dk / 32 : dk * a.dv / 1024);
   b.dir_blocks = (int)dir;
   b.elems = dk * a.dv;
   MixBwdArgs first = b;  // its own units are in no order yet: the last block makes it
   first.new_order = const_cast<int32_t*>(b.m.order);
   first.m.order = nullptr;
+  first.all_slots = a.slots;
+  first.m.slots = (int)places;
   const int rc = launch_kernel(pick_segments<T, BOTH>(dk, a.dv, delta),
                                (unsigned)(((BOTH ? 2 : 1) + delta) * dir + 1), 4 * a.dv, 0, stream, first);
   if (rc) return rc;

@@ -58,18 +58,13 @@ RSSM_HD static inline int seg_base(const int32_t* cu, int i, int seg, int tokens
   const int a = cu[i];
   return (a < 0 ? 0 : (a > tokens ? tokens : a)) / seg + i;
 }
-RSSM_HD static inline Segment find_segment(const int32_t* cu, int nseq, int tokens, int seg,
-                                              int slot) {
-  int lo = 0, hi = nseq;
-  while (hi - lo > 1) {
-    const int m = (lo + hi) >> 1;
-    if (seg_base(cu, m, seg, tokens) <= slot) lo = m; else hi = m;
-  }
-  const SeqSpan sp = seq_span(cu, lo, nseq, tokens);
+// Segment k of sequence i.
+RSSM_HD static inline Segment segment_of(const int32_t* cu, int i, int nseq, int tokens, int seg, int k) {
+  const SeqSpan sp = seq_span(cu, i, nseq, tokens);
   Segment r;
-  r.seq = lo;
+  r.seq = i;
   r.bad = sp.bad;
-  r.k = slot - seg_base(cu, lo, seg, tokens);
+  r.k = k;
   const long off = (long)r.k * seg;
   r.empty = sp.len == 0 && r.k == 0;
   r.len = r.k < 0 || off >= sp.len ? 0 : (sp.len - off < seg ? (int)(sp.len - off) : seg);
@@ -78,9 +73,44 @@ RSSM_HD static inline Segment find_segment(const int32_t* cu, int nseq, int toke
   r.last = off + seg >= sp.len;
   return r;
 }
+RSSM_HD static inline Segment find_segment(const int32_t* cu, int nseq, int tokens, int seg,
+                                              int slot) {
+  int lo = 0, hi = nseq;
+  while (hi - lo > 1) {
+    const int m = (lo + hi) >> 1;
+    if (seg_base(cu, m, seg, tokens) <= slot) lo = m; else hi = m;
+  }
+  return segment_of(cu, lo, nseq, tokens, seg, slot - seg_base(cu, lo, seg, tokens));
+}
 
 // Slots that the segments of a call may take.
 RSSM_HD static inline long scan_slots(long tokens, long seqs, long seg) { return tokens / seg + seqs; }
+
+// Places of the segments of sequences longer than one, where each keeps whole states:
+// short sequences, however many, add none.  Sequence i's begin at start_i/seg + i as
+// above while there are few sequences, and otherwise at 2 start_i/seg: n tokens, n > seg,
+// have n/seg (rounded up) segments, and 2 n/seg (rounded down) are at least as many.
+// At most 4 tokens/seg places.  (13 sequences of 16383 tokens, segments of 2048: the first
+// way 20 places, the second 15, whose search takes the combining launch 20 us for 8.)
+RSSM_HD static inline bool long_few(long tokens, long seqs, long seg) { return seqs <= 3 * (tokens / seg); }
+RSSM_HD static inline long long_places(long tokens, long seqs, long seg) {
+  return long_few(tokens, seqs, seg) ? tokens / seg + seqs : 2 * tokens / seg;
+}
+RSSM_HD static inline int long_base(const int32_t* cu, int i, int seg, int tokens, bool few) {
+  if (few || !cu) return seg_base(cu, i, seg, tokens);
+  const int a = cu[i];
+  return (int)(2L * (a < 0 ? 0 : (a > tokens ? tokens : a)) / seg);
+}
+// The segment of a place: the last sequence that begins at it or before (later ones
+// begin behind a long one's places).  Sequences of one segment are `first` and `last`.
+RSSM_HD static inline Segment find_long(const int32_t* cu, int nseq, int tokens, int seg, bool few, int place) {
+  int lo = 0, hi = nseq;
+  while (hi - lo > 1) {
+    const int m = (lo + hi) >> 1;
+    if (long_base(cu, m, seg, tokens, few) <= place) lo = m; else hi = m;
+  }
+  return segment_of(cu, lo, nseq, tokens, seg, place - long_base(cu, lo, seg, tokens, few));
+}
 
 // Columns of the two tiles of a pair (32 columns) interleave in granules of 4,
 // tile j's index i standing for column 8*(i/4) + 4*j + i%4: a lane that holds
