@@ -498,9 +498,9 @@ static int mix_backward(const rssm_mixer_dims* dims, bool delta, MixBwdArgs b, v
   const bool f32 = d.io_dtype == RSSM_F32;
   b.cslots = scan_slots(d.tokens, d.seqs, kQ);
   seg_fill(a, d, l.seg, workspace);
-  const long dir = mix_grid(a.slots, d.k_heads, a.vpk), mgrid = b.cslots * d.k_heads;
-  if (!segments_fit(a, d.dk) || !grid_fits(mgrid, 4 * d.dk) ||
-      !grid_fits(b.cslots * ((d.v_heads + 3) / 4), 256))
+  const long dir = mix_grid(scan_slots(d.tokens, d.seqs, a.seg), d.k_heads, a.vpk), mgrid = b.cslots * d.k_heads;
+  if (!grid_fits(2 * dir, 4 * d.dv) || !segments_fit(a, d.dk, delta, true) || !grid_fits(mgrid, 4 * d.dk) ||
+      (delta && !grid_fits(b.cslots * ((d.v_heads + 3) / 4), 256)))
     return RSSM_ESHAPE;
   b.dir_blocks = (int)dir;
   if (d.tokens == 0) {  // no chunks, and no gradient of a decay but zero

@@ -320,8 +320,8 @@ static size_t mix_forward_bytes(const rssm_mixer_dims* dims, bool delta) {
 // both halves' workgroups, since a chunk takes less time with one wave a SIMD than with
 // two, and every half does the tokens' products again (delta rule, 32 heads of 128, 512
 // tokens: 60 us instead of 69; fp32 122 instead of 170).
-static int forward_columns(const rssm_mixer_dims& d, const MixArgs& a) {
-  return d.dv == 128 && (long)a.slots * d.v_heads <= 128 ? 64 : d.dv;
+static int forward_columns(const rssm_mixer_dims& d, long slots) {
+  return d.dv == 128 && slots * d.v_heads <= 128 ? 64 : d.dv;
 }
 template <typename T>
 static const void* pick_forward(int dk, int columns, bool delta) {
@@ -372,10 +372,12 @@ static int mix_forward(const rssm_mixer_dims* dims, bool delta, const void* q, c
   a.tinv = static_cast<char*>(workspace) + l.tinv;
   seg_fill(a, d, l.seg, workspace);
   a.seg_grad = nullptr;  // no gradients to combine
-  const long cslots = scan_slots(d.tokens, d.seqs, kQ);
-  const int columns = forward_columns(d, a);
-  const long grid = mix_grid(a.slots, d.k_heads, a.vpk * (d.dv / columns));
-  if (!segments_fit(a, d.dk) || (delta && !grid_fits(cslots * ((d.v_heads + 3) / 4), 256))) return RSSM_ESHAPE;
+  const long cslots = scan_slots(d.tokens, d.seqs, kQ), slots = scan_slots(d.tokens, d.seqs, a.seg);
+  const int columns = forward_columns(d, slots);
+  const long grid = mix_grid(slots, d.k_heads, a.vpk * (d.dv / columns));
+  if (!grid_fits(grid, 4 * columns) || !segments_fit(a, d.dk, delta, false) ||
+      (delta && !grid_fits(cslots * ((d.v_heads + 3) / 4), 256)))
+    return RSSM_ESHAPE;
   if (delta && d.tokens > 0) {
     rc = f32 ? launch_inverse<float, false>(a, d.dk, cslots, stream)
              : launch_inverse<bf16, false>(a, d.dk, cslots, stream);

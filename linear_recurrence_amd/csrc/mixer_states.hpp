@@ -603,10 +603,22 @@ static __global__ void __launch_bounds__(256) mix_combine_decay_kernel(const Mix
   }
 }
 
-// Whether those launches hold fewer than 2^32 threads each.
-static inline bool segments_fit(const MixArgs& a, int dk) {
-  const long dir = mix_grid(a.slots, a.k_heads, a.vpk), seqs = a.few ? a.seqs : long_places(a.tokens, a.seqs, a.seg);
-  return grid_fits(3 * dir + 1, 512) && grid_fits(2 * seqs * a.v_heads * (dk * a.dv / 1024), 256);
+// Blocks of those launches, in one direction: of a recurrence over the segments, and of
+// the combination.
+struct SegGrids {
+  long dir, combine;
+};
+static inline SegGrids segment_grids(const MixArgs& a, int dk, bool delta) {
+  const long places = long_places(a.tokens, a.seqs, a.seg);
+  return {mix_grid(places, a.k_heads, a.vpk),
+          (a.few ? a.seqs : places) * a.v_heads * (delta ? dk / 32 : dk * a.dv / 1024)};
+}
+// Whether they hold fewer than 2^32 threads each, where a call has them.
+static inline bool segments_fit(const MixArgs& a, int dk, bool delta, bool both) {
+  if (a.tokens <= a.seg) return true;
+  const SegGrids n = segment_grids(a, dk, delta);
+  const int ways = both ? 2 : 1;
+  return grid_fits((ways + delta) * n.dir + 1, 4 * a.dv) && grid_fits(ways * n.combine, delta ? 2 * dk : 256);
 }
 
 template <typename T, bool BOTH>
@@ -625,24 +637,23 @@ static const void* pick_segments(int dk, int dv, bool delta) {
 template <typename T, bool BOTH>
 static int launch_segments(MixBwdArgs b, int dk, bool delta, hipStream_t stream) {
   const MixArgs& a = b.m;
-  const long places = long_places(a.tokens, a.seqs, a.seg), dir = mix_grid(places, a.k_heads, a.vpk);
-  const long cdir = (a.few ? a.seqs : places) * a.v_heads * (delta ? dk / 32 : dk * a.dv / 1024);
-  b.dir_blocks = (int)dir;
+  const SegGrids n = segment_grids(a, dk, delta);
+  b.dir_blocks = (int)n.dir;
   b.elems = dk * a.dv;
   MixBwdArgs first = b;  // its own units are in no order yet: the last block makes it
   first.new_order = const_cast<int32_t*>(b.m.order);
   first.m.order = nullptr;
   first.all_slots = a.slots;
-  first.m.slots = (int)places;
+  first.m.slots = (int)long_places(a.tokens, a.seqs, a.seg);
   const int rc = launch_kernel(pick_segments<T, BOTH>(dk, a.dv, delta),
-                               (unsigned)(((BOTH ? 2 : 1) + delta) * dir + 1), 4 * a.dv, 0, stream, first);
+                               (unsigned)(((BOTH ? 2 : 1) + delta) * n.dir + 1), 4 * a.dv, 0, stream, first);
   if (rc) return rc;
-  b.dir_blocks = (int)cdir;
+  b.dir_blocks = (int)n.combine;
   const void* fn = reinterpret_cast<const void*>(&mix_combine_decay_kernel);
   if (delta)
     fn = dk == 64 ? reinterpret_cast<const void*>(&mix_combine_kernel<T, 64>)
                   : reinterpret_cast<const void*>(&mix_combine_kernel<T, 128>);
-  return launch_kernel(fn, (unsigned)((BOTH ? 2 : 1) * cdir), delta ? 2 * dk : 256, 0, stream, b);
+  return launch_kernel(fn, (unsigned)((BOTH ? 2 : 1) * n.combine), delta ? 2 * dk : 256, 0, stream, b);
 }
 
 }  // namespace rssm

@@ -126,3 +126,25 @@ def test_many_sequences_the_same_bits():
         kept = [t.clone() for t in got]
         for a, b in zip(both(), kept):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("delta", [False, True])
+@pytest.mark.parametrize("T", [300, 16500])
+def test_a_batch_of_16500_sequences(T, delta):
+    """Of one token or none, from zeros: o = scale beta (q.k) v.  With 32 heads of 128
+    the launches hold fewer than 2^32 threads, and those of segments, which such a
+    batch has none of, do not count."""
+    n, HK, HV, K = 16500, 16, 32, 128
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    q, k, v = (torch.randn(T, h, K, generator=gen, device="cuda").to(BF16) for h in (HK, HK, HV))
+    g, beta = -torch.rand(T, HV, generator=gen, device="cuda"), torch.rand(T, HV, generator=gen, device="cuda")
+    cu = torch.arange(n + 1, device="cuda").clamp(max=T).to(torch.int32)
+    if delta:
+        o = R.gdn_scan_forward(q, k, v, g, beta, cu_seqlens=cu)
+    else:
+        o, beta = R.linear_attention_forward(q, k, v, g, cu_seqlens=cu), torch.ones_like(beta)
+    qk = (q.double() * k.double()).sum(2).repeat_interleave(2, 1)
+    want = (beta.double() * qk / math.sqrt(K))[:, :, None] * v.double()
+    # 128 products, each and their sums off by 2^-24 of |q| |k|, and the bf16 result
+    size = (q.double().norm(dim=2) * k.double().norm(dim=2)).repeat_interleave(2, 1) / math.sqrt(K)
+    assert ((o.double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -17 * size[:, :, None] * v.double().abs()).all()

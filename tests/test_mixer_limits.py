@@ -4,7 +4,7 @@ their ranges: on the host, before any HIP call."""
 import pytest
 
 import linear_recurrence_amd as R
-from test_mixer_refusals import EINVAL, OK, _mix
+from test_mixer_refusals import EINVAL, ESHAPE, OK, SEQ, _mix
 
 
 @pytest.fixture(scope="module")
@@ -17,3 +17,13 @@ def test_a_heads_decay_always_has_a_gradient(lib):
     for seqs in (0, 2):
         assert _mix(lib, "linear_attention_backward", decay=1, tokens=0, seqs=seqs, gg=None) == EINVAL
     assert _mix(lib, "linear_attention_backward", decay=2, tokens=0, seqs=0, gg=None) == OK
+
+
+@pytest.mark.parametrize("fn", SEQ)
+def test_launches_of_2_32_threads_are_refused(lib, fn):
+    """Where only one kind of launch would be too large, and where the number of
+    segment slots passes 32 bits."""
+    for dims in (dict(tokens=8, seqs=1 << 23), dict(tokens=8, seqs=1 << 22, dk=64 if "linear" in fn else 128, dv=128),
+                 dict(tokens=4096, seqs=(1 << 31) - 1), dict(tokens=(1 << 31) - 1, seqs=(1 << 31) - 1),
+                 dict(tokens=(1 << 31) - 1, k_heads=256, v_heads=1 << 20), dict(tokens=8, v_heads=1 << 20, seqs=1 << 6)):
+        assert _mix(lib, fn, **dims, ws=1 << 62) == ESHAPE, dims
