@@ -797,7 +797,7 @@ int gdn_scan_backward(const rssm_mixer_dims* dims, const void* dout, const void*
  */
 typedef struct rssm_rotary_dims {
   int32_t tokens;
-  int32_t heads;
+  int32_t heads;        /* up to 2^30                                       */
   int32_t dim;          /* elements of a head, up to 1024                   */
   int32_t rotary_dim;   /* even, 2 to dim                                   */
   int32_t io_dtype;

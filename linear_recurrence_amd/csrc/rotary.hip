@@ -129,7 +129,8 @@ static int rotary(const rssm_rotary_dims* dims, const void* x, const void* posit
   if (d.tokens < 0 || d.heads < 1 || d.dim < 2 || d.rotary_dim < 2 || d.rotary_dim > d.dim || d.rotary_dim % 2)
     return RSSM_EINVAL;
   if (!valid_dtype(d.io_dtype)) return RSSM_EDTYPE;
-  if (d.dim > 1024) return RSSM_ESHAPE;
+  // a thread's head, and the one that it steps to, are counted in 32 bits
+  if (d.dim > 1024 || d.heads > 1 << 30) return RSSM_ESHAPE;
   const long row = (long)d.heads * d.dim, es = d.io_dtype == RSSM_F32 ? 4 : 2;
   if ((d.x_stride && d.x_stride < row) || (d.y_stride && d.y_stride < row)) return RSSM_EINVAL;
   if (d.tokens == 0) return RSSM_OK;
@@ -160,7 +161,7 @@ static int rotary(const rssm_rotary_dims* dims, const void* x, const void* posit
   // Tokens enough for a thread each in the table, while there are 1024 workgroups;
   // then the heads are split until there are, down to one round of the threads.
   a.tok = 256 / a.half < 1 ? 1 : 256 / a.half;
-  while (a.tok > 1 && (d.tokens + a.tok - 1) / a.tok < 1024) a.tok = (a.tok + 1) / 2;
+  while (a.tok > 1 && ((long)d.tokens + a.tok - 1) / a.tok < 1024) a.tok = (a.tok + 1) / 2;
   const long blocks = ((long)d.tokens + a.tok - 1) / a.tok;
   const int step = 256 / a.items;
   a.hpg = d.heads;

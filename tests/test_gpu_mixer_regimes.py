@@ -4,11 +4,13 @@ batches of more sequences than a wave has lanes."""
 
 import math
 
+import numpy as np
 import pytest
 import torch
 
 import linear_recurrence_amd as R
-from test_gpu_mixer import BF16, F32, Mix
+from oracle import mixer as X
+from test_gpu_mixer import BF16, F32, Mix, _near, _np
 
 pytestmark = pytest.mark.gpu
 
@@ -148,3 +150,16 @@ def test_a_batch_of_16500_sequences(T, delta):
     # 128 products, each and their sums off by 2^-24 of |q| |k|, and the bf16 result
     size = (q.double().norm(dim=2) * k.double().norm(dim=2)).repeat_interleave(2, 1) / math.sqrt(K)
     assert ((o.double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -17 * size[:, :, None] * v.double().abs()).all()
+
+
+def test_rotary_of_the_most_tokens():
+    """2^31 - 1 of them, one head of one pair: in place, a few against the oracle."""
+    T = 2 ** 31 - 1
+    x = torch.full((T, 1, 2), 0.5, dtype=BF16, device="cuda")
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    f = torch.tensor([0.37], device="cuda")
+    R.rotary_forward(x, pos, f, out=x)
+    at = torch.tensor([0, 1, 255, 256, 2 ** 24 + 3, 2 ** 30, T - 257, T - 1], device="cuda")
+    want = X.rotary(np.full((len(at), 1, 2), 0.5), _np(pos[at]), _np(f))
+    # the angle, up to 2^30, is off by 2^-53 of itself a step: 2^-20 covers it
+    _near(x[at], want, 2.0 ** -8 * abs(want) + 2.0 ** -20, "turned")

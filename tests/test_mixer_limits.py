@@ -4,7 +4,7 @@ their ranges: on the host, before any HIP call."""
 import pytest
 
 import linear_recurrence_amd as R
-from test_mixer_refusals import EINVAL, ESHAPE, OK, SEQ, _mix
+from test_mixer_refusals import EINVAL, ESHAPE, OK, SEQ, V, _mix, _rot
 
 
 @pytest.fixture(scope="module")
@@ -27,3 +27,10 @@ def test_launches_of_2_32_threads_are_refused(lib, fn):
                  dict(tokens=4096, seqs=(1 << 31) - 1), dict(tokens=(1 << 31) - 1, seqs=(1 << 31) - 1),
                  dict(tokens=(1 << 31) - 1, k_heads=256, v_heads=1 << 20), dict(tokens=8, v_heads=1 << 20, seqs=1 << 6)):
         assert _mix(lib, fn, **dims, ws=1 << 62) == ESHAPE, dims
+
+
+@pytest.mark.parametrize("fn", ["rotary_forward", "rotary_backward"])
+@pytest.mark.parametrize("heads", [(1 << 30) + 1, (1 << 31) - 1])
+def test_rotary_heads_are_counted_in_32_bits(lib, fn, heads):
+    """A thread steps past the last of them: past 2^31 it would begin at -2^31 again."""
+    assert _rot(lib, fn, y=V(1 << 50), tokens=1, heads=heads, dim=2, rotary_dim=2) == ESHAPE
