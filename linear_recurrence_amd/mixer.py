@@ -72,8 +72,8 @@ def _heads(q, k, v, decay, beta, scale, delta):
     _sizes(v, "v")
     HV, V = v.shape[1], v.shape[2]
     d = MixerDims(T, 1, HK, HV, K, V, 0, _DT[io], _NONE, 0.0 if scale is None else scale)
-    if scale is not None and not scale > 0:
-        raise ValueError(f"scale is {scale}, expected a positive number (None: 1/sqrt(dk))")
+    if scale is not None and not 0 < d.scale < math.inf:   # as the library gets it, in 32 bits
+        raise ValueError(f"scale is {scale}, expected a positive float32 number (None: 1/sqrt(dk))")
     d.q_stride = _rows(q, "q", io, (T, HK, K), dev)
     d.k_stride = _rows(k, "k", io, (T, HK, K), dev)
     d.v_stride = _rows(v, "v", io, (T, HV, V), dev)
