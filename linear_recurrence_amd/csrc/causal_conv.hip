@@ -500,13 +500,8 @@ static bool elt_aligned(const void* p, int32_t dtype) {
 // rows out[0..rows), channels of either io_dtype elements: workgroups read up to
 // W-1 rows that another one's results would replace.
 static bool rows_meet(const void* in, long stride, const void* out, const rssm_conv_dims& d) {
-  if (!in || !out || d.tokens == 0) return false;
-  const long es = d.io_dtype == RSSM_F32 ? 4 : 2, len = d.channels * es, step = stride * es;
-  const intptr_t a = reinterpret_cast<intptr_t>(in), b = reinterpret_cast<intptr_t>(out);
-  const intptr_t end = b + d.tokens * len;
-  // the first row that ends behind the output's start
-  const long k = a + len > b ? 0 : (b - a - len) / step + 1;
-  return k < d.tokens && a + k * step < end;
+  const long es = d.io_dtype == RSSM_F32 ? 4 : 2, len = d.channels * es;
+  return rows_meet(in, stride * es, len, d.tokens, out, d.tokens * len);
 }
 
 #define RSSM_CONV_PICK(name, d)                                                        \

@@ -502,6 +502,17 @@ static int mix_backward(const rssm_mixer_dims* dims, bool delta, MixBwdArgs b, v
   if (!grid_fits(2 * dir, 4 * d.dv) || !segments_fit(a, d.dk, delta, true) || !grid_fits(mgrid, 4 * d.dk) ||
       (delta && !grid_fits(b.cslots * ((d.v_heads + 3) / 4), 256)))
     return RSSM_ESHAPE;
+  const long es = f32 ? 4 : 2, qk = (long)d.k_heads * d.dk, vw = (long)d.v_heads * d.dv;
+  void* const results[] = {b.dq, b.dk, b.dv};
+  for (void* p : results) {
+    const long columns = p == b.dv ? vw : qk;
+    if (mix_meets(a, d, p, columns) || rows_meet(b.dout, b.do_stride * es, vw * es, d.tokens, p, d.tokens * columns * es))
+      return RSSM_EINVAL;
+  }
+  if (b.dinit) {  // by sequence, the pool by slot
+    const long state = (long)d.v_heads * d.dv * d.dk * 4;
+    if (rows_meet(a.init, state, state, d.num_slots, b.dinit, d.seqs * state)) return RSSM_EINVAL;
+  }
   b.dir_blocks = (int)dir;
   if (d.tokens == 0) {  // no chunks, and no gradient of a decay but zero
     b.cslots = 0;

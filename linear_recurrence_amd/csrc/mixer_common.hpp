@@ -598,6 +598,21 @@ static inline void mix_fill(MixArgs& a, const rssm_mixer_dims& d) {
   a.scale = d.scale > 0.f ? d.scale : 1.f / sqrtf((float)d.dk);
 }
 
+// Whether a dense result with these heads' rows shares memory with q, k or v, which other
+// workgroups may still read when it is written.
+static inline bool mix_meets(const MixArgs& a, const rssm_mixer_dims& d, const void* out, long columns) {
+  const long es = d.io_dtype == RSSM_F32 ? 4 : 2, qk = (long)d.k_heads * d.dk * es, v = (long)d.v_heads * d.dv * es;
+  const long bytes = d.tokens * columns * es;
+  return rows_meet(a.q, a.q_stride * es, qk, d.tokens, out, bytes) ||
+         rows_meet(a.k, a.k_stride * es, qk, d.tokens, out, bytes) ||
+         rows_meet(a.v, a.v_stride * es, v, d.tokens, out, bytes);
+}
+// Whether two pools that are not one share memory: a slot's new state would be over another's.
+static inline bool pools_meet(const rssm_mixer_dims& d, const float* in, const float* out) {
+  const long bytes = (long)d.num_slots * d.v_heads * d.dv * d.dk * 4;
+  return in != out && rows_meet(in, bytes, bytes, d.num_slots > 0, out, bytes);
+}
+
 // Tokens of a segment.  A sequence longer than this is worked on in segments: what each
 // adds from zero and (the delta rule) the matrix that its start goes through, then
 // their combination, then all segments at once.  That is up to three times the

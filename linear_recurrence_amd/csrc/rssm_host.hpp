@@ -20,6 +20,16 @@ static inline bool valid_dtype(int32_t t) { return t == RSSM_F32 || t == RSSM_BF
 // A launch holds fewer than 2^32 threads.
 static inline bool grid_fits(long grid, long threads) { return grid * threads < (1L << 32); }
 
+// Whether any of so many rows of len bytes, step bytes apart, shares memory with the
+// bytes of out.
+static inline bool rows_meet(const void* in, long step, long len, long rows, const void* out, long bytes) {
+  if (!in || !out || rows == 0) return false;
+  const intptr_t a = reinterpret_cast<intptr_t>(in), b = reinterpret_cast<intptr_t>(out);
+  // the first row that ends behind the output's start
+  const long k = a + len > b ? 0 : (b - a - len) / step + 1;
+  return k < rows && a + k * step < b + bytes;
+}
+
 // Launch with the error code of the launch itself (not a stale one left in
 // the thread's last-error slot by earlier runtime calls).
 template <typename Args>

@@ -4,7 +4,7 @@ their ranges: on the host, before any HIP call."""
 import pytest
 
 import linear_recurrence_amd as R
-from test_mixer_refusals import EINVAL, ESHAPE, OK, SEQ, V, _mix, _rot
+from test_mixer_refusals import EINVAL, ESHAPE, NAMES, OK, SEQ, V, _mix, _rot
 
 
 @pytest.fixture(scope="module")
@@ -34,3 +34,31 @@ def test_launches_of_2_32_threads_are_refused(lib, fn):
 def test_rotary_heads_are_counted_in_32_bits(lib, fn, heads):
     """A thread steps past the last of them: past 2^31 it would begin at -2^31 again."""
     assert _rot(lib, fn, y=V(1 << 50), tokens=1, heads=heads, dim=2, rotary_dim=2) == ESHAPE
+
+
+FAR = {n: V((i + 2) << 40) for i, n in enumerate(
+    "q k v do g beta cu has slot init final state new o gq gk gv gg gbeta dfinal dinit ws".split())}
+
+
+@pytest.mark.parametrize("fn", list(NAMES))
+def test_results_over_inputs_are_refused(lib, fn):
+    """Only refused calls: the pointers are made up.  8 tokens of bf16, 2 key and 4 value
+    heads of 64: rows of 256 and 512 bytes."""
+    names, back = NAMES[fn].split(), "backward" in fn
+
+    def call(out, over, at, **dims):
+        base = FAR[over].value
+        return _mix(lib, fn, **{**{n: FAR[n] for n in names if n != "ws"}, **dims, out: V(base + at)})
+    for out, row in (("gq", 256), ("gk", 256), ("gv", 512)) if back else (("o", 512),):
+        for over, width in (("q", 256), ("k", 256), ("v", 512)) + ((("do", 512),) if back else ()):
+            for at in (0, 16, 8 * width - 16, 16 - 8 * row):
+                assert call(out, over, at) == EINVAL, (out, over, at)
+            if over == "do":
+                continue
+            # rows of wider ones: over the last, and up to the second
+            for at in (7 * 2048 + width - 16, 2048 - 8 * row + 16):
+                assert call(out, over, at, **{over + "_stride": 1024}) == EINVAL, (out, over, at)
+    pool = 4 * 64 * 64 * 4   # bytes of a slot: two of them
+    pairs = dict(linear_attention_decode=("new", "state")).get(fn, ("dinit", "init") if back else ("final", "init"))
+    for at in (16, 2 * pool - 16, 16 - 2 * pool) + ((0,) if back else ()):
+        assert call(*pairs, at) == EINVAL, at
