@@ -110,9 +110,15 @@ static __global__ void __launch_bounds__(4 * V, BOTH || sizeof(typename Mat<T>::
   // heads; this takes 6).
   if (!STORE && a.seqs > 1 && a.seqs <= 64 &&
       !__any(lane < a.seqs && seq_span(a.cu, lane, a.seqs, a.tokens).len > a.seg)) return;
-  const bool back = BOTH && (int)blockIdx.x >= b.dir_blocks && (int)blockIdx.x < 2 * b.dir_blocks;
-  const bool trans = !STORE && DELTA && (int)blockIdx.x >= (BOTH ? 2 : 1) * b.dir_blocks;
-  const MixUnit un = mix_unit(a, blockIdx.x - (trans ? (BOTH ? 2 : 1) : back) * b.dir_blocks, a.vpk);
+  // The kinds of a segment's block stand side by side: in parts of the grid of their own,
+  // the second's live blocks met the first's on some units and left others idle, or did
+  // not, by the time that empty blocks took (16383 tokens of 13 sequences: 175 us or 260).
+  constexpr int KINDS = STORE ? 1 : 1 + BOTH + DELTA;
+  const int second = STORE && (int)blockIdx.x >= b.dir_blocks;
+  const int turn = blockIdx.x >> 3, kind = STORE ? second : turn % KINDS;  // (the lowest bits: the die)
+  const bool back = BOTH && kind == 1, trans = !STORE && DELTA && kind == KINDS - 1;
+  const MixUnit un = mix_unit(a, STORE ? blockIdx.x - second * b.dir_blocks
+                                       : turn / KINDS * 8 + (blockIdx.x & 7), a.vpk);
   if (STORE && blockIdx.x == 0) check_table(a.cu, a.seqs, a.tokens, a.status);
   if (!un.live) return;
   const int hv = un.hk * a.vpk + un.rest;
@@ -603,22 +609,21 @@ static __global__ void __launch_bounds__(256) mix_combine_decay_kernel(const Mix
   }
 }
 
-// Blocks of those launches, in one direction: of a recurrence over the segments, and of
-// the combination.
+// Blocks of those launches: of the recurrences over the segments, and of one direction's
+// combination.
 struct SegGrids {
-  long dir, combine;
+  long states, combine;
 };
-static inline SegGrids segment_grids(const MixArgs& a, int dk, bool delta) {
+static inline SegGrids segment_grids(const MixArgs& a, int dk, bool delta, bool both) {
   const long places = long_places(a.tokens, a.seqs, a.seg);
-  return {mix_grid(places, a.k_heads, a.vpk),
+  return {mix_grid(places, a.k_heads, a.vpk) * (1 + both + delta) + 1,
           (a.few ? a.seqs : places) * a.v_heads * (delta ? dk / 32 : dk * a.dv / 1024)};
 }
 // Whether they hold fewer than 2^32 threads each, where a call has them.
 static inline bool segments_fit(const MixArgs& a, int dk, bool delta, bool both) {
   if (a.tokens <= a.seg) return true;
-  const SegGrids n = segment_grids(a, dk, delta);
-  const int ways = both ? 2 : 1;
-  return grid_fits((ways + delta) * n.dir + 1, 4 * a.dv) && grid_fits(ways * n.combine, delta ? 2 * dk : 256);
+  const SegGrids n = segment_grids(a, dk, delta, both);
+  return grid_fits(n.states, 4 * a.dv) && grid_fits((1 + both) * n.combine, delta ? 2 * dk : 256);
 }
 
 template <typename T, bool BOTH>
@@ -637,8 +642,7 @@ static const void* pick_segments(int dk, int dv, bool delta) {
 template <typename T, bool BOTH>
 static int launch_segments(MixBwdArgs b, int dk, bool delta, hipStream_t stream) {
   const MixArgs& a = b.m;
-  const SegGrids n = segment_grids(a, dk, delta);
-  b.dir_blocks = (int)n.dir;
+  const SegGrids n = segment_grids(a, dk, delta, BOTH);
   b.elems = dk * a.dv;
   MixBwdArgs first = b;  // its own units are in no order yet: the last block makes it
   first.new_order = const_cast<int32_t*>(b.m.order);
@@ -646,14 +650,14 @@ static int launch_segments(MixBwdArgs b, int dk, bool delta, hipStream_t stream)
   first.all_slots = a.slots;
   first.m.slots = (int)long_places(a.tokens, a.seqs, a.seg);
   const int rc = launch_kernel(pick_segments<T, BOTH>(dk, a.dv, delta),
-                               (unsigned)(((BOTH ? 2 : 1) + delta) * n.dir + 1), 4 * a.dv, 0, stream, first);
+                               (unsigned)n.states, 4 * a.dv, 0, stream, first);
   if (rc) return rc;
   b.dir_blocks = (int)n.combine;
   const void* fn = reinterpret_cast<const void*>(&mix_combine_decay_kernel);
   if (delta)
     fn = dk == 64 ? reinterpret_cast<const void*>(&mix_combine_kernel<T, 64>)
                   : reinterpret_cast<const void*>(&mix_combine_kernel<T, 128>);
-  return launch_kernel(fn, (unsigned)((BOTH ? 2 : 1) * n.combine), delta ? 2 * dk : 256, 0, stream, b);
+  return launch_kernel(fn, (unsigned)((1 + BOTH) * n.combine), delta ? 2 * dk : 256, 0, stream, b);
 }
 
 }  // namespace rssm
