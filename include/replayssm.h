@@ -768,7 +768,9 @@ int linear_attention_decode(const rssm_mixer_dims* dims, const float* state,
  * gdn_scan_forward - the recurrence of gdn_standard_decode applied to every
  * token of packed sequences, with g = exp(log_g):
  *     S = g*S;  S += beta * outer(v - S@k, k);  o = scale * S@q
- * log_g, beta [tokens, HV] float32; the rest as linear_attention_forward.
+ * log_g, beta [tokens, HV] float32; the rest as linear_attention_forward.  With
+ * beta |k|^2 from 0 to 2 a token enlarges nothing, and neither do the kernels
+ * enlarge a rounding; beyond that the recurrence itself grows.
  */
 size_t gdn_scan_forward_workspace(const rssm_mixer_dims* dims);
 int gdn_scan_forward(const rssm_mixer_dims* dims, const void* q, const void* k,

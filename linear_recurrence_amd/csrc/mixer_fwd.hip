@@ -36,11 +36,13 @@ struct ForwardLds {
 // start; at the second the tiles of q, v and T are no longer read, and take the next
 // chunk's (K, read to the end, has two).  The outputs cross LDS and go to memory behind
 // the next barrier, a row's neighbours together: as the lanes hold them, 32 bytes of a
-// row a wave, their stores took a fifth of the time.  A chunk of the delta rule takes 6.7
-// us, of them 3 for the products (190 a wave, 16 cycles each) and as much for splitting
-// and weighing their factors: the two do not overlap, not even between waves.  4096
-// tokens of 32 heads of 128: 73 us (linear attention 47) for 8 chunks a workgroup; 16383
-// tokens: 312 and 194.  Waves of 32 columns, one a SIMD, were slower (89 us for 75).
+// row a wave, their stores took a fifth of the time.  A chunk of the delta rule takes 8.1
+// us: 3.0 of the matrix units (224 products a wave, 16 cycles each), 2.2 of the vector
+// units (splitting and weighing the products' factors) and 2.8 of LDS, a third of it bank
+// conflicts; they overlap little in one workgroup a compute unit.  One of linear attention
+// takes 5.7: 1.6, 1.5 and 1.9, and its bytes 3.5 at a copy's rate.  4096 tokens of 32 heads
+// of 128: 72 us (linear attention 51) for 8 chunks a workgroup; 16383 tokens: 300 and 196.
+// Waves of 32 columns, one a SIMD, were slower (a fifth).
 template <typename T, int K, int V, bool DELTA>
 __global__ void __launch_bounds__(4 * V, 2) mix_forward_kernel(const MixArgs a) {
   typedef Mat<T> M;
@@ -319,7 +321,7 @@ static size_t mix_forward_bytes(const rssm_mixer_dims* dims, bool delta) {
 // Columns of a head that a workgroup takes: 64 of 128 while there are compute units for
 // both halves' workgroups, since a chunk takes less time with one wave a SIMD than with
 // two, and every half does the tokens' products again (delta rule, 32 heads of 128, 512
-// tokens: 60 us instead of 69; fp32 122 instead of 170).
+// tokens: 62 us instead of 74; fp32 122 instead of 170; linear attention 39 instead of 43).
 static int forward_columns(const rssm_mixer_dims& d, long slots) {
   return d.dv == 128 && slots * d.v_heads <= 128 ? 64 : d.dv;
 }

@@ -47,7 +47,7 @@ struct StatesLds {
 // The segment slots by length, the longest first and those without a segment last, by one
 // workgroup (64 classes of length; the order within one does not matter to any result):
 // uneven sequences otherwise leave the longest to the end (16383 tokens of 13 sequences,
-// delta rule: the outputs' launch 315 us instead of 376).
+// delta rule: the outputs' launch takes a sixth less).
 __device__ static inline void order_segments(const MixArgs& a, int slots, int32_t* order) {
   __shared__ int count[65];
   for (int i = threadIdx.x; i < 65; i += blockDim.x) count[i] = 0;
@@ -78,10 +78,11 @@ __device__ static inline void order_segments(const MixArgs& a, int slots, int32_
 // segment adds and, as columns that start from the identity without V, the matrix that
 // its starting state is multiplied by, as first operands: rows of it and (BOTH) of its
 // transpose, which gradients go through.
-// With STORE it is memory bound: 8 x 1024 tokens of 32 heads of the delta rule write 0.8
-// GB and take 330 us, 254 with the products taken out and 208 with the loads and stores
-// taken out.  Without, products and what splits their factors bound it: 8 chunks a segment
-// take 80 us, two workgroups a compute unit (four waves a SIMD; one took 87).
+// With STORE memory bounds it more than products do: 8 x 1024 tokens of 32 heads of the
+// delta rule write 0.8 GB (and read 0.2) and take 288 us, three quarters of that with the
+// products taken out and five eighths with the loads and stores taken out.  Without,
+// products and what splits their factors bound it: 8 chunks a segment take 71 us, two
+// workgroups a compute unit (four waves a SIMD; two take a tenth longer).
 template <typename T, int K, int V, bool DELTA, bool STORE, bool BOTH>
 static __global__ void __launch_bounds__(4 * V, BOTH || sizeof(typename Mat<T>::E) == 4 ? 2 : 4) mix_states_kernel(const MixBwdArgs b) {
   typedef Mat<T> M;
@@ -107,7 +108,7 @@ static __global__ void __launch_bounds__(4 * V, BOTH || sizeof(typename Mat<T>::
   }
   // Batches without a sequence of several segments: found by one look at the table (the
   // blocks' searches, one a compute unit at a time, took 13 us for 8 sequences of 32
-  // heads; this takes 6).
+  // heads; this takes 5 to 7).
   if (!STORE && a.seqs > 1 && a.seqs <= 64 &&
       !__any(lane < a.seqs && seq_span(a.cu, lane, a.seqs, a.tokens).len > a.seg)) return;
   // The kinds of a segment's block stand side by side: in parts of the grid of their own,

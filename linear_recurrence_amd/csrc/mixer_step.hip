@@ -1,10 +1,10 @@
 // One token of linear attention for a batch of rows: S = g S + v k^T, o = scale S q.
 //
-// Memory bound: every state is read and written once (8 K V bytes for 9 K V
+// Memory bound: every state is read and written once (8 K V bytes for 5 K V
 // operations).  A workgroup takes one row and value head, 16 vectors of four state
-// elements a thread (8 where K or V is 64), all of them in flight before the first
-// is used; the lanes of a state row add up o by a transposing butterfly.  256 rows of 32
-// heads of 128 x 128: 1.07 GB in 180 us, 6.0 TB/s (a large copy on this card 4.7 to 5.1).
+// elements a thread (8 where K or V is 64, 4 where both are), all of them in flight
+// before the first is used; the lanes of a state row add up o by a transposing butterfly.  256 rows of 32
+// heads of 128 x 128: 1.07 GB in 187 us, 5.8 TB/s (a large copy on this card 4.7 to 5.1).
 #include "mixer_common.hpp"
 
 namespace rssm {
