@@ -715,7 +715,8 @@ typedef struct rssm_mixer_dims {
  * and final_state[s] = S (may be initial_state, or NULL).  q, k, v, o [16B]
  * with token strides that are multiples of 16 bytes; o [tokens, HV, V] dense.
  * Results that share memory with rows of q, k or v (backward: or do), and pools
- * that share memory with each other unless they are the same, are refused.
+ * that share memory with each other, are refused; o may be v itself where v is
+ * dense, and the pools may be one.
  * A slot out of range sets RSSM_ST_BAD_SLOT: its sequence starts from zeros and
  * stores no state.  Tokens are worked on in chunks of 64 of one sequence: a NaN
  * or infinity in a token's inputs may also show in the up to 63 tokens of its

@@ -607,6 +607,14 @@ static inline bool mix_meets(const MixArgs& a, const rssm_mixer_dims& d, const v
          rows_meet(a.k, a.k_stride * es, qk, d.tokens, out, bytes) ||
          rows_meet(a.v, a.v_stride * es, v, d.tokens, out, bytes);
 }
+// The same of o, which may be v itself: a head's columns of v are read by the workgroup
+// that writes them, each chunk's before its outputs go there.
+static inline bool output_meets(const MixArgs& a, const rssm_mixer_dims& d, const void* o) {
+  const long v = (long)d.v_heads * d.dv;
+  MixArgs other = a;
+  if (o == a.v && a.v_stride == v) other.v = nullptr;
+  return mix_meets(other, d, o, v);
+}
 // Whether two pools that are not one share memory: a slot's new state would be over another's.
 static inline bool pools_meet(const rssm_mixer_dims& d, const float* in, const float* out) {
   const long bytes = (long)d.num_slots * d.v_heads * d.dv * d.dk * 4;

@@ -380,7 +380,7 @@ static int mix_forward(const rssm_mixer_dims* dims, bool delta, const void* q, c
   if (!grid_fits(grid, 4 * columns) || !segments_fit(a, d.dk, delta, false) ||
       (delta && !grid_fits(cslots * ((d.v_heads + 3) / 4), 256)))
     return RSSM_ESHAPE;
-  if (mix_meets(a, d, o, (long)d.v_heads * d.dv) || pools_meet(d, initial_state, final_state)) return RSSM_EINVAL;
+  if (output_meets(a, d, o) || pools_meet(d, initial_state, final_state)) return RSSM_EINVAL;
   if (delta && d.tokens > 0) {
     rc = f32 ? launch_inverse<float, false>(a, d.dk, cslots, stream)
              : launch_inverse<bf16, false>(a, d.dk, cslots, stream);

@@ -99,7 +99,7 @@ extern "C" int linear_attention_decode(const rssm_mixer_dims* dims, const float*
   mix_fill(s.m, d);
   const long grid = (long)d.tokens * d.v_heads;
   if (!grid_fits(grid, 256)) return RSSM_ESHAPE;
-  if (mix_meets(s.m, d, o, (long)d.v_heads * d.dv) || pools_meet(d, state, new_state)) return RSSM_EINVAL;
+  if (output_meets(s.m, d, o) || pools_meet(d, state, new_state)) return RSSM_EINVAL;
   const void* fn = d.io_dtype == RSSM_F32 ? pick_step<float>(d.dk, d.dv) : pick_step<bf16>(d.dk, d.dv);
   return launch_kernel(fn, (unsigned)grid, 256, 0, stream, s);
 }

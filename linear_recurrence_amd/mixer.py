@@ -169,8 +169,8 @@ def linear_attention_forward(q, k, v, log_decay=None, cu_seqlens=None, initial_s
     cu_seqlens int32 [seqs + 1].  Sequence i starts from
     initial_state[slot_idx[i]] (float32 [slots, HV, V, K]; zeros without one or
     where has_initial[i], uint8, is 0) and stores final_state[slot_idx[i]],
-    which may be the same pool.  o shares no memory with q, k or v.  scale None:
-    1/sqrt(K).
+    which may be the same pool.  o shares no memory with q, k or
+    v, unless it is v.  scale None: 1/sqrt(K).
     """
     return _forward(False, q, k, v, log_decay, None, scale, cu_seqlens, initial_state, has_initial,
                     final_state, slot_idx, o, status, stream)

@@ -52,6 +52,8 @@ def test_results_over_inputs_are_refused(lib, fn):
     for out, row in (("gq", 256), ("gk", 256), ("gv", 512)) if back else (("o", 512),):
         for over, width in (("q", 256), ("k", 256), ("v", 512)) + ((("do", 512),) if back else ()):
             for at in (0, 16, 8 * width - 16, 16 - 8 * row):
+                if (out, over, at) == ("o", "v", 0):
+                    continue   # in place
                 assert call(out, over, at) == EINVAL, (out, over, at)
             if over == "do":
                 continue
